@@ -143,13 +143,14 @@ def _routing(T, K, E, B, gen):
 
 def _pack(h):
     """8-bit codes and scale bytes of pre-activations h [N, 2, I, B]: groups of 32 slots of one feature share
-    the power of two 2^(byte - 127), the codes are integers of at most 127."""
+    the power of two 2^(byte - 127), the codes are integers of at most 127.  The bytes are laid out
+    [N, 2, B/128, I/32, 4, 32]: 128 slots, 32 features, group, feature."""
     N, two, I, B = h.shape
     g = h.float().reshape(N, two, I, B // 32, 32)
     exponent = torch.frexp(g.abs().amax(-1))[1] - 1 + 127          # exponent field of the largest magnitude
     byte = (exponent - 6).clamp(1, 254)
     q = torch.round(torch.ldexp(g, (127 - byte)[..., None])).clamp(-127, 127)
-    scales = byte.reshape(N, two, I, B // 128, 4).permute(0, 1, 3, 2, 4)
+    scales = byte.reshape(N, two, I // 32, 32, B // 128, 4).permute(0, 1, 4, 2, 5, 3)
     return q.reshape(N, two, I, B).to(torch.int8), scales.contiguous().to(torch.uint8)
 
 
@@ -298,7 +299,7 @@ def _plain_pack(st, c):
 def _plain_moe_bwd8(st, c):
     T, H, I, E, K, B = (c[k] for k in ("T", "H", "I", "E", "K", "B"))
     cap = st["capacity"]
-    scale = st["sf"].float().permute(0, 1, 3, 2, 4).reshape(st["N"], 2, I, B // 32)
+    scale = st["sf"].float().permute(0, 1, 3, 5, 2, 4).reshape(st["N"], 2, I, B // 32)
     h = st["q"].float().reshape(st["N"], 2, I, B // 32, 32) * torch.exp2(scale - 127)[..., None]
     h = h.reshape(st["N"], 2 * I, B).transpose(1, 2).reshape(-1, 2 * I)[st["slot"]]
     at = st["expert"] * cap + st["place"]                # each grouped row's place in [E, cap]
@@ -464,7 +465,7 @@ def exact(case, seed):
             continue
         slot, flat = st["slot"][mine], st["order"][mine]
         b, j = slot // B, slot % B
-        saved = st["q"].double()[b, :, :, j] * sf[b, :, j // 128, :, j % 128 // 32]
+        saved = st["q"].double()[b, :, :, j] * sf[b, :, j // 128, :, j % 128 // 32].reshape(-1, 2, I)
         xw = x[flat // K] @ W1[e]
         h = saved.reshape(-1, 2 * I) + (xw - xw.detach())
         y = (torch.nn.functional.silu(h[:, :I]) * h[:, I:]) @ W2[e]
