@@ -55,8 +55,10 @@ enum {
 enum {
   MOE_STATUS_BAD_EXPERT_ID = 1, /* some ids[t,k] outside [0,E); those rows are skipped */
   MOE_STATUS_TIMEOUT = 2,       /* a pipeline wait exceeded its time limit; outputs invalid */
-  MOE_STATUS_BAD_ROUTE_META = 4 /* caller-supplied routing metadata is not a routing of the ids
+  MOE_STATUS_BAD_ROUTE_META = 4, /* caller-supplied routing metadata is not a routing of the ids
                                    (moe_bwd with expert_offsets given); outputs invalid */
+  MOE_STATUS_BAD_SEGMENTS = 8   /* sequence offsets decrease or leave [0, T] (moe_router_fwd,
+                                   moe_balance_fwd, moe_balance_bwd); outputs invalid */
 };
 
 enum { MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1 };
@@ -75,8 +77,10 @@ enum { MOE_SF_PLAIN = 0, MOE_SF_TILED = 1 };
  *             hidden_states and the gate/up weights (the pre-activation that checkpoint stores;
  *             its forward is h = x W1_e + b1_e of the routed SwiGLU layer), written to a
  *             checkpoint of the same layout in the workspace, rounded to bf16 like the stored one.
- *             Costs 4*T*K*H*I extra FLOPs and saves the caller the [N,2,I,B] tensor. */
-enum { MOE_ACT_CHECKPOINT = 0, MOE_ACT_RECOMPUTE = 1 };
+ *             Costs 4*T*K*H*I extra FLOPs and saves the caller the [N,2,I,B] tensor.
+ * CHECKPOINT8: read from the checkpoint in 8 bits (gate_up_ckpt_q, gate_up_ckpt_sf; see moe_glu_fwd),
+ *             33/64 of its bytes. */
+enum { MOE_ACT_CHECKPOINT = 0, MOE_ACT_RECOMPUTE = 1, MOE_ACT_CHECKPOINT8 = 2 };
 /* Gated activation a = act(gate) * up (sonic-moe `activation_type`): SwiGLU act = SiLU, GeGLU
  * act = GELU with the exact normal CDF, GELU(z) = z * Phi(z). */
 enum { MOE_GLU_SWIGLU = 0, MOE_GLU_GEGLU = 1 };
@@ -277,6 +281,8 @@ typedef struct MoeBwdArgs {
   const int32_t* block_offsets;        /* [E+1] first block of each expert in the block layout */
   const int32_t* token_position_to_id; /* [N*B] or NULL: [BW] slot -> token (checked only) */
   const int32_t* block_to_expert;      /* [N] or NULL: [BW] block -> expert (checked only) */
+  const int8_t* gate_up_ckpt_q;   /* (device) CHECKPOINT8: int8 codes [N,2,I,B] of the gate/up checkpoint */
+  const uint8_t* gate_up_ckpt_sf; /*          its scale bytes [N,2,B/128,I/32,4,32]; both 16-byte aligned */
 } MoeBwdArgs;
 
 /* Bytes of workspace moe_bwd needs for these shapes and options (pointers are not read). */
@@ -356,6 +362,122 @@ enum {
  * are skipped.  fp32 arithmetic.  T = 0: nothing is written (the pointers may be null). */
 int moe_router_bwd(int mode, int renorm, const float* logits, const float* scores, const float* dscores,
                    const int32_t* ids, int T, int K, int E, float* dlogits, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Router forward, load-balance and z losses                                                    */
+/* ------------------------------------------------------------------------------------------ */
+
+/* Bytes of workspace moe_router_fwd (with the losses) and moe_balance_fwd need; 0 for sizes they reject. */
+size_t moe_balance_workspace_size(int T, int K, int E, int num_seq);
+
+/* Top-K selection of a router, in the forms moe_router_bwd differentiates, and optionally the losses that
+ * keep its experts in balance, from one pass over the logits.
+ *
+ * logits (device) fp32 [T,E] with row stride ld_logits.  The K largest logits of each token are selected in
+ * descending order, equal ones by ascending expert; -0 equals +0, and a NaN counts as larger than every
+ * number (it reaches the scores).  A logit of -inf masks its expert: a slot that only masked experts are
+ * left for gets id -1 (the unused slot of moe_bwd and moe_route_meta) and score 0.
+ *   scores (device) fp32 [T,K], ids (device) int32 [T,K]: SOFTMAX_OVER_TOPK, TOPK_OVER_SOFTMAX (divided by
+ *   their sum with `renorm`) or TOPK (see moe_router_bwd).
+ *   lse (device, nullable) fp32 [T]: logsumexp of the token's logits, -inf with every expert masked.
+ * seg_offsets (device, nullable) int32 [num_seq+1]: sequence s is tokens seg_offsets[s] ..
+ *   seg_offsets[s+1]-1, nondecreasing in [0,T] (empty sequences are fine); tokens before the first and
+ *   behind the last are padding: ids -1, scores 0, lse -inf, no part in the losses.  NULL (num_seq 1): one
+ *   sequence of all T tokens.
+ * The losses (counts, prob_sum, loss all given, or all NULL), with n_s the tokens of sequence s, n their sum,
+ * p = softmax(logits):
+ *   counts (device) int32 [num_seq,E]: slots of s routed to e;  prob_sum (device) fp32 [num_seq,E]: sum of p_te
+ *   loss (device) fp32 [2]: alpha sum_s (n_s/n) sum_e (E counts_se / (K n_s)) (prob_sum_se / n_s)   (balance)
+ *                           beta / n sum_t lse_t^2                                               (z)
+ * A token with every expert masked counts in n_s and adds nothing else.
+ * status_dev (device, nullable) int32 [1]: reset, then MOE_STATUS_BAD_SEGMENTS for bad offsets (checked with
+ * the losses; outputs then invalid, no access leaves its buffer).
+ * 1 <= K <= E <= 1024, K <= 64.  Sums in fp32 in a fixed order (bit-reproducible).  T = 0: counts, prob_sum
+ * and loss are zeroed, nothing else is written.  The workspace is only needed with the losses. */
+int moe_router_fwd(int mode, int renorm, const float* logits, int64_t ld_logits, int T, int K, int E,
+                   const int32_t* seg_offsets, int num_seq, float alpha, float beta, float* scores, int32_t* ids,
+                   float* lse, int32_t* counts, float* prob_sum, float* loss, int32_t* status_dev, void* workspace,
+                   size_t workspace_bytes, moe_stream_t stream);
+
+/* The losses alone, for ids (device) int32 [T,K] selected elsewhere (ids outside [0,E) are not counted). */
+int moe_balance_fwd(const float* logits, int64_t ld_logits, const int32_t* ids, int T, int K, int E,
+                    const int32_t* seg_offsets, int num_seq, float alpha, float beta, float* lse, int32_t* counts,
+                    float* prob_sum, float* loss, int32_t* status_dev, void* workspace, size_t workspace_bytes,
+                    moe_stream_t stream);
+
+/* Gradient of dloss[0] * balance + dloss[1] * z by the logits (the counts are constants):
+ *   dlogits[t,j] = dloss0 alpha E / (K n n_s) p_tj (counts_sj - sum_e counts_se p_te) + dloss1 2 beta / n lse_t p_tj
+ * plus add[t,j] when given (device, fp32 [T,E], row stride ld_add; e.g. moe_router_bwd's dlogits; it may be
+ * dlogits itself).  lse and counts are the forward's.  dloss (device, nullable: ones) fp32 [2].  Padding
+ * tokens and tokens with every expert masked get `add` alone, or 0.  dlogits (device) fp32 [T,E], fully written. */
+int moe_balance_bwd(const float* logits, int64_t ld_logits, const float* lse, const int32_t* counts, int T, int K,
+                    int E, const int32_t* seg_offsets, int num_seq, float alpha, float beta, const float* dloss,
+                    const float* add, int64_t ld_add, float* dlogits, int32_t* status_dev, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Gated activation with the 8-bit checkpoint                                                    */
+/* ------------------------------------------------------------------------------------------ */
+
+/* a = act(gate) * up of the forward, and the gate/up checkpoint in 8 bits for moe_bwd (CHECKPOINT8).
+ *
+ * h (device) bf16 [rows,2I], row stride ldh (a multiple of 8): pre-activations of the grouped rows (the order
+ *   of moe_route_meta's x_gather_idx), columns by gate_up_layout.
+ * expert_offsets, block_offsets [E+1], block_to_expert [num_blocks] (device): moe_route_meta's; num_blocks is
+ *   the checkpoint's N.  Rows at or past expert_offsets[E] (or `rows`) are not touched.
+ * s (device, nullable) fp32 [num_slots = T*K] with s_scatter_idx (device) int32 [rows]: a is multiplied by the
+ *   row's score (0 for an index outside [0,num_slots)).
+ * a (device) bf16 [rows,I], rounded once from fp32.
+ * ckpt_q, ckpt_sf (device, both or neither): int8 codes [N,2,I,B] in the layout of gate_up_ckpt and scale bytes
+ *   [N,2,B/128,I/32,4,32] (128-slot tile, 32 features, 32-slot group, feature).  32 consecutive slots of one
+ *   feature share byte = max(1, exponent field of their largest magnitude - 6); a code is
+ *   round-to-nearest-even(v 2^(127-byte)) clamped to +-127 and stands for code 2^(byte-127), so a value is off
+ *   by at most half a step, 1/128 of the group's largest magnitude (a step where the clamp acts; groups whose
+ *   largest magnitude is under 2^-120 keep the step 2^-126).  A group holding a NaN or an infinity gets byte
+ *   255 and reads as NaN (in moe_bwd NaN or infinite).  Slots of a 128-slot tile behind the expert's last row
+ *   are zeros; tiles without a row are not written.
+ * I a multiple of 64 (moe_bwd: of 128); tensors 16-byte aligned.  rows = 0: nothing is written. */
+int moe_glu_fwd(const void* h, int64_t ldh, int64_t rows, int I, int E, int block_size, int64_t num_blocks, int glu,
+                int gate_up_layout, const int32_t* expert_offsets, const int32_t* block_offsets,
+                const int32_t* block_to_expert, const float* s, const int32_t* s_scatter_idx, int64_t num_slots,
+                void* a, int8_t* ckpt_q, uint8_t* ckpt_sf, moe_stream_t stream);
+
+/* The 8-bit checkpoint's values (bf16 holds them exactly) as grouped rows h [rows,2I]. */
+int moe_ckpt8_unpack(const int8_t* ckpt_q, const uint8_t* ckpt_sf, int64_t rows, int I, int E, int block_size,
+                     int64_t num_blocks, int gate_up_layout, const int32_t* expert_offsets, const int32_t* block_offsets,
+                     const int32_t* block_to_expert, void* h, int64_t ldh, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Layer normalisation                                                                          */
+/* ------------------------------------------------------------------------------------------ */
+
+enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 };
+/* LAYER: (s - mean) / sqrt(var + eps);  RMS: s / sqrt(mean(s^2) + eps). */
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
+
+/* y = norm(s) * gamma + beta over rows of H, with s = x, or with a residual s = x + residual rounded to the
+ * rows' type and stored to `sum` (the updated residual stream; it may be x or residual itself when that is
+ * dense).  x, residual (device) x_dtype [T,H] with row strides ldx, ldr; y, sum (device) x_dtype [T,H] dense;
+ * gamma, beta (device) w_dtype [H], beta nullable; mean (LAYER), rstd (device) fp32 [T]: the backward's.
+ * Statistics and arithmetic in fp32, y rounded once.  Any H >= 1; T = 0 writes nothing. */
+int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* gamma,
+                   const void* beta, int x_dtype, int w_dtype, int64_t T, int64_t H, float eps, void* y, void* sum,
+                   float* mean, float* rstd, moe_stream_t stream);
+
+/* Bytes of workspace layer_norm_bwd needs. */
+size_t layer_norm_bwd_workspace_size(int64_t T, int64_t H);
+
+/* Gradients of layer_norm_fwd, x being the normalised rows (with a residual: its `sum`):
+ *   dx = rstd (w - mean(w) - xh mean(w xh)) + dres,  w = dy gamma, xh = (x - mean) rstd   (RMS: no mean(w))
+ *   dgamma = sum_t dy xh,  dbeta = sum_t dy
+ * dy, x, dres (device) x_dtype [T,H] with row strides; dres nullable: the gradient that reaches s past the norm
+ * (the skip connection).  dx (device) x_dtype [T,H] dense, rounded once; it is the gradient of x and of the
+ * residual alike, and may be dres itself when that is dense.  dgamma, dbeta (device) fp32 [H], dbeta nullable;
+ * accumulate = 1 adds to them.  Sums over rows in fp32 in a fixed order (bit-reproducible).  T = 0: dgamma and
+ * dbeta are zeroed, or left as they are with accumulate. */
+int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gamma,
+                   const float* mean, const float* rstd, const void* dres, int64_t ldres, int x_dtype, int w_dtype,
+                   int64_t T, int64_t H, void* dx, float* dgamma, float* dbeta, int accumulate, void* workspace,
+                   size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
 /* Instrumentation                                                                             */

@@ -19,10 +19,12 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoebwd.s
 
 QUANT_ROWWISE, QUANT_COLWISE = 0, 1
 SF_PLAIN, SF_TILED = 0, 1
-STATUS_BAD_EXPERT_ID, STATUS_TIMEOUT, STATUS_BAD_ROUTE_META = 1, 2, 4
-ACT_CHECKPOINT, ACT_RECOMPUTE = 0, 1
+STATUS_BAD_EXPERT_ID, STATUS_TIMEOUT, STATUS_BAD_ROUTE_META, STATUS_BAD_SEGMENTS = 1, 2, 4, 8
+ACT_CHECKPOINT, ACT_RECOMPUTE, ACT_CHECKPOINT8 = 0, 1, 2
 GLU_SWIGLU, GLU_GEGLU = 0, 1
 GATE_UP_CONCAT, GATE_UP_INTERLEAVED = 0, 1
+DT_BF16, DT_F32 = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
 
 WS_REGIONS = ["EXPERT_OFFSETS", "TILE_OFFSETS", "BLOCK_OFFSETS", "TILE_ROW_FLAT", "FLAT_TILE_ROW",
               "DOUT_G", "DOUT_G_SF", "DOUT_GT", "DOUT_GT_SF", "X_GT", "X_GT_SF", "DH", "DH_SF",
@@ -32,7 +34,9 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_num_blocks_bound", "moe_route_
             "moe_route_meta", "mxfp8_quantize", "moe_bwd_workspace_size", "moe_bwd",
             "moe_bwd_workspace_region", "moe_tile_rows_capacity", "linear_bwd_workspace_size",
             "linear_bwd", "moe_profile_enable", "moe_profile_read", "moe_kernel_launches",
-            "moe_route_meta_noalloc", "moe_router_bwd", "moe_set_option", "moe_get_option"]
+            "moe_route_meta_noalloc", "moe_router_bwd", "moe_set_option", "moe_get_option",
+            "moe_balance_workspace_size", "moe_router_fwd", "moe_balance_fwd", "moe_balance_bwd", "moe_glu_fwd",
+            "moe_ckpt8_unpack", "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd"]
 
 # library options (moe_set_option)
 OPTIONS = ["WAIT_LIMIT_NS", "PAIR_GEMMS", "PAIR_TILE_N", "G1_TILE_N", "G2_TILE_N", "G3_TILE_N", "G4_TILE_N",
@@ -58,7 +62,8 @@ class MoeBwdArgs(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("intermediate_ckpt", "scaled_intermediate_ckpt", "down_proj_act_ckpt",
                                                "gate_act_ckpt")] + \
                [(n, ctypes.c_void_p) for n in ("expert_offsets", "s_scatter_idx", "block_offsets",
-                                               "token_position_to_id", "block_to_expert")]
+                                               "token_position_to_id", "block_to_expert")] + \
+               [(n, ctypes.c_void_p) for n in ("gate_up_ckpt_q", "gate_up_ckpt_sf")]
 
 ROUTE_META_FIELDS = ("expert_offsets", "s_scatter_idx", "block_offsets", "token_position_to_id", "block_to_expert")
 
@@ -74,7 +79,7 @@ def lib():
     if not os.path.exists(LIB_PATH):
         raise MoeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
     L = ctypes.CDLL(LIB_PATH)
-    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "moe_last_error": ([], ctypes.c_char_p),
         "moe_version": ([], ctypes.c_char_p),
@@ -96,6 +101,16 @@ def lib():
         "moe_router_bwd": ([i32, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp], i32),
         "moe_set_option": ([i32, i64], i32),
         "moe_get_option": ([i32], i64),
+        "moe_balance_workspace_size": ([i32] * 4, sz),
+        "moe_router_fwd": ([i32, i32, vp, i64, i32, i32, i32, vp, i32, f32, f32] + [vp] * 8 + [sz, vp], i32),
+        "moe_balance_fwd": ([vp, i64, vp, i32, i32, i32, vp, i32, f32, f32] + [vp] * 6 + [sz, vp], i32),
+        "moe_balance_bwd": ([vp, i64, vp, vp, i32, i32, i32, vp, i32, f32, f32, vp, vp, i64, vp, vp, vp], i32),
+        "moe_glu_fwd": ([vp, i64, i64, i32, i32, i32, i64, i32, i32] + [vp] * 5 + [i64, vp, vp, vp, vp], i32),
+        "moe_ckpt8_unpack": ([vp, vp, i64, i32, i32, i32, i64, i32, vp, vp, vp, vp, i64, vp], i32),
+        "layer_norm_fwd": ([i32, vp, i64, vp, i64, vp, vp, i32, i32, i64, i64, f32, vp, vp, vp, vp, vp], i32),
+        "layer_norm_bwd_workspace_size": ([i64, i64], sz),
+        "layer_norm_bwd": ([i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, i32, i32, i64, i64, vp, vp, vp, i32, vp, sz,
+                            vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -274,10 +289,11 @@ class MoeBwd:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._keep = []
 
-    def bind(self, *, x, dout, s, ids, ckpt=None, W1=None, W2=None, W1_q=None, W1_sf=None, W2_q=None, W2_sf=None,
+    def bind(self, *, x, dout, s, ids, ckpt=None, ckpt_q=None, ckpt_sf=None, W1=None, W2=None, W1_q=None, W1_sf=None, W2_q=None, W2_sf=None,
              b2=None, W1t=None, W1t_q=None, W1t_sf=None, b1=None, num_valid_tokens=None, intermediate_ckpt=None,
              scaled_intermediate_ckpt=None, down_proj_act_ckpt=None, gate_act_ckpt=None, route_meta=None):
-        """ckpt: the [N,2,I,B] checkpoint (act_src ACT_CHECKPOINT).  W1t (bf16 [E,2I,H]) or W1t_q/W1t_sf
+        """ckpt: the [N,2,I,B] checkpoint (act_src ACT_CHECKPOINT); ckpt_q, ckpt_sf: its 8-bit form, as
+        glu_fwd returns it (act_src ACT_CHECKPOINT8).  W1t (bf16 [E,2I,H]) or W1t_q/W1t_sf
         and optionally b1 [E,2I]: the operands of the recomputation (act_src ACT_RECOMPUTE).
         intermediate_ckpt / scaled_intermediate_ckpt / gate_act_ckpt [N,I,B] and down_proj_act_ckpt
         [N,B,H] (bf16, block layout): saved forward values, see the MoeBwdArgs fields.
@@ -285,7 +301,7 @@ class MoeBwd:
         s_scatter_idx, block_offsets and optionally token_position_to_id, block_to_expert -- e.g.
         route_meta()'s result); None: moe_bwd computes it from ids."""
         _need_cuda(x, dout, s, ids, ckpt, W1, W2, W1_q, W1_sf, W2_q, W2_sf, b2, W1t, W1t_q, W1t_sf, b1, num_valid_tokens,
-                   intermediate_ckpt, scaled_intermediate_ckpt, down_proj_act_ckpt, gate_act_ckpt)
+                   intermediate_ckpt, scaled_intermediate_ckpt, down_proj_act_ckpt, gate_act_ckpt, ckpt_q, ckpt_sf)
         if num_valid_tokens is not None:
             assert num_valid_tokens.dtype == torch.int32 and num_valid_tokens.numel() == 1
         a = self.a
@@ -302,6 +318,10 @@ class MoeBwd:
             N = num_blocks_bound(a.T, a.K, a.E, a.block_size)
             assert ckpt.dtype == torch.bfloat16
             assert tuple(ckpt.shape) == (N, 2, a.I, a.block_size), (tuple(ckpt.shape), N)
+        if ckpt_q is not None:
+            assert ckpt_q.dtype == torch.int8 and tuple(ckpt_q.shape) == (Nb, 2, a.I, a.block_size)
+        if ckpt_sf is not None:
+            assert ckpt_sf.dtype == torch.uint8 and tuple(ckpt_sf.shape) == ckpt8_sf_shape(Nb, a.I, a.block_size)
         if W1t is not None:
             assert W1t.dtype == torch.bfloat16 and tuple(W1t.shape) == (a.E, 2 * a.I, a.H)
         if b1 is not None:
@@ -310,7 +330,8 @@ class MoeBwd:
                             W1_sf=W1_sf, W2_q=W2_q, W2_sf=W2_sf, b2=b2, W1t=W1t, W1t_q=W1t_q, W1t_sf=W1t_sf,
                             b1=b1, num_valid_tokens=num_valid_tokens, intermediate_ckpt=intermediate_ckpt,
                             scaled_intermediate_ckpt=scaled_intermediate_ckpt,
-                            down_proj_act_ckpt=down_proj_act_ckpt, gate_act_ckpt=gate_act_ckpt).items():
+                            down_proj_act_ckpt=down_proj_act_ckpt, gate_act_ckpt=gate_act_ckpt,
+                            gate_up_ckpt_q=ckpt_q, gate_up_ckpt_sf=ckpt_sf).items():
             setattr(a, name, None if t is None else t.data_ptr())
         for name in ("dx", "dW1", "dW2", "ds", "db1", "db2", "ds_masked", "status"):
             t = getattr(self, name)
@@ -324,7 +345,7 @@ class MoeBwd:
         a.workspace_bytes = self.workspace.numel()
         self._keep = [x, dout, s, ids, ckpt, W1, W2, W1_q, W1_sf, W2_q, W2_sf, b2, W1t, W1t_q, W1t_sf, b1,
                       num_valid_tokens, intermediate_ckpt, scaled_intermediate_ckpt, down_proj_act_ckpt, gate_act_ckpt,
-                      *rm.values()]
+                      ckpt_q, ckpt_sf, *rm.values()]
         return self
 
     def run(self, stream=None):
@@ -348,18 +369,20 @@ class MoeBwd:
         return tile_rows_capacity(self.a.T, self.a.K, self.a.E)
 
 
-def moe_bwd(*, x, dout, s, ids, E, I, block_size, ckpt=None, W1=None, W2=None, W1_q=None, W1_sf=None, W2_q=None,
+def moe_bwd(*, x, dout, s, ids, E, I, block_size, ckpt=None, ckpt_q=None, ckpt_sf=None, W1=None, W2=None, W1_q=None, W1_sf=None, W2_q=None,
             W2_sf=None, b2=None, W1t=None, W1t_q=None, W1t_sf=None, b1=None, precision=PREC_BF16,
             affinity=AFFINITY_ON_H, fp8_act=FP8_E5M2, fp8_w=FP8_E4M3, accumulate=False, stream=None) -> dict:
     """One-shot MoE backward (allocates outputs and workspace).  Returns dx, dW1, dW2, ds, db1, db2
-    and the device status word (nonzero: invalid expert ids or a pipeline timeout).  Without ckpt the
-    gate/up pre-activations are recomputed from x and W1t (or W1t_q/W1t_sf) plus b1."""
+    and the device status word (nonzero: invalid expert ids or a pipeline timeout).  The gate/up
+    pre-activations come from ckpt, from its 8-bit form ckpt_q/ckpt_sf, or, with neither, from a
+    recomputation of x and W1t (or W1t_q/W1t_sf) plus b1."""
     T, H = x.shape
     K = ids.shape[1]
     op = MoeBwd(T=T, H=H, I=I, E=E, K=K, block_size=block_size, precision=precision, affinity=affinity,
                 fp8_act=fp8_act, fp8_w=fp8_w, has_bias=b2 is not None, accumulate=accumulate,
-                act_src=ACT_CHECKPOINT if ckpt is not None else ACT_RECOMPUTE, device=x.device)
-    op.bind(x=x, dout=dout, s=s, ids=ids, ckpt=ckpt, W1=W1, W2=W2, W1_q=W1_q, W1_sf=W1_sf, W2_q=W2_q,
+                act_src=(ACT_CHECKPOINT if ckpt is not None else ACT_CHECKPOINT8 if ckpt_q is not None
+                         else ACT_RECOMPUTE), device=x.device)
+    op.bind(x=x, dout=dout, s=s, ids=ids, ckpt=ckpt, ckpt_q=ckpt_q, ckpt_sf=ckpt_sf, W1=W1, W2=W2, W1_q=W1_q, W1_sf=W1_sf, W2_q=W2_q,
             W2_sf=W2_sf, b2=b2, W1t=W1t, W1t_q=W1t_q, W1t_sf=W1t_sf, b1=b1).run(stream)
     out = op.outputs()
     out["_op"] = op
@@ -379,6 +402,254 @@ def router_bwd(mode: int, ids: torch.Tensor, dscores: torch.Tensor, E: int, logi
                               _ptr(out), _stream(stream))
     _check(rc, "moe_router_bwd")
     return out
+
+
+def _rows(t, dtype, shape, name, dev):
+    """Row stride of a 2-D CUDA tensor whose rows are dense; raises on anything else."""
+    if not t.is_cuda or t.device != dev:
+        raise MoeError(f"{name} must be a CUDA tensor on {dev} (there is no CPU path)")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise MoeError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise MoeError(f"{name} must have dense rows")
+    return max(t.stride(0), shape[1]) if shape[0] <= 1 else t.stride(0)
+
+
+def _dense(t, dtype, shape, name, dev):
+    """Pointer of a dense CUDA tensor of this type and shape, None for None; raises on anything else."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != dev:
+        raise MoeError(f"{name} must be a CUDA tensor on {dev} (there is no CPU path)")
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+class _on:
+    """The stream a call runs on.  What the call allocates belongs to that stream, so that nothing else is
+    given its memory while the call may still use it; tensors made on another stream are the caller's to order
+    (Stream.wait_stream) and to keep."""
+
+    def __init__(self, stream, dev):
+        if dev.type != "cuda":
+            raise MoeError("tensors must be CUDA tensors (there is no CPU path)")
+        if dev.index != torch.cuda.current_device():
+            raise MoeError(f"tensors are on {dev}, which is not the current device")
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc) if self.ctx is not None else False
+
+
+_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+
+
+def _norm_types(x, gamma, what):
+    if x.dim() != 2:
+        raise MoeError(f"{what}: x must be [T, H]")
+    if x.dtype not in _DT or gamma.dtype not in _DT:
+        raise MoeError(f"{what}: rows and weights must be bfloat16 or float32")
+    return x.shape[0], x.shape[1], x.device
+
+
+def layer_norm_fwd(x, gamma, beta=None, eps: float = 1e-5, residual=None, kind: int = NORM_LAYER, stream=None) -> dict:
+    """layer_norm_fwd on rows x [T, H] (bf16 or fp32, dense rows of any stride), plus `residual` when given.
+    Returns y, mean (NORM_LAYER, else None), rstd, and sum = x + residual (None without a residual), the
+    rows that layer_norm_bwd takes as its x.  gamma, beta [H] in bf16 or fp32."""
+    T, H, dev = _norm_types(x, gamma, "layer_norm_fwd")
+    ldx = _rows(x, x.dtype, (T, H), "x", dev)
+    ldr = 0 if residual is None else _rows(residual, x.dtype, (T, H), "residual", dev)
+    g, b = _dense(gamma, gamma.dtype, (H,), "gamma", dev), _dense(beta, gamma.dtype, (H,), "beta", dev)
+    with _on(stream, dev) as st:
+        y = torch.empty(T, H, dtype=x.dtype, device=dev)
+        total = None if residual is None else torch.empty(T, H, dtype=x.dtype, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        mean = torch.empty(T, dtype=torch.float32, device=dev) if kind == NORM_LAYER else None
+        rc = lib().layer_norm_fwd(kind, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, g, b,
+                                  _DT[x.dtype], _DT[gamma.dtype], T, H, eps, y.data_ptr(),
+                                  None if total is None else total.data_ptr(),
+                                  None if mean is None else mean.data_ptr(), rstd.data_ptr(), st)
+    _check(rc, "layer_norm_fwd")
+    return dict(y=y, mean=mean, rstd=rstd, sum=total)
+
+
+def layer_norm_bwd(dy, x, gamma, mean, rstd, dres=None, kind: int = NORM_LAYER, dbeta: bool = True,
+                   accumulate_into=None, stream=None) -> dict:
+    """layer_norm_bwd: dx (plus `dres`, the gradient that reaches the rows past the norm), dgamma and, with a
+    mean and unless dbeta is False, dbeta, in fp32.  x are the normalised rows (with a residual: the forward's
+    sum).  accumulate_into: an earlier result whose dgamma and dbeta are added to in place."""
+    T, H, dev = _norm_types(x, gamma, "layer_norm_bwd")
+    ldx, lddy = _rows(x, x.dtype, (T, H), "x", dev), _rows(dy, x.dtype, (T, H), "dy", dev)
+    ldres = 0 if dres is None else _rows(dres, x.dtype, (T, H), "dres", dev)
+    g, r = _dense(gamma, gamma.dtype, (H,), "gamma", dev), _dense(rstd, torch.float32, (T,), "rstd", dev)
+    m = _dense(mean, torch.float32, (T,), "mean", dev) if kind == NORM_LAYER else None
+    with _on(stream, dev) as st:
+        dx = torch.empty(T, H, dtype=x.dtype, device=dev)
+        if accumulate_into is not None:
+            dg, db = accumulate_into["dgamma"], accumulate_into["dbeta"]
+            _dense(dg, torch.float32, (H,), "dgamma", dev)
+            _dense(db, torch.float32, (H,), "dbeta", dev)
+        else:
+            dg = torch.empty(H, dtype=torch.float32, device=dev)
+            db = torch.empty(H, dtype=torch.float32, device=dev) if dbeta and kind == NORM_LAYER else None
+        ws = _ws(lib().layer_norm_bwd_workspace_size(T, H), dev)
+        rc = lib().layer_norm_bwd(kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, g, m, r,
+                                  None if dres is None else dres.data_ptr(), ldres, _DT[x.dtype], _DT[gamma.dtype], T, H,
+                                  dx.data_ptr(), dg.data_ptr(), None if db is None else db.data_ptr(),
+                                  int(accumulate_into is not None), ws.data_ptr(), ws.numel(), st)
+    _check(rc, "layer_norm_bwd")
+    return dict(dx=dx, dgamma=dg, dbeta=db)
+
+
+def _segments(seg_offsets, dev):
+    if seg_offsets is None:
+        return None, 1
+    if seg_offsets.dim() != 1 or seg_offsets.numel() < 2:
+        raise MoeError("seg_offsets must be int32 [num_seq + 1]")
+    n = seg_offsets.numel()
+    return _dense(seg_offsets, torch.int32, (n,), "seg_offsets", dev), n - 1
+
+
+def _balance_outputs(T, K, E, S, dev):
+    return (torch.empty(S, E, dtype=torch.int32, device=dev), torch.empty(S, E, dtype=torch.float32, device=dev),
+            torch.empty(2, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
+            _ws(lib().moe_balance_workspace_size(T, K, E, S), dev))
+
+
+def router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False, seg_offsets=None, alpha: float = 0.0,
+               beta: float = 0.0, balance: bool = True, stream=None) -> dict:
+    """moe_router_fwd: top-K of fp32 logits [T, E] (dense rows of any stride).  Returns scores [T, K], ids [T, K],
+    lse [T] and, unless balance is False, counts and prob_sum [num_seq, E], loss [2] = (balance, z) and status."""
+    if logits.dim() != 2:
+        raise MoeError("logits must be [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    ld = _rows(logits, torch.float32, (T, E), "logits", dev)
+    off, S = _segments(seg_offsets, dev)
+    with _on(stream, dev) as st:
+        scores = torch.empty(T, K, dtype=torch.float32, device=dev)
+        ids = torch.empty(T, K, dtype=torch.int32, device=dev)
+        out = dict(scores=scores, ids=ids, lse=torch.empty(T, dtype=torch.float32, device=dev))
+        p = [None] * 4
+        ws = None
+        if balance:
+            counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
+            out.update(counts=counts, prob_sum=prob, loss=loss, status=status)
+            p = [counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr()]
+        rc = lib().moe_router_fwd(mode, int(renorm), logits.data_ptr(), ld, T, K, E, off, S, alpha, beta,
+                                  scores.data_ptr(), ids.data_ptr(), out["lse"].data_ptr(), *p,
+                                  None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st)
+    _check(rc, "moe_router_fwd")
+    return out
+
+
+def balance_fwd(logits: torch.Tensor, ids: torch.Tensor, seg_offsets=None, alpha: float = 0.0, beta: float = 0.0,
+                stream=None) -> dict:
+    """moe_balance_fwd: the losses of router_fwd for ids [T, K] selected elsewhere.  Returns lse, counts, prob_sum,
+    loss and status."""
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise MoeError("logits must be [T, E] and ids [T, K]")
+    (T, E), K, dev = logits.shape, ids.shape[1], logits.device
+    ld = _rows(logits, torch.float32, (T, E), "logits", dev)
+    idp = _dense(ids, torch.int32, (T, K), "ids", dev)
+    off, S = _segments(seg_offsets, dev)
+    with _on(stream, dev) as st:
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
+        rc = lib().moe_balance_fwd(logits.data_ptr(), ld, idp, T, K, E, off, S, alpha, beta, lse.data_ptr(),
+                                   counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), st)
+    _check(rc, "moe_balance_fwd")
+    return dict(lse=lse, counts=counts, prob_sum=prob, loss=loss, status=status)
+
+
+def balance_bwd(logits: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor, K: int, seg_offsets=None,
+                alpha: float = 0.0, beta: float = 0.0, dloss=None, add=None, stream=None) -> torch.Tensor:
+    """moe_balance_bwd: gradient of dloss[0] * balance + dloss[1] * z by the logits [T, E], plus `add` (e.g.
+    router_bwd's result).  lse and counts are the forward's."""
+    if logits.dim() != 2:
+        raise MoeError("logits must be [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    ld = _rows(logits, torch.float32, (T, E), "logits", dev)
+    ld_add = 0 if add is None else _rows(add, torch.float32, (T, E), "add", dev)
+    off, S = _segments(seg_offsets, dev)
+    lp, cp = _dense(lse, torch.float32, (T,), "lse", dev), _dense(counts, torch.int32, (S, E), "counts", dev)
+    dl = _dense(dloss, torch.float32, (2,), "dloss", dev)
+    with _on(stream, dev) as st:
+        out = torch.empty(T, E, dtype=torch.float32, device=dev)
+        rc = lib().moe_balance_bwd(logits.data_ptr(), ld, lp, cp, T, K, E, off, S, alpha, beta, dl,
+                                   None if add is None else add.data_ptr(), ld_add, out.data_ptr(), None, st)
+    _check(rc, "moe_balance_bwd")
+    return out
+
+
+def ckpt8_sf_shape(N: int, I: int, block_size: int) -> tuple:
+    """Shape of the scale bytes of an 8-bit checkpoint: 128-slot tile, 32 features, 32-slot group, feature."""
+    return (N, 2, block_size // 128, I // 32, 4, 32)
+
+
+def _meta_ptrs(route_meta, dev):
+    eo, bo, b2e = (route_meta[k] for k in ("expert_offsets", "block_offsets", "block_to_expert"))
+    E = eo.numel() - 1
+    return (_dense(eo, torch.int32, (E + 1,), "expert_offsets", dev), _dense(bo, torch.int32, (E + 1,), "block_offsets", dev),
+            _dense(b2e, torch.int32, (b2e.numel(),), "block_to_expert", dev), E, b2e.numel())
+
+
+def glu_fwd(h: torch.Tensor, route_meta: dict, block_size: int, glu: int = GLU_SWIGLU,
+            gate_up_layout: int = GATE_UP_CONCAT, s=None, checkpoint: bool = True, stream=None) -> dict:
+    """moe_glu_fwd on the grouped rows h bf16 [rows, 2I]: a = act(gate) * up [rows, I] (times the row's score
+    with s [T, K], whose s_scatter_idx route_meta then holds) and, unless checkpoint is False, the 8-bit
+    checkpoint ckpt_q [N, 2, I, B], ckpt_sf for moe_bwd.  route_meta: route_meta()'s dict."""
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise MoeError("h must be [rows, 2I]")
+    rows, I, dev = h.shape[0], h.shape[1] // 2, h.device
+    ldh = _rows(h, torch.bfloat16, (rows, 2 * I), "h", dev)
+    eo, bo, b2e, E, N = _meta_ptrs(route_meta, dev)
+    sp = sip = None
+    slots = 0
+    if s is not None:
+        slots = s.numel()
+        sp = _dense(s, torch.float32, tuple(s.shape), "s", dev)
+        idx = route_meta["s_scatter_idx"]
+        if idx.numel() < rows:
+            raise MoeError("s_scatter_idx is shorter than the rows of h")
+        sip = _dense(idx, torch.int32, tuple(idx.shape), "s_scatter_idx", dev)
+    with _on(stream, dev) as st:
+        a = torch.empty(rows, I, dtype=torch.bfloat16, device=dev)
+        q = sf = None
+        if checkpoint:
+            q = torch.empty(N, 2, I, block_size, dtype=torch.int8, device=dev)
+            sf = torch.empty(ckpt8_sf_shape(N, I, block_size), dtype=torch.uint8, device=dev)
+        rc = lib().moe_glu_fwd(h.data_ptr(), ldh, rows, I, E, block_size, N, glu, gate_up_layout, eo, bo, b2e, sp, sip,
+                               slots, a.data_ptr(), None if q is None else q.data_ptr(),
+                               None if sf is None else sf.data_ptr(), st)
+    _check(rc, "moe_glu_fwd")
+    return dict(a=a, ckpt_q=q, ckpt_sf=sf)
+
+
+def ckpt8_unpack(ckpt_q: torch.Tensor, ckpt_sf: torch.Tensor, route_meta: dict, rows: int,
+                 gate_up_layout: int = GATE_UP_CONCAT, stream=None) -> torch.Tensor:
+    """moe_ckpt8_unpack: the 8-bit checkpoint's values as grouped rows bf16 [rows, 2I] (rows that no expert has
+    are left unwritten)."""
+    if ckpt_q.dim() != 4:
+        raise MoeError("ckpt_q must be [N, 2, I, B]")
+    N, _, I, B = ckpt_q.shape
+    dev = ckpt_q.device
+    eo, bo, b2e, E, Nb = _meta_ptrs(route_meta, dev)
+    qp = _dense(ckpt_q, torch.int8, (Nb, 2, I, B), "ckpt_q", dev)
+    sp = _dense(ckpt_sf, torch.uint8, ckpt8_sf_shape(N, I, B), "ckpt_sf", dev)
+    with _on(stream, dev) as st:
+        h = torch.empty(rows, 2 * I, dtype=torch.bfloat16, device=dev)
+        rc = lib().moe_ckpt8_unpack(qp, sp, rows, I, E, B, Nb, gate_up_layout, eo, bo, b2e, h.data_ptr(), 2 * I, st)
+    _check(rc, "moe_ckpt8_unpack")
+    return h
 
 
 class LinearBwd:

@@ -1,0 +1,622 @@
+// Router forward (top-K selection) with the load-balance and z losses, and the losses' gradient.
+//
+//   p_t = softmax(l_t) over all E logits,  lse_t = log sum exp l_t
+//   sequences s of n_s tokens, n = sum_s n_s,  c_se = slots of s routed to e,  P_se = sum_{t in s} p_te
+//   L_bal = alpha sum_s (n_s / n) sum_e (E c_se / (K n_s)) (P_se / n_s)
+//   L_z   = beta / n sum_t lse_t^2
+//   dL_bal / dl_tj = alpha E / (K n n_s) p_tj (c_sj - sum_e c_se p_te),   dL_z / dl_tj = 2 beta / n lse_t p_tj
+//
+// The counts are constants of the gradient.  A logit of -inf is a masked expert (p = 0); a token with none
+// left has p = 0, lse = -inf and no gradient.  NaN and +inf reach the token's scores and the losses.
+//
+// Work split: the tokens are cut at every multiple of C (a chunk) and at every sequence boundary.  Walking
+// along the tokens, each step enters the next chunk or the next sequence, so the piece (chunk c, sequence i)
+// has the number c + i of its own, at most chunks + sequences of them, and one CTA per number finds its piece
+// by a binary search over the offsets.  No CTA's tokens lie in two sequences: its column sums of p and its
+// counts are one partial row, which a second kernel adds per sequence in a fixed order.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "moebwd_internal.h"
+
+namespace moebwd {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / 32;
+
+struct BalanceArgs {
+  const float* logits;
+  int64_t ld;
+  int T, K, E;
+  const int32_t* off;  // [S + 1] sequence offsets, or null: one sequence of all T tokens
+  int S, C;            // sequences; tokens per chunk
+  int pieces;          // chunks + S + 1: numbers c + i of the pieces (padding before, S sequences, padding behind)
+  float alpha, beta;
+  // forward
+  int mode, renorm;
+  float* scores;
+  int32_t* ids;           // written by the top-K, else read
+  float* lse;             // [T]
+  int32_t* part_c;        // [pieces][E]
+  float* part_p;          // [pieces][E]
+  float* part_z;          // [pieces]
+  float* part_l;          // [S][column tiles + 1]
+  unsigned* ticket;
+  int32_t* counts;        // [S][E]
+  float* prob_sum;        // [S][E]
+  float* loss;            // [2]
+  int32_t* status;
+  // backward
+  const float* dloss;     // [2] or null (ones)
+  const float* add;       // [T, E] or null
+  int64_t ld_add;
+  float* dlogits;
+};
+
+// Start of segment i of the S + 2: padding before the sequences, the sequences, padding behind them.
+__device__ __forceinline__ int seg_start(const BalanceArgs& a, int i) {
+  if (i == 0) return 0;
+  if (i > a.S + 1) return a.T;
+  if (!a.off) return i == 1 ? 0 : a.T;
+  return min(max(a.off[i - 1], 0), a.T);
+}
+
+// Segment and tokens [lo, hi) of piece p; false when the piece is empty.
+__device__ __forceinline__ bool find_piece(const BalanceArgs& a, int p, int& seg, int& lo, int& hi) {
+  int l = 0, h = a.S + 1;  // the last segment i whose first piece, start / C + i, is not behind p
+  while (l < h) {
+    const int m = (l + h + 1) >> 1;
+    if (seg_start(a, m) / a.C + m <= p)
+      l = m;
+    else
+      h = m - 1;
+  }
+  seg = l;
+  const int64_t c0 = (int64_t)(p - l) * a.C;
+  lo = (int)max((int64_t)seg_start(a, l), min(c0, (int64_t)a.T));
+  hi = (int)min((int64_t)seg_start(a, l + 1), min(c0 + a.C, (int64_t)a.T));
+  return lo < hi;
+}
+
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lane_max(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Lane sl of a token's LANES lanes holds its logits 4 (LANES j + sl) .. + 3, j < NV, -inf past E.
+template <int NV, int LANES, bool VEC>
+__device__ __forceinline__ void load_row(const float* row, int E, int sl, bool live, float (&v)[4 * NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = 4 * (LANES * j + sl);
+    if constexpr (VEC) {
+      const float4 f = live && c < E ? *reinterpret_cast<const float4*>(row + c)
+                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      v[4 * j] = f.x;
+      v[4 * j + 1] = f.y;
+      v[4 * j + 2] = f.z;
+      v[4 * j + 3] = f.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = live && c + i < E ? row[c + i] : -INFINITY;
+    }
+  }
+}
+
+// 32-bit keys in the order of the values: -inf below every number, +inf, then every NaN; -0 equals +0.
+// 0 is below them all (no value has it).
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  const uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  return x != x ? 0xffffffffu : k;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+constexpr uint32_t kKeyNegInf = 0x007fffffu;
+
+// TOPK: selects and writes scores and ids (else reads ids).  One token per LANES lanes.
+template <int NV, int LANES, bool VEC, bool TOPK>
+__global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceArgs a) {
+  constexpr int SEGS = 32 / LANES, N = 4 * NV;
+  constexpr int SLOTS = LANES == 32 ? 2 : 1;  // slots of the token that a lane holds (K <= 64 at 32 lanes)
+  extern __shared__ float sm[];               // [kBalWarps][E] partial sums of p, then [E] counts, [kBalWarps] z
+  int* hist = reinterpret_cast<int*>(sm + kBalWarps * a.E);
+  float* zs = sm + (kBalWarps + 1) * a.E;
+  pdl_wait();
+  pdl_trigger();
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, seg = lane / LANES, sl = lane % LANES;
+  const bool stats = a.part_p != nullptr;
+  if (stats && a.off && a.status && blockIdx.x == 0)  // offsets have to lie in [0, T] and not decrease
+    for (int i = threadIdx.x; i <= a.S; i += kBalThreads)
+      if (a.off[i] < 0 || a.off[i] > a.T || (i && a.off[i] < a.off[i - 1]))
+        atomicOr(a.status, MOE_STATUS_BAD_SEGMENTS);
+  if (stats && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  int which, lo, hi;
+  if (!find_piece(a, blockIdx.x, which, lo, hi)) return;
+  if (which == 0 || which == a.S + 1) {  // padding tokens: no slot is used
+    for (int64_t i = (int64_t)lo * a.K + threadIdx.x; TOPK && i < (int64_t)hi * a.K; i += kBalThreads) {
+      a.ids[i] = -1;
+      a.scores[i] = 0.f;
+    }
+    for (int t = lo + threadIdx.x; a.lse && t < hi; t += kBalThreads) a.lse[t] = -INFINITY;
+    return;
+  }
+  if (stats)
+    for (int i = threadIdx.x; i < a.E; i += kBalThreads) hist[i] = 0;
+  __syncthreads();
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+  float z = 0.f;
+  for (int tb = lo + w * SEGS; tb < hi; tb += kBalWarps * SEGS) {
+    const int t = tb + seg;
+    const bool live = t < hi;
+    float v[N];
+    load_row<NV, LANES, VEC>(a.logits + (int64_t)t * a.ld, a.E, sl, live, v);
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
+    m = lane_max<LANES>(m);
+    const float base = m > -INFINITY ? m : 0.f;
+    uint32_t key[N];
+    if constexpr (TOPK) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
+        key[j] = c < a.E ? order_key(v[j]) : 0u;
+      }
+    }
+    float total = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = __expf(v[j] - base);
+      total += v[j];
+    }
+    total = lane_sum<LANES>(total);
+    const float inv = total != 0.f ? 1.f / total : 0.f;  // 0: every expert masked (or no token here)
+    const float lse = base + logf(total);
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
+    if (sl == 0 && live) {
+      if (a.lse) a.lse[t] = lse;
+      if (total != 0.f) z = fmaf(lse, lse, z);
+    }
+    if constexpr (TOPK) {
+      // K rounds: the largest key left, its lowest column, and that one taken out
+      uint32_t mk[SLOTS] = {};
+      int mi[SLOTS];
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) mi[s] = -1;
+      for (int r = 0; r < a.K; ++r) {
+        uint32_t g = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) g = max(g, key[j]);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+        int c = 1 << 30;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) c = key[j] == g ? 4 * (LANES * (j >> 2) + sl) + (j & 3) : c;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) c = min(c, __shfl_xor_sync(0xffffffffu, c, o));
+#pragma unroll
+        for (int j = 0; j < N; ++j) key[j] = c == 4 * (LANES * (j >> 2) + sl) + (j & 3) ? 0u : key[j];
+        if (r % LANES == sl) {
+#pragma unroll
+          for (int s = 0; s < SLOTS; ++s)
+            if (r / LANES == s) {
+              mk[s] = g;
+              mi[s] = g > kKeyNegInf ? c : -1;  // -inf: a masked expert takes no slot
+            }
+        }
+      }
+      float e[SLOTS], sum = 0.f;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        e[s] = mi[s] >= 0 ? __expf(key_value(mk[s]) - base) : 0.f;
+        sum += e[s];
+      }
+      sum = lane_sum<LANES>(sum);
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        const int k = s * LANES + sl;
+        if (live && k < a.K) {
+          float sc = 0.f;
+          if (mi[s] >= 0)
+            sc = a.mode == MOE_ROUTER_TOPK ? key_value(mk[s])
+                 : a.mode == MOE_ROUTER_TOPK_OVER_SOFTMAX && !a.renorm ? e[s] * inv
+                                                                       : e[s] / sum;
+          a.scores[(int64_t)t * a.K + k] = sc;
+          a.ids[(int64_t)t * a.K + k] = mi[s];
+          if (stats && mi[s] >= 0) atomicAdd(&hist[mi[s]], 1);  // integers: any order gives the same counts
+        }
+      }
+    } else {
+      for (int k = sl; live && k < a.K; k += LANES) {
+        const int id = a.ids[(int64_t)t * a.K + k];
+        if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
+      }
+    }
+  }
+  if (!stats) return;
+  // the warp's tokens, then the warps, in a fixed order
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
+    if (seg == 0 && c < a.E) sm[w * a.E + c] = acc[j];
+  }
+  z = lane_sum<32>(z);
+  if (lane == 0) zs[w] = z;
+  __syncthreads();
+  const int64_t row = (int64_t)blockIdx.x * a.E;
+  for (int i = threadIdx.x; i < a.E; i += kBalThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kBalWarps; ++k) s += sm[k * a.E + i];
+    a.part_p[row + i] = s;
+    a.part_c[row + i] = hist[i];
+  }
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kBalWarps; ++k) s += zs[k];
+    a.part_z[blockIdx.x] = s;
+  }
+}
+
+// counts and prob_sum of sequence blockIdx.x, columns blockIdx.y * 32 .. + 31, from its pieces; each block's
+// share of the losses, which the block that comes last adds up in a fixed order.
+__global__ void __launch_bounds__(kBalThreads) balance_reduce_kernel(const BalanceArgs a) {
+  __shared__ float sp[kBalWarps][32], sz[kBalWarps];
+  __shared__ int sc[kBalWarps][32];
+  __shared__ bool last;
+  pdl_wait();
+  pdl_trigger();
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.x, col = blockIdx.y * 32 + lane, tiles = gridDim.y;
+  const int b0 = seg_start(a, s + 1), b1 = seg_start(a, s + 2);
+  const int p0 = b0 / a.C + s + 1, p1 = b1 > b0 ? min((b1 - 1) / a.C + s + 2, a.pieces) : p0;
+  float p = 0.f, z = 0.f;
+  int c = 0;
+  if (col < a.E)
+    for (int i = p0 + w; i < p1; i += kBalWarps) {
+      p += a.part_p[(int64_t)i * a.E + col];
+      c += a.part_c[(int64_t)i * a.E + col];
+    }
+  if (blockIdx.y == 0)
+    for (int i = p0 + (int)threadIdx.x; i < p1; i += kBalThreads) z += a.part_z[i];
+  sp[w][lane] = p;
+  sc[w][lane] = c;
+  z = lane_sum<32>(z);
+  if (lane == 0) sz[w] = z;
+  __syncthreads();
+  if (w == 0) {
+    p = 0.f;
+    c = 0;
+    z = 0.f;
+#pragma unroll
+    for (int k = 0; k < kBalWarps; ++k) {
+      p += sp[k][lane];
+      c += sc[k][lane];
+      z += sz[k];
+    }
+    float l = 0.f;
+    if (col < a.E) {
+      a.counts[(int64_t)s * a.E + col] = c;
+      a.prob_sum[(int64_t)s * a.E + col] = p;
+      l = b1 > b0 ? (float)c * p / (float)(b1 - b0) : 0.f;
+    }
+    l = lane_sum<32>(l);
+    if (lane == 0) {
+      a.part_l[(int64_t)s * (tiles + 1) + blockIdx.y] = l;
+      if (blockIdx.y == 0) a.part_l[(int64_t)s * (tiles + 1) + tiles] = z;
+      __threadfence();
+      last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float lb = 0.f, lz = 0.f;
+  for (int i = threadIdx.x; i < a.S * (tiles + 1); i += kBalThreads) {
+    const float v = __ldcg(a.part_l + i);
+    if (i % (tiles + 1) == tiles)
+      lz += v;
+    else
+      lb += v;
+  }
+  lb = lane_sum<32>(lb);
+  lz = lane_sum<32>(lz);
+  __syncthreads();
+  if (lane == 0) {
+    sp[0][w] = lb;
+    sz[w] = lz;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    lb = lz = 0.f;
+    for (int k = 0; k < kBalWarps; ++k) {
+      lb += sp[0][k];
+      lz += sz[k];
+    }
+    const float n = (float)max(seg_start(a, a.S + 1) - seg_start(a, 1), 1);
+    a.loss[0] = a.alpha * (float)a.E / ((float)a.K * n) * lb;
+    a.loss[1] = a.beta / n * lz;
+  }
+}
+
+template <int NV, int LANES, bool VEC>
+__global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceArgs a) {
+  constexpr int SEGS = 32 / LANES, N = 4 * NV;
+  pdl_wait();
+  pdl_trigger();
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, seg = lane / LANES, sl = lane % LANES;
+  if (a.off && a.status && blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.S; i += kBalThreads)
+      if (a.off[i] < 0 || a.off[i] > a.T || (i && a.off[i] < a.off[i - 1]))
+        atomicOr(a.status, MOE_STATUS_BAD_SEGMENTS);
+  int which, lo, hi;
+  if (!find_piece(a, blockIdx.x, which, lo, hi)) return;
+  const bool pad = which == 0 || which == a.S + 1;
+  const float n = (float)max(seg_start(a, a.S + 1) - seg_start(a, 1), 1);
+  const float n_s = (float)(seg_start(a, which + 1) - seg_start(a, which));
+  const float wb = (a.dloss ? a.dloss[0] : 1.f) * a.alpha * (float)a.E / ((float)a.K * n * n_s);
+  const float wz = (a.dloss ? a.dloss[1] : 1.f) * 2.f * a.beta / n;
+  float cnt[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
+    cnt[j] = !pad && c < a.E ? (float)a.counts[(int64_t)(which - 1) * a.E + c] : 0.f;
+  }
+  for (int tb = lo + w * SEGS; tb < hi; tb += kBalWarps * SEGS) {
+    const int t = tb + seg;
+    const bool live = t < hi;
+    float v[N], b[N];
+    const float lse = live && !pad ? a.lse[t] : -INFINITY;
+    load_row<NV, LANES, VEC>(a.logits + (int64_t)t * a.ld, a.E, sl, live && !pad, v);
+    if (a.add) {
+      load_row<NV, LANES, VEC>(a.add + (int64_t)t * a.ld_add, a.E, sl, live, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) b[j] = 0.f;
+    }
+    const bool none = lse == -INFINITY;  // nothing left by the mask, or a padding token
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = none ? 0.f : __expf(v[j] - lse);
+      dot = fmaf(cnt[j], v[j], dot);
+    }
+    dot = lane_sum<LANES>(dot);
+    const float zt = none ? 0.f : wz * lse;
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = fmaf(v[j], fmaf(wb, cnt[j] - dot, zt), b[j]);
+    if (!live) continue;
+    float* out = a.dlogits + (int64_t)t * a.E;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = 4 * (LANES * j + sl);
+      if constexpr (VEC) {
+        if (c < a.E) *reinterpret_cast<float4*>(out + c) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < a.E) out[c + i] = v[4 * j + i];
+      }
+    }
+  }
+}
+
+// Lanes per token: 8 for up to 256 experts and K <= 8, 16 for up to 512 and K <= 16, else a warp.
+static int bal_lanes(int K, int E) { return E <= 256 && K <= 8 ? 8 : E <= 512 && K <= 16 ? 16 : 32; }
+
+// Tokens per chunk: one pass of a CTA's warps, more where that would be over four CTAs per SM.
+static int bal_chunk(int T, int lanes) {
+  const int step = kBalThreads / lanes;
+  const int64_t steps = ((int64_t)T + step - 1) / step, most = 4 * 152;
+  return (int)((steps + most - 1) / most) * step;
+}
+
+struct BalLayout {
+  size_t c, p, z, l, ticket, total;
+  int C, pieces;
+};
+
+static BalLayout bal_layout(int T, int K, int E, int S) {
+  BalLayout L{};
+  L.C = bal_chunk(T, bal_lanes(K, E));
+  L.pieces = (int)(((int64_t)T + L.C - 1) / L.C) + S + 1;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = align_up(off + n, 256);
+    return at;
+  };
+  L.c = take(sizeof(int32_t) * (size_t)L.pieces * E);
+  L.p = take(sizeof(float) * (size_t)L.pieces * E);
+  L.z = take(sizeof(float) * (size_t)L.pieces);
+  L.l = take(sizeof(float) * (size_t)S * ((E + 31) / 32 + 1));
+  L.ticket = take(sizeof(unsigned));
+  L.total = off;
+  return L;
+}
+
+static int bal_check(const char* who, int T, int K, int E, int S) {
+  if (T < 0 || K <= 0 || E <= 0 || K > E || S < 1) return fail(MOE_ERR_INVALID, "%s: bad sizes (need 1 <= K <= E, T >= 0, num_seq >= 1)", who);
+  if (E > kMaxExperts || K > 64) return fail(MOE_ERR_UNSUPPORTED, "%s: E above %d or K above 64", who, kMaxExperts);
+  if (T > INT32_MAX - (1 << 20) || S > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tokens or sequences", who);
+  return MOE_OK;
+}
+
+#define BAL_PICK(KERN, NV_, ...)                                                                   \
+  (lanes == 8 ? (NV_ <= 1 ? KERN<1, 8, __VA_ARGS__> : NV_ <= 2 ? KERN<2, 8, __VA_ARGS__>           \
+                 : NV_ <= 4 ? KERN<4, 8, __VA_ARGS__> : KERN<8, 8, __VA_ARGS__>)                   \
+   : lanes == 16 ? (NV_ <= 1 ? KERN<1, 16, __VA_ARGS__> : NV_ <= 2 ? KERN<2, 16, __VA_ARGS__>      \
+                    : NV_ <= 4 ? KERN<4, 16, __VA_ARGS__> : KERN<8, 16, __VA_ARGS__>)              \
+                 : (NV_ <= 1 ? KERN<1, 32, __VA_ARGS__> : NV_ <= 2 ? KERN<2, 32, __VA_ARGS__>      \
+                    : NV_ <= 4 ? KERN<4, 32, __VA_ARGS__> : KERN<8, 32, __VA_ARGS__>))
+
+typedef void (*BalKernel)(const BalanceArgs);
+
+static BalKernel fwd_kernel(int lanes, int nv, bool vec, bool topk) {
+  if (vec) return topk ? BAL_PICK(router_fwd_kernel, nv, true, true) : BAL_PICK(router_fwd_kernel, nv, true, false);
+  return topk ? BAL_PICK(router_fwd_kernel, nv, false, true) : BAL_PICK(router_fwd_kernel, nv, false, false);
+}
+
+static BalKernel bwd_kernel(int lanes, int nv, bool vec) {
+  return vec ? BAL_PICK(balance_bwd_kernel, nv, true) : BAL_PICK(balance_bwd_kernel, nv, false);
+}
+
+// Both forward entry points: the top-K (scores given) or the caller's ids, with or without the losses.
+static int launch_router(BalanceArgs a, bool topk, bool stats, const BalLayout& L, void* workspace, cudaStream_t st) {
+  char* ws = static_cast<char*>(workspace);
+  a.C = L.C;
+  a.pieces = L.pieces;
+  if (stats) {
+    a.part_c = reinterpret_cast<int32_t*>(ws + L.c);
+    a.part_p = reinterpret_cast<float*>(ws + L.p);
+    a.part_z = reinterpret_cast<float*>(ws + L.z);
+    a.part_l = reinterpret_cast<float*>(ws + L.l);
+    a.ticket = reinterpret_cast<unsigned*>(ws + L.ticket);
+  }
+  const int lanes = bal_lanes(a.K, a.E), nv = (a.E + 4 * lanes - 1) / (4 * lanes);
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
+  const size_t smem = sizeof(float) * ((size_t)(kBalWarps + 1) * a.E + kBalWarps);
+  int rc = launch_pdl(fwd_kernel(lanes, nv, vec, topk), dim3(a.pieces), dim3(kBalThreads), smem, st, "router_fwd", a);
+  if (rc || !stats) return rc;
+  return launch_pdl(balance_reduce_kernel, dim3(a.S, (a.E + 31) / 32), dim3(kBalThreads), 0, st, "balance_reduce", a);
+}
+
+// T = 0: no counts, no probabilities, no loss
+static int balance_empty(int E, int S, int32_t* counts, float* prob_sum, float* loss, cudaStream_t st) {
+  int rc = cuda_check(cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)S * E, st), "memset counts");
+  if (!rc) rc = cuda_check(cudaMemsetAsync(prob_sum, 0, sizeof(float) * (size_t)S * E, st), "memset prob_sum");
+  if (!rc) rc = cuda_check(cudaMemsetAsync(loss, 0, 2 * sizeof(float), st), "memset loss");
+  return rc;
+}
+
+}  // namespace moebwd
+
+using namespace moebwd;
+
+extern "C" size_t moe_balance_workspace_size(int T, int K, int E, int num_seq) {
+  if (bal_check("moe_balance_workspace_size", T, K, E, num_seq) != MOE_OK) return 0;
+  return bal_layout(T, K, E, num_seq).total;
+}
+
+static int router_entry(const char* who, bool topk, int mode, int renorm, const float* logits, int64_t ld_logits, int T,
+                        int K, int E, const int32_t* seg_offsets, int num_seq, float alpha, float beta, float* scores,
+                        int32_t* ids, float* lse, int32_t* counts, float* prob_sum, float* loss, int32_t* status_dev,
+                        void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  clear_error();
+  int rc = bal_check(who, T, K, E, num_seq);
+  if (rc) return rc;
+  if (topk && mode != MOE_ROUTER_SOFTMAX_OVER_TOPK && mode != MOE_ROUTER_TOPK_OVER_SOFTMAX && mode != MOE_ROUTER_TOPK)
+    return fail(MOE_ERR_INVALID, "%s: bad mode", who);
+  if (!seg_offsets && num_seq != 1) return fail(MOE_ERR_INVALID, "%s: several sequences need seg_offsets", who);
+  const int given = (counts != nullptr) + (prob_sum != nullptr) + (loss != nullptr);
+  if (given != 3 && (given != 0 || !topk))
+    return fail(MOE_ERR_INVALID, "%s: counts, prob_sum and loss come together", who);
+  const bool stats = given == 3;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (status_dev && (rc = cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status"))) return rc;
+  if (T == 0) return stats ? balance_empty(E, num_seq, counts, prob_sum, loss, st) : MOE_OK;
+  if (!logits || !ids || (topk && !scores)) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
+  if (ld_logits < E) return fail(MOE_ERR_INVALID, "%s: row stride below E", who);
+  const BalLayout L = bal_layout(T, K, E, num_seq);
+  if (stats) {
+    if (!workspace) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255)
+      return fail(MOE_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
+    if (workspace_bytes < L.total)
+      return fail(MOE_ERR_INVALID, "%s: workspace too small (%zu < %zu)", who, workspace_bytes, L.total);
+  }
+  BalanceArgs a{};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.T = T;
+  a.K = K;
+  a.E = E;
+  a.off = seg_offsets;
+  a.S = num_seq;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.mode = mode;
+  a.renorm = renorm;
+  a.scores = scores;
+  a.ids = ids;
+  a.lse = lse;
+  a.counts = counts;
+  a.prob_sum = prob_sum;
+  a.loss = loss;
+  a.status = status_dev;
+  return launch_router(a, topk, stats, L, workspace, st);
+}
+
+extern "C" int moe_router_fwd(int mode, int renorm, const float* logits, int64_t ld_logits, int T, int K, int E,
+                              const int32_t* seg_offsets, int num_seq, float alpha, float beta, float* scores,
+                              int32_t* ids, float* lse, int32_t* counts, float* prob_sum, float* loss,
+                              int32_t* status_dev, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return router_entry("moe_router_fwd", true, mode, renorm, logits, ld_logits, T, K, E, seg_offsets, num_seq, alpha,
+                      beta, scores, ids, lse, counts, prob_sum, loss, status_dev, workspace, workspace_bytes, stream);
+}
+
+extern "C" int moe_balance_fwd(const float* logits, int64_t ld_logits, const int32_t* ids, int T, int K, int E,
+                               const int32_t* seg_offsets, int num_seq, float alpha, float beta, float* lse,
+                               int32_t* counts, float* prob_sum, float* loss, int32_t* status_dev, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream) {
+  return router_entry("moe_balance_fwd", false, MOE_ROUTER_TOPK, 0, logits, ld_logits, T, K, E, seg_offsets, num_seq,
+                      alpha, beta, nullptr, const_cast<int32_t*>(ids), lse, counts, prob_sum, loss, status_dev,
+                      workspace, workspace_bytes, stream);
+}
+
+extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const float* lse, const int32_t* counts, int T,
+                               int K, int E, const int32_t* seg_offsets, int num_seq, float alpha, float beta,
+                               const float* dloss, const float* add, int64_t ld_add, float* dlogits,
+                               int32_t* status_dev, moe_stream_t stream) {
+  clear_error();
+  int rc = bal_check("moe_balance_bwd", T, K, E, num_seq);
+  if (rc) return rc;
+  if (!seg_offsets && num_seq != 1) return fail(MOE_ERR_INVALID, "moe_balance_bwd: several sequences need seg_offsets");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (status_dev && (rc = cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status"))) return rc;
+  if (T == 0) return MOE_OK;
+  if (!logits || !lse || !counts || !dlogits) return fail(MOE_ERR_INVALID, "moe_balance_bwd: null pointer");
+  if (ld_logits < E || (add && ld_add < E)) return fail(MOE_ERR_INVALID, "moe_balance_bwd: row stride below E");
+  const BalLayout L = bal_layout(T, K, E, num_seq);
+  BalanceArgs a{};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.T = T;
+  a.K = K;
+  a.E = E;
+  a.off = seg_offsets;
+  a.S = num_seq;
+  a.C = L.C;
+  a.pieces = L.pieces;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.lse = const_cast<float*>(lse);
+  a.counts = const_cast<int32_t*>(counts);
+  a.dloss = dloss;
+  a.add = add;
+  a.ld_add = ld_add;
+  a.dlogits = dlogits;
+  a.status = status_dev;
+  const int lanes = bal_lanes(K, E), nv = (E + 4 * lanes - 1) / (4 * lanes);
+  const bool vec = E % 4 == 0 && ld_logits % 4 == 0 && (!add || ld_add % 4 == 0) &&
+                   ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(add) |
+                     reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
+  return launch_pdl(bwd_kernel(lanes, nv, vec), dim3(a.pieces), dim3(kBalThreads), 0, st, "balance_bwd", a);
+}

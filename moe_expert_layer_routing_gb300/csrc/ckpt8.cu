@@ -1,0 +1,304 @@
+// Gated activation of the forward with the 8-bit gate/up checkpoint, and the checkpoint read back.
+//
+//   a = act(g) u (times the row's routing score when given), g and u the gate and up pre-activations
+//   checkpoint: per feature, groups of 32 consecutive slots of the block layout share one power of two;
+//     byte = max(1, exponent field of the group's largest magnitude - 6)      (E8M0, value 2^(byte - 127))
+//     code = round(v 2^(127 - byte)), ties to even, clamped to +-127          (int8)
+//   so a group's largest code is 64 .. 127, and a value is off by at most half of 2^(byte - 127) (a whole one
+//   where 127.5 or more is clamped).  A group with a NaN or an infinity gets byte 255 and reads as NaN.
+//   Every value code 2^(byte - 127) has 7 significant bits: bf16 holds it exactly.
+//
+// Layout: codes int8 [N, 2, I, B], the bf16 checkpoint's; scale bytes [N, 2, B/128, I/32, 4, 32], so that the
+// 32 features x 128 rows of a GEMM epilogue's chunk have their bytes in 128 consecutive ones, those of one
+// 32-row quarter side by side.
+//
+// A CTA takes 128 slots (one GEMM tile's rows) and 64 features: the rows of h come into shared memory by
+// 16-byte asynchronous copies (128 consecutive bytes of gate and of up per row), the activation is computed
+// along rows (16-byte stores), the codes along columns: a thread owns one 32-bit word column, two values of
+// each of 32 rows, so its two groups' maxima and codes need no exchange, and consecutive lanes read
+// consecutive words.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "moebwd_internal.h"
+#include "mx_device.cuh"
+#include "ptx.cuh"
+
+namespace moebwd {
+
+constexpr int kGluThreads = 256;
+constexpr int kGluFeat = 64;  // features per CTA
+constexpr int kGluRows = 128;
+
+struct GluArgs {
+  const uint16_t* h;  // [rows, 2I]
+  int64_t ldh;
+  uint16_t* a;        // [rows, I]
+  int8_t* q;          // [N, 2, I, B] or null
+  uint8_t* sf;        // [N, 2, B/128, I/32, 4, 32]
+  const float* s;     // routing scores or null
+  const int32_t* s_scatter_idx;
+  const int32_t *expert_offsets, *block_offsets, *block_to_expert;
+  int64_t rows;       // rows of h; no row at or past it is touched
+  int64_t slots;      // T*K: scores
+  int I, B, E, glu, interleaved, tiles_per_block;
+};
+
+// Rows [r0, r0 + n) of the grouped order that lie in the 128 slots of tile `tile`; n <= 0: none.
+__device__ __forceinline__ void glu_tile_rows(const int32_t* eo, const int32_t* bo, const int32_t* b2e, int E, int B,
+                                              int tiles_per_block, int64_t rows, int64_t tile, int64_t& r0, int& n) {
+  const int64_t blk = tile / tiles_per_block;
+  const int e = b2e[blk];
+  n = 0;
+  if (e < 0 || e >= E) return;
+  const int64_t j0 = (blk - bo[e]) * B + (tile - blk * tiles_per_block) * kGluRows;
+  r0 = eo[e] + j0;
+  const int64_t r1 = min((int64_t)eo[e + 1], rows);
+  if (j0 < 0 || r0 < 0) return;
+  n = (int)max((int64_t)0, min((int64_t)kGluRows, r1 - r0));
+}
+
+// Scale byte of feature f, 32-slot group g of 128-slot tile tb of half `bu` (2 block + gate|up).
+__device__ __forceinline__ int64_t sf_offset(int64_t bu, int tiles_per_block, int tb, int I, int f, int g) {
+  return (((bu * tiles_per_block + tb) * (I >> 5) + (f >> 5)) * 4 + g) * 32 + (f & 31);
+}
+
+// act(g) of the forward: SiLU(g) = g / (1 + e^-g), or GELU(g) = g Phi(g)
+__device__ __forceinline__ float glu_act(float g, int glu) {
+  if (glu == MOE_GLU_GEGLU) return g * (0.5f * (1.f + erff(g * 0.70710678118654752f)));
+  return __fdividef(g, 1.f + __expf(-g));
+}
+
+__global__ void __launch_bounds__(kGluThreads) glu_fwd_kernel(const GluArgs p) {
+  __shared__ __align__(16) uint32_t tile[kGluRows][kGluFeat];  // words: 32 gate pairs | 32 up pairs, or 64 (gate, up)
+  pdl_wait();
+  pdl_trigger();
+  const int chunks = p.I / kGluFeat;
+  const int64_t t = blockIdx.x / chunks;
+  const int f0 = (int)(blockIdx.x - t * chunks) * kGluFeat;
+  int64_t r0 = 0;
+  int n;
+  glu_tile_rows(p.expert_offsets, p.block_offsets, p.block_to_expert, p.E, p.B, p.tiles_per_block, p.rows, t, r0, n);
+  if (n == 0) return;
+  // 16 pieces of 16 bytes per row; rows past the expert's last are zeros
+  for (int i = threadIdx.x; i < kGluRows * 16; i += kGluThreads) {
+    const int r = i >> 4, c = i & 15;
+    const int col = p.interleaved ? 2 * f0 + c * 8 : c < 8 ? f0 + c * 8 : p.I + f0 + (c - 8) * 8;
+    const uint16_t* src = p.h + (r0 + (r < n ? r : 0)) * p.ldh + col;
+    cp_async_16_zfill(smem_u32(&tile[r][c * 4]), src, r < n ? 16 : 0);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncthreads();
+  // a: eight features of a row at a time
+  for (int i = threadIdx.x; i < n * 8; i += kGluThreads) {
+    const int r = i >> 3, c = i & 7;
+    uint32_t g[4], u[4];
+    if (p.interleaved) {
+      const uint4 w0 = *reinterpret_cast<const uint4*>(&tile[r][c * 8]), w1 = *reinterpret_cast<const uint4*>(&tile[r][c * 8 + 4]);
+      g[0] = __byte_perm(w0.x, w0.y, 0x5410);
+      u[0] = __byte_perm(w0.x, w0.y, 0x7632);
+      g[1] = __byte_perm(w0.z, w0.w, 0x5410);
+      u[1] = __byte_perm(w0.z, w0.w, 0x7632);
+      g[2] = __byte_perm(w1.x, w1.y, 0x5410);
+      u[2] = __byte_perm(w1.x, w1.y, 0x7632);
+      g[3] = __byte_perm(w1.z, w1.w, 0x5410);
+      u[3] = __byte_perm(w1.z, w1.w, 0x7632);
+    } else {
+      const uint4 w0 = *reinterpret_cast<const uint4*>(&tile[r][c * 4]), w1 = *reinterpret_cast<const uint4*>(&tile[r][32 + c * 4]);
+      g[0] = w0.x; g[1] = w0.y; g[2] = w0.z; g[3] = w0.w;
+      u[0] = w1.x; u[1] = w1.y; u[2] = w1.z; u[3] = w1.w;
+    }
+    float sv = 1.f;
+    if (p.s) {
+      const int f = p.s_scatter_idx[r0 + r];
+      sv = f >= 0 && f < p.slots ? p.s[f] : 0.f;
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a0 = glu_act(__uint_as_float(g[k] << 16), p.glu) * __uint_as_float(u[k] << 16);
+      const float a1 = glu_act(__uint_as_float(g[k] & 0xffff0000u), p.glu) * __uint_as_float(u[k] & 0xffff0000u);
+      o[k] = pack_bf16x2(sv * a0, sv * a1);
+    }
+    *reinterpret_cast<uint4*>(p.a + (r0 + r) * (int64_t)p.I + f0 + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (!p.q) return;
+  // codes: word column wc of the 32 rows of group gr
+  const int wc = threadIdx.x & 63, gr = threadIdx.x >> 6;
+  uint32_t v[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = tile[32 * gr + k][wc];
+  const uint32_t am = bf16x2_absmax32(v);  // a NaN drops out of the maximum
+  bool bad0 = false, bad1 = false;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    bad0 |= (v[k] & 0x7f80u) == 0x7f80u;
+    bad1 |= (v[k] & 0x7f800000u) == 0x7f800000u;
+  }
+  const int64_t blk = t / p.tiles_per_block;
+  const int tb = (int)(t - blk * p.tiles_per_block);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int exponent = (half ? am >> 23 : am >> 7) & 0xff;
+    const bool bad = half ? bad1 : bad0;
+    const int byte = bad ? 255 : max(1, exponent - 6);
+    // 2^(127 - byte); byte <= 248 for finite values
+    const float inv = __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = v[4 * k + i];
+        const float f = __uint_as_float(half ? x & 0xffff0000u : x << 16) * inv;
+        // + 1.5 * 2^23 rounds to an integer in the low mantissa bits (two's complement in the low byte)
+        b[i] = __float_as_uint(fminf(fmaxf(f, -127.f), 127.f) + 12582912.f);
+      }
+      w[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    const int f = p.interleaved ? f0 + wc : f0 + 2 * (wc & 31) + half;  // feature
+    const int up = p.interleaved ? half : wc >> 5;
+    int8_t* dst = p.q + ((blk * 2 + up) * (int64_t)p.I + f) * p.B + tb * kGluRows + 32 * gr;
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    p.sf[sf_offset(blk * 2 + up, p.tiles_per_block, tb, p.I, f, gr)] = (uint8_t)byte;
+  }
+}
+
+struct UnpackArgs {
+  const int8_t* q;
+  const uint8_t* sf;
+  uint16_t* h;
+  int64_t ldh, rows;
+  const int32_t *expert_offsets, *block_offsets, *block_to_expert;
+  int I, B, E, interleaved, tiles_per_block;
+};
+
+// The checkpoint's values as rows [rows, 2I] in the grouped order.
+__global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackArgs p) {
+  __shared__ __align__(16) int8_t code[2 * kGluFeat][kGluRows + 16];
+  __shared__ __align__(16) uint8_t scale[2 * kGluFeat][4];
+  pdl_wait();
+  pdl_trigger();
+  const int chunks = p.I / kGluFeat;
+  const int64_t t = blockIdx.x / chunks;
+  const int f0 = (int)(blockIdx.x - t * chunks) * kGluFeat;
+  int64_t r0 = 0;
+  int n;
+  glu_tile_rows(p.expert_offsets, p.block_offsets, p.block_to_expert, p.E, p.B, p.tiles_per_block, p.rows, t, r0, n);
+  if (n == 0) return;
+  const int64_t blk = t / p.tiles_per_block;
+  const int tb = (int)(t - blk * p.tiles_per_block);
+  for (int i = threadIdx.x; i < 2 * kGluFeat * 8; i += kGluThreads) {
+    const int f = i >> 3, c = i & 7;  // f < 64: gate, else up
+    const int8_t* src = p.q + ((blk * 2 + f / kGluFeat) * (int64_t)p.I + f0 + f % kGluFeat) * p.B + tb * kGluRows + c * 16;
+    cp_async_16(smem_u32(&code[f][c * 16]), src);
+  }
+  cp_async_commit();
+  for (int i = threadIdx.x; i < 2 * kGluFeat * 4; i += kGluThreads) {
+    const int f = i & (2 * kGluFeat - 1), g = i / (2 * kGluFeat);
+    scale[f][g] = p.sf[sf_offset(blk * 2 + f / kGluFeat, p.tiles_per_block, tb, p.I, f0 + f % kGluFeat, g)];
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * 16; i += kGluThreads) {
+    const int r = i >> 4, c = i & 15;  // eight consecutive columns of the row
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float x[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = c * 8 + 2 * k + j;
+        const int f = p.interleaved ? (col >> 1) + (col & 1) * kGluFeat : col;
+        x[j] = (float)code[f][r] * __uint_as_float((uint32_t)scale[f][r >> 5] << 23);  // byte 255: inf or NaN
+        if (scale[f][r >> 5] == 255) x[j] = __uint_as_float(0x7fc00000u);
+      }
+      o[k] = pack_bf16x2(x[0], x[1]);
+    }
+    const int col = p.interleaved ? 2 * f0 + c * 8 : c < 8 ? f0 + c * 8 : p.I + f0 + (c - 8) * 8;
+    *reinterpret_cast<uint4*>(p.h + (r0 + r) * p.ldh + col) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+static int ckpt8_check(const char* who, int64_t rows, int I, int E, int block_size, int64_t num_blocks, int gate_up_layout) {
+  if (rows < 0 || num_blocks < 0 || I <= 0 || E <= 0) return fail(MOE_ERR_INVALID, "%s: bad sizes", who);
+  if (I % kGluFeat) return fail(MOE_ERR_UNSUPPORTED, "%s: I must be a multiple of %d", who, kGluFeat);
+  if (E > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "%s: E above %d", who, kMaxExperts);
+  if (block_size != 128 && block_size != 256 && block_size != 512 && block_size != 1024)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: block_size must be 128, 256, 512 or 1024", who);
+  if (gate_up_layout != MOE_GATE_UP_CONCAT && gate_up_layout != MOE_GATE_UP_INTERLEAVED)
+    return fail(MOE_ERR_INVALID, "%s: bad gate_up_layout", who);
+  if (num_blocks * (block_size / kGluRows) * (I / kGluFeat) > INT32_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+  return MOE_OK;
+}
+
+}  // namespace moebwd
+
+using namespace moebwd;
+
+extern "C" int moe_glu_fwd(const void* h, int64_t ldh, int64_t rows, int I, int E, int block_size, int64_t num_blocks,
+                           int glu, int gate_up_layout, const int32_t* expert_offsets, const int32_t* block_offsets,
+                           const int32_t* block_to_expert, const float* s, const int32_t* s_scatter_idx,
+                           int64_t num_slots, void* a, int8_t* ckpt_q, uint8_t* ckpt_sf, moe_stream_t stream) {
+  clear_error();
+  int rc = ckpt8_check("moe_glu_fwd", rows, I, E, block_size, num_blocks, gate_up_layout);
+  if (rc) return rc;
+  if (glu != MOE_GLU_SWIGLU && glu != MOE_GLU_GEGLU) return fail(MOE_ERR_INVALID, "moe_glu_fwd: bad glu");
+  if ((ckpt_q == nullptr) != (ckpt_sf == nullptr))
+    return fail(MOE_ERR_INVALID, "moe_glu_fwd: ckpt_q and ckpt_sf come together");
+  if ((s == nullptr) != (s_scatter_idx == nullptr))
+    return fail(MOE_ERR_INVALID, "moe_glu_fwd: s and s_scatter_idx come together");
+  if (rows == 0 || num_blocks == 0) return MOE_OK;
+  if (!h || !a || !expert_offsets || !block_offsets || !block_to_expert)
+    return fail(MOE_ERR_INVALID, "moe_glu_fwd: null pointer");
+  if (ldh < 2 * (int64_t)I || ldh % 8) return fail(MOE_ERR_INVALID, "moe_glu_fwd: row stride of h must be a multiple of 8, at least 2I");
+  for (const void* q : {h, static_cast<const void*>(a), static_cast<const void*>(ckpt_q), static_cast<const void*>(ckpt_sf)})
+    if (reinterpret_cast<uintptr_t>(q) & 15) return fail(MOE_ERR_INVALID, "moe_glu_fwd: tensors must be 16-byte aligned");
+  GluArgs p{};
+  p.h = static_cast<const uint16_t*>(h);
+  p.ldh = ldh;
+  p.a = static_cast<uint16_t*>(a);
+  p.q = ckpt_q;
+  p.sf = ckpt_sf;
+  p.s = s;
+  p.s_scatter_idx = s_scatter_idx;
+  p.slots = num_slots;
+  p.expert_offsets = expert_offsets;
+  p.block_offsets = block_offsets;
+  p.block_to_expert = block_to_expert;
+  p.rows = rows;
+  p.I = I;
+  p.B = block_size;
+  p.E = E;
+  p.glu = glu;
+  p.interleaved = gate_up_layout == MOE_GATE_UP_INTERLEAVED;
+  p.tiles_per_block = block_size / kGluRows;
+  const int64_t grid = num_blocks * p.tiles_per_block * (I / kGluFeat);
+  return launch_pdl(glu_fwd_kernel, dim3((unsigned)grid), dim3(kGluThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                    "glu_fwd", p);
+}
+
+extern "C" int moe_ckpt8_unpack(const int8_t* ckpt_q, const uint8_t* ckpt_sf, int64_t rows, int I, int E, int block_size,
+                                int64_t num_blocks, int gate_up_layout, const int32_t* expert_offsets,
+                                const int32_t* block_offsets, const int32_t* block_to_expert, void* h, int64_t ldh,
+                                moe_stream_t stream) {
+  clear_error();
+  int rc = ckpt8_check("moe_ckpt8_unpack", rows, I, E, block_size, num_blocks, gate_up_layout);
+  if (rc) return rc;
+  if (rows == 0 || num_blocks == 0) return MOE_OK;
+  if (!ckpt_q || !ckpt_sf || !h || !expert_offsets || !block_offsets || !block_to_expert)
+    return fail(MOE_ERR_INVALID, "moe_ckpt8_unpack: null pointer");
+  if (ldh < 2 * (int64_t)I || ldh % 8) return fail(MOE_ERR_INVALID, "moe_ckpt8_unpack: row stride of h must be a multiple of 8, at least 2I");
+  for (const void* q : {static_cast<const void*>(ckpt_q), static_cast<const void*>(ckpt_sf), static_cast<const void*>(h)})
+    if (reinterpret_cast<uintptr_t>(q) & 15) return fail(MOE_ERR_INVALID, "moe_ckpt8_unpack: tensors must be 16-byte aligned");
+  UnpackArgs p{ckpt_q, ckpt_sf, static_cast<uint16_t*>(h), ldh, rows, expert_offsets, block_offsets, block_to_expert, I,
+               block_size, E, gate_up_layout == MOE_GATE_UP_INTERLEAVED, block_size / kGluRows};
+  const int64_t grid = num_blocks * p.tiles_per_block * (I / kGluFeat);
+  return launch_pdl(ckpt8_unpack_kernel, dim3((unsigned)grid), dim3(kGluThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), "ckpt8_unpack", p);
+}

@@ -10,6 +10,9 @@ int launch_gemm_bf16(int BN, const GemmParams& p, const void* tmA, const void* t
   if (p.epi == kEpiStore)
     return BN == 256 ? gemm_launch_instance<false, 256, kEpiStore>(p, tmA, tmB, tmC, grid, st)
                      : gemm_launch_instance<false, 128, kEpiStore>(p, tmA, tmB, tmC, grid, st);
+  if (p.epi == kEpiDSwiGLU8)  // G1 on an 8-bit checkpoint
+    return BN == 256 ? gemm_launch_instance<false, 256, kEpiDSwiGLU8>(p, tmA, tmB, tmC, grid, st)
+                     : gemm_launch_instance<false, 128, kEpiDSwiGLU8>(p, tmA, tmB, tmC, grid, st);
   return BN == 256 ? gemm_launch_instance<false, 256, kEpiDSwiGLU>(p, tmA, tmB, tmC, grid, st)
                    : gemm_launch_instance<false, 128, kEpiDSwiGLU>(p, tmA, tmB, tmC, grid, st);
 }

@@ -49,7 +49,10 @@ struct GemmCfg {
   static constexpr int G1_NC = 32 / kG1Subs;
   // dSwiGLU epilogues; kEpiDSwiGLU2 runs two groups of 4 * kG1Subs warps, group g taking the chunks
   // c = g, g + 2, ... of every tile, with three checkpoint buffers (each group one chunk ahead)
-  static constexpr bool DSW = EPI == kEpiDSwiGLU || EPI == kEpiDSwiGLU2;
+  static constexpr bool DSW = EPI == kEpiDSwiGLU || EPI == kEpiDSwiGLU2 || EPI == kEpiDSwiGLU8;
+  // the checkpoint in 8 bits: a chunk is [gate|up][32 features][128 rows] codes, then [gate|up][4 quarters]
+  // [32 features] scale bytes
+  static constexpr bool CK8 = EPI == kEpiDSwiGLU8;
   static constexpr int G1_GROUPS = EPI == kEpiDSwiGLU2 ? 2 : 1;
   static constexpr int CK_BUFS = G1_GROUPS == 2 ? 3 : 2;
   // fp32 transpose buffers per warp: MXFP8, and BF16 at 256 columns, share one between the three
@@ -62,7 +65,8 @@ struct GemmCfg {
   // MXFP8 row-wise dh: the two column slices of a quarter swap 16-byte halves of their quantised gate
   // and up columns ([quarter][slice][lane] uint4), so that each writes one whole 32-byte sector
   static constexpr int QX_BYTES = (DSW && MX && G1_NC == 16) ? G1_GROUPS * 4 * 2 * 32 * 16 : 0;
-  static constexpr int CK_CHUNK_BYTES = 2 * 32 * 128 * 2;
+  static constexpr int CK_HALF_BYTES = 32 * 128 * (CK8 ? 1 : 2);
+  static constexpr int CK_CHUNK_BYTES = 2 * CK_HALF_BYTES + (CK8 ? 2 * 128 : 0);
   static constexpr int CK_BYTES = DSW ? CK_BUFS * CK_CHUNK_BYTES : 0;
   // Store epilogue with a single TMEM accumulator: the tile is drained into a 128B-swizzled bf16
   // staging tile in shared memory (TMEM released at once) and written by TMA stores.
@@ -320,7 +324,9 @@ __device__ __forceinline__ void group_bar(int id) {
 // GENERIC with `ga` (this row's slot in a saved act(gate) checkpoint [N,I,B], feature stride B):
 // act(gate) is read from it, act'(gate) still computed from the pre-activation.
 // Padding rows produce zeros.
-template <bool MX, int NC, int AF, bool GENERIC, bool SHARED_TBUF>
+// CK8: the chunk holds int8 codes and the scale bytes of their 32-row groups (value code 2^(byte - 127)); a
+// TMEM lane quarter is one group, so a warp's NC features take their scales from one or two broadcast loads.
+template <bool MX, int NC, int AF, bool GENERIC, bool SHARED_TBUF, bool CK8>
 __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t taddr, int64_t prow, int m, int lane,
                                                  bool valid, float sv, int i0, int sub, const uint16_t* ck,
                                                  const uint16_t* ga, float* tbuf, float* xchg, uint4* qx,
@@ -336,6 +342,40 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
   else
     tmem_ld_32x32b_x8(taddr, r);
   float dg[NC], du[NC], ap[NC];  // act(g), a and up * act'(g) first, the gradients after the load
+  // the checkpoint's values: gate (which 0) and up (1) of the warp's feature jj, one or two at a time
+  uint32_t sfw[CK8 ? 2 : 1][CK8 ? NC / 4 : 1];
+  if constexpr (CK8) {
+    const uint8_t* sfb = reinterpret_cast<const uint8_t*>(ck) + 2 * 32 * 128 + (m >> 5) * 32 + sub * NC;
+#pragma unroll
+    for (int wh = 0; wh < 2; ++wh)
+#pragma unroll
+      for (int i = 0; i < NC / 4; i += 2) {  // 8-byte aligned: NC is 8 or 16
+        const uint2 v = *reinterpret_cast<const uint2*>(sfb + wh * 128 + 4 * i);
+        sfw[wh][i] = v.x;
+        sfw[wh][i + 1] = v.y;
+      }
+  }
+  // 2^23 + 128 + code as a float, from the code byte with its sign bit flipped in the low mantissa bits
+  auto ck8_biased = [&](int which, int jj) {
+    const uint32_t c = reinterpret_cast<const uint8_t*>(ck)[which * 32 * 128 + (sub * NC + jj) * 128 + m];
+    return __uint_as_float((c ^ 0x80u) | 0x4B000000u);
+  };
+  auto ck8_scale = [&](int which, int jj) {
+    return __uint_as_float(((sfw[CK8 ? which : 0][CK8 ? jj / 4 : 0] >> (8 * (jj & 3))) & 0xffu) << 23);
+  };
+  auto ck_one = [&](int which, int jj) {
+    if constexpr (CK8)
+      return (ck8_biased(which, jj) - 8388736.f) * ck8_scale(which, jj);
+    else
+      return bf16_bits_to_float(ck[which * 32 * 128 + (sub * NC + jj) * 128 + m]);
+  };
+  auto ck_two = [&](int which, int jj) {
+    if constexpr (CK8)
+      return f2_mul(f2_add(f2_pack(ck8_biased(which, jj), ck8_biased(which, jj + 1)), f2_splat(-8388736.f)),
+                    f2_pack(ck8_scale(which, jj), ck8_scale(which, jj + 1)));
+    else
+      return f2_pack(ck_one(which, jj), ck_one(which, jj + 1));
+  };
   // GENERIC: the activation, the gate/up layout and a saved act(gate) are read at run time;
   // otherwise SwiGLU, concat
   float sa[GENERIC ? NC : 1];
@@ -350,8 +390,8 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
   if (GENERIC && p.glu == MOE_GLU_GEGLU) {  // GELU(g) = g Phi(g), GELU'(g) = Phi(g) + g phi(g)
 #pragma unroll
     for (int jj = 0; jj < NC; ++jj) {
-      float g = bf16_bits_to_float(ck[(sub * NC + jj) * 128 + m]);
-      float u = bf16_bits_to_float(ck[32 * 128 + (sub * NC + jj) * 128 + m]);
+      float g = ck_one(0, jj);
+      float u = ck_one(1, jj);
       if (!valid) g = u = 0.f;
       const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
       const float pdf = 0.39894228040143268f * __expf(-0.5f * g * g);
@@ -364,8 +404,8 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
   } else if constexpr (GENERIC) {  // SiLU(g) = g sigma(g), SiLU'(g) = sigma(g) (1 + g (1 - sigma(g)))
 #pragma unroll
     for (int jj = 0; jj < NC; ++jj) {
-      float g = bf16_bits_to_float(ck[(sub * NC + jj) * 128 + m]);
-      float u = bf16_bits_to_float(ck[32 * 128 + (sub * NC + jj) * 128 + m]);
+      float g = ck_one(0, jj);
+      float u = ck_one(1, jj);
       if (!valid) g = u = 0.f;
       const float sg = __fdividef(1.f, 1.f + __expf(-g));
       float sl = g * sg;
@@ -380,12 +420,7 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     const uint64_t one2 = f2_splat(1.f), neg1 = f2_splat(-1.f), nl2e = f2_splat(-1.4426950408889634f);
 #pragma unroll
     for (int jj = 0; jj < NC; jj += 2) {
-      float g0 = bf16_bits_to_float(ck[(sub * NC + jj) * 128 + m]);
-      float g1 = bf16_bits_to_float(ck[(sub * NC + jj + 1) * 128 + m]);
-      float u0 = bf16_bits_to_float(ck[32 * 128 + (sub * NC + jj) * 128 + m]);
-      float u1 = bf16_bits_to_float(ck[32 * 128 + (sub * NC + jj + 1) * 128 + m]);
-      if (!valid) g0 = g1 = u0 = u1 = 0.f;
-      const uint64_t G = f2_pack(g0, g1), U = f2_pack(u0, u1);
+      const uint64_t G = valid ? ck_two(0, jj) : f2_splat(0.f), U = valid ? ck_two(1, jj) : f2_splat(0.f);
       float x0, x1;
       f2_unpack(f2_mul(G, nl2e), x0, x1);
       float e0, e1, s0, s1;
@@ -908,7 +943,15 @@ __global__ void __launch_bounds__((GemmCfg<MX, BN, EPI>::THREADS), 1) __maxnreg_
           const int i0 = tn.nt * BN + c * 32;
           mbar_arrive_expect_tx(&ck_full[buf], C::CK_CHUNK_BYTES);
           tma_load_2d(dst, &tmC, &ck_full[buf], b0, (int)((blk * 2 + 0) * p.I + i0));
-          tma_load_2d(dst + C::CK_CHUNK_BYTES / 2, &tmC, &ck_full[buf], b0, (int)((blk * 2 + 1) * p.I + i0));
+          tma_load_2d(dst + C::CK_HALF_BYTES, &tmC, &ck_full[buf], b0, (int)((blk * 2 + 1) * p.I + i0));
+          if constexpr (C::CK8) {  // the chunk's scale bytes, 128 consecutive ones of gate and of up
+            const int tiles = p.B >> 7;
+#pragma unroll
+            for (int wh = 0; wh < 2; ++wh)
+              bulk_load(dst + 2 * C::CK_HALF_BYTES + wh * 128,
+                        p.ck8_sf + (((blk * 2 + wh) * tiles + (b0 >> 7)) * (p.I >> 5) + (i0 >> 5)) * 128, 128,
+                        &ck_full[buf]);
+          }
           ++issued;
         }
       }
@@ -1114,17 +1157,17 @@ __global__ void __launch_bounds__((GemmCfg<MX, BN, EPI>::THREADS), 1) __maxnreg_
             float* tb = reinterpret_cast<float*>(wsm);
             if (!MX || p.fmt_act == MOE_FP8_E5M2) {
               if (generic)
-                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E5M2, true, C::G1_TBUFS == 1>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
+                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E5M2, true, C::G1_TBUFS == 1, C::CK8>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
                                                                   xc, qx, bar_id, ds_acc);
               else
-                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E5M2, false, C::G1_TBUFS == 1>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
+                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E5M2, false, C::G1_TBUFS == 1, C::CK8>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
                                                                    xc, qx, bar_id, ds_acc);
             } else {
               if (generic)
-                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E4M3, true, C::G1_TBUFS == 1>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
+                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E4M3, true, C::G1_TBUFS == 1, C::CK8>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
                                                                   xc, qx, bar_id, ds_acc);
               else
-                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E4M3, false, C::G1_TBUFS == 1>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
+                epi_dswiglu_part<MX, C::G1_NC, MOE_FP8_E4M3, false, C::G1_TBUFS == 1, C::CK8>(p, ta, prow, m, lane, valid, sv, i0, half, ckb, ga, tb,
                                                                    xc, qx, bar_id, ds_acc);
             }
           }

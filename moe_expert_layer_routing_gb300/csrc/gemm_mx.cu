@@ -15,6 +15,10 @@ int launch_gemm_mx(int BN, const GemmParams& p, const void* tmA, const void* tmB
   if (p.epi == kEpiDSwiGLU2)
     return BN == 192 ? gemm_launch_instance<true, 192, kEpiDSwiGLU2>(p, tmA, tmB, tmC, grid, st)
                      : gemm_launch_instance<true, 128, kEpiDSwiGLU2>(p, tmA, tmB, tmC, grid, st);
+  if (p.epi == kEpiDSwiGLU8)  // G1 on an 8-bit checkpoint
+    return BN == 192   ? gemm_launch_instance<true, 192, kEpiDSwiGLU8>(p, tmA, tmB, tmC, grid, st)
+           : BN == 256 ? gemm_launch_instance<true, 256, kEpiDSwiGLU8>(p, tmA, tmB, tmC, grid, st)
+                       : gemm_launch_instance<true, 128, kEpiDSwiGLU8>(p, tmA, tmB, tmC, grid, st);
   // G1: 192 columns (two TMEM accumulators, scales of W2 re-tiled per tile) where I allows
   if (BN == 192) return gemm_launch_instance<true, 192, kEpiDSwiGLU>(p, tmA, tmB, tmC, grid, st);
   return BN == 256 ? gemm_launch_instance<true, 256, kEpiDSwiGLU>(p, tmA, tmB, tmC, grid, st)

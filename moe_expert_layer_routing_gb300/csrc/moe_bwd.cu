@@ -53,7 +53,8 @@ int launch_gemm(bool mx, int BN, const GemmParams& p_in, const void* A, int64_t 
                     p.b_mn ? 64 : pair ? (uint32_t)pbn / 2 : (uint32_t)BN, p.b_mn ? 64 : bke))
     return MOE_ERR_INVALID;
   if (ckpt) {  // checkpoint chunks: 32 features x 128 rows of the [N*2*I, B] view, unswizzled
-    if (!make_tmap_2d(&tc, ckpt, 2, (uint64_t)ck_rows, (uint64_t)ck_cols, (uint64_t)ck_cols * 2, 32, 128, false))
+    const int cs = p.epi == kEpiDSwiGLU8 ? 1 : 2;
+    if (!make_tmap_2d(&tc, ckpt, cs, (uint64_t)ck_rows, (uint64_t)ck_cols, (uint64_t)ck_cols * cs, 32, 128, false))
       return MOE_ERR_INVALID;
   } else if (p.epi == kEpiStore) {  // output [rows, N] bf16, 64-column x 128-row boxes, 128B swizzle
     const int64_t out_rows = p.mode == kMGrouped ? (int64_t)p.m_tiles * 128 : (int64_t)p.num_experts * p.M;
@@ -151,7 +152,7 @@ static Layout make_layout(const MoeBwdArgs& a) {
   L.BN4 = bn_option(MOE_OPT_G4_TILE_N, L.BN4, 2 * a.I);
   {  // sixteen G1 epilogue warps (MXFP8, 128- or 192-column tiles) only on request: measured no faster
     const int64_t w = option(MOE_OPT_G1_WARPS);
-    const bool two = w == 16;
+    const bool two = w == 16 && a.act_src != MOE_ACT_CHECKPOINT8;
     L.g1_groups = (mx && two && (L.BN1 == 128 || L.BN1 == 192)) ? 2 : 1;
   }
   const int64_t P = L.P, H = a.H, I = a.I, E = a.E;
@@ -233,7 +234,7 @@ static int check_args(const MoeBwdArgs* a, bool need_ptrs) {
     return fail(MOE_ERR_INVALID, "moe_bwd: bad fp8 format");
   if (mx && a->has_bias && a->down_proj_act_ckpt)
     return fail(MOE_ERR_UNSUPPORTED, "moe_bwd: MXFP8 bias gradients with a saved down_proj_act_ckpt are not implemented");
-  if (a->act_src != MOE_ACT_CHECKPOINT && a->act_src != MOE_ACT_RECOMPUTE)
+  if (a->act_src != MOE_ACT_CHECKPOINT && a->act_src != MOE_ACT_RECOMPUTE && a->act_src != MOE_ACT_CHECKPOINT8)
     return fail(MOE_ERR_INVALID, "moe_bwd: bad act_src");
   if (a->glu != MOE_GLU_SWIGLU && a->glu != MOE_GLU_GEGLU) return fail(MOE_ERR_INVALID, "moe_bwd: bad glu");
   if (a->gate_up_layout != MOE_GATE_UP_CONCAT && a->gate_up_layout != MOE_GATE_UP_INTERLEAVED)
@@ -249,7 +250,7 @@ static int check_args(const MoeBwdArgs* a, bool need_ptrs) {
   }
   if (a->gate_up_layout == MOE_GATE_UP_INTERLEAVED && kG1Subs != 2)
     return fail(MOE_ERR_UNSUPPORTED, "moe_bwd: the interleaved layout needs 16 columns per G1 epilogue warp");
-  const bool rec = a->act_src == MOE_ACT_RECOMPUTE;
+  const bool rec = a->act_src == MOE_ACT_RECOMPUTE, ck8 = a->act_src == MOE_ACT_CHECKPOINT8;
   if (!need_ptrs) return MOE_OK;
   // token-sized arrays may be null when there are no tokens (T = 0: only the weight gradients, zeroed)
   const void* req_tok[] = {a->x, a->dout, a->s, a->ids, a->dx, a->ds};
@@ -260,7 +261,11 @@ static int check_args(const MoeBwdArgs* a, bool need_ptrs) {
     if (!q) return fail(MOE_ERR_INVALID, "moe_bwd: required pointer is null");
   for (const void* q : req_tok)
     if (!q && a->T > 0) return fail(MOE_ERR_INVALID, "moe_bwd: required pointer is null");
-  if (!rec && !a->gate_up_ckpt && a->T > 0) return fail(MOE_ERR_INVALID, "moe_bwd: gate_up_ckpt is null");
+  if (!rec && !ck8 && !a->gate_up_ckpt && a->T > 0) return fail(MOE_ERR_INVALID, "moe_bwd: gate_up_ckpt is null");
+  if (ck8 && (!a->gate_up_ckpt_q || !a->gate_up_ckpt_sf) && a->T > 0)
+    return fail(MOE_ERR_INVALID, "moe_bwd: the 8-bit checkpoint needs gate_up_ckpt_q and gate_up_ckpt_sf");
+  if (ck8 && ((reinterpret_cast<uintptr_t>(a->gate_up_ckpt_q) | reinterpret_cast<uintptr_t>(a->gate_up_ckpt_sf)) & 15))
+    return fail(MOE_ERR_INVALID, "moe_bwd: gate_up_ckpt_q and gate_up_ckpt_sf must be 16-byte aligned");
   {
     const int given = (a->expert_offsets != nullptr) + (a->s_scatter_idx != nullptr) + (a->block_offsets != nullptr);
     if (given != 0 && given != 3)
@@ -562,7 +567,8 @@ extern "C" int moe_bwd(const MoeBwdArgs* args, moe_stream_t stream) {
   prof_mark(st, slot, 2);
 
   // 2b. G0 (recompute): h = x_g W1_e + b1_e written into a block checkpoint in the workspace
-  const void* ckpt = a.gate_up_ckpt;
+  const bool ck8 = a.act_src == MOE_ACT_CHECKPOINT8;
+  const void* ckpt = ck8 ? static_cast<const void*>(a.gate_up_ckpt_q) : a.gate_up_ckpt;
   if (rec) {
     GemmParams p{};
     p.mode = kMGrouped;
@@ -617,7 +623,8 @@ extern "C" int moe_bwd(const MoeBwdArgs* args, moe_stream_t stream) {
     }
     p.sfa_ktiles = p.sfb_ktiles = (int)(H / 128);
     p.fmt_a = a.fp8_act; p.fmt_b = a.fp8_w;
-    p.epi = L.g1_groups == 2 ? kEpiDSwiGLU2 : kEpiDSwiGLU;
+    p.epi = ck8 ? kEpiDSwiGLU8 : L.g1_groups == 2 ? kEpiDSwiGLU2 : kEpiDSwiGLU;
+    p.ck8_sf = a.gate_up_ckpt_sf;
     p.s = a.s;
     p.tile_row_flat = tile_row_flat;
     p.e_tile_offsets = tile_offsets;

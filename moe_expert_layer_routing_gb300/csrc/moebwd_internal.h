@@ -176,8 +176,9 @@ int launch_linear_quant(const uint16_t* dY, const uint16_t* W, const uint16_t* X
 // ------------------------------------------------------------------------------------------
 enum GemmMode { kMGrouped = 0, kKGrouped = 1 };
 // kEpiDSwiGLU2: the dSwiGLU epilogue with two groups of epilogue warps taking alternate 32-feature
-// chunks (sixteen warps, three checkpoint buffers, one pipeline stage fewer)
-enum EpiKind { kEpiStore = 0, kEpiDSwiGLU = 1, kEpiCkpt = 2, kEpiDSwiGLU2 = 3 };
+// chunks (sixteen warps, three checkpoint buffers, one pipeline stage fewer); kEpiDSwiGLU8: the dSwiGLU
+// epilogue on an 8-bit checkpoint
+enum EpiKind { kEpiStore = 0, kEpiDSwiGLU = 1, kEpiCkpt = 2, kEpiDSwiGLU2 = 3, kEpiDSwiGLU8 = 4 };
 // dSwiGLU epilogue (G1): warps per TMEM lane quarter; each takes 32 / kG1Subs of every 32 columns
 // and writes one ds partial per (row, N tile).
 #ifndef MOEBWD_G1_SUBS
@@ -213,6 +214,7 @@ struct GemmParams {
   const int32_t* e_tile_offsets;
   const int32_t* block_offsets;
   const uint16_t* ckpt;         // [N,2,I,B]
+  const uint8_t* ck8_sf;        // kEpiDSwiGLU8: scale bytes [N,2,B/128,I/32,4,32] of the int8 codes
   const uint16_t* b1;           // G0 (checkpoint epilogue): [E,2I] bias or null
   int I, B, affinity_on_i, fmt_act;
   int glu;                      // MOE_GLU_SWIGLU or MOE_GLU_GEGLU

@@ -1,0 +1,206 @@
+"""GPU parity of layer_norm_fwd / layer_norm_bwd against the float64 oracle: both kinds, types and weight types,
+widths that are odd, below a warp and above a block, row strides, unaligned rows, a single row, none, one column,
+the residual and the skip gradient.
+
+Bounds: u = 2^-24 is fp32's rounding unit and a sum of H terms in any order is off by at most H u times the sum
+of magnitudes, so with the row's mean and rstd each carrying H u (1 + mean|s| rstd), every intermediate is off
+by at most (4 H + 64) u (1 + mean|s| rstd) times the sum of the magnitudes it is made of; the result is then
+rounded to its type, by at most 2^-8 (bf16) or u (fp32) of itself."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import np64
+from oracle import norm as on
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+EPS = 1e-5
+
+
+def _mb():
+    import moe_expert_layer_routing_gb300 as mb
+    return mb
+
+
+def _rand(shape, dtype, seed, stride=None, shift=0):
+    """Rows on the GPU; stride: elements from row to row; shift: elements off the allocation's start."""
+    gen = torch.Generator().manual_seed(seed)
+    T, H = shape
+    v = torch.randn(T, H, generator=gen).to(dtype)
+    stride = stride or H
+    buf = torch.full((T * stride + shift,), float("nan"), dtype=dtype, device="cuda")
+    out = buf[shift:shift + T * stride].view(T, stride)[:, :H] if T else buf[:0].view(0, H)
+    out.copy_(v)
+    return out
+
+
+def _unit(dtype):
+    return 2.0 ** -8 if dtype == torch.bfloat16 else U
+
+
+CASES = [(1, 1), (1, 2048), (3, 7), (5, 64), (2, 100), (4, 1111), (3, 1024), (2, 4096), (2, 5000), (3, 8192), (2, 12288),
+         (70, 256), (333, 96), (150, 520)]
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", CASES)
+@pytest.mark.parametrize("how", ["plain", "residual", "strided"])
+def test_forward(kind, dtype, T, H, how):
+    mb = _mb()
+    wt = torch.float32 if (T + H) % 2 else torch.bfloat16
+    strided = how == "strided"
+    x = _rand((T, H), dtype, 1, H + 24 if strided else None, 1 if strided else 0)
+    x += 0.5
+    r = _rand((T, H), dtype, 2, H + 3 if strided else None) if how != "plain" else None
+    gamma, beta = _rand((1, H), wt, 3)[0], _rand((1, H), wt, 4)[0]
+    out = mb.layer_norm_fwd(x, gamma, beta if how != "strided" else None, eps=EPS, residual=r, kind=kind)
+    torch.cuda.synchronize()
+    s = x if r is None else (x.float() + r.float()).to(dtype)
+    if r is not None:
+        assert torch.equal(out["sum"], s)
+    else:
+        assert out["sum"] is None
+    b = None if strided else np64(beta)
+    y, mean, rstd = on.forward(np64(s), np64(gamma), b, EPS, kind)
+    grow = (4 * H + 64) * U * (1 + np.abs(np64(s)).mean(1) * rstd)
+    assert np.all(np.abs(np64(out["rstd"]) - rstd) <= grow * rstd)
+    if kind == 0:
+        assert np.all(np.abs(np64(out["mean"]) - mean) <= H * U * np.abs(np64(s)).mean(1) + U * np.abs(mean))
+    else:
+        assert out["mean"] is None
+    parts = (np.abs(np64(s)) + np.abs(mean)[:, None]) * rstd[:, None] * np.abs(np64(gamma))
+    bound = grow[:, None] * (parts + (0 if b is None else np.abs(b))) + _unit(dtype) * np.abs(y)
+    assert np.all(np.abs(np64(out["y"]) - y) <= bound)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", CASES)
+@pytest.mark.parametrize("how", ["plain", "skip", "strided"])
+def test_backward(kind, dtype, T, H, how):
+    if H > 6000:
+        T = 1          # the oracle's Jacobian is H x H
+    mb = _mb()
+    wt = torch.float32 if (T + H) % 2 else torch.bfloat16
+    strided = how == "strided"
+    x = _rand((T, H), dtype, 1, H + 24 if strided else None, 1 if strided else 0)
+    x += 0.25
+    dy = _rand((T, H), dtype, 5, H + 8 if strided else None)
+    dres = _rand((T, H), dtype, 6, H + 5 if strided else None) if how != "plain" else None
+    gamma = _rand((1, H), wt, 3)[0]
+    xs, dys, g = np64(x), np64(dy), np64(gamma)
+    _, mean, rstd = on.forward(xs, g, None, EPS, kind)
+    f32 = lambda v: torch.from_numpy(v).float().cuda()  # noqa: E731
+    out = mb.layer_norm_bwd(dy, x, gamma, f32(mean) if kind == 0 else None, f32(rstd), dres=dres, kind=kind)
+    torch.cuda.synchronize()
+    dx, dg, db = on.backward(dys, xs, g, EPS, kind, None if dres is None else np64(dres))
+    w, xh = dys * g, (xs - mean[:, None]) * rstd[:, None]
+    grow = ((4 * H + 64) * U * (1 + np.abs(xs).mean(1) * rstd))[:, None]
+    parts = rstd[:, None] * (np.abs(w) + np.abs(w).mean(1, keepdims=True)
+                             + (np.abs(xh) + 1) * np.abs(w * xh).mean(1, keepdims=True))
+    if dres is not None:
+        parts = parts + np.abs(np64(dres))
+    assert np.all(np.abs(np64(out["dx"]) - dx) <= grow * parts + _unit(dtype) * np.abs(dx))
+    rows = (T + 64) * U + 8 * U * (1 + np.abs(mean) * rstd).max()
+    assert np.all(np.abs(np64(out["dgamma"]) - dg) <= rows * (np.abs(dys) * (np.abs(xh) + 1)).sum(0))
+    if kind == 0:
+        assert np.all(np.abs(np64(out["dbeta"]) - db) <= (T + 64) * U * np.abs(dys).sum(0))
+    else:
+        assert out["dbeta"] is None
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_mean_and_constant_rows(dtype):
+    """The variance is of differences from the mean: rows far from zero keep it, a constant row has rstd
+    1 / sqrt(eps) and y = beta."""
+    mb = _mb()
+    H = 512
+    x = torch.full((2, H), 96.0, dtype=dtype, device="cuda")
+    x[1, ::2] += 1.0    # exact in bf16: 96 and 97, variance 1/4
+    one, zero = torch.ones(H, device="cuda"), torch.zeros(H, device="cuda")
+    out = mb.layer_norm_fwd(x, one, zero + 3, eps=EPS)
+    torch.cuda.synchronize()
+    assert torch.equal(out["y"][0].float(), torch.full((H,), 3.0, device="cuda"))
+    np.testing.assert_allclose(np64(out["rstd"]), [EPS ** -0.5, (0.25 + EPS) ** -0.5], rtol=1e-5)
+    assert np64(out["mean"]).tolist() == [96.0, 96.5]
+
+
+def test_gradient_against_differences_of_the_forward():
+    """dx by central differences of the GPU's own fp32 forward: step 2^-6, so rounding is about 2^-24 sqrt(H) |y|
+    / 2^-6 ~ 1e-4 of the gradient's scale and truncation about 2^-12."""
+    mb = _mb()
+    T, H = 3, 24
+    x, dy, gamma, beta = (_rand((t, H), torch.float32, k) for t, k in ((T, 1), (T, 2), (1, 3), (1, 4)))
+    gamma, beta = gamma[0], beta[0]
+    f = mb.layer_norm_fwd(x, gamma, beta, eps=1e-2)
+    g = np64(mb.layer_norm_bwd(dy, x, gamma, f["mean"], f["rstd"])["dx"])
+    h = 2.0 ** -6
+    num = np.zeros((T, H))
+    for i in range(H):
+        d = torch.zeros(T, H, device="cuda")
+        d[:, i] = h
+        y1, y0 = (mb.layer_norm_fwd(x + s * d, gamma, beta, eps=1e-2)["y"] for s in (1, -1))
+        num[:, i] = ((np64(y1) - np64(y0)) * np64(dy)).sum(1) / (2 * h)
+    assert np.abs(num - g).max() <= 2e-3 * np.abs(g).max()
+
+
+def test_accumulate_repeats_and_streams():
+    """dgamma and dbeta added to an earlier result; the same call twice, and on another stream, gives the same bits."""
+    mb = _mb()
+    T, H = 1000, 384
+    x, dy = _rand((T, H), torch.bfloat16, 1), _rand((T, H), torch.bfloat16, 2)
+    gamma = torch.ones(H, device="cuda")
+    f = mb.layer_norm_fwd(x, gamma, gamma)
+    a = mb.layer_norm_bwd(dy, x, gamma, f["mean"], f["rstd"])
+    ga, ba = a["dgamma"].clone(), a["dbeta"].clone()
+    mb.layer_norm_bwd(dy, x, gamma, f["mean"], f["rstd"], accumulate_into=a)
+    torch.cuda.synchronize()
+    assert torch.equal(a["dgamma"], ga + ga) and torch.equal(a["dbeta"], ba + ba)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b = mb.layer_norm_bwd(dy, x, gamma, f["mean"], f["rstd"], stream=side)
+    side.synchronize()
+    for k in ("dx",):
+        assert torch.equal(b[k], a[k])
+    assert torch.equal(b["dgamma"], ga) and torch.equal(b["dbeta"], ba)
+
+
+def test_residual_stream_updated_in_place():
+    """sum may be x or the residual themselves (C entry point)."""
+    mb = _mb()
+    T, H = 5, 640
+    x, r = _rand((T, H), torch.bfloat16, 1), _rand((T, H), torch.bfloat16, 2)
+    gamma = torch.ones(H, device="cuda")
+    ref = mb.layer_norm_fwd(x, gamma, gamma, residual=r)
+    for target in (x.clone(), r.clone()):
+        xx, rr = (target, r) if torch.equal(target, x) else (x, target)
+        y, mean, rstd = torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        rc = mb.lib().layer_norm_fwd(0, xx.data_ptr(), H, rr.data_ptr(), H, gamma.data_ptr(), gamma.data_ptr(), 0, 1, T, H,
+                                     1e-5, y.data_ptr(), target.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.equal(target, ref["sum"]) and torch.equal(y, ref["y"])
+
+
+def test_empty_and_refusals():
+    mb = _mb()
+    g = torch.ones(8, device="cuda")
+    e = torch.empty(0, 8, device="cuda")
+    z = torch.empty(0, device="cuda")
+    assert mb.layer_norm_fwd(e, g)["y"].shape == (0, 8)
+    out = mb.layer_norm_bwd(e, e, g, z, z)
+    torch.cuda.synchronize()
+    assert not out["dgamma"].any() and not out["dbeta"].any()
+    x = torch.ones(2, 8, device="cuda")
+    s = torch.ones(2, device="cuda")
+    for bad in (lambda: mb.layer_norm_fwd(x.half(), g), lambda: mb.layer_norm_fwd(x, g[:7]),
+                lambda: mb.layer_norm_fwd(x.t(), torch.ones(2, device="cuda")), lambda: mb.layer_norm_fwd(x.cpu(), g),
+                lambda: mb.layer_norm_fwd(x, g, residual=x[:1]), lambda: mb.layer_norm_fwd(x, g, eps=-1.0),
+                lambda: mb.layer_norm_fwd(x[:1].expand(2, 8), g), lambda: mb.layer_norm_fwd(x, g, kind=2),
+                lambda: mb.layer_norm_bwd(x.bfloat16(), x, g, s, s), lambda: mb.layer_norm_bwd(x, x, g, s[:1], s),
+                lambda: mb.layer_norm_bwd(x, x, g, None, s)):
+        with pytest.raises(mb.MoeError):
+            bad()
