@@ -13,9 +13,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "moebwd_internal.h"
 #include "mx_device.cuh"
+#include "ptx.cuh"
 
 namespace moebwd {
 
@@ -193,8 +195,411 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_reduce_kernel(const float* 
   }
 }
 
+// ------------------------------------------------------------------------------------------
+// Rows in registers
+// ------------------------------------------------------------------------------------------
+// A row belongs to a group of GT = 32 WPR threads (a warp, or the block of eight warps) and passes once: a
+// thread holds CPT of its columns, as NV 16-byte vectors VEC wide (thread li of the group: vectors v GT + li), or,
+// where rows are not 16-byte aligned, as single elements (VEC = 1).  Blocks are persistent.  Vectors come through a
+// ring of rows in shared memory by 16-byte asynchronous copies: every thread copies what it alone reads,
+// so the ring needs no barrier, and the rows in flight cost no registers.
+template <typename X, int CPT, int WPR, bool ALIGNED>
+struct LnTile {
+  static constexpr int VEC = ALIGNED ? 16 / (int)sizeof(X) : 1;
+  static constexpr int NV = CPT / VEC;
+  static constexpr int GT = 32 * WPR;
+  static constexpr int GROUPS = kLnThreads / GT;
+  __device__ static int col(int v, int li) { return (v * GT + li) * VEC; }
+  __device__ static int group() { return WPR == 1 ? threadIdx.x >> 5 : 0; }
+  __device__ static int li() { return WPR == 1 ? threadIdx.x & 31 : threadIdx.x; }
+};
+
+__device__ __forceinline__ void ln_unpack(const uint4& w, float (&f)[4]) {
+  f[0] = __uint_as_float(w.x);
+  f[1] = __uint_as_float(w.y);
+  f[2] = __uint_as_float(w.z);
+  f[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void ln_unpack(const uint4& w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 ln_pack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 ln_pack(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// VEC weights from column c on, in fp32 (16-byte loads when VEC > 1)
+template <int VEC>
+__device__ __forceinline__ void ln_weights(const void* p, int bf16, int c, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = bf16 ? bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p) + c)) : __ldg(static_cast<const float*>(p) + c);
+  } else if (!bf16) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + i));
+      f[i] = w.x;
+      f[i + 1] = w.y;
+      f[i + 2] = w.z;
+      f[i + 3] = w.w;
+    }
+  } else if constexpr (VEC == 8) {
+    ln_unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c)), f);
+  } else {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c));
+    f[0] = __uint_as_float(w.x << 16);
+    f[1] = __uint_as_float(w.x & 0xffff0000u);
+    f[2] = __uint_as_float(w.y << 16);
+    f[3] = __uint_as_float(w.y & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ float ln_warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Ring slot (stage, tensor, vector) of this thread.
+template <int TENSORS, int NV>
+__device__ __forceinline__ uint4* ln_slot(uint4* ring, int stage, int tensor, int v) {
+  return ring + ((stage * TENSORS + tensor) * NV + v) * kLnThreads + threadIdx.x;
+}
+
+// Rows of the ring: what fits four (forward) and two (backward) blocks of 4096 columns on an SM.
+__host__ __device__ constexpr int ln_fwd_stages(int es) { return es == 2 ? 3 : 2; }
+__host__ __device__ constexpr int ln_bwd_stages(int es) { return es == 2 ? 4 : 2; }
+
+// Forward.  The statistics of a row: each warp takes the mean and the squared differences of its own columns (two
+// shuffle sums), the warps' pairs (n, mean, M2) are combined exactly: M2 = sum M2_w + n_w (mean_w - mean)^2.  So a
+// row costs one barrier and no difference of squares.
+template <typename X, int CPT, int WPR, bool ALIGNED>
+__global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 2 : 4) ln_fwd_kernel(const LnFwdArgs a, int w_bf16) {
+  using L = LnTile<X, CPT, WPR, ALIGNED>;
+  constexpr int VEC = L::VEC, NV = L::NV, S = ln_fwd_stages(sizeof(X));
+  extern __shared__ uint4 ring[];
+  __shared__ float wn[8], wmean[2][8], wm2[2][8];
+  const X *x = static_cast<const X*>(a.x), *r = static_cast<const X*>(a.r);
+  X *y = static_cast<X*>(a.y), *sum = static_cast<X*>(a.sum);
+  const int li = L::li(), w = threadIdx.x >> 5;
+  const int64_t step = (int64_t)gridDim.x * L::GROUPS;
+  const float inv = 1.f / (float)a.H;
+  float n_w = 0.f;  // columns of this warp
+#pragma unroll
+  for (int v = 0; v < NV; ++v) n_w += L::col(v, li) < a.H ? (float)VEC : 0.f;
+  n_w = ln_warp_sum(n_w);
+  if (WPR > 1) {
+    if ((threadIdx.x & 31) == 0) wn[w] = n_w;
+    __syncthreads();
+  }
+  pdl_wait();
+  pdl_trigger();
+  auto fetch = [&](int64_t t, int stage) {
+    if constexpr (ALIGNED) {
+      if (t < a.T) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = L::col(v, li);
+          if (c < a.H) {
+            cp_async_16(smem_u32(ln_slot<2, NV>(ring, stage, 0, v)), x + t * a.ldx + c);
+            if (r) cp_async_16(smem_u32(ln_slot<2, NV>(ring, stage, 1, v)), r + t * a.ldr + c);
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * L::GROUPS + L::group();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
+  int stage = 0, par = 0;
+  // a warp of its own leaves when its rows are through; a block's warps share t
+  for (; t < a.T; t += step) {
+    float f[NV][VEC];
+    if constexpr (ALIGNED) {
+      fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);  // the slot read last time round
+      cp_async_wait<S - 1>();
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = L::col(v, li);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[v][i] = 0.f;
+      if (c < a.H) {
+        if constexpr (ALIGNED) {
+          ln_unpack(*ln_slot<2, NV>(ring, stage, 0, v), f[v]);
+          if (r) {
+            float q[VEC];
+            ln_unpack(*ln_slot<2, NV>(ring, stage, 1, v), q);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[v][i] = ln_round(f[v][i] + q[i], x);
+          }
+          if (sum) *reinterpret_cast<uint4*>(sum + t * a.H + c) = ln_pack(f[v]);
+        } else {
+          f[v][0] = ln_ld(x, t * a.ldx + c);
+          if (r) f[v][0] = ln_round(f[v][0] + ln_ld(r, t * a.ldr + c), x);
+          if (sum) ln_st(sum, t * a.H + c, f[v][0]);
+        }
+      }
+    }
+    float mu = 0.f, m2 = 0.f;
+    if (!a.rms) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) mu += f[v][i];
+      mu = n_w > 0.f ? ln_warp_sum(mu) / n_w : 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (L::col(v, li) < a.H)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float d = f[v][i] - mu;
+          m2 = fmaf(d, d, m2);
+        }
+    m2 = ln_warp_sum(m2);
+    if constexpr (WPR > 1) {
+      if ((threadIdx.x & 31) == 0) {
+        wmean[par][w] = mu;
+        wm2[par][w] = m2;
+      }
+      __syncthreads();  // the buffers alternate: the next row's writes meet no reader of this one
+      mu = m2 = 0.f;
+      if (!a.rms) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mu = fmaf(wn[k], wmean[par][k], mu);
+        mu *= inv;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = wmean[par][k] - mu;
+        m2 += a.rms ? wm2[par][k] : fmaf(wn[k] * d, d, wm2[par][k]);
+      }
+      par ^= 1;
+    }
+    const float rs = 1.f / sqrtf(m2 * inv + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = L::col(v, li);
+      if (c < a.H) {
+        float g[VEC], b[VEC];
+        ln_weights<VEC>(a.gamma, w_bf16, c, g);
+        if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, b);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          f[v][i] = (f[v][i] - mu) * rs * g[i];
+          if (a.beta) f[v][i] += b[i];
+        }
+        if constexpr (ALIGNED)
+          *reinterpret_cast<uint4*>(y + t * a.H + c) = ln_pack(f[v]);
+        else
+          ln_st(y, t * a.H + c, f[v][0]);
+      }
+    }
+    if (li == 0) {
+      if (a.mean) a.mean[t] = mu;
+      a.rstd[t] = rs;
+    }
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+}
+
+// Backward: dx and, in the thread's registers over all rows of its group, dgamma and dbeta of its columns; a
+// block leaves one partial row of each.
+template <typename X, int CPT, int WPR, bool ALIGNED>
+__global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(const LnBwdArgs a, int w_bf16) {
+  using L = LnTile<X, CPT, WPR, ALIGNED>;
+  constexpr int VEC = L::VEC, NV = L::NV, GT = L::GT, S = ln_bwd_stages(sizeof(X));
+  extern __shared__ uint4 ring[];
+  __shared__ float r1[2][8], r2[2][8];
+  const X *dy = static_cast<const X*>(a.dy), *x = static_cast<const X*>(a.x), *dres = static_cast<const X*>(a.dres);
+  X* dx = static_cast<X*>(a.dx);
+  const int li = L::li(), w = threadIdx.x >> 5;
+  const int64_t step = (int64_t)gridDim.x * L::GROUPS;
+  const float inv = 1.f / (float)a.H;
+  pdl_wait();
+  pdl_trigger();
+  float gamma[NV][VEC], ag[NV][VEC], ab[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) gamma[v][i] = ag[v][i] = ab[v][i] = 0.f;
+    if (L::col(v, li) < a.H) ln_weights<VEC>(a.gamma, w_bf16, L::col(v, li), gamma[v]);
+  }
+  auto fetch = [&](int64_t t, int stage) {
+    if constexpr (ALIGNED) {
+      if (t < a.T) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = L::col(v, li);
+          if (c < a.H) {
+            cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 0, v)), dy + t * a.lddy + c);
+            cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 1, v)), x + t * a.ldx + c);
+            if (dres) cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 2, v)), dres + t * a.ldres + c);
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * L::GROUPS + L::group();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
+  int stage = 0, par = 0;
+  for (; t < a.T; t += step) {
+    if constexpr (ALIGNED) {
+      fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+      cp_async_wait<S - 1>();
+    }
+    const float mu = a.rms ? 0.f : __ldg(a.mean + t), rs = __ldg(a.rstd + t);
+    float wd[NV][VEC], xh[NV][VEC], c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = L::col(v, li);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) wd[v][i] = xh[v][i] = 0.f;
+      if (c < a.H) {
+        if constexpr (ALIGNED) {
+          ln_unpack(*ln_slot<3, NV>(ring, stage, 0, v), wd[v]);
+          ln_unpack(*ln_slot<3, NV>(ring, stage, 1, v), xh[v]);
+        } else {
+          wd[v][0] = ln_ld(dy, t * a.lddy + c);
+          xh[v][0] = ln_ld(x, t * a.ldx + c);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float d = wd[v][i];
+          xh[v][i] = (xh[v][i] - mu) * rs;
+          ag[v][i] = fmaf(d, xh[v][i], ag[v][i]);
+          ab[v][i] += d;
+          wd[v][i] = d * gamma[v][i];
+          c1 = fmaf(wd[v][i], xh[v][i], c1);
+          c2 += wd[v][i];
+        }
+      }
+    }
+    c1 = ln_warp_sum(c1);
+    c2 = ln_warp_sum(c2);
+    if constexpr (WPR > 1) {
+      if ((threadIdx.x & 31) == 0) {
+        r1[par][w] = c1;
+        r2[par][w] = c2;
+      }
+      __syncthreads();
+      c1 = c2 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        c1 += r1[par][k];
+        c2 += r2[par][k];
+      }
+      par ^= 1;
+    }
+    c1 *= inv;
+    c2 = a.rms ? 0.f : c2 * inv;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = L::col(v, li);
+      if (c < a.H) {
+        float d[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) d[i] = rs * (wd[v][i] - c2 - xh[v][i] * c1);
+        if (dres) {
+          float q[VEC];
+          if constexpr (ALIGNED)
+            ln_unpack(*ln_slot<3, NV>(ring, stage, 2, v), q);
+          else
+            q[0] = ln_ld(dres, t * a.ldres + c);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) d[i] += q[i];
+        }
+        if constexpr (ALIGNED)
+          *reinterpret_cast<uint4*>(dx + t * a.H + c) = ln_pack(d);
+        else
+          ln_st(dx, t * a.H + c, d[0]);
+      }
+    }
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+  // the block's partial rows: with a warp per row the eight warps' sums first, in order, through shared memory
+  float* sm = reinterpret_cast<float*>(ring);
+  if constexpr (WPR == 1) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if constexpr (ALIGNED) cp_async_wait<0>();
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sm[w * (GT * CPT) + L::col(v, li) + i] = half ? ab[v][i] : ag[v][i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.H; c += kLnThreads) {
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q += sm[k * (GT * CPT) + c];
+        a.part[((int64_t)half * a.G + blockIdx.x) * a.H + c] = q;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = L::col(v, li);
+      if (c < a.H)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          a.part[(int64_t)blockIdx.x * a.H + c + i] = ag[v][i];
+          a.part[((int64_t)a.G + blockIdx.x) * a.H + c + i] = ab[v][i];
+        }
+    }
+  }
+}
+
+// Variants: a warp per row up to 1024 columns (8, 16 or 32 a thread), a block per row up to 8192.
+typedef void (*LnFwdKernel)(const LnFwdArgs, int);
+typedef void (*LnBwdKernel)(const LnBwdArgs, int);
+constexpr int kLnMaxH = 8192;
+
+#define LN_PICK(KERN, X, AL)                                                                        \
+  (H <= 256 ? KERN<X, 8, 1, AL> : H <= 512 ? KERN<X, 16, 1, AL> : H <= 1024 ? KERN<X, 32, 1, AL>    \
+   : H <= 2048 ? KERN<X, 8, 8, AL> : H <= 4096 ? KERN<X, 16, 8, AL> : KERN<X, 32, 8, AL>)
+
+static int ln_cpt(int64_t H) { return H <= 256 ? 8 : H <= 512 ? 16 : H <= 1024 ? 32 : H <= 2048 ? 8 : H <= 4096 ? 16 : 32; }
+static int ln_rows_per_block(int64_t H) { return H <= 1024 ? 8 : 1; }
+
+// Bytes of the ring: stages x tensors x a block's rows; the backward's also holds eight warps' column sums
+static size_t ln_ring(int stages, int tensors, int64_t H, int es) {
+  return (size_t)stages * tensors * kLnThreads * ln_cpt(H) * es;
+}
+
 // Row groups of the backward's partial sums.
-static int ln_groups(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(1024, (T + 31) / 32)); }
+static int ln_groups(int64_t T, int64_t H) {
+  if (H > kLnMaxH) return (int)std::max<int64_t>(1, std::min<int64_t>(304, (T + 31) / 32));
+  const int rows = ln_rows_per_block(H);  // as many blocks as stay resident on 152 SMs
+  return (int)std::min<int64_t>(ln_cpt(H) == 32 ? 152 : 304, (T + rows - 1) / rows);
+}
+
+static bool ln_vectors(int64_t H, int es, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> strides) {
+  const int vec = 16 / es;
+  if (H % vec) return false;
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  for (int64_t ld : strides)
+    if (ld % vec) return false;
+  return true;
+}
+
+// Shared memory above what every kernel may have (48 KB, the static part included).
+static int ln_smem(const void* kern, size_t bytes) {
+  if (bytes <= 40 * 1024) return MOE_OK;
+  return cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
+                    "cudaFuncSetAttribute(layer_norm)");
+}
 
 static int ln_check(const char* who, int kind, int x_dtype, int w_dtype, int64_t T, int64_t H) {
   if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) return fail(MOE_ERR_INVALID, "%s: bad kind", who);
@@ -233,8 +638,20 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
     if ((rc = ln_aligned("layer_norm_fwd", p, w_dtype))) return rc;
   LnFwdArgs a{x, residual, gamma, beta, y, sum, kind == MOE_NORM_LAYER ? mean : nullptr, rstd, ldx, ldr, T, (int)H,
               kind == MOE_NORM_RMS, eps};
-  const int grid = (int)std::min<int64_t>(T, 65536);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool b16 = x_dtype == MOE_DT_BF16;
+  if (H <= kLnMaxH) {
+    const bool al = ln_vectors(H, b16 ? 2 : 4, {x, residual, y, sum, gamma, beta}, {ldx, ldr});
+    LnFwdKernel k = b16 ? (al ? LN_PICK(ln_fwd_kernel, uint16_t, true) : LN_PICK(ln_fwd_kernel, uint16_t, false))
+                        : (al ? LN_PICK(ln_fwd_kernel, float, true) : LN_PICK(ln_fwd_kernel, float, false));
+    const size_t smem = al ? ln_ring(ln_fwd_stages(b16 ? 2 : 4), 2, H, b16 ? 2 : 4) : 0;
+    if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem))) return rc;
+    const int rows = ln_rows_per_block(H);
+    const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * (ln_cpt(H) == 32 ? 2 : 4));
+    return launch_pdl(k, dim3((unsigned)grid), dim3(kLnThreads), smem, st, "layer_norm_fwd", a,
+                      (int)(w_dtype == MOE_DT_BF16));
+  }
+  const int grid = (int)std::min<int64_t>(T, 65536);
   auto kern = x_dtype == MOE_DT_BF16
                   ? (w_dtype == MOE_DT_BF16 ? ln_fwd_any_kernel<uint16_t, uint16_t> : ln_fwd_any_kernel<uint16_t, float>)
                   : (w_dtype == MOE_DT_BF16 ? ln_fwd_any_kernel<float, uint16_t> : ln_fwd_any_kernel<float, float>);
@@ -243,7 +660,7 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
 
 extern "C" size_t layer_norm_bwd_workspace_size(int64_t T, int64_t H) {
   if (T <= 0 || H <= 0 || H > INT32_MAX / 8) return 0;
-  return sizeof(float) * 2 * (size_t)ln_groups(T) * (size_t)H;
+  return sizeof(float) * 2 * (size_t)ln_groups(T, H) * (size_t)H;
 }
 
 extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gamma,
@@ -274,17 +691,32 @@ extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void
   if (workspace_bytes < need)
     return fail(MOE_ERR_INVALID, "layer_norm_bwd: workspace too small (%zu < %zu)", workspace_bytes, need);
   LnBwdArgs a{dy, x, gamma, dres, mean, rstd, dx, static_cast<float*>(workspace), lddy, ldx, ldres, T, (int)H,
-              kind == MOE_NORM_RMS, ln_groups(T)};
+              kind == MOE_NORM_RMS, ln_groups(T, H)};
+  const int tiles = (int)((H + 31) / 32);
+  auto weights = [&]() {
+    return launch_pdl(ln_bwd_reduce_kernel, dim3(tiles, dbeta ? 2 : 1), dim3(kLnThreads), 0, st,
+                      "layer_norm_bwd weight gradients", static_cast<const float*>(a.part), a.G, (int)H, dgamma, dbeta,
+                      accumulate);
+  };
+  if (H <= kLnMaxH) {
+    const bool b16 = x_dtype == MOE_DT_BF16;
+    const bool al = ln_vectors(H, b16 ? 2 : 4, {dy, x, dres, dx, gamma}, {lddy, ldx, ldres});
+    LnBwdKernel k = b16 ? (al ? LN_PICK(ln_bwd_kernel, uint16_t, true) : LN_PICK(ln_bwd_kernel, uint16_t, false))
+                        : (al ? LN_PICK(ln_bwd_kernel, float, true) : LN_PICK(ln_bwd_kernel, float, false));
+    const size_t sums = H <= 1024 ? sizeof(float) * kLnThreads * ln_cpt(H) : 0;
+    const size_t smem = std::max(al ? ln_ring(ln_bwd_stages(b16 ? 2 : 4), 3, H, b16 ? 2 : 4) : 0, sums);
+    if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem)) ||
+        (rc = launch_pdl(k, dim3(a.G), dim3(kLnThreads), smem, st, "layer_norm_bwd", a, (int)(w_dtype == MOE_DT_BF16))))
+      return rc;
+    return weights();
+  }
   const int grid = (int)std::min<int64_t>(T, 65536);
   auto kern = x_dtype == MOE_DT_BF16 ? (w_dtype == MOE_DT_BF16 ? ln_bwd_dx_any_kernel<uint16_t, uint16_t>
                                                                : ln_bwd_dx_any_kernel<uint16_t, float>)
                                      : (w_dtype == MOE_DT_BF16 ? ln_bwd_dx_any_kernel<float, uint16_t>
                                                                : ln_bwd_dx_any_kernel<float, float>);
-  const int tiles = (int)((H + 31) / 32);
   auto part = x_dtype == MOE_DT_BF16 ? ln_bwd_part_any_kernel<uint16_t> : ln_bwd_part_any_kernel<float>;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kLnThreads), 0, st, "layer_norm_bwd dx", a))) return rc;
   if ((rc = launch_pdl(part, dim3(tiles, a.G), dim3(kLnThreads), 0, st, "layer_norm_bwd partial sums", a))) return rc;
-  return launch_pdl(ln_bwd_reduce_kernel, dim3(tiles, dbeta ? 2 : 1), dim3(kLnThreads), 0, st,
-                    "layer_norm_bwd weight gradients", static_cast<const float*>(a.part), a.G, (int)H, dgamma, dbeta,
-                    accumulate);
+  return weights();
 }
