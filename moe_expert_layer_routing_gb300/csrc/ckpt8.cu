@@ -70,7 +70,46 @@ __device__ __forceinline__ float glu_act(float g, int glu) {
   return __fdividef(g, 1.f + __expf(-g));
 }
 
-__global__ void __launch_bounds__(kGluThreads) glu_fwd_kernel(const GluArgs p) {
+// Per half, max |x| over 32 words of two bf16 values each; a NaN or an infinity gives an exponent field of 255.
+__device__ __forceinline__ uint32_t absmax32_nan(const uint32_t (&w)[32]) {
+  uint32_t t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(t[i]) : "r"(w[i]), "r"(w[i + 16]));
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(t[i]) : "r"(t[i]), "r"(t[i + n]));
+  return t[0] & 0x7FFF7FFFu;
+}
+
+// Codes of the low (half 0) or high values of 32 words.  Adding 1.5 * 2^23 rounds to an integer (ties to even) in
+// the low mantissa bits, two's complement in the low byte.
+template <bool CLAMP>
+__device__ __forceinline__ void codes32(const uint32_t (&v)[32], int half, uint64_t inv, uint32_t (&w)[8]) {
+  const uint64_t magic = f2_splat(12582912.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t x0 = v[4 * k + i], x1 = v[4 * k + i + 1];
+      uint64_t f = f2_mul(f2_pack(__uint_as_float(half ? x0 & 0xffff0000u : x0 << 16),
+                                  __uint_as_float(half ? x1 & 0xffff0000u : x1 << 16)), inv);
+      if constexpr (CLAMP) {
+        float a, c;
+        f2_unpack(f, a, c);
+        f = f2_pack(fminf(fmaxf(a, -127.f), 127.f), fminf(fmaxf(c, -127.f), 127.f));
+      }
+      float a, c;
+      f2_unpack(f2_add(f, magic), a, c);
+      b[i] = __float_as_uint(a);
+      b[i + 1] = __float_as_uint(c);
+    }
+    w[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  }
+}
+
+__global__ void __launch_bounds__(kGluThreads, 3) glu_fwd_kernel(const GluArgs p) {
   __shared__ __align__(16) uint32_t tile[kGluRows][kGluFeat];  // words: 32 gate pairs | 32 up pairs, or 64 (gate, up)
   pdl_wait();
   pdl_trigger();
@@ -130,42 +169,32 @@ __global__ void __launch_bounds__(kGluThreads) glu_fwd_kernel(const GluArgs p) {
   uint32_t v[32];
 #pragma unroll
   for (int k = 0; k < 32; ++k) v[k] = tile[32 * gr + k][wc];
-  const uint32_t am = bf16x2_absmax32(v);  // a NaN drops out of the maximum
-  bool bad0 = false, bad1 = false;
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    bad0 |= (v[k] & 0x7f80u) == 0x7f80u;
-    bad1 |= (v[k] & 0x7f800000u) == 0x7f800000u;
-  }
+  const uint32_t am = absmax32_nan(v);
   const int64_t blk = t / p.tiles_per_block;
   const int tb = (int)(t - blk * p.tiles_per_block);
+  uint32_t bytes = 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int exponent = (half ? am >> 23 : am >> 7) & 0xff;
-    const bool bad = half ? bad1 : bad0;
-    const int byte = bad ? 255 : max(1, exponent - 6);
+    const int byte = exponent == 255 ? 255 : max(1, exponent - 6);
+    bytes |= (uint32_t)byte << (8 * half);
     // 2^(127 - byte); byte <= 248 for finite values
-    const float inv = __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);
+    const uint64_t inv = f2_splat(__uint_as_float((uint32_t)(254 - min(byte, 253)) << 23));
     uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = v[4 * k + i];
-        const float f = __uint_as_float(half ? x & 0xffff0000u : x << 16) * inv;
-        // + 1.5 * 2^23 rounds to an integer in the low mantissa bits (two's complement in the low byte)
-        b[i] = __float_as_uint(fminf(fmaxf(f, -127.f), 127.f) + 12582912.f);
-      }
-      w[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    }
+    // a bf16 of 8 significant bits times 2^(127 - byte) is at most 127.5 in magnitude, and only that rounds to 128
+    if (((half ? am >> 16 : am) & 0x7f) != 0x7f)
+      codes32<false>(v, half, inv, w);
+    else
+      codes32<true>(v, half, inv, w);
     const int f = p.interleaved ? f0 + wc : f0 + 2 * (wc & 31) + half;  // feature
     const int up = p.interleaved ? half : wc >> 5;
     int8_t* dst = p.q + ((blk * 2 + up) * (int64_t)p.I + f) * p.B + tb * kGluRows + 32 * gr;
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    p.sf[sf_offset(blk * 2 + up, p.tiles_per_block, tb, p.I, f, gr)] = (uint8_t)byte;
+    st_global_32b_or_halves(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+    if (p.interleaved) p.sf[sf_offset(blk * 2 + up, p.tiles_per_block, tb, p.I, f, gr)] = (uint8_t)byte;
   }
+  if (!p.interleaved)  // two features side by side
+    *reinterpret_cast<uint16_t*>(p.sf + sf_offset(blk * 2 + (wc >> 5), p.tiles_per_block, tb, p.I, f0 + 2 * (wc & 31), gr)) =
+        (uint16_t)bytes;
 }
 
 struct UnpackArgs {
@@ -177,10 +206,14 @@ struct UnpackArgs {
   int I, B, E, interleaved, tiles_per_block;
 };
 
-// The checkpoint's values as rows [rows, 2I] in the grouped order.
+// The checkpoint's values as rows [rows, 2I] in the grouped order.  The tile's 128 columns (64 gate | 64 up, or 64
+// pairs) lie in shared memory as 128-byte rows of codes whose 16-byte pieces are swizzled by the column quad, so
+// that a warp's four word loads (8 column quads x 4 slot quads) meet no bank twice; a thread turns 4 columns x 4
+// slots and writes 8 bytes of each of four rows.
 __global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackArgs p) {
-  __shared__ __align__(16) int8_t code[2 * kGluFeat][kGluRows + 16];
-  __shared__ __align__(16) uint8_t scale[2 * kGluFeat][4];
+  constexpr int COLS = 2 * kGluFeat;
+  __shared__ __align__(16) uint32_t code[COLS][kGluRows / 4];
+  __shared__ __align__(16) float scale[4][COLS];
   pdl_wait();
   pdl_trigger();
   const int chunks = p.I / kGluFeat;
@@ -192,35 +225,45 @@ __global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackA
   if (n == 0) return;
   const int64_t blk = t / p.tiles_per_block;
   const int tb = (int)(t - blk * p.tiles_per_block);
-  for (int i = threadIdx.x; i < 2 * kGluFeat * 8; i += kGluThreads) {
-    const int f = i >> 3, c = i & 7;  // f < 64: gate, else up
-    const int8_t* src = p.q + ((blk * 2 + f / kGluFeat) * (int64_t)p.I + f0 + f % kGluFeat) * p.B + tb * kGluRows + c * 16;
-    cp_async_16(smem_u32(&code[f][c * 16]), src);
+  // column c of the tile: feature and half
+  auto feature = [&](int c) { return f0 + (p.interleaved ? c >> 1 : c & (kGluFeat - 1)); };
+  auto half = [&](int c) { return blk * 2 + (p.interleaved ? c & 1 : c / kGluFeat); };
+  for (int i = threadIdx.x; i < COLS * 8; i += kGluThreads) {
+    const int c = i >> 3, piece = i & 7;
+    cp_async_16(smem_u32(&code[c][(piece ^ ((c >> 2) & 7)) * 4]),
+                p.q + (half(c) * (int64_t)p.I + feature(c)) * p.B + tb * kGluRows + piece * 16);
   }
   cp_async_commit();
-  for (int i = threadIdx.x; i < 2 * kGluFeat * 4; i += kGluThreads) {
-    const int f = i & (2 * kGluFeat - 1), g = i / (2 * kGluFeat);
-    scale[f][g] = p.sf[sf_offset(blk * 2 + f / kGluFeat, p.tiles_per_block, tb, p.I, f0 + f % kGluFeat, g)];
+  for (int i = threadIdx.x; i < COLS * 4; i += kGluThreads) {
+    const int c = i & (COLS - 1), g = i / COLS;
+    const uint32_t byte = p.sf[sf_offset(half(c), p.tiles_per_block, tb, p.I, feature(c), g)];
+    scale[g][c] = __uint_as_float(byte == 255 ? 0x7fc00000u : byte << 23);
   }
   cp_async_wait<0>();
   __syncthreads();
-  for (int i = threadIdx.x; i < n * 16; i += kGluThreads) {
-    const int r = i >> 4, c = i & 15;  // eight consecutive columns of the row
-    uint32_t o[4];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float x[2];
+  for (int k = 0; k < 4; ++k) {
+    // warp w: column quads 8 (w & 3) .. + 7, slot quads 16 (w >> 2) + 4 k .. + 3
+    const int cq = 8 * (w & 3) + (lane & 7), sq = 16 * (w >> 2) + 4 * k + (lane >> 3);
+    if (4 * sq >= n) continue;
+    const int c = 4 * cq;
+    const float4 sc4 = *reinterpret_cast<const float4*>(&scale[sq >> 3][c]);
+    const float sc[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+    float x[4][4];  // [column][slot]
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = c * 8 + 2 * k + j;
-        const int f = p.interleaved ? (col >> 1) + (col & 1) * kGluFeat : col;
-        x[j] = (float)code[f][r] * __uint_as_float((uint32_t)scale[f][r >> 5] << 23);  // byte 255: inf or NaN
-        if (scale[f][r >> 5] == 255) x[j] = __uint_as_float(0x7fc00000u);
-      }
-      o[k] = pack_bf16x2(x[0], x[1]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t v = code[c + j][((sq >> 2) ^ (cq & 7)) * 4 + (sq & 3)] ^ 0x80808080u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // 2^23 + 128 + code
+        x[j][i] = (__uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650 + i)) - 8388736.f) * sc[j];
     }
-    const int col = p.interleaved ? 2 * f0 + c * 8 : c < 8 ? f0 + c * 8 : p.I + f0 + (c - 8) * 8;
-    *reinterpret_cast<uint4*>(p.h + (r0 + r) * p.ldh + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int col = p.interleaved ? 2 * f0 + c : c < kGluFeat ? f0 + c : p.I + f0 + c - kGluFeat;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * sq + i < n)
+        *reinterpret_cast<uint2*>(p.h + (r0 + 4 * sq + i) * p.ldh + col) =
+            make_uint2(pack_bf16x2(x[0][i], x[1][i]), pack_bf16x2(x[2][i], x[3][i]));
   }
 }
 
