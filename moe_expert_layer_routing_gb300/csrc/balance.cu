@@ -79,6 +79,16 @@ __device__ __forceinline__ bool find_piece(const BalanceArgs& a, int p, int& seg
   return lo < hi;
 }
 
+// The status word, from the first block: the offsets have to lie in [0, T] and not decrease.
+__device__ __forceinline__ void check_offsets(const BalanceArgs& a) {
+  if (!a.status || blockIdx.x) return;
+  int bad = 0;
+  for (int i = threadIdx.x; a.off && i <= a.S; i += kBalThreads)
+    bad |= a.off[i] < 0 || a.off[i] > a.T || (i && a.off[i] < a.off[i - 1]);
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *a.status = bad ? MOE_STATUS_BAD_SEGMENTS : 0;
+}
+
 template <int LANES>
 __device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
@@ -119,10 +129,107 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
   return x != x ? 0xffffffffu : k;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+
+// The K selected logits of a token, slot k held by lane k % LANES (as col[k / LANES]; K <= 64 at 32 lanes), by exact
+// keys: K rounds of the largest key left, its lowest column, and that one taken out.
+template <int NV, int LANES, bool VEC, int SLOTS>
+__device__ __noinline__ void topk_exact(const float* row, int E, int K, int sl, bool live, int (&col)[SLOTS]) {
+  constexpr int N = 4 * NV;
+  uint32_t key[N];
+  {
+    float v[N];
+    load_row<NV, LANES, VEC>(row, E, sl, live, v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) key[j] = 4 * (LANES * (j >> 2) + sl) + (j & 3) < E ? order_key(v[j]) : 0u;
+  }
+  for (int r = 0; r < K; ++r) {
+    uint32_t g = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) g = max(g, key[j]);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+    int c = 1 << 30;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j) c = key[j] == g ? 4 * (LANES * (j >> 2) + sl) + (j & 3) : c;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) c = min(c, __shfl_xor_sync(0xffffffffu, c, o));
+#pragma unroll
+    for (int j = 0; j < N; ++j) key[j] = c == 4 * (LANES * (j >> 2) + sl) + (j & 3) ? 0u : key[j];
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (r == s * LANES + sl) col[s] = c;
+  }
 }
-constexpr uint32_t kKeyNegInf = 0x007fffffu;
+
+// The same with unique 31-bit keys: a value's leading bits, then its column counted backwards (CB bits), so that a
+// round is one maximum and no search, and "smaller than the last" is a subtraction: key - m as unsigned is 2^31 or
+// more exactly for the keys below m.  `odd` marks rows that need exact keys all the same: NaN or +inf (given by the
+// caller), or values that differ in the dropped bits alone and came out of order, or might have at the end.
+template <int NV, int LANES, int SLOTS>
+__device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], const float* row, int E, int K, int sl, bool live,
+                                            int (&col)[SLOTS]) {
+  constexpr int N = 4 * NV;
+  constexpr int CAP = N * LANES;  // columns
+  constexpr uint32_t CM = CAP - 1;
+  static_assert((CAP & (CAP - 1)) == 0, "column bits");
+  uint32_t key[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
+    const int b = __float_as_int(v[j] + 0.f);
+    const uint32_t k = ((uint32_t)(b ^ (b >> 31 | (int)0x80000000)) >> 1 & ~CM) | (CM - (uint32_t)c);
+    key[j] = c < E ? k : 0u;
+  }
+  uint32_t m = 0x80000000u, mk[SLOTS] = {}, next[SLOTS] = {};
+  const int rounds = min(K + 1, E);
+  for (int r = 0; r < rounds; ++r) {
+    uint32_t d = 0;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) d = __vimax3_u32(d, key[j] - m, key[j + 1] - m);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) d = max(d, __shfl_xor_sync(0xffffffffu, d, o));
+    m += d;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      if (r == s * LANES + sl) mk[s] = m;
+      if (r == s * LANES + sl + 1) next[s] = m;
+    }
+  }
+  // exact keys of the slot and of the one behind it, from the logits re-read (cache hits)
+  bool odd = false;
+  uint32_t exact[SLOTS];
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int k = s * LANES + sl;
+    col[s] = (int)(CM - (mk[s] & CM));
+    exact[s] = 0;
+    if (live && k < K) {
+      exact[s] = order_key(row[col[s]]);
+      if (k + 1 < rounds && (mk[s] ^ next[s]) <= CM)  // the same leading bits
+        odd |= exact[s] < order_key(row[CM - (next[s] & CM)]);
+    }
+  }
+  // at the end: a value left out may be larger in the dropped bits than the last one taken
+  if (rounds > K) {
+    const int kl = K - 1;
+    uint32_t last = 0, ek = 0;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (kl / LANES == s) {
+        last = mk[s];
+        ek = exact[s];
+      }
+    last = __shfl_sync(0xffffffffu, last, kl % LANES, LANES);
+    ek = __shfl_sync(0xffffffffu, ek, kl % LANES, LANES);
+    const bool tie = live && (last ^ m) <= CM;
+    if (__any_sync(0xffffffffu, tie)) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        odd |= tie && key[j] < last && (key[j] ^ last) <= CM && order_key(v[j]) > ek;
+    }
+  }
+  return odd;
+}
 
 // TOPK: selects and writes scores and ids (else reads ids).  One token per LANES lanes.
 template <int NV, int LANES, bool VEC, bool TOPK>
@@ -136,10 +243,7 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
   pdl_trigger();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, seg = lane / LANES, sl = lane % LANES;
   const bool stats = a.part_p != nullptr;
-  if (stats && a.off && a.status && blockIdx.x == 0)  // offsets have to lie in [0, T] and not decrease
-    for (int i = threadIdx.x; i <= a.S; i += kBalThreads)
-      if (a.off[i] < 0 || a.off[i] > a.T || (i && a.off[i] < a.off[i - 1]))
-        atomicOr(a.status, MOE_STATUS_BAD_SEGMENTS);
+  check_offsets(a);
   if (stats && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   int which, lo, hi;
   if (!find_piece(a, blockIdx.x, which, lo, hi)) return;
@@ -168,14 +272,10 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
     for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
     m = lane_max<LANES>(m);
     const float base = m > -INFINITY ? m : 0.f;
-    uint32_t key[N];
-    if constexpr (TOPK) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
-        key[j] = c < a.E ? order_key(v[j]) : 0u;
-      }
-    }
+    const float* row = a.logits + (int64_t)t * a.ld;
+    int col[SLOTS];
+    bool odd = false;
+    if constexpr (TOPK) odd = topk_packed<NV, LANES, SLOTS>(v, row, a.E, a.K, sl, live, col);
     float total = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -192,37 +292,22 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
       if (total != 0.f) z = fmaf(lse, lse, z);
     }
     if constexpr (TOPK) {
-      // K rounds: the largest key left, its lowest column, and that one taken out
-      uint32_t mk[SLOTS] = {};
-      int mi[SLOTS];
+      odd |= total != total;  // NaN or +inf among the logits
+      if (__any_sync(0xffffffffu, odd)) {
+        int ex[SLOTS];
+        topk_exact<NV, LANES, VEC, SLOTS>(row, a.E, a.K, sl, live, ex);
+        const unsigned mine = (LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u)) << (LANES * seg);
+        if (__ballot_sync(0xffffffffu, odd) & mine) {
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s) mi[s] = -1;
-      for (int r = 0; r < a.K; ++r) {
-        uint32_t g = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) g = max(g, key[j]);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-        int c = 1 << 30;
-#pragma unroll
-        for (int j = N - 1; j >= 0; --j) c = key[j] == g ? 4 * (LANES * (j >> 2) + sl) + (j & 3) : c;
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) c = min(c, __shfl_xor_sync(0xffffffffu, c, o));
-#pragma unroll
-        for (int j = 0; j < N; ++j) key[j] = c == 4 * (LANES * (j >> 2) + sl) + (j & 3) ? 0u : key[j];
-        if (r % LANES == sl) {
-#pragma unroll
-          for (int s = 0; s < SLOTS; ++s)
-            if (r / LANES == s) {
-              mk[s] = g;
-              mi[s] = g > kKeyNegInf ? c : -1;  // -inf: a masked expert takes no slot
-            }
+          for (int s = 0; s < SLOTS; ++s) col[s] = ex[s];
         }
       }
-      float e[SLOTS], sum = 0.f;
+      float x[SLOTS], e[SLOTS], sum = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
-        e[s] = mi[s] >= 0 ? __expf(key_value(mk[s]) - base) : 0.f;
+        x[s] = live && s * LANES + sl < a.K ? row[col[s]] : -INFINITY;
+        if (x[s] == -INFINITY) col[s] = -1;  // a masked expert takes no slot
+        e[s] = __expf(x[s] - base);
         sum += e[s];
       }
       sum = lane_sum<LANES>(sum);
@@ -231,13 +316,13 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
         const int k = s * LANES + sl;
         if (live && k < a.K) {
           float sc = 0.f;
-          if (mi[s] >= 0)
-            sc = a.mode == MOE_ROUTER_TOPK ? key_value(mk[s])
+          if (col[s] >= 0)
+            sc = a.mode == MOE_ROUTER_TOPK ? x[s]
                  : a.mode == MOE_ROUTER_TOPK_OVER_SOFTMAX && !a.renorm ? e[s] * inv
                                                                        : e[s] / sum;
           a.scores[(int64_t)t * a.K + k] = sc;
-          a.ids[(int64_t)t * a.K + k] = mi[s];
-          if (stats && mi[s] >= 0) atomicAdd(&hist[mi[s]], 1);  // integers: any order gives the same counts
+          a.ids[(int64_t)t * a.K + k] = col[s];
+          if (stats && col[s] >= 0) atomicAdd(&hist[col[s]], 1);  // integers: any order gives the same counts
         }
       }
     } else {
@@ -362,10 +447,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
   pdl_wait();
   pdl_trigger();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, seg = lane / LANES, sl = lane % LANES;
-  if (a.off && a.status && blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.S; i += kBalThreads)
-      if (a.off[i] < 0 || a.off[i] > a.T || (i && a.off[i] < a.off[i - 1]))
-        atomicOr(a.status, MOE_STATUS_BAD_SEGMENTS);
+  check_offsets(a);
   int which, lo, hi;
   if (!find_piece(a, blockIdx.x, which, lo, hi)) return;
   const bool pad = which == 0 || which == a.S + 1;
@@ -418,8 +500,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
   }
 }
 
-// Lanes per token: 8 for up to 256 experts and K <= 8, 16 for up to 512 and K <= 16, else a warp.
-static int bal_lanes(int K, int E) { return E <= 256 && K <= 8 ? 8 : E <= 512 && K <= 16 ? 16 : 32; }
+// Lanes per token: 8 for up to 128 experts and K <= 8, 16 for up to 256 and K <= 16, else a warp (16 logits a lane;
+// 32 above 512 experts).
+static int bal_lanes(int K, int E) { return E <= 128 && K <= 8 ? 8 : E <= 256 && K <= 16 ? 16 : 32; }
+// The gradient keeps no keys and no slots: up to 32 logits a lane (131072 x 256 experts: 69 us, 76 us at 16 a lane).
+static int bal_bwd_lanes(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : 32; }
 
 // Tokens per chunk: one pass of a CTA's warps, more where that would be over four CTAs per SM.
 static int bal_chunk(int T, int lanes) {
@@ -427,6 +512,8 @@ static int bal_chunk(int T, int lanes) {
   const int64_t steps = ((int64_t)T + step - 1) / step, most = 4 * 152;
   return (int)((steps + most - 1) / most) * step;
 }
+
+static int bal_pieces(int T, int C, int S) { return (int)(((int64_t)T + C - 1) / C) + S + 1; }
 
 struct BalLayout {
   size_t c, p, z, l, ticket, total;
@@ -436,7 +523,7 @@ struct BalLayout {
 static BalLayout bal_layout(int T, int K, int E, int S) {
   BalLayout L{};
   L.C = bal_chunk(T, bal_lanes(K, E));
-  L.pieces = (int)(((int64_t)T + L.C - 1) / L.C) + S + 1;
+  L.pieces = bal_pieces(T, L.C, S);
   size_t off = 0;
   auto take = [&](size_t n) {
     const size_t at = off;
@@ -530,7 +617,7 @@ static int router_entry(const char* who, bool topk, int mode, int renorm, const 
     return fail(MOE_ERR_INVALID, "%s: counts, prob_sum and loss come together", who);
   const bool stats = given == 3;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (status_dev && (rc = cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status"))) return rc;
+  if (T == 0 && status_dev && (rc = cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status"))) return rc;
   if (T == 0) return stats ? balance_empty(E, num_seq, counts, prob_sum, loss, st) : MOE_OK;
   if (!logits || !ids || (topk && !scores)) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
   if (ld_logits < E) return fail(MOE_ERR_INVALID, "%s: row stride below E", who);
@@ -590,11 +677,10 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   if (rc) return rc;
   if (!seg_offsets && num_seq != 1) return fail(MOE_ERR_INVALID, "moe_balance_bwd: several sequences need seg_offsets");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (status_dev && (rc = cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status"))) return rc;
-  if (T == 0) return MOE_OK;
+  if (T == 0) return status_dev ? cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status") : MOE_OK;
   if (!logits || !lse || !counts || !dlogits) return fail(MOE_ERR_INVALID, "moe_balance_bwd: null pointer");
   if (ld_logits < E || (add && ld_add < E)) return fail(MOE_ERR_INVALID, "moe_balance_bwd: row stride below E");
-  const BalLayout L = bal_layout(T, K, E, num_seq);
+  const int lanes = bal_bwd_lanes(E), nv = (E + 4 * lanes - 1) / (4 * lanes);
   BalanceArgs a{};
   a.logits = logits;
   a.ld = ld_logits;
@@ -603,8 +689,8 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   a.E = E;
   a.off = seg_offsets;
   a.S = num_seq;
-  a.C = L.C;
-  a.pieces = L.pieces;
+  a.C = bal_chunk(T, lanes);
+  a.pieces = bal_pieces(T, a.C, num_seq);
   a.alpha = alpha;
   a.beta = beta;
   a.lse = const_cast<float*>(lse);
@@ -614,7 +700,6 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   a.ld_add = ld_add;
   a.dlogits = dlogits;
   a.status = status_dev;
-  const int lanes = bal_lanes(K, E), nv = (E + 4 * lanes - 1) / (4 * lanes);
   const bool vec = E % 4 == 0 && ld_logits % 4 == 0 && (!add || ld_add % 4 == 0) &&
                    ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(add) |
                      reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
