@@ -426,25 +426,16 @@ def _dense(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
-class _on:
-    """The stream a call runs on.  What the call allocates belongs to that stream, so that nothing else is
-    given its memory while the call may still use it; tensors made on another stream are the caller's to order
-    (Stream.wait_stream) and to keep."""
-
-    def __init__(self, stream, dev):
-        if dev.type != "cuda":
-            raise MoeError("tensors must be CUDA tensors (there is no CPU path)")
-        if dev.index != torch.cuda.current_device():
-            raise MoeError(f"tensors are on {dev}, which is not the current device")
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc) if self.ctx is not None else False
+def _here(dev):
+    """Handle of the current stream of the tensors' device, which has to be the current one.  What a call allocates
+    belongs to that stream, so that nothing else is given its memory while the call may still use it; with a
+    `stream` argument a call therefore runs with that stream made current.  Tensors made on another stream are
+    the caller's to order (Stream.wait_stream) and to keep."""
+    if dev.type != "cuda":
+        raise MoeError("tensors must be CUDA tensors (there is no CPU path)")
+    if dev.index != torch._C._cuda_getDevice():
+        raise MoeError(f"tensors are on {dev}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 _DT = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
@@ -462,19 +453,22 @@ def layer_norm_fwd(x, gamma, beta=None, eps: float = 1e-5, residual=None, kind: 
     """layer_norm_fwd on rows x [T, H] (bf16 or fp32, dense rows of any stride), plus `residual` when given.
     Returns y, mean (NORM_LAYER, else None), rstd, and sum = x + residual (None without a residual), the
     rows that layer_norm_bwd takes as its x.  gamma, beta [H] in bf16 or fp32."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_fwd(x, gamma, beta, eps, residual, kind)
     T, H, dev = _norm_types(x, gamma, "layer_norm_fwd")
     ldx = _rows(x, x.dtype, (T, H), "x", dev)
     ldr = 0 if residual is None else _rows(residual, x.dtype, (T, H), "residual", dev)
     g, b = _dense(gamma, gamma.dtype, (H,), "gamma", dev), _dense(beta, gamma.dtype, (H,), "beta", dev)
-    with _on(stream, dev) as st:
-        y = torch.empty(T, H, dtype=x.dtype, device=dev)
-        total = None if residual is None else torch.empty(T, H, dtype=x.dtype, device=dev)
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-        mean = torch.empty(T, dtype=torch.float32, device=dev) if kind == NORM_LAYER else None
-        rc = lib().layer_norm_fwd(kind, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, g, b,
-                                  _DT[x.dtype], _DT[gamma.dtype], T, H, eps, y.data_ptr(),
-                                  None if total is None else total.data_ptr(),
-                                  None if mean is None else mean.data_ptr(), rstd.data_ptr(), st)
+    st = _here(dev)
+    y = torch.empty(T, H, dtype=x.dtype, device=dev)
+    total = None if residual is None else torch.empty(T, H, dtype=x.dtype, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    mean = torch.empty(T, dtype=torch.float32, device=dev) if kind == NORM_LAYER else None
+    rc = lib().layer_norm_fwd(kind, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, g, b,
+                              _DT[x.dtype], _DT[gamma.dtype], T, H, eps, y.data_ptr(),
+                              None if total is None else total.data_ptr(),
+                              None if mean is None else mean.data_ptr(), rstd.data_ptr(), st)
     _check(rc, "layer_norm_fwd")
     return dict(y=y, mean=mean, rstd=rstd, sum=total)
 
@@ -484,25 +478,28 @@ def layer_norm_bwd(dy, x, gamma, mean, rstd, dres=None, kind: int = NORM_LAYER, 
     """layer_norm_bwd: dx (plus `dres`, the gradient that reaches the rows past the norm), dgamma and, with a
     mean and unless dbeta is False, dbeta, in fp32.  x are the normalised rows (with a residual: the forward's
     sum).  accumulate_into: an earlier result whose dgamma and dbeta are added to in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_bwd(dy, x, gamma, mean, rstd, dres, kind, dbeta, accumulate_into)
     T, H, dev = _norm_types(x, gamma, "layer_norm_bwd")
     ldx, lddy = _rows(x, x.dtype, (T, H), "x", dev), _rows(dy, x.dtype, (T, H), "dy", dev)
     ldres = 0 if dres is None else _rows(dres, x.dtype, (T, H), "dres", dev)
     g, r = _dense(gamma, gamma.dtype, (H,), "gamma", dev), _dense(rstd, torch.float32, (T,), "rstd", dev)
     m = _dense(mean, torch.float32, (T,), "mean", dev) if kind == NORM_LAYER else None
-    with _on(stream, dev) as st:
-        dx = torch.empty(T, H, dtype=x.dtype, device=dev)
-        if accumulate_into is not None:
-            dg, db = accumulate_into["dgamma"], accumulate_into["dbeta"]
-            _dense(dg, torch.float32, (H,), "dgamma", dev)
-            _dense(db, torch.float32, (H,), "dbeta", dev)
-        else:
-            dg = torch.empty(H, dtype=torch.float32, device=dev)
-            db = torch.empty(H, dtype=torch.float32, device=dev) if dbeta and kind == NORM_LAYER else None
-        ws = _ws(lib().layer_norm_bwd_workspace_size(T, H), dev)
-        rc = lib().layer_norm_bwd(kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, g, m, r,
-                                  None if dres is None else dres.data_ptr(), ldres, _DT[x.dtype], _DT[gamma.dtype], T, H,
-                                  dx.data_ptr(), dg.data_ptr(), None if db is None else db.data_ptr(),
-                                  int(accumulate_into is not None), ws.data_ptr(), ws.numel(), st)
+    st = _here(dev)
+    dx = torch.empty(T, H, dtype=x.dtype, device=dev)
+    if accumulate_into is not None:
+        dg, db = accumulate_into["dgamma"], accumulate_into["dbeta"]
+        _dense(dg, torch.float32, (H,), "dgamma", dev)
+        _dense(db, torch.float32, (H,), "dbeta", dev)
+    else:
+        dg = torch.empty(H, dtype=torch.float32, device=dev)
+        db = torch.empty(H, dtype=torch.float32, device=dev) if dbeta and kind == NORM_LAYER else None
+    ws = _ws(lib().layer_norm_bwd_workspace_size(T, H), dev)
+    rc = lib().layer_norm_bwd(kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, g, m, r,
+                              None if dres is None else dres.data_ptr(), ldres, _DT[x.dtype], _DT[gamma.dtype], T, H,
+                              dx.data_ptr(), dg.data_ptr(), None if db is None else db.data_ptr(),
+                              int(accumulate_into is not None), ws.data_ptr(), ws.numel(), st)
     _check(rc, "layer_norm_bwd")
     return dict(dx=dx, dgamma=dg, dbeta=db)
 
@@ -526,25 +523,28 @@ def router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False, se
                beta: float = 0.0, balance: bool = True, stream=None) -> dict:
     """moe_router_fwd: top-K of fp32 logits [T, E] (dense rows of any stride).  Returns scores [T, K], ids [T, K],
     lse [T] and, unless balance is False, counts and prob_sum [num_seq, E], loss [2] = (balance, z) and status."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return router_fwd(mode, logits, K, renorm, seg_offsets, alpha, beta, balance)
     if logits.dim() != 2:
         raise MoeError("logits must be [T, E]")
     T, E = logits.shape
     dev = logits.device
     ld = _rows(logits, torch.float32, (T, E), "logits", dev)
     off, S = _segments(seg_offsets, dev)
-    with _on(stream, dev) as st:
-        scores = torch.empty(T, K, dtype=torch.float32, device=dev)
-        ids = torch.empty(T, K, dtype=torch.int32, device=dev)
-        out = dict(scores=scores, ids=ids, lse=torch.empty(T, dtype=torch.float32, device=dev))
-        p = [None] * 4
-        ws = None
-        if balance:
-            counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
-            out.update(counts=counts, prob_sum=prob, loss=loss, status=status)
-            p = [counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr()]
-        rc = lib().moe_router_fwd(mode, int(renorm), logits.data_ptr(), ld, T, K, E, off, S, alpha, beta,
-                                  scores.data_ptr(), ids.data_ptr(), out["lse"].data_ptr(), *p,
-                                  None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st)
+    st = _here(dev)
+    scores = torch.empty(T, K, dtype=torch.float32, device=dev)
+    ids = torch.empty(T, K, dtype=torch.int32, device=dev)
+    out = dict(scores=scores, ids=ids, lse=torch.empty(T, dtype=torch.float32, device=dev))
+    p = [None] * 4
+    ws = None
+    if balance:
+        counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
+        out.update(counts=counts, prob_sum=prob, loss=loss, status=status)
+        p = [counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr()]
+    rc = lib().moe_router_fwd(mode, int(renorm), logits.data_ptr(), ld, T, K, E, off, S, alpha, beta,
+                              scores.data_ptr(), ids.data_ptr(), out["lse"].data_ptr(), *p,
+                              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st)
     _check(rc, "moe_router_fwd")
     return out
 
@@ -553,18 +553,21 @@ def balance_fwd(logits: torch.Tensor, ids: torch.Tensor, seg_offsets=None, alpha
                 stream=None) -> dict:
     """moe_balance_fwd: the losses of router_fwd for ids [T, K] selected elsewhere.  Returns lse, counts, prob_sum,
     loss and status."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return balance_fwd(logits, ids, seg_offsets, alpha, beta)
     if logits.dim() != 2 or ids.dim() != 2:
         raise MoeError("logits must be [T, E] and ids [T, K]")
     (T, E), K, dev = logits.shape, ids.shape[1], logits.device
     ld = _rows(logits, torch.float32, (T, E), "logits", dev)
     idp = _dense(ids, torch.int32, (T, K), "ids", dev)
     off, S = _segments(seg_offsets, dev)
-    with _on(stream, dev) as st:
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-        counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
-        rc = lib().moe_balance_fwd(logits.data_ptr(), ld, idp, T, K, E, off, S, alpha, beta, lse.data_ptr(),
-                                   counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), st)
+    st = _here(dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
+    rc = lib().moe_balance_fwd(logits.data_ptr(), ld, idp, T, K, E, off, S, alpha, beta, lse.data_ptr(),
+                               counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr(),
+                               ws.data_ptr(), ws.numel(), st)
     _check(rc, "moe_balance_fwd")
     return dict(lse=lse, counts=counts, prob_sum=prob, loss=loss, status=status)
 
@@ -573,6 +576,9 @@ def balance_bwd(logits: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor, K
                 alpha: float = 0.0, beta: float = 0.0, dloss=None, add=None, stream=None) -> torch.Tensor:
     """moe_balance_bwd: gradient of dloss[0] * balance + dloss[1] * z by the logits [T, E], plus `add` (e.g.
     router_bwd's result).  lse and counts are the forward's."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return balance_bwd(logits, lse, counts, K, seg_offsets, alpha, beta, dloss, add)
     if logits.dim() != 2:
         raise MoeError("logits must be [T, E]")
     T, E = logits.shape
@@ -582,10 +588,10 @@ def balance_bwd(logits: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor, K
     off, S = _segments(seg_offsets, dev)
     lp, cp = _dense(lse, torch.float32, (T,), "lse", dev), _dense(counts, torch.int32, (S, E), "counts", dev)
     dl = _dense(dloss, torch.float32, (2,), "dloss", dev)
-    with _on(stream, dev) as st:
-        out = torch.empty(T, E, dtype=torch.float32, device=dev)
-        rc = lib().moe_balance_bwd(logits.data_ptr(), ld, lp, cp, T, K, E, off, S, alpha, beta, dl,
-                                   None if add is None else add.data_ptr(), ld_add, out.data_ptr(), None, st)
+    st = _here(dev)
+    out = torch.empty(T, E, dtype=torch.float32, device=dev)
+    rc = lib().moe_balance_bwd(logits.data_ptr(), ld, lp, cp, T, K, E, off, S, alpha, beta, dl,
+                               None if add is None else add.data_ptr(), ld_add, out.data_ptr(), None, st)
     _check(rc, "moe_balance_bwd")
     return out
 
@@ -607,6 +613,9 @@ def glu_fwd(h: torch.Tensor, route_meta: dict, block_size: int, glu: int = GLU_S
     """moe_glu_fwd on the grouped rows h bf16 [rows, 2I]: a = act(gate) * up [rows, I] (times the row's score
     with s [T, K], whose s_scatter_idx route_meta then holds) and, unless checkpoint is False, the 8-bit
     checkpoint ckpt_q [N, 2, I, B], ckpt_sf for moe_bwd.  route_meta: route_meta()'s dict."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return glu_fwd(h, route_meta, block_size, glu, gate_up_layout, s, checkpoint)
     if h.dim() != 2 or h.shape[1] % 2:
         raise MoeError("h must be [rows, 2I]")
     rows, I, dev = h.shape[0], h.shape[1] // 2, h.device
@@ -621,15 +630,15 @@ def glu_fwd(h: torch.Tensor, route_meta: dict, block_size: int, glu: int = GLU_S
         if idx.numel() < rows:
             raise MoeError("s_scatter_idx is shorter than the rows of h")
         sip = _dense(idx, torch.int32, tuple(idx.shape), "s_scatter_idx", dev)
-    with _on(stream, dev) as st:
-        a = torch.empty(rows, I, dtype=torch.bfloat16, device=dev)
-        q = sf = None
-        if checkpoint:
-            q = torch.empty(N, 2, I, block_size, dtype=torch.int8, device=dev)
-            sf = torch.empty(ckpt8_sf_shape(N, I, block_size), dtype=torch.uint8, device=dev)
-        rc = lib().moe_glu_fwd(h.data_ptr(), ldh, rows, I, E, block_size, N, glu, gate_up_layout, eo, bo, b2e, sp, sip,
-                               slots, a.data_ptr(), None if q is None else q.data_ptr(),
-                               None if sf is None else sf.data_ptr(), st)
+    st = _here(dev)
+    a = torch.empty(rows, I, dtype=torch.bfloat16, device=dev)
+    q = sf = None
+    if checkpoint:
+        q = torch.empty(N, 2, I, block_size, dtype=torch.int8, device=dev)
+        sf = torch.empty(ckpt8_sf_shape(N, I, block_size), dtype=torch.uint8, device=dev)
+    rc = lib().moe_glu_fwd(h.data_ptr(), ldh, rows, I, E, block_size, N, glu, gate_up_layout, eo, bo, b2e, sp, sip,
+                           slots, a.data_ptr(), None if q is None else q.data_ptr(),
+                           None if sf is None else sf.data_ptr(), st)
     _check(rc, "moe_glu_fwd")
     return dict(a=a, ckpt_q=q, ckpt_sf=sf)
 
@@ -638,6 +647,9 @@ def ckpt8_unpack(ckpt_q: torch.Tensor, ckpt_sf: torch.Tensor, route_meta: dict, 
                  gate_up_layout: int = GATE_UP_CONCAT, stream=None) -> torch.Tensor:
     """moe_ckpt8_unpack: the 8-bit checkpoint's values as grouped rows bf16 [rows, 2I] (rows that no expert has
     are left unwritten)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ckpt8_unpack(ckpt_q, ckpt_sf, route_meta, rows, gate_up_layout)
     if ckpt_q.dim() != 4:
         raise MoeError("ckpt_q must be [N, 2, I, B]")
     N, _, I, B = ckpt_q.shape
@@ -645,9 +657,9 @@ def ckpt8_unpack(ckpt_q: torch.Tensor, ckpt_sf: torch.Tensor, route_meta: dict, 
     eo, bo, b2e, E, Nb = _meta_ptrs(route_meta, dev)
     qp = _dense(ckpt_q, torch.int8, (Nb, 2, I, B), "ckpt_q", dev)
     sp = _dense(ckpt_sf, torch.uint8, ckpt8_sf_shape(N, I, B), "ckpt_sf", dev)
-    with _on(stream, dev) as st:
-        h = torch.empty(rows, 2 * I, dtype=torch.bfloat16, device=dev)
-        rc = lib().moe_ckpt8_unpack(qp, sp, rows, I, E, B, Nb, gate_up_layout, eo, bo, b2e, h.data_ptr(), 2 * I, st)
+    st = _here(dev)
+    h = torch.empty(rows, 2 * I, dtype=torch.bfloat16, device=dev)
+    rc = lib().moe_ckpt8_unpack(qp, sp, rows, I, E, B, Nb, gate_up_layout, eo, bo, b2e, h.data_ptr(), 2 * I, st)
     _check(rc, "moe_ckpt8_unpack")
     return h
 
