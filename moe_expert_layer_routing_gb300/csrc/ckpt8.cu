@@ -42,17 +42,18 @@ struct GluArgs {
   const int32_t *expert_offsets, *block_offsets, *block_to_expert;
   int64_t rows;       // rows of h; no row at or past it is touched
   int64_t slots;      // T*K: scores
-  int I, B, E, glu, interleaved, tiles_per_block;
+  int64_t items;      // 128-slot tiles x 64-feature chunks
+  int I, B, E, glu, interleaved, tpb_shift;  // B = 128 << tpb_shift
 };
 
 // Rows [r0, r0 + n) of the grouped order that lie in the 128 slots of tile `tile`; n <= 0: none.
 __device__ __forceinline__ void glu_tile_rows(const int32_t* eo, const int32_t* bo, const int32_t* b2e, int E, int B,
-                                              int tiles_per_block, int64_t rows, int64_t tile, int64_t& r0, int& n) {
-  const int64_t blk = tile / tiles_per_block;
+                                              int tpb_shift, int64_t rows, int tile, int64_t& r0, int& n) {
+  const int blk = tile >> tpb_shift;
   const int e = b2e[blk];
   n = 0;
   if (e < 0 || e >= E) return;
-  const int64_t j0 = (blk - bo[e]) * B + (tile - blk * tiles_per_block) * kGluRows;
+  const int64_t j0 = (int64_t)(blk - bo[e]) * B + (tile - (blk << tpb_shift)) * kGluRows;
   r0 = eo[e] + j0;
   const int64_t r1 = min((int64_t)eo[e + 1], rows);
   if (j0 < 0 || r0 < 0) return;
@@ -60,8 +61,8 @@ __device__ __forceinline__ void glu_tile_rows(const int32_t* eo, const int32_t* 
 }
 
 // Scale byte of feature f, 32-slot group g of 128-slot tile tb of half `bu` (2 block + gate|up).
-__device__ __forceinline__ int64_t sf_offset(int64_t bu, int tiles_per_block, int tb, int I, int f, int g) {
-  return (((bu * tiles_per_block + tb) * (I >> 5) + (f >> 5)) * 4 + g) * 32 + (f & 31);
+__device__ __forceinline__ int64_t sf_offset(int64_t bu, int tpb_shift, int tb, int I, int f, int g) {
+  return ((((bu << tpb_shift) + tb) * (I >> 5) + (f >> 5)) * 4 + g) * 32 + (f & 31);
 }
 
 // act(g) of the forward: SiLU(g) = g / (1 + e^-g), or GELU(g) = g Phi(g)
@@ -109,27 +110,8 @@ __device__ __forceinline__ void codes32(const uint32_t (&v)[32], int half, uint6
   }
 }
 
-__global__ void __launch_bounds__(kGluThreads, 3) glu_fwd_kernel(const GluArgs p) {
-  __shared__ __align__(16) uint32_t tile[kGluRows][kGluFeat];  // words: 32 gate pairs | 32 up pairs, or 64 (gate, up)
-  pdl_wait();
-  pdl_trigger();
-  const int chunks = p.I / kGluFeat;
-  const int64_t t = blockIdx.x / chunks;
-  const int f0 = (int)(blockIdx.x - t * chunks) * kGluFeat;
-  int64_t r0 = 0;
-  int n;
-  glu_tile_rows(p.expert_offsets, p.block_offsets, p.block_to_expert, p.E, p.B, p.tiles_per_block, p.rows, t, r0, n);
-  if (n == 0) return;
-  // 16 pieces of 16 bytes per row; rows past the expert's last are zeros
-  for (int i = threadIdx.x; i < kGluRows * 16; i += kGluThreads) {
-    const int r = i >> 4, c = i & 15;
-    const int col = p.interleaved ? 2 * f0 + c * 8 : c < 8 ? f0 + c * 8 : p.I + f0 + (c - 8) * 8;
-    const uint16_t* src = p.h + (r0 + (r < n ? r : 0)) * p.ldh + col;
-    cp_async_16_zfill(smem_u32(&tile[r][c * 4]), src, r < n ? 16 : 0);
-  }
-  cp_async_commit();
-  cp_async_wait<0>();
-  __syncthreads();
+__device__ __forceinline__ void glu_tile(const GluArgs& p, int t, int f0, int64_t r0, int n,
+                                         const uint32_t (*tile)[kGluFeat]) {
   // a: eight features of a row at a time
   for (int i = threadIdx.x; i < n * 8; i += kGluThreads) {
     const int r = i >> 3, c = i & 7;
@@ -170,8 +152,8 @@ __global__ void __launch_bounds__(kGluThreads, 3) glu_fwd_kernel(const GluArgs p
 #pragma unroll
   for (int k = 0; k < 32; ++k) v[k] = tile[32 * gr + k][wc];
   const uint32_t am = absmax32_nan(v);
-  const int64_t blk = t / p.tiles_per_block;
-  const int tb = (int)(t - blk * p.tiles_per_block);
+  const int64_t blk = t >> p.tpb_shift;
+  const int tb = t & ((1 << p.tpb_shift) - 1);
   uint32_t bytes = 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -190,11 +172,58 @@ __global__ void __launch_bounds__(kGluThreads, 3) glu_fwd_kernel(const GluArgs p
     const int up = p.interleaved ? half : wc >> 5;
     int8_t* dst = p.q + ((blk * 2 + up) * (int64_t)p.I + f) * p.B + tb * kGluRows + 32 * gr;
     st_global_32b_or_halves(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-    if (p.interleaved) p.sf[sf_offset(blk * 2 + up, p.tiles_per_block, tb, p.I, f, gr)] = (uint8_t)byte;
+    if (p.interleaved) p.sf[sf_offset(blk * 2 + up, p.tpb_shift, tb, p.I, f, gr)] = (uint8_t)byte;
   }
   if (!p.interleaved)  // two features side by side
-    *reinterpret_cast<uint16_t*>(p.sf + sf_offset(blk * 2 + (wc >> 5), p.tiles_per_block, tb, p.I, f0 + 2 * (wc & 31), gr)) =
+    *reinterpret_cast<uint16_t*>(p.sf + sf_offset(blk * 2 + (wc >> 5), p.tpb_shift, tb, p.I, f0 + 2 * (wc & 31), gr)) =
         (uint16_t)bytes;
+}
+
+constexpr int kGluBlocks = 3;  // resident blocks: two 32 KB tiles each
+
+// Persistent: block i takes items i, i + grid, ... (an item is 64 features of a 128-slot tile, features fastest);
+// the next item's rows are on their way while this one is computed.
+__global__ void __launch_bounds__(kGluThreads, kGluBlocks) glu_fwd_kernel(const GluArgs p) {
+  extern __shared__ __align__(16) uint32_t tiles[];  // two tiles [128][64] of words: 32 gate pairs | 32 up pairs, or 64 (gate, up)
+  pdl_wait();
+  const uint32_t chunks = p.I / kGluFeat;
+  struct Item {
+    int64_t r0;
+    int t, f0, n;
+  };
+  auto fetch = [&](int64_t item, uint32_t* tile) {
+    Item it{};
+    if (item < p.items) {
+      it.t = (int)((uint32_t)item / chunks);
+      it.f0 = (int)((uint32_t)item - it.t * chunks) * kGluFeat;
+      glu_tile_rows(p.expert_offsets, p.block_offsets, p.block_to_expert, p.E, p.B, p.tpb_shift, p.rows, it.t, it.r0,
+                    it.n);
+      if (it.n > 0) {
+        // 16 pieces of 16 bytes per row; rows past the expert's last are zeros
+        const int c = threadIdx.x & 15;
+        const int col = p.interleaved ? 2 * it.f0 + c * 8 : c < 8 ? it.f0 + c * 8 : p.I + it.f0 + (c - 8) * 8;
+        const uint16_t* src = p.h + it.r0 * p.ldh + col;
+#pragma unroll
+        for (int k = 0; k < kGluRows / 16; ++k) {
+          const int r = k * 16 + (threadIdx.x >> 4);
+          cp_async_16_zfill(smem_u32(tile + r * kGluFeat + c * 4), src + (r < it.n ? r : 0) * p.ldh, r < it.n ? 16 : 0);
+        }
+      }
+    }
+    cp_async_commit();
+    return it;
+  };
+  int buf = 0;
+  Item now = fetch(blockIdx.x, tiles);
+  for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x, buf ^= 1) {
+    const Item next = fetch(item + gridDim.x, tiles + (buf ^ 1) * (kGluRows * kGluFeat));
+    cp_async_wait<1>();
+    __syncthreads();
+    if (now.n > 0) glu_tile(p, now.t, now.f0, now.r0, now.n, reinterpret_cast<const uint32_t(*)[kGluFeat]>(tiles + buf * (kGluRows * kGluFeat)));
+    __syncthreads();  // the buffer is read; it is filled again next time round
+    now = next;
+  }
+  pdl_trigger();  // not earlier: the next kernel's blocks would take the place of this one's late ones
 }
 
 struct UnpackArgs {
@@ -203,7 +232,7 @@ struct UnpackArgs {
   uint16_t* h;
   int64_t ldh, rows;
   const int32_t *expert_offsets, *block_offsets, *block_to_expert;
-  int I, B, E, interleaved, tiles_per_block;
+  int I, B, E, interleaved, tpb_shift;  // B = 128 << tpb_shift
 };
 
 // The checkpoint's values as rows [rows, 2I] in the grouped order.  The tile's 128 columns (64 gate | 64 up, or 64
@@ -216,15 +245,15 @@ __global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackA
   __shared__ __align__(16) float scale[4][COLS];
   pdl_wait();
   pdl_trigger();
-  const int chunks = p.I / kGluFeat;
-  const int64_t t = blockIdx.x / chunks;
+  const uint32_t chunks = p.I / kGluFeat;
+  const int t = (int)(blockIdx.x / chunks);
   const int f0 = (int)(blockIdx.x - t * chunks) * kGluFeat;
   int64_t r0 = 0;
   int n;
-  glu_tile_rows(p.expert_offsets, p.block_offsets, p.block_to_expert, p.E, p.B, p.tiles_per_block, p.rows, t, r0, n);
+  glu_tile_rows(p.expert_offsets, p.block_offsets, p.block_to_expert, p.E, p.B, p.tpb_shift, p.rows, t, r0, n);
   if (n == 0) return;
-  const int64_t blk = t / p.tiles_per_block;
-  const int tb = (int)(t - blk * p.tiles_per_block);
+  const int64_t blk = t >> p.tpb_shift;
+  const int tb = t & ((1 << p.tpb_shift) - 1);
   // column c of the tile: feature and half
   auto feature = [&](int c) { return f0 + (p.interleaved ? c >> 1 : c & (kGluFeat - 1)); };
   auto half = [&](int c) { return blk * 2 + (p.interleaved ? c & 1 : c / kGluFeat); };
@@ -236,7 +265,7 @@ __global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackA
   cp_async_commit();
   for (int i = threadIdx.x; i < COLS * 4; i += kGluThreads) {
     const int c = i & (COLS - 1), g = i / COLS;
-    const uint32_t byte = p.sf[sf_offset(half(c), p.tiles_per_block, tb, p.I, feature(c), g)];
+    const uint32_t byte = p.sf[sf_offset(half(c), p.tpb_shift, tb, p.I, feature(c), g)];
     scale[g][c] = __uint_as_float(byte == 255 ? 0x7fc00000u : byte << 23);
   }
   cp_async_wait<0>();
@@ -266,6 +295,8 @@ __global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackA
             make_uint2(pack_bf16x2(x[0][i], x[1][i]), pack_bf16x2(x[2][i], x[3][i]));
   }
 }
+
+static int tile_shift(int block_size) { return block_size == 128 ? 0 : block_size == 256 ? 1 : block_size == 512 ? 2 : 3; }
 
 static int ckpt8_check(const char* who, int64_t rows, int I, int E, int block_size, int64_t num_blocks, int gate_up_layout) {
   if (rows < 0 || num_blocks < 0 || I <= 0 || E <= 0) return fail(MOE_ERR_INVALID, "%s: bad sizes", who);
@@ -320,10 +351,14 @@ extern "C" int moe_glu_fwd(const void* h, int64_t ldh, int64_t rows, int I, int 
   p.E = E;
   p.glu = glu;
   p.interleaved = gate_up_layout == MOE_GATE_UP_INTERLEAVED;
-  p.tiles_per_block = block_size / kGluRows;
-  const int64_t grid = num_blocks * p.tiles_per_block * (I / kGluFeat);
-  return launch_pdl(glu_fwd_kernel, dim3((unsigned)grid), dim3(kGluThreads), 0, reinterpret_cast<cudaStream_t>(stream),
-                    "glu_fwd", p);
+  p.tpb_shift = tile_shift(block_size);
+  p.items = (num_blocks << p.tpb_shift) * (I / kGluFeat);
+  constexpr size_t smem = 2 * sizeof(uint32_t) * kGluRows * kGluFeat;
+  if ((rc = cuda_check(cudaFuncSetAttribute(glu_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                       "cudaFuncSetAttribute(glu_fwd)")))
+    return rc;
+  return launch_pdl(glu_fwd_kernel, dim3((unsigned)std::min<int64_t>(p.items, kGluBlocks * device_sm_count())),
+                    dim3(kGluThreads), smem, reinterpret_cast<cudaStream_t>(stream), "glu_fwd", p);
 }
 
 extern "C" int moe_ckpt8_unpack(const int8_t* ckpt_q, const uint8_t* ckpt_sf, int64_t rows, int I, int E, int block_size,
@@ -340,8 +375,8 @@ extern "C" int moe_ckpt8_unpack(const int8_t* ckpt_q, const uint8_t* ckpt_sf, in
   for (const void* q : {static_cast<const void*>(ckpt_q), static_cast<const void*>(ckpt_sf), static_cast<const void*>(h)})
     if (reinterpret_cast<uintptr_t>(q) & 15) return fail(MOE_ERR_INVALID, "moe_ckpt8_unpack: tensors must be 16-byte aligned");
   UnpackArgs p{ckpt_q, ckpt_sf, static_cast<uint16_t*>(h), ldh, rows, expert_offsets, block_offsets, block_to_expert, I,
-               block_size, E, gate_up_layout == MOE_GATE_UP_INTERLEAVED, block_size / kGluRows};
-  const int64_t grid = num_blocks * p.tiles_per_block * (I / kGluFeat);
+               block_size, E, gate_up_layout == MOE_GATE_UP_INTERLEAVED, tile_shift(block_size)};
+  const int64_t grid = (num_blocks << p.tpb_shift) * (I / kGluFeat);
   return launch_pdl(ckpt8_unpack_kernel, dim3((unsigned)grid), dim3(kGluThreads), 0,
                     reinterpret_cast<cudaStream_t>(stream), "ckpt8_unpack", p);
 }

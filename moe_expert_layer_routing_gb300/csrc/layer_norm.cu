@@ -272,16 +272,19 @@ __device__ __forceinline__ uint4* ln_slot(uint4* ring, int stage, int tensor, in
   return ring + ((stage * TENSORS + tensor) * NV + v) * kLnThreads + threadIdx.x;
 }
 
-// Rows of the ring: what fits four (forward) and two (backward) blocks of 4096 columns on an SM.
-__host__ __device__ constexpr int ln_fwd_stages(int es) { return es == 2 ? 3 : 2; }
+// Resident blocks of the forward: registers for 16 columns a thread with their weights allow three.
+__host__ __device__ constexpr int ln_fwd_blocks(int cpt) { return cpt == 32 ? 2 : cpt == 16 ? 3 : 4; }
+// Rows of the ring: what fits three (forward) and two (backward) blocks of 4096 bf16 columns on an SM.
+__host__ __device__ constexpr int ln_fwd_stages(int es) { return es == 2 ? 4 : 2; }
 __host__ __device__ constexpr int ln_bwd_stages(int es) { return es == 2 ? 4 : 2; }
 
 // Forward.  The statistics of a row: each warp takes the mean and the squared differences of its own columns (two
 // shuffle sums), the warps' pairs (n, mean, M2) are combined exactly: M2 = sum M2_w + n_w (mean_w - mean)^2.  So a
 // row costs one barrier and no difference of squares.
 template <typename X, int CPT, int WPR, bool ALIGNED>
-__global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 2 : 4) ln_fwd_kernel(const LnFwdArgs a, int w_bf16) {
+__global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT)) ln_fwd_kernel(const LnFwdArgs a, int w_bf16) {
   using L = LnTile<X, CPT, WPR, ALIGNED>;
+  constexpr bool KEEP = CPT <= 16;  // gamma and beta stay in registers
   constexpr int VEC = L::VEC, NV = L::NV, S = ln_fwd_stages(sizeof(X));
   extern __shared__ uint4 ring[];
   __shared__ float wn[8], wmean[2][8], wm2[2][8];
@@ -300,6 +303,19 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 2 : 4) ln_fwd_kernel(c
   }
   pdl_wait();
   pdl_trigger();
+  float gk[KEEP ? NV : 1][VEC], bk[KEEP ? NV : 1][VEC];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = L::col(v, li);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) gk[v][i] = bk[v][i] = 0.f;
+      if (c < a.H) {
+        ln_weights<VEC>(a.gamma, w_bf16, c, gk[v]);
+        if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, bk[v]);
+      }
+    }
+  }
   auto fetch = [&](int64_t t, int stage) {
     if constexpr (ALIGNED) {
       if (t < a.T) {
@@ -389,13 +405,15 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 2 : 4) ln_fwd_kernel(c
     for (int v = 0; v < NV; ++v) {
       const int c = L::col(v, li);
       if (c < a.H) {
-        float g[VEC], b[VEC];
-        ln_weights<VEC>(a.gamma, w_bf16, c, g);
-        if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, b);
+        if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          f[v][i] = (f[v][i] - mu) * rs * g[i];
-          if (a.beta) f[v][i] += b[i];
+          for (int i = 0; i < VEC; ++i) f[v][i] = fmaf((f[v][i] - mu) * rs, gk[v][i], bk[v][i]);
+        } else {
+          float g[VEC], b[VEC] = {};
+          ln_weights<VEC>(a.gamma, w_bf16, c, g);
+          if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, b);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) f[v][i] = fmaf((f[v][i] - mu) * rs, g[i], b[i]);
         }
         if constexpr (ALIGNED)
           *reinterpret_cast<uint4*>(y + t * a.H + c) = ln_pack(f[v]);
@@ -433,7 +451,7 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
     for (int i = 0; i < VEC; ++i) gamma[v][i] = ag[v][i] = ab[v][i] = 0.f;
     if (L::col(v, li) < a.H) ln_weights<VEC>(a.gamma, w_bf16, L::col(v, li), gamma[v]);
   }
-  auto fetch = [&](int64_t t, int stage) {
+  auto fetch = [&](int64_t t, int stage) {  // dy and x of row t
     if constexpr (ALIGNED) {
       if (t < a.T) {
 #pragma unroll
@@ -442,8 +460,18 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
           if (c < a.H) {
             cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 0, v)), dy + t * a.lddy + c);
             cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 1, v)), x + t * a.ldx + c);
-            if (dres) cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 2, v)), dres + t * a.ldres + c);
           }
+        }
+      }
+    }
+  };
+  auto fetch_skip = [&](int64_t t, int stage) {  // its skip gradient; the row's copies are one group
+    if constexpr (ALIGNED) {
+      if (dres && t < a.T) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = L::col(v, li);
+          if (c < a.H) cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 2, v)), dres + t * a.ldres + c);
         }
       }
       cp_async_commit();
@@ -451,14 +479,23 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
   };
   int64_t t = (int64_t)blockIdx.x * L::GROUPS + L::group();
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
+  for (int s = 0; s < S; ++s) {
+    fetch(t + s * step, s);
+    fetch_skip(t + s * step, s);
+  }
   int stage = 0, par = 0;
-  for (; t < a.T; t += step) {
-    if constexpr (ALIGNED) {
-      fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-      cp_async_wait<S - 1>();
+  float mu_next = 0.f, rs_next = 0.f;  // a row ahead, like the ring
+  auto stats = [&](int64_t t) {
+    if (t < a.T) {
+      mu_next = a.rms ? 0.f : __ldg(a.mean + t);
+      rs_next = __ldg(a.rstd + t);
     }
-    const float mu = a.rms ? 0.f : __ldg(a.mean + t), rs = __ldg(a.rstd + t);
+  };
+  stats(t);
+  for (; t < a.T; t += step) {
+    const float mu = mu_next, rs = rs_next;
+    stats(t + step);
+    if constexpr (ALIGNED) cp_async_wait<S - 1>();
     float wd[NV][VEC], xh[NV][VEC], c1 = 0.f, c2 = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -485,6 +522,7 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
         }
       }
     }
+    fetch(t + S * step, stage);  // the slots just read
     c1 = ln_warp_sum(c1);
     c2 = ln_warp_sum(c2);
     if constexpr (WPR > 1) {
@@ -525,6 +563,7 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
           ln_st(dx, t * a.H + c, d[0]);
       }
     }
+    fetch_skip(t + S * step, stage);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
   // the block's partial rows: with a warp per row the eight warps' sums first, in order, through shared memory
@@ -647,7 +686,7 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
     const size_t smem = al ? ln_ring(ln_fwd_stages(b16 ? 2 : 4), 2, H, b16 ? 2 : 4) : 0;
     if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem))) return rc;
     const int rows = ln_rows_per_block(H);
-    const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * (ln_cpt(H) == 32 ? 2 : 4));
+    const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * ln_fwd_blocks(ln_cpt(H)));
     return launch_pdl(k, dim3((unsigned)grid), dim3(kLnThreads), smem, st, "layer_norm_fwd", a,
                       (int)(w_dtype == MOE_DT_BF16));
   }
