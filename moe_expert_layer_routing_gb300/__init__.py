@@ -404,25 +404,28 @@ def router_bwd(mode: int, ids: torch.Tensor, dscores: torch.Tensor, E: int, logi
     return out
 
 
-def _rows(t, dtype, shape, name, dev):
-    """Row stride of a 2-D CUDA tensor whose rows are dense; raises on anything else."""
+def _refuse(t, dtype, shape, name, dev, how):
     if not t.is_cuda or t.device != dev:
         raise MoeError(f"{name} must be a CUDA tensor on {dev} (there is no CPU path)")
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise MoeError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise MoeError(f"{name} must have dense rows")
-    return max(t.stride(0), shape[1]) if shape[0] <= 1 else t.stride(0)
+    raise MoeError(f"{name} must be {dtype} {shape} {how}, got {t.dtype} {tuple(t.shape)} of strides {t.stride()}")
+
+
+def _rows(t, dtype, shape, name, dev):
+    """Row stride of a 2-D CUDA tensor of this type and shape whose rows are dense; raises on anything else."""
+    if t.device != dev or not t.is_cuda or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, dtype, shape, name, dev, "with dense rows")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        _refuse(t, dtype, shape, name, dev, "with dense rows")
+    return ld if shape[0] > 1 else max(ld, shape[1])
 
 
 def _dense(t, dtype, shape, name, dev):
     """Pointer of a dense CUDA tensor of this type and shape, None for None; raises on anything else."""
     if t is None:
         return None
-    if not t.is_cuda or t.device != dev:
-        raise MoeError(f"{name} must be a CUDA tensor on {dev} (there is no CPU path)")
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise MoeError(f"{name} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != dev or not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dtype, shape, name, dev, "and contiguous")
     return t.data_ptr()
 
 

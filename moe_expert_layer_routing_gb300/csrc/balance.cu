@@ -19,11 +19,13 @@
 #include <algorithm>
 
 #include "moebwd_internal.h"
+#include "ptx.cuh"
 
 namespace moebwd {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalStages = 2;
 
 struct BalanceArgs {
   const float* logits;
@@ -102,6 +104,15 @@ __device__ __forceinline__ float lane_max(float v) {
   return v;
 }
 
+// e^(x - base) as 2^(x log2 e - base log2 e), b2 = base log2 e: one fused multiply-add and one exponential.  The
+// rounding of b2 is common to a row (it cancels in a probability and is below lse's own rounding).
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_from(float x, float b2) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x, kLog2e, -b2)));
+  return e;
+}
+
 // Lane sl of a token's LANES lanes holds its logits 4 (LANES j + sl) .. + 3, j < NV, -inf past E.
 template <int NV, int LANES, bool VEC>
 __device__ __forceinline__ void load_row(const float* row, int E, int sl, bool live, float (&v)[4 * NV]) {
@@ -161,12 +172,39 @@ __device__ __noinline__ void topk_exact(const float* row, int E, int K, int sl, 
   }
 }
 
-// The same with unique 31-bit keys: a value's leading bits, then its column counted backwards (CB bits), so that a
-// round is one maximum and no search, and "smaller than the last" is a subtraction: key - m as unsigned is 2^31 or
-// more exactly for the keys below m.  `odd` marks rows that need exact keys all the same: NaN or +inf (given by the
-// caller), or values that differ in the dropped bits alone and came out of order, or might have at the end.
-template <int NV, int LANES, int SLOTS>
-__device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], const float* row, int E, int K, int sl, bool live,
+// The same with unique 31-bit keys: a value's leading bits, then its column counted backwards (CB bits), so that the
+// larger key is the value to take and no search for columns follows.  True marks rows that need exact keys all the
+// same: values that differ in the dropped bits alone and came out of order, or might have at the end.
+//
+// K <= 8 (LIST): a sorted list of the eight largest per lane (a sorting network of 19 comparators per 8 values), then
+// merged with the lists of the lanes 1, 2, 4, ... away: max(a_i, b_7-i) holds the eight largest of both and is
+// bitonic, twelve comparators sort it.  log2(LANES) dependent shuffle steps, all comparators of a level independent.
+// K > 8: rounds of one maximum.  "Smaller than the last" is a subtraction: key - m as unsigned is 2^31 or more
+// exactly for the keys below m.
+__device__ __forceinline__ void sort_desc(uint32_t& a, uint32_t& b) {
+  const uint32_t h = max(a, b);
+  b = min(a, b);
+  a = h;
+}
+__device__ __forceinline__ void sort8(uint32_t (&a)[8]) {
+  sort_desc(a[0], a[2]); sort_desc(a[1], a[3]); sort_desc(a[4], a[6]); sort_desc(a[5], a[7]);
+  sort_desc(a[0], a[4]); sort_desc(a[1], a[5]); sort_desc(a[2], a[6]); sort_desc(a[3], a[7]);
+  sort_desc(a[0], a[1]); sort_desc(a[2], a[3]); sort_desc(a[4], a[5]); sort_desc(a[6], a[7]);
+  sort_desc(a[2], a[4]); sort_desc(a[3], a[5]);
+  sort_desc(a[1], a[4]); sort_desc(a[3], a[6]);
+  sort_desc(a[1], a[2]); sort_desc(a[3], a[4]); sort_desc(a[5], a[6]);
+}
+// a bitonic list into descending order
+__device__ __forceinline__ void merge8(uint32_t (&a)[8]) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) sort_desc(a[i], a[i + d]);
+}
+
+template <int NV, int LANES, int SLOTS, bool LIST, typename Logit>
+__device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], Logit logit, int E, int K, int sl, bool live,
                                             int (&col)[SLOTS]) {
   constexpr int N = 4 * NV;
   constexpr int CAP = N * LANES;  // columns
@@ -177,66 +215,103 @@ __device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], const floa
   for (int j = 0; j < N; ++j) {
     const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
     const int b = __float_as_int(v[j] + 0.f);
-    const uint32_t k = ((uint32_t)(b ^ (b >> 31 | (int)0x80000000)) >> 1 & ~CM) | (CM - (uint32_t)c);
-    key[j] = c < E ? k : 0u;
+    // columns past E hold -inf, behind every logit: they are taken last (K <= E), or in a row with a NaN of negative
+    // sign, which is done over
+    key[j] = ((uint32_t)(b ^ (b >> 31 | (int)0x80000000)) >> 1 & ~CM) | (CM - (uint32_t)c);
   }
-  uint32_t m = 0x80000000u, mk[SLOTS] = {}, next[SLOTS] = {};
-  const int rounds = min(K + 1, E);
-  for (int r = 0; r < rounds; ++r) {
-    uint32_t d = 0;
+  uint32_t mk[SLOTS] = {}, next[SLOTS] = {};
+  uint32_t last, behind;  // the K-th key, and the largest of this lane's (LIST) or of all below it
+  if constexpr (LIST) {
+    uint32_t top[8];
 #pragma unroll
-    for (int j = 0; j < N; j += 2) d = __vimax3_u32(d, key[j] - m, key[j + 1] - m);
+    for (int j = 0; j < 8; ++j) top[j] = j < N ? key[j] : 0u;
+    sort8(top);
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) d = max(d, __shfl_xor_sync(0xffffffffu, d, o));
-    m += d;
+    for (int g = 8; g < N; g += 8) {
+      uint32_t more[8];
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      if (r == s * LANES + sl) mk[s] = m;
-      if (r == s * LANES + sl + 1) next[s] = m;
+      for (int j = 0; j < 8; ++j) more[j] = key[g + j];
+      sort8(more);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top[j] = max(top[j], more[7 - j]);
+      merge8(top);
     }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+      uint32_t other[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) other[j] = __shfl_xor_sync(0xffffffffu, top[7 - j], o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top[j] = max(top[j], other[j]);
+      merge8(top);
+    }
+    // slot sl, by the bits of sl
+    const uint32_t h0 = sl & 4 ? top[4] : top[0], h1 = sl & 4 ? top[5] : top[1], h2 = sl & 4 ? top[6] : top[2],
+                   h3 = sl & 4 ? top[7] : top[3];
+    const uint32_t q0 = sl & 2 ? h2 : h0, q1 = sl & 2 ? h3 : h1;
+    mk[0] = sl & 1 ? q1 : q0;
+    next[0] = __shfl_down_sync(0xffffffffu, mk[0], 1, LANES);
+    last = __shfl_sync(0xffffffffu, mk[0], K - 1, LANES);
+    behind = 0;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) behind = __vimax3_u32(behind, key[j] - last, key[j + 1] - last);
+    behind = behind >= 0x80000000u ? behind + last : 0u;
+  } else {
+    uint32_t m = 0x80000000u;
+    last = 0;
+    for (int r = 0; r <= K; ++r) {
+      uint32_t d = 0;
+#pragma unroll
+      for (int j = 0; j < N; j += 2) d = __vimax3_u32(d, key[j] - m, key[j + 1] - m);
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) d = max(d, __shfl_xor_sync(0xffffffffu, d, o));
+      m = d < 0x80000000u ? 0u : m + d;  // 0: none is left (K = E)
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        if (r == s * LANES + sl) mk[s] = m;
+        if (r == s * LANES + sl + 1) next[s] = m;
+      }
+      if (r == K - 1) last = m;
+    }
+    behind = m;
   }
-  // exact keys of the slot and of the one behind it, from the logits re-read (cache hits)
+  // exact keys of the slot and of the one behind it
   bool odd = false;
-  uint32_t exact[SLOTS];
+  uint32_t ek = 0;  // exact key of slot K - 1, in the lane that holds it
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
     const int k = s * LANES + sl;
-    col[s] = (int)(CM - (mk[s] & CM));
-    exact[s] = 0;
-    if (live && k < K) {
-      exact[s] = order_key(row[col[s]]);
-      if (k + 1 < rounds && (mk[s] ^ next[s]) <= CM)  // the same leading bits
-        odd |= exact[s] < order_key(row[CM - (next[s] & CM)]);
+    col[s] = min((int)(CM - (mk[s] & CM)), E - 1);
+    if (live && k < K && (k + 1 == K || (mk[s] ^ next[s]) <= CM)) {  // the same leading bits
+      const uint32_t exact = order_key(logit(col[s]));
+      if (k + 1 < K)
+        odd |= exact < order_key(logit(min((int)(CM - (next[s] & CM)), E - 1)));
+      else
+        ek = exact;
     }
   }
   // at the end: a value left out may be larger in the dropped bits than the last one taken
-  if (rounds > K) {
-    const int kl = K - 1;
-    uint32_t last = 0, ek = 0;
+  const bool tie = live && behind != 0 && (last ^ behind) <= CM;
+  if (__any_sync(0xffffffffu, tie)) {
+    ek = __shfl_sync(0xffffffffu, ek, (K - 1) % LANES, LANES);
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-      if (kl / LANES == s) {
-        last = mk[s];
-        ek = exact[s];
-      }
-    last = __shfl_sync(0xffffffffu, last, kl % LANES, LANES);
-    ek = __shfl_sync(0xffffffffu, ek, kl % LANES, LANES);
-    const bool tie = live && (last ^ m) <= CM;
-    if (__any_sync(0xffffffffu, tie)) {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        odd |= tie && key[j] < last && (key[j] ^ last) <= CM && order_key(v[j]) > ek;
-    }
+    for (int j = 0; j < N; ++j) odd |= tie && key[j] < last && (key[j] ^ last) <= CM &&
+             order_key(logit(min((int)(CM - (key[j] & CM)), E - 1))) > ek;
   }
   return odd;
 }
 
-// TOPK: selects and writes scores and ids (else reads ids).  One token per LANES lanes.
-template <int NV, int LANES, bool VEC, bool TOPK>
-__global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceArgs a) {
+// Selects and writes scores and ids (else reads ids).  One token per LANES lanes.
+enum TopK { kIdsGiven = 0, kTopKList = 1, kTopKRounds = 2 };
+template <int NV, int LANES, bool VEC, int HOW>
+__global__ void __launch_bounds__(kBalThreads, NV <= 4 ? 3 : 1) router_fwd_kernel(const BalanceArgs a) {
   constexpr int SEGS = 32 / LANES, N = 4 * NV;
-  constexpr int SLOTS = LANES == 32 ? 2 : 1;  // slots of the token that a lane holds (K <= 64 at 32 lanes)
-  extern __shared__ float sm[];               // [kBalWarps][E] partial sums of p, then [E] counts, [kBalWarps] z
+  constexpr bool TOPK = HOW != kIdsGiven;
+  constexpr int SLOTS = LANES == 32 && HOW == kTopKRounds ? 2 : 1;  // slots a lane holds (K <= 64 at 32 lanes)
+  // VEC: a ring of kBalStages rows per segment, filled by 16-byte asynchronous copies a pass ahead; then [kBalWarps][E]
+  // partial sums of p, [E] counts, [kBalWarps] z
+  extern __shared__ float4 ring[];
+  float* sm = reinterpret_cast<float*>(ring + (VEC ? kBalStages * NV * kBalThreads : 0));
   int* hist = reinterpret_cast<int*>(sm + kBalWarps * a.E);
   float* zs = sm + (kBalWarps + 1) * a.E;
   pdl_wait();
@@ -262,28 +337,80 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
   float z = 0.f;
+  auto slot = [&](int stage, int j) { return ring + (stage * NV + j) * kBalThreads + threadIdx.x; };
+  auto fetch = [&](int t, int stage) {
+    if constexpr (VEC) {
+      if (t < hi) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = 4 * (LANES * j + sl);
+          if (c < a.E) cp_async_16(smem_u32(slot(stage, j)), a.logits + (int64_t)t * a.ld + c);
+        }
+      }
+      cp_async_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kBalStages - 1; ++s) fetch(lo + (w + s * kBalWarps) * SEGS + seg, s);
+  int stage = 0;
   for (int tb = lo + w * SEGS; tb < hi; tb += kBalWarps * SEGS) {
     const int t = tb + seg;
     const bool live = t < hi;
-    float v[N];
-    load_row<NV, LANES, VEC>(a.logits + (int64_t)t * a.ld, a.E, sl, live, v);
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
-    m = lane_max<LANES>(m);
-    const float base = m > -INFINITY ? m : 0.f;
     const float* row = a.logits + (int64_t)t * a.ld;
+    float v[N];
+    auto read = [&](float (&u)[N]) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const float4 f = live && 4 * (LANES * j + sl) < a.E ? *slot(stage, j)
+                                                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        u[4 * j] = f.x;
+        u[4 * j + 1] = f.y;
+        u[4 * j + 2] = f.z;
+        u[4 * j + 3] = f.w;
+      }
+    };
+    if constexpr (VEC) {
+      __syncwarp();  // the slot filled next was read by the whole segment
+      fetch(t + (kBalStages - 1) * kBalWarps * SEGS, stage == 0 ? kBalStages - 1 : stage - 1);
+      cp_async_wait<kBalStages - 1>();
+      __syncwarp();
+      read(v);
+    } else {
+      load_row<NV, LANES, VEC>(row, a.E, sl, live, v);
+    }
+    // one logit of the row: from the lane that copied it
+    auto logit = [&](int c) {
+      if constexpr (VEC)
+        return reinterpret_cast<const float*>(ring + (stage * NV + c / (4 * LANES)) * kBalThreads + threadIdx.x - sl +
+                                              (c >> 2) % LANES)[c & 3];
+      else
+        return row[c];
+    };
     int col[SLOTS];
     bool odd = false;
-    if constexpr (TOPK) odd = topk_packed<NV, LANES, SLOTS>(v, row, a.E, a.K, sl, live, col);
+    float m = -INFINITY;  // the row's maximum, or (top-K) one that differs from it in the dropped bits at most
+    if constexpr (TOPK) {
+      odd = topk_packed<NV, LANES, SLOTS, HOW == kTopKList>(v, logit, a.E, a.K, sl, live, col);
+      if (live && sl == 0) m = logit(col[0]);
+      m = __shfl_sync(0xffffffffu, m, 0, LANES);
+      if constexpr (VEC) {  // read again rather than kept through the selection: registers
+        asm volatile("" ::: "memory");
+        read(v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
+      m = lane_max<LANES>(m);
+    }
+    const float base = m == -INFINITY ? 0.f : m, b2 = base * kLog2e;
     float total = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      v[j] = __expf(v[j] - base);
+      v[j] = exp_from(v[j], b2);
       total += v[j];
     }
     total = lane_sum<LANES>(total);
-    const float inv = total != 0.f ? 1.f / total : 0.f;  // 0: every expert masked (or no token here)
+    const float inv = total != 0.f ? __fdividef(1.f, total) : 0.f;  // 0: every expert masked (or no token here)
     const float lse = base + logf(total);
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
@@ -305,9 +432,9 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
       float x[SLOTS], e[SLOTS], sum = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
-        x[s] = live && s * LANES + sl < a.K ? row[col[s]] : -INFINITY;
+        x[s] = live && s * LANES + sl < a.K ? logit(col[s]) : -INFINITY;
         if (x[s] == -INFINITY) col[s] = -1;  // a masked expert takes no slot
-        e[s] = __expf(x[s] - base);
+        e[s] = exp_from(x[s], b2);
         sum += e[s];
       }
       sum = lane_sum<LANES>(sum);
@@ -319,7 +446,7 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
           if (col[s] >= 0)
             sc = a.mode == MOE_ROUTER_TOPK ? x[s]
                  : a.mode == MOE_ROUTER_TOPK_OVER_SOFTMAX && !a.renorm ? e[s] * inv
-                                                                       : e[s] / sum;
+                                                                       : __fdividef(e[s], sum);
           a.scores[(int64_t)t * a.K + k] = sc;
           a.ids[(int64_t)t * a.K + k] = col[s];
           if (stats && col[s] >= 0) atomicAdd(&hist[col[s]], 1);  // integers: any order gives the same counts
@@ -331,6 +458,7 @@ __global__ void __launch_bounds__(kBalThreads) router_fwd_kernel(const BalanceAr
         if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
       }
     }
+    stage = stage + 1 == kBalStages ? 0 : stage + 1;
   }
   if (!stats) return;
   // the warp's tokens, then the warps, in a fixed order
@@ -477,7 +605,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      v[j] = none ? 0.f : __expf(v[j] - lse);
+      v[j] = none ? 0.f : exp_from(v[j], lse * kLog2e);
       dot = fmaf(cnt[j], v[j], dot);
     }
     dot = lane_sum<LANES>(dot);
@@ -509,7 +637,7 @@ static int bal_bwd_lanes(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : 32; }
 // Tokens per chunk: one pass of a CTA's warps, more where that would be over four CTAs per SM.
 static int bal_chunk(int T, int lanes) {
   const int step = kBalThreads / lanes;
-  const int64_t steps = ((int64_t)T + step - 1) / step, most = 4 * 152;
+  const int64_t steps = ((int64_t)T + step - 1) / step, most = 3 * 152 - 8;
   return (int)((steps + most - 1) / most) * step;
 }
 
@@ -546,23 +674,51 @@ static int bal_check(const char* who, int T, int K, int E, int S) {
   return MOE_OK;
 }
 
-#define BAL_PICK(KERN, NV_, ...)                                                                   \
-  (lanes == 8 ? (NV_ <= 1 ? KERN<1, 8, __VA_ARGS__> : NV_ <= 2 ? KERN<2, 8, __VA_ARGS__>           \
-                 : NV_ <= 4 ? KERN<4, 8, __VA_ARGS__> : KERN<8, 8, __VA_ARGS__>)                   \
-   : lanes == 16 ? (NV_ <= 1 ? KERN<1, 16, __VA_ARGS__> : NV_ <= 2 ? KERN<2, 16, __VA_ARGS__>      \
-                    : NV_ <= 4 ? KERN<4, 16, __VA_ARGS__> : KERN<8, 16, __VA_ARGS__>)              \
-                 : (NV_ <= 1 ? KERN<1, 32, __VA_ARGS__> : NV_ <= 2 ? KERN<2, 32, __VA_ARGS__>      \
-                    : NV_ <= 4 ? KERN<4, 32, __VA_ARGS__> : KERN<8, 32, __VA_ARGS__>))
-
 typedef void (*BalKernel)(const BalanceArgs);
 
-static BalKernel fwd_kernel(int lanes, int nv, bool vec, bool topk) {
-  if (vec) return topk ? BAL_PICK(router_fwd_kernel, nv, true, true) : BAL_PICK(router_fwd_kernel, nv, true, false);
-  return topk ? BAL_PICK(router_fwd_kernel, nv, false, true) : BAL_PICK(router_fwd_kernel, nv, false, false);
+// Instances by lanes per token and float4 groups a lane; only what bal_lanes and bal_bwd_lanes ask for.
+template <bool VEC>
+static BalKernel fwd_kernel(int lanes, int nv, int how) {
+  if (how == kTopKList) {
+    if (lanes == 8)
+      return nv <= 1   ? router_fwd_kernel<1, 8, VEC, kTopKList>
+             : nv <= 2 ? router_fwd_kernel<2, 8, VEC, kTopKList>
+                       : router_fwd_kernel<4, 8, VEC, kTopKList>;
+    if (lanes == 16) return router_fwd_kernel<4, 16, VEC, kTopKList>;  // above 128 experts
+    return nv <= 4 ? router_fwd_kernel<4, 32, VEC, kTopKList> : router_fwd_kernel<8, 32, VEC, kTopKList>;
+  }
+  if (how == kTopKRounds) {
+    if (lanes == 16)
+      return nv <= 1   ? router_fwd_kernel<1, 16, VEC, kTopKRounds>
+             : nv <= 2 ? router_fwd_kernel<2, 16, VEC, kTopKRounds>
+                       : router_fwd_kernel<4, 16, VEC, kTopKRounds>;
+    return nv <= 1   ? router_fwd_kernel<1, 32, VEC, kTopKRounds>
+           : nv <= 2 ? router_fwd_kernel<2, 32, VEC, kTopKRounds>
+           : nv <= 4 ? router_fwd_kernel<4, 32, VEC, kTopKRounds>
+                     : router_fwd_kernel<8, 32, VEC, kTopKRounds>;
+  }
+  if (lanes == 8)
+    return nv <= 1   ? router_fwd_kernel<1, 8, VEC, kIdsGiven>
+           : nv <= 2 ? router_fwd_kernel<2, 8, VEC, kIdsGiven>
+                     : router_fwd_kernel<4, 8, VEC, kIdsGiven>;
+  if (lanes == 16)
+    return nv <= 1   ? router_fwd_kernel<1, 16, VEC, kIdsGiven>
+           : nv <= 2 ? router_fwd_kernel<2, 16, VEC, kIdsGiven>
+                     : router_fwd_kernel<4, 16, VEC, kIdsGiven>;
+  return nv <= 1   ? router_fwd_kernel<1, 32, VEC, kIdsGiven>
+         : nv <= 2 ? router_fwd_kernel<2, 32, VEC, kIdsGiven>
+         : nv <= 4 ? router_fwd_kernel<4, 32, VEC, kIdsGiven>
+                   : router_fwd_kernel<8, 32, VEC, kIdsGiven>;
 }
 
-static BalKernel bwd_kernel(int lanes, int nv, bool vec) {
-  return vec ? BAL_PICK(balance_bwd_kernel, nv, true) : BAL_PICK(balance_bwd_kernel, nv, false);
+template <bool VEC>
+static BalKernel bwd_kernel(int lanes, int nv) {
+  if (lanes == 8)
+    return nv <= 1   ? balance_bwd_kernel<1, 8, VEC>
+           : nv <= 2 ? balance_bwd_kernel<2, 8, VEC>
+           : nv <= 4 ? balance_bwd_kernel<4, 8, VEC>
+                     : balance_bwd_kernel<8, 8, VEC>;
+  return lanes == 16 ? balance_bwd_kernel<8, 16, VEC> : balance_bwd_kernel<8, 32, VEC>;
 }
 
 // Both forward entry points: the top-K (scores given) or the caller's ids, with or without the losses.
@@ -579,8 +735,17 @@ static int launch_router(BalanceArgs a, bool topk, bool stats, const BalLayout& 
   }
   const int lanes = bal_lanes(a.K, a.E), nv = (a.E + 4 * lanes - 1) / (4 * lanes);
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
-  const size_t smem = sizeof(float) * ((size_t)(kBalWarps + 1) * a.E + kBalWarps);
-  int rc = launch_pdl(fwd_kernel(lanes, nv, vec, topk), dim3(a.pieces), dim3(kBalThreads), smem, st, "router_fwd", a);
+  const int groups = nv <= 1 ? 1 : nv <= 2 ? 2 : nv <= 4 ? 4 : 8;
+  const size_t smem = sizeof(float) * ((size_t)(kBalWarps + 1) * a.E + kBalWarps) +
+                      (vec ? sizeof(float4) * kBalStages * groups * kBalThreads : 0);
+  const int how = !topk ? kIdsGiven : a.K <= 8 ? kTopKList : kTopKRounds;
+  const BalKernel kern = vec ? fwd_kernel<true>(lanes, groups, how) : fwd_kernel<false>(lanes, groups, how);
+  int rc = MOE_OK;
+  if (smem > 40 * 1024 &&
+      (rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                       "cudaFuncSetAttribute(router_fwd)")))
+    return rc;
+  rc = launch_pdl(kern, dim3(a.pieces), dim3(kBalThreads), smem, st, "router_fwd", a);
   if (rc || !stats) return rc;
   return launch_pdl(balance_reduce_kernel, dim3(a.S, (a.E + 31) / 32), dim3(kBalThreads), 0, st, "balance_reduce", a);
 }
@@ -703,5 +868,5 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   const bool vec = E % 4 == 0 && ld_logits % 4 == 0 && (!add || ld_add % 4 == 0) &&
                    ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(add) |
                      reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
-  return launch_pdl(bwd_kernel(lanes, nv, vec), dim3(a.pieces), dim3(kBalThreads), 0, st, "balance_bwd", a);
+  return launch_pdl((vec ? bwd_kernel<true>(lanes, nv) : bwd_kernel<false>(lanes, nv)), dim3(a.pieces), dim3(kBalThreads), 0, st, "balance_bwd", a);
 }
