@@ -172,25 +172,26 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_part_any_kernel(const LnBwd
   }
 }
 
-// dgamma and dbeta (grid.y) from the partial sums of the G row groups: thread columns of 32, the groups
-// split over eight warps, all in a fixed order.
-__global__ void __launch_bounds__(kLnThreads) ln_bwd_reduce_kernel(const float* part, int G, int H, float* dgamma,
-                                                                   float* dbeta, int accumulate) {
-  __shared__ float red[8][32];
+// dgamma and dbeta (grid.y) from the partial sums of the G row groups: a block takes 32 columns, its 32 warps every
+// 32nd group, all in a fixed order.
+constexpr int kLnReduceThreads = 1024;
+__global__ void __launch_bounds__(kLnReduceThreads) ln_bwd_reduce_kernel(const float* part, int G, int H, float* dgamma,
+                                                                         float* dbeta, int accumulate) {
+  __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? dbeta : dgamma;
   float s = 0.f;
-  if (i < H && out)
-    for (int g = w; g < G; g += 8) s += part[((int64_t)blockIdx.y * G + g) * H + i];
+  if (i < H)
+    for (int g = w; g < G; g += 32) s += part[((int64_t)blockIdx.y * G + g) * H + i];
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && i < H && out) {
+  if (w == 0 && i < H) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += red[k][lane];
+    for (int k = 0; k < 32; ++k) v += red[k][lane];
     out[i] = accumulate ? out[i] + v : v;
   }
 }
@@ -199,19 +200,68 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_reduce_kernel(const float* 
 // Rows in registers
 // ------------------------------------------------------------------------------------------
 // A row belongs to a group of GT = 32 WPR threads (a warp, or the block of eight warps) and passes once: a
-// thread holds CPT of its columns, as NV 16-byte vectors VEC wide (thread li of the group: vectors v GT + li), or,
-// where rows are not 16-byte aligned, as single elements (VEC = 1).  Blocks are persistent.  Vectors come through a
-// ring of rows in shared memory by 16-byte asynchronous copies: every thread copies what it alone reads,
-// so the ring needs no barrier, and the rows in flight cost no registers.
-template <typename X, int CPT, int WPR, bool ALIGNED>
+// thread holds CPT of its columns.  Blocks are persistent; rows come through a ring in shared memory by 16-byte
+// asynchronous copies, so the rows in flight cost no registers.
+//   vectors   rows and strides are multiples of 16 bytes: a thread holds NV vectors VEC wide (v GT + li of the
+//             row) and copies what it alone reads, so the ring needs no barrier
+//   shifted   rows of any width on an aligned base: the 16-byte pieces a row touches are copied as they lie (the
+//             first begins in the row before it, the last is cut at the row's end), thread li reads the single
+//             elements v GT + li behind a barrier
+//   direct    an unaligned base: single elements from global memory
+enum LnMode { kLnDirect = 0, kLnVector = 1, kLnShifted = 2 };
+
+template <typename X, int CPT, int WPR, int MODE>
 struct LnTile {
-  static constexpr int VEC = ALIGNED ? 16 / (int)sizeof(X) : 1;
+  static constexpr int VEC = MODE == kLnVector ? 16 / (int)sizeof(X) : 1;
   static constexpr int NV = CPT / VEC;
   static constexpr int GT = 32 * WPR;
   static constexpr int GROUPS = kLnThreads / GT;
   __device__ static int col(int v, int li) { return (v * GT + li) * VEC; }
   __device__ static int group() { return WPR == 1 ? threadIdx.x >> 5 : 0; }
   __device__ static int li() { return WPR == 1 ? threadIdx.x & 31 : threadIdx.x; }
+  __device__ static void sync() {
+    if constexpr (WPR == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  }
+};
+
+// Bytes of a row's slot in the shifted ring.
+__host__ __device__ constexpr int ln_row_bytes(int H, int es) { return ((H * es + 15) / 16 + 1) * 16; }
+
+// One tensor's rows in the ring: tensor `which` of TENSORS.
+template <typename X, int CPT, int WPR, int MODE, int TENSORS>
+struct LnStream {
+  using L = LnTile<X, CPT, WPR, MODE>;
+  const X* p;
+  int64_t ld;
+  int H, which;
+  char* ring;
+  __device__ char* slot(int stage) const {  // shifted
+    return ring + ((stage * TENSORS + which) * L::GROUPS + L::group()) * ln_row_bytes(H, sizeof(X));
+  }
+  __device__ uint4* slot(int stage, int v) const {  // vectors
+    return reinterpret_cast<uint4*>(ring) + ((stage * TENSORS + which) * L::NV + v) * kLnThreads + threadIdx.x;
+  }
+  __device__ int shift(int64_t t) const { return (int)(reinterpret_cast<uintptr_t>(p + t * ld) & 15); }
+  // copies of row t (nothing for a null tensor)
+  __device__ void fetch(int64_t t, int stage) const {
+    if (!p) return;
+    const int li = L::li();
+    if constexpr (MODE == kLnVector) {
+#pragma unroll
+      for (int v = 0; v < L::NV; ++v)
+        if (L::col(v, li) < H) cp_async_16(smem_u32(slot(stage, v)), p + t * ld + L::col(v, li));
+    } else if constexpr (MODE == kLnShifted) {
+      const char* row = reinterpret_cast<const char*>(p + t * ld);
+      const int d = shift(t), end = d + H * (int)sizeof(X);
+      char* dst = slot(stage);
+      for (int c = 16 * li; c < end; c += 16 * L::GT) cp_async_16_zfill(smem_u32(dst + c), row - d + c, min(16, end - c));
+    }
+  }
+  // columns col(v, li) .. of row t, which the group's copies have brought (c < H)
+  __device__ void read(int64_t t, int stage, int v, int c, float (&f)[L::VEC]) const;
 };
 
 __device__ __forceinline__ void ln_unpack(const uint4& w, float (&f)[4]) {
@@ -266,29 +316,36 @@ __device__ __forceinline__ float ln_warp_sum(float v) {
   return v;
 }
 
-// Ring slot (stage, tensor, vector) of this thread.
-template <int TENSORS, int NV>
-__device__ __forceinline__ uint4* ln_slot(uint4* ring, int stage, int tensor, int v) {
-  return ring + ((stage * TENSORS + tensor) * NV + v) * kLnThreads + threadIdx.x;
+template <typename X, int CPT, int WPR, int MODE, int TENSORS>
+__device__ __forceinline__ void LnStream<X, CPT, WPR, MODE, TENSORS>::read(int64_t t, int stage, int v, int c,
+                                                                           float (&f)[L::VEC]) const {
+  if constexpr (MODE == kLnVector)
+    ln_unpack(*slot(stage, v), f);
+  else if constexpr (MODE == kLnShifted)
+    f[0] = ln_ld(reinterpret_cast<const X*>(slot(stage) + shift(t)), c);
+  else
+    f[0] = ln_ld(p, t * ld + c);
 }
 
-// Resident blocks of the forward: registers for 16 columns a thread with their weights allow three.
-__host__ __device__ constexpr int ln_fwd_blocks(int cpt) { return cpt == 32 ? 2 : cpt == 16 ? 3 : 4; }
-// Rows of the ring: what fits three (forward) and two (backward) blocks of 4096 bf16 columns on an SM.
-__host__ __device__ constexpr int ln_fwd_stages(int es) { return es == 2 ? 4 : 2; }
-__host__ __device__ constexpr int ln_bwd_stages(int es) { return es == 2 ? 4 : 2; }
+// Resident blocks (registers) and rows of the ring, as many as 192 KB an SM hold.
+__host__ __device__ constexpr int ln_fwd_blocks(int cpt, int es) { return cpt == 8 ? 4 : cpt == 16 ? 3 : es == 2 ? 2 : 1; }
+__host__ __device__ constexpr int ln_bwd_blocks(int cpt) { return cpt == 32 ? 1 : 2; }
+__host__ __device__ constexpr int ln_stages(int blocks, int tensors, int cpt, int es) {
+  return 196608 / (blocks * tensors * kLnThreads * cpt * es) > 6 ? 6 : 196608 / (blocks * tensors * kLnThreads * cpt * es);
+}
 
 // Forward.  The statistics of a row: each warp takes the mean and the squared differences of its own columns (two
 // shuffle sums), the warps' pairs (n, mean, M2) are combined exactly: M2 = sum M2_w + n_w (mean_w - mean)^2.  So a
 // row costs one barrier and no difference of squares.
-template <typename X, int CPT, int WPR, bool ALIGNED>
-__global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT)) ln_fwd_kernel(const LnFwdArgs a, int w_bf16) {
-  using L = LnTile<X, CPT, WPR, ALIGNED>;
+template <typename X, int CPT, int WPR, int MODE>
+__global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT, sizeof(X))) ln_fwd_kernel(const LnFwdArgs a, int w_bf16) {
+  using L = LnTile<X, CPT, WPR, MODE>;
   constexpr bool KEEP = CPT <= 16;  // gamma and beta stay in registers
-  constexpr int VEC = L::VEC, NV = L::NV, S = ln_fwd_stages(sizeof(X));
+  constexpr int VEC = L::VEC, NV = L::NV, S = ln_stages(ln_fwd_blocks(CPT, sizeof(X)), 2, CPT, sizeof(X));
   extern __shared__ uint4 ring[];
   __shared__ float wn[8], wmean[2][8], wm2[2][8];
-  const X *x = static_cast<const X*>(a.x), *r = static_cast<const X*>(a.r);
+  const LnStream<X, CPT, WPR, MODE, 2> x{static_cast<const X*>(a.x), a.ldx, a.H, 0, reinterpret_cast<char*>(ring)};
+  const LnStream<X, CPT, WPR, MODE, 2> r{static_cast<const X*>(a.r), a.ldr, a.H, 1, reinterpret_cast<char*>(ring)};
   X *y = static_cast<X*>(a.y), *sum = static_cast<X*>(a.sum);
   const int li = L::li(), w = threadIdx.x >> 5;
   const int64_t step = (int64_t)gridDim.x * L::GROUPS;
@@ -317,16 +374,10 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT)) ln_fwd_kernel(
     }
   }
   auto fetch = [&](int64_t t, int stage) {
-    if constexpr (ALIGNED) {
+    if constexpr (MODE != kLnDirect) {
       if (t < a.T) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = L::col(v, li);
-          if (c < a.H) {
-            cp_async_16(smem_u32(ln_slot<2, NV>(ring, stage, 0, v)), x + t * a.ldx + c);
-            if (r) cp_async_16(smem_u32(ln_slot<2, NV>(ring, stage, 1, v)), r + t * a.ldr + c);
-          }
-        }
+        x.fetch(t, stage);
+        r.fetch(t, stage);
       }
       cp_async_commit();
     }
@@ -338,29 +389,28 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT)) ln_fwd_kernel(
   // a warp of its own leaves when its rows are through; a block's warps share t
   for (; t < a.T; t += step) {
     float f[NV][VEC];
-    if constexpr (ALIGNED) {
-      fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);  // the slot read last time round
-      cp_async_wait<S - 1>();
-    }
+    if constexpr (MODE == kLnShifted && WPR == 1) __syncwarp();  // the slot filled next is read by the whole warp
+    fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);  // the slot read last time round
+    if constexpr (MODE != kLnDirect) cp_async_wait<S - 1>();
+    if constexpr (MODE == kLnShifted) L::sync();
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = L::col(v, li);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) f[v][i] = 0.f;
       if (c < a.H) {
-        if constexpr (ALIGNED) {
-          ln_unpack(*ln_slot<2, NV>(ring, stage, 0, v), f[v]);
-          if (r) {
-            float q[VEC];
-            ln_unpack(*ln_slot<2, NV>(ring, stage, 1, v), q);
+        x.read(t, stage, v, c, f[v]);
+        if (r.p) {
+          float q[VEC];
+          r.read(t, stage, v, c, q);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f[v][i] = ln_round(f[v][i] + q[i], x);
-          }
-          if (sum) *reinterpret_cast<uint4*>(sum + t * a.H + c) = ln_pack(f[v]);
-        } else {
-          f[v][0] = ln_ld(x, t * a.ldx + c);
-          if (r) f[v][0] = ln_round(f[v][0] + ln_ld(r, t * a.ldr + c), x);
-          if (sum) ln_st(sum, t * a.H + c, f[v][0]);
+          for (int i = 0; i < VEC; ++i) f[v][i] = ln_round(f[v][i] + q[i], x.p);
+        }
+        if (sum) {
+          if constexpr (MODE == kLnVector)
+            *reinterpret_cast<uint4*>(sum + t * a.H + c) = ln_pack(f[v]);
+          else
+            ln_st(sum, t * a.H + c, f[v][0]);
         }
       }
     }
@@ -415,7 +465,7 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT)) ln_fwd_kernel(
 #pragma unroll
           for (int i = 0; i < VEC; ++i) f[v][i] = fmaf((f[v][i] - mu) * rs, g[i], b[i]);
         }
-        if constexpr (ALIGNED)
+        if constexpr (MODE == kLnVector)
           *reinterpret_cast<uint4*>(y + t * a.H + c) = ln_pack(f[v]);
         else
           ln_st(y, t * a.H + c, f[v][0]);
@@ -430,14 +480,17 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT)) ln_fwd_kernel(
 }
 
 // Backward: dx and, in the thread's registers over all rows of its group, dgamma and dbeta of its columns; a
-// block leaves one partial row of each.
-template <typename X, int CPT, int WPR, bool ALIGNED>
-__global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(const LnBwdArgs a, int w_bf16) {
-  using L = LnTile<X, CPT, WPR, ALIGNED>;
-  constexpr int VEC = L::VEC, NV = L::NV, GT = L::GT, S = ln_bwd_stages(sizeof(X));
+// block leaves one partial row of each.  With vectors a thread refills a slot as soon as it has read it (dy and x
+// before the row's sums, the skip gradient at the row's end): S rows in flight.
+template <typename X, int CPT, int WPR, int MODE>
+__global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(const LnBwdArgs a, int w_bf16) {
+  using L = LnTile<X, CPT, WPR, MODE>;
+  constexpr int VEC = L::VEC, NV = L::NV, GT = L::GT, S = ln_stages(ln_bwd_blocks(CPT), 3, CPT, sizeof(X));
   extern __shared__ uint4 ring[];
   __shared__ float r1[2][8], r2[2][8];
-  const X *dy = static_cast<const X*>(a.dy), *x = static_cast<const X*>(a.x), *dres = static_cast<const X*>(a.dres);
+  const LnStream<X, CPT, WPR, MODE, 3> dy{static_cast<const X*>(a.dy), a.lddy, a.H, 0, reinterpret_cast<char*>(ring)};
+  const LnStream<X, CPT, WPR, MODE, 3> x{static_cast<const X*>(a.x), a.ldx, a.H, 1, reinterpret_cast<char*>(ring)};
+  const LnStream<X, CPT, WPR, MODE, 3> dres{static_cast<const X*>(a.dres), a.ldres, a.H, 2, reinterpret_cast<char*>(ring)};
   X* dx = static_cast<X*>(a.dx);
   const int li = L::li(), w = threadIdx.x >> 5;
   const int64_t step = (int64_t)gridDim.x * L::GROUPS;
@@ -451,37 +504,25 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
     for (int i = 0; i < VEC; ++i) gamma[v][i] = ag[v][i] = ab[v][i] = 0.f;
     if (L::col(v, li) < a.H) ln_weights<VEC>(a.gamma, w_bf16, L::col(v, li), gamma[v]);
   }
-  auto fetch = [&](int64_t t, int stage) {  // dy and x of row t
-    if constexpr (ALIGNED) {
-      if (t < a.T) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = L::col(v, li);
-          if (c < a.H) {
-            cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 0, v)), dy + t * a.lddy + c);
-            cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 1, v)), x + t * a.ldx + c);
-          }
-        }
-      }
-    }
-  };
-  auto fetch_skip = [&](int64_t t, int stage) {  // its skip gradient; the row's copies are one group
-    if constexpr (ALIGNED) {
-      if (dres && t < a.T) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = L::col(v, li);
-          if (c < a.H) cp_async_16(smem_u32(ln_slot<3, NV>(ring, stage, 2, v)), dres + t * a.ldres + c);
-        }
-      }
-      cp_async_commit();
-    }
-  };
   int64_t t = (int64_t)blockIdx.x * L::GROUPS + L::group();
+  // a row's copies are one group: with vectors S of them ahead, shifted S - 1
+  constexpr int AHEAD = MODE == kLnVector ? S : S - 1;
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T) {
+      dy.fetch(t, stage);
+      x.fetch(t, stage);
+    }
+  };
+  auto fetch_skip = [&](int64_t t, int stage) {
+    if (t < a.T) dres.fetch(t, stage);
+    cp_async_commit();
+  };
+  if constexpr (MODE != kLnDirect) {
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    fetch(t + s * step, s);
-    fetch_skip(t + s * step, s);
+    for (int s = 0; s < AHEAD; ++s) {
+      fetch(t + s * step, s);
+      fetch_skip(t + s * step, s);
+    }
   }
   int stage = 0, par = 0;
   float mu_next = 0.f, rs_next = 0.f;  // a row ahead, like the ring
@@ -495,7 +536,8 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
   for (; t < a.T; t += step) {
     const float mu = mu_next, rs = rs_next;
     stats(t + step);
-    if constexpr (ALIGNED) cp_async_wait<S - 1>();
+    if constexpr (MODE != kLnDirect) cp_async_wait<AHEAD - 1>();
+    if constexpr (MODE == kLnShifted) L::sync();
     float wd[NV][VEC], xh[NV][VEC], c1 = 0.f, c2 = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -503,13 +545,8 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
 #pragma unroll
       for (int i = 0; i < VEC; ++i) wd[v][i] = xh[v][i] = 0.f;
       if (c < a.H) {
-        if constexpr (ALIGNED) {
-          ln_unpack(*ln_slot<3, NV>(ring, stage, 0, v), wd[v]);
-          ln_unpack(*ln_slot<3, NV>(ring, stage, 1, v), xh[v]);
-        } else {
-          wd[v][0] = ln_ld(dy, t * a.lddy + c);
-          xh[v][0] = ln_ld(x, t * a.ldx + c);
-        }
+        dy.read(t, stage, v, c, wd[v]);
+        x.read(t, stage, v, c, xh[v]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           const float d = wd[v][i];
@@ -522,7 +559,7 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
         }
       }
     }
-    fetch(t + S * step, stage);  // the slots just read
+    if constexpr (MODE == kLnVector) fetch(t + S * step, stage);  // the slots just read
     c1 = ln_warp_sum(c1);
     c2 = ln_warp_sum(c2);
     if constexpr (WPR > 1) {
@@ -539,6 +576,12 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
       }
       par ^= 1;
     }
+    if constexpr (MODE == kLnShifted) {  // the group is through with the row before this one
+      if constexpr (WPR == 1) __syncwarp();
+      const int before = stage == 0 ? S - 1 : stage - 1;
+      fetch(t + (S - 1) * step, before);
+      fetch_skip(t + (S - 1) * step, before);
+    }
     c1 *= inv;
     c2 = a.rms ? 0.f : c2 * inv;
 #pragma unroll
@@ -548,22 +591,19 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
         float d[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) d[i] = rs * (wd[v][i] - c2 - xh[v][i] * c1);
-        if (dres) {
+        if (dres.p) {
           float q[VEC];
-          if constexpr (ALIGNED)
-            ln_unpack(*ln_slot<3, NV>(ring, stage, 2, v), q);
-          else
-            q[0] = ln_ld(dres, t * a.ldres + c);
+          dres.read(t, stage, v, c, q);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) d[i] += q[i];
         }
-        if constexpr (ALIGNED)
+        if constexpr (MODE == kLnVector)
           *reinterpret_cast<uint4*>(dx + t * a.H + c) = ln_pack(d);
         else
           ln_st(dx, t * a.H + c, d[0]);
       }
     }
-    fetch_skip(t + S * step, stage);
+    if constexpr (MODE == kLnVector) fetch_skip(t + S * step, stage);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
   // the block's partial rows: with a warp per row the eight warps' sums first, in order, through shared memory
@@ -571,7 +611,7 @@ __global__ void __launch_bounds__(kLnThreads, CPT == 32 ? 1 : 2) ln_bwd_kernel(c
   if constexpr (WPR == 1) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if constexpr (ALIGNED) cp_async_wait<0>();
+      if constexpr (MODE != kLnDirect) cp_async_wait<0>();
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -611,26 +651,47 @@ constexpr int kLnMaxH = 8192;
 static int ln_cpt(int64_t H) { return H <= 256 ? 8 : H <= 512 ? 16 : H <= 1024 ? 32 : H <= 2048 ? 8 : H <= 4096 ? 16 : 32; }
 static int ln_rows_per_block(int64_t H) { return H <= 1024 ? 8 : 1; }
 
-// Bytes of the ring: stages x tensors x a block's rows; the backward's also holds eight warps' column sums
-static size_t ln_ring(int stages, int tensors, int64_t H, int es) {
-  return (size_t)stages * tensors * kLnThreads * ln_cpt(H) * es;
+// Bytes of the ring.
+static size_t ln_ring(int mode, int stages, int tensors, int64_t H, int es) {
+  if (mode == kLnDirect) return 0;
+  if (mode == kLnVector) return (size_t)stages * tensors * kLnThreads * ln_cpt(H) * es;
+  return (size_t)stages * tensors * ln_rows_per_block(H) * ln_row_bytes((int)H, es);
+}
+
+// A kernel instance by mode and width.
+template <typename X>
+static LnFwdKernel ln_fwd_pick(int mode, int64_t H) {
+  return mode == kLnVector    ? LN_PICK(ln_fwd_kernel, X, kLnVector)
+         : mode == kLnShifted ? LN_PICK(ln_fwd_kernel, X, kLnShifted)
+                              : LN_PICK(ln_fwd_kernel, X, kLnDirect);
+}
+template <typename X>
+static LnBwdKernel ln_bwd_pick(int mode, int64_t H) {
+  return mode == kLnVector    ? LN_PICK(ln_bwd_kernel, X, kLnVector)
+         : mode == kLnShifted ? LN_PICK(ln_bwd_kernel, X, kLnShifted)
+                              : LN_PICK(ln_bwd_kernel, X, kLnDirect);
 }
 
 // Row groups of the backward's partial sums.
 static int ln_groups(int64_t T, int64_t H) {
   if (H > kLnMaxH) return (int)std::max<int64_t>(1, std::min<int64_t>(304, (T + 31) / 32));
-  const int rows = ln_rows_per_block(H);  // as many blocks as stay resident on 152 SMs
-  return (int)std::min<int64_t>(ln_cpt(H) == 32 ? 152 : 304, (T + rows - 1) / rows);
+  // as many blocks as stay resident on 152 SMs, four passes each at least: a partial row costs like a pass
+  const int rows = 4 * ln_rows_per_block(H);
+  return (int)std::min<int64_t>(152 * ln_bwd_blocks(ln_cpt(H)), (T + rows - 1) / rows);
 }
 
-static bool ln_vectors(int64_t H, int es, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> strides) {
+// How rows are read: see LnMode.  `in`: the row tensors read, `rest`: the other tensors that vectors would touch.
+static int ln_mode(int64_t H, int es, std::initializer_list<const void*> in, std::initializer_list<const void*> rest,
+                   std::initializer_list<int64_t> strides) {
   const int vec = 16 / es;
-  if (H % vec) return false;
-  for (const void* p : ptrs)
-    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  for (const void* p : in)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return kLnDirect;
+  if (H % vec) return kLnShifted;
+  for (const void* p : rest)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return kLnShifted;
   for (int64_t ld : strides)
-    if (ld % vec) return false;
-  return true;
+    if (ld % vec) return kLnShifted;
+  return kLnVector;
 }
 
 // Shared memory above what every kernel may have (48 KB, the static part included).
@@ -680,13 +741,13 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool b16 = x_dtype == MOE_DT_BF16;
   if (H <= kLnMaxH) {
-    const bool al = ln_vectors(H, b16 ? 2 : 4, {x, residual, y, sum, gamma, beta}, {ldx, ldr});
-    LnFwdKernel k = b16 ? (al ? LN_PICK(ln_fwd_kernel, uint16_t, true) : LN_PICK(ln_fwd_kernel, uint16_t, false))
-                        : (al ? LN_PICK(ln_fwd_kernel, float, true) : LN_PICK(ln_fwd_kernel, float, false));
-    const size_t smem = al ? ln_ring(ln_fwd_stages(b16 ? 2 : 4), 2, H, b16 ? 2 : 4) : 0;
+    const int es = b16 ? 2 : 4, mode = ln_mode(H, es, {x, residual}, {y, sum, gamma, beta}, {ldx, ldr});
+    const LnFwdKernel k = b16 ? ln_fwd_pick<uint16_t>(mode, H) : ln_fwd_pick<float>(mode, H);
+    const int blocks = ln_fwd_blocks(ln_cpt(H), es);
+    const size_t smem = ln_ring(mode, ln_stages(blocks, 2, ln_cpt(H), es), 2, H, es);
     if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem))) return rc;
     const int rows = ln_rows_per_block(H);
-    const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * ln_fwd_blocks(ln_cpt(H)));
+    const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * blocks);
     return launch_pdl(k, dim3((unsigned)grid), dim3(kLnThreads), smem, st, "layer_norm_fwd", a,
                       (int)(w_dtype == MOE_DT_BF16));
   }
@@ -733,17 +794,16 @@ extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void
               kind == MOE_NORM_RMS, ln_groups(T, H)};
   const int tiles = (int)((H + 31) / 32);
   auto weights = [&]() {
-    return launch_pdl(ln_bwd_reduce_kernel, dim3(tiles, dbeta ? 2 : 1), dim3(kLnThreads), 0, st,
+    return launch_pdl(ln_bwd_reduce_kernel, dim3(tiles, dbeta ? 2 : 1), dim3(kLnReduceThreads), 0, st,
                       "layer_norm_bwd weight gradients", static_cast<const float*>(a.part), a.G, (int)H, dgamma, dbeta,
                       accumulate);
   };
   if (H <= kLnMaxH) {
     const bool b16 = x_dtype == MOE_DT_BF16;
-    const bool al = ln_vectors(H, b16 ? 2 : 4, {dy, x, dres, dx, gamma}, {lddy, ldx, ldres});
-    LnBwdKernel k = b16 ? (al ? LN_PICK(ln_bwd_kernel, uint16_t, true) : LN_PICK(ln_bwd_kernel, uint16_t, false))
-                        : (al ? LN_PICK(ln_bwd_kernel, float, true) : LN_PICK(ln_bwd_kernel, float, false));
+    const int es = b16 ? 2 : 4, mode = ln_mode(H, es, {dy, x, dres}, {dx, gamma}, {lddy, ldx, ldres});
+    const LnBwdKernel k = b16 ? ln_bwd_pick<uint16_t>(mode, H) : ln_bwd_pick<float>(mode, H);
     const size_t sums = H <= 1024 ? sizeof(float) * kLnThreads * ln_cpt(H) : 0;
-    const size_t smem = std::max(al ? ln_ring(ln_bwd_stages(b16 ? 2 : 4), 3, H, b16 ? 2 : 4) : 0, sums);
+    const size_t smem = std::max(ln_ring(mode, ln_stages(ln_bwd_blocks(ln_cpt(H)), 3, ln_cpt(H), es), 3, H, es), sums);
     if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem)) ||
         (rc = launch_pdl(k, dim3(a.G), dim3(kLnThreads), smem, st, "layer_norm_bwd", a, (int)(w_dtype == MOE_DT_BF16))))
       return rc;

@@ -112,6 +112,34 @@ def test_backward(kind, dtype, T, H, how):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,pad,shift", [(5000, 200, 0, 0), (9001, 333, 0, 0), (4100, 1001, 3, 0), (3000, 1536, 8, 0),
+                                           (2500, 2049, 0, 0), (1300, 4095, 0, 0), (900, 6001, 1, 0), (3000, 771, 5, 1)])
+def test_many_rows(dtype, T, H, pad, shift):
+    """Many rows per block: every slot of the ring is filled again several times, in each way of reading rows
+    (vectors, rows that begin anywhere in a 16-byte piece, an unaligned base).  Against torch's float64 layer norm
+    and its automatic differentiation, with the bounds above."""
+    mb = _mb()
+    x, r, dy, dres = (_rand((T, H), dtype, k, H + pad, shift) for k in (1, 2, 5, 6))
+    gamma, beta = _rand((1, H), torch.float32, 3)[0], _rand((1, H), torch.float32, 4)[0]
+    f = mb.layer_norm_fwd(x, gamma, beta, eps=EPS, residual=r)
+    b = mb.layer_norm_bwd(dy, f["sum"], gamma, f["mean"], f["rstd"], dres=dres)
+    assert torch.equal(f["sum"], (x.float() + r.float()).to(dtype))
+    s64, g64, b64 = f["sum"].double().requires_grad_(), gamma.double().requires_grad_(), beta.double().requires_grad_()
+    y = torch.nn.functional.layer_norm(s64, (H,), g64, b64, EPS)
+    (y * dy.double()).sum().backward()
+    grow = (4 * H + 64) * U * 2
+    y, d = y.detach(), s64.grad + dres.double()
+    xh = (s64.detach() - f["mean"].double()[:, None]) * f["rstd"].double()[:, None]
+    assert torch.all((f["y"].double() - y).abs() <= grow * (xh.abs() * gamma.abs() + beta.abs() + 1) + _unit(dtype) * y.abs())
+    w = (dy.double() * gamma).abs()
+    parts = f["rstd"].double()[:, None] * (w + w.mean(1, keepdim=True) + (xh.abs() + 1) * (w * xh.abs()).mean(1, keepdim=True))
+    assert torch.all((b["dx"].double() - d).abs() <= grow * (parts + dres.double().abs()) + _unit(dtype) * d.abs())
+    rows = (T + 64) * U
+    assert torch.all((b["dgamma"].double() - g64.grad).abs() <= 2 * rows * (dy.double().abs() * (xh.abs() + 1)).sum(0))
+    assert torch.all((b["dbeta"].double() - b64.grad).abs() <= rows * dy.double().abs().sum(0))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_large_mean_and_constant_rows(dtype):
     """The variance is of differences from the mean: rows far from zero keep it, a constant row has rstd
     1 / sqrt(eps) and y = beta."""
