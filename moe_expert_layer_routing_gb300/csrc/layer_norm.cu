@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kLnReduceThreads) ln_bwd_reduce_kernel(const f
 // ------------------------------------------------------------------------------------------
 // Rows in registers
 // ------------------------------------------------------------------------------------------
-// A row belongs to a group of GT = 32 WPR threads (a warp, or the block of eight warps) and passes once: a
+// A row belongs to a group of GT = 32 WPR threads (one to all eight warps of the block) and passes once: a
 // thread holds CPT of its columns.  Blocks are persistent; rows come through a ring in shared memory by 16-byte
 // asynchronous copies, so the rows in flight cost no registers.
 //   vectors   rows and strides are multiples of 16 bytes: a thread holds NV vectors VEC wide (v GT + li of the
@@ -217,13 +217,13 @@ struct LnTile {
   static constexpr int GT = 32 * WPR;
   static constexpr int GROUPS = kLnThreads / GT;
   __device__ static int col(int v, int li) { return (v * GT + li) * VEC; }
-  __device__ static int group() { return WPR == 1 ? threadIdx.x >> 5 : 0; }
-  __device__ static int li() { return WPR == 1 ? threadIdx.x & 31 : threadIdx.x; }
-  __device__ static void sync() {
+  __device__ static int group() { return threadIdx.x / GT; }
+  __device__ static int li() { return threadIdx.x % GT; }
+  __device__ static void sync() {  // the group
     if constexpr (WPR == 1)
       __syncwarp();
     else
-      __syncthreads();
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group()), "n"(GT) : "memory");
   }
 };
 
@@ -340,14 +340,13 @@ __host__ __device__ constexpr int ln_stages(int blocks, int tensors, int cpt, in
 template <typename X, int CPT, int WPR, int MODE>
 __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT, sizeof(X))) ln_fwd_kernel(const LnFwdArgs a, int w_bf16) {
   using L = LnTile<X, CPT, WPR, MODE>;
-  constexpr bool KEEP = CPT <= 16;  // gamma and beta stay in registers
   constexpr int VEC = L::VEC, NV = L::NV, S = ln_stages(ln_fwd_blocks(CPT, sizeof(X)), 2, CPT, sizeof(X));
   extern __shared__ uint4 ring[];
   __shared__ float wn[8], wmean[2][8], wm2[2][8];
   const LnStream<X, CPT, WPR, MODE, 2> x{static_cast<const X*>(a.x), a.ldx, a.H, 0, reinterpret_cast<char*>(ring)};
   const LnStream<X, CPT, WPR, MODE, 2> r{static_cast<const X*>(a.r), a.ldr, a.H, 1, reinterpret_cast<char*>(ring)};
   X *y = static_cast<X*>(a.y), *sum = static_cast<X*>(a.sum);
-  const int li = L::li(), w = threadIdx.x >> 5;
+  const int li = L::li(), w = threadIdx.x >> 5, w0 = L::group() * WPR;
   const int64_t step = (int64_t)gridDim.x * L::GROUPS;
   const float inv = 1.f / (float)a.H;
   float n_w = 0.f;  // columns of this warp
@@ -360,17 +359,15 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT, sizeof(X))) ln_
   }
   pdl_wait();
   pdl_trigger();
-  float gk[KEEP ? NV : 1][VEC], bk[KEEP ? NV : 1][VEC];
-  if constexpr (KEEP) {
+  float gamma[NV][VEC], beta[NV][VEC];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = L::col(v, li);
+  for (int v = 0; v < NV; ++v) {
+    const int c = L::col(v, li);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) gk[v][i] = bk[v][i] = 0.f;
-      if (c < a.H) {
-        ln_weights<VEC>(a.gamma, w_bf16, c, gk[v]);
-        if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, bk[v]);
-      }
+    for (int i = 0; i < VEC; ++i) gamma[v][i] = beta[v][i] = 0.f;
+    if (c < a.H) {
+      ln_weights<VEC>(a.gamma, w_bf16, c, gamma[v]);
+      if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, beta[v]);
     }
   }
   auto fetch = [&](int64_t t, int stage) {
@@ -386,10 +383,10 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT, sizeof(X))) ln_
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
   int stage = 0, par = 0;
-  // a warp of its own leaves when its rows are through; a block's warps share t
+  // a group leaves when its rows are through
   for (; t < a.T; t += step) {
     float f[NV][VEC];
-    if constexpr (MODE == kLnShifted && WPR == 1) __syncwarp();  // the slot filled next is read by the whole warp
+    if constexpr (MODE == kLnShifted && WPR == 1) __syncwarp();  // the slot filled next was read by the whole group
     fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);  // the slot read last time round
     if constexpr (MODE != kLnDirect) cp_async_wait<S - 1>();
     if constexpr (MODE == kLnShifted) L::sync();
@@ -436,17 +433,17 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT, sizeof(X))) ln_
         wmean[par][w] = mu;
         wm2[par][w] = m2;
       }
-      __syncthreads();  // the buffers alternate: the next row's writes meet no reader of this one
+      L::sync();  // the buffers alternate: the next row's writes meet no reader of this one
       mu = m2 = 0.f;
       if (!a.rms) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mu = fmaf(wn[k], wmean[par][k], mu);
+        for (int k = 0; k < WPR; ++k) mu = fmaf(wn[w0 + k], wmean[par][w0 + k], mu);
         mu *= inv;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = wmean[par][k] - mu;
-        m2 += a.rms ? wm2[par][k] : fmaf(wn[k] * d, d, wm2[par][k]);
+      for (int k = 0; k < WPR; ++k) {
+        const float d = wmean[par][w0 + k] - mu;
+        m2 += a.rms ? wm2[par][w0 + k] : fmaf(wn[w0 + k] * d, d, wm2[par][w0 + k]);
       }
       par ^= 1;
     }
@@ -455,16 +452,8 @@ __global__ void __launch_bounds__(kLnThreads, ln_fwd_blocks(CPT, sizeof(X))) ln_
     for (int v = 0; v < NV; ++v) {
       const int c = L::col(v, li);
       if (c < a.H) {
-        if constexpr (KEEP) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) f[v][i] = fmaf((f[v][i] - mu) * rs, gk[v][i], bk[v][i]);
-        } else {
-          float g[VEC], b[VEC] = {};
-          ln_weights<VEC>(a.gamma, w_bf16, c, g);
-          if (a.beta) ln_weights<VEC>(a.beta, w_bf16, c, b);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) f[v][i] = fmaf((f[v][i] - mu) * rs, g[i], b[i]);
-        }
+        for (int i = 0; i < VEC; ++i) f[v][i] = fmaf((f[v][i] - mu) * rs, gamma[v][i], beta[v][i]);
         if constexpr (MODE == kLnVector)
           *reinterpret_cast<uint4*>(y + t * a.H + c) = ln_pack(f[v]);
         else
@@ -492,7 +481,7 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
   const LnStream<X, CPT, WPR, MODE, 3> x{static_cast<const X*>(a.x), a.ldx, a.H, 1, reinterpret_cast<char*>(ring)};
   const LnStream<X, CPT, WPR, MODE, 3> dres{static_cast<const X*>(a.dres), a.ldres, a.H, 2, reinterpret_cast<char*>(ring)};
   X* dx = static_cast<X*>(a.dx);
-  const int li = L::li(), w = threadIdx.x >> 5;
+  const int li = L::li(), w = threadIdx.x >> 5, w0 = L::group() * WPR;
   const int64_t step = (int64_t)gridDim.x * L::GROUPS;
   const float inv = 1.f / (float)a.H;
   pdl_wait();
@@ -567,12 +556,12 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
         r1[par][w] = c1;
         r2[par][w] = c2;
       }
-      __syncthreads();
+      L::sync();
       c1 = c2 = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        c1 += r1[par][k];
-        c2 += r2[par][k];
+      for (int k = 0; k < WPR; ++k) {
+        c1 += r1[par][w0 + k];
+        c2 += r2[par][w0 + k];
       }
       par ^= 1;
     }
@@ -606,9 +595,9 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
     if constexpr (MODE == kLnVector) fetch_skip(t + S * step, stage);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
-  // the block's partial rows: with a warp per row the eight warps' sums first, in order, through shared memory
+  // the block's partial rows: several groups' sums first, in order, through shared memory
   float* sm = reinterpret_cast<float*>(ring);
-  if constexpr (WPR == 1) {
+  if constexpr (WPR < 8) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if constexpr (MODE != kLnDirect) cp_async_wait<0>();
@@ -616,12 +605,12 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sm[w * (GT * CPT) + L::col(v, li) + i] = half ? ab[v][i] : ag[v][i];
+        for (int i = 0; i < VEC; ++i) sm[L::group() * (GT * CPT) + L::col(v, li) + i] = half ? ab[v][i] : ag[v][i];
       __syncthreads();
       for (int c = threadIdx.x; c < a.H; c += kLnThreads) {
         float q = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q += sm[k * (GT * CPT) + c];
+        for (int k = 0; k < L::GROUPS; ++k) q += sm[k * (GT * CPT) + c];
         a.part[((int64_t)half * a.G + blockIdx.x) * a.H + c] = q;
       }
     }
@@ -639,17 +628,18 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
   }
 }
 
-// Variants: a warp per row up to 1024 columns (8, 16 or 32 a thread), a block per row up to 8192.
+// Variants by width: 16 columns a thread and one, two, four or eight warps a row (8 columns up to 256, 32 above
+// 4096): narrower groups hold several rows of a block in flight, wider threads pay a row's sums over more columns.
 typedef void (*LnFwdKernel)(const LnFwdArgs, int);
 typedef void (*LnBwdKernel)(const LnBwdArgs, int);
 constexpr int kLnMaxH = 8192;
 
-#define LN_PICK(KERN, X, AL)                                                                        \
-  (H <= 256 ? KERN<X, 8, 1, AL> : H <= 512 ? KERN<X, 16, 1, AL> : H <= 1024 ? KERN<X, 32, 1, AL>    \
-   : H <= 2048 ? KERN<X, 8, 8, AL> : H <= 4096 ? KERN<X, 16, 8, AL> : KERN<X, 32, 8, AL>)
+#define LN_PICK(KERN, X, MODE)                                                                                     \
+  (H <= 256 ? KERN<X, 8, 1, MODE> : H <= 512 ? KERN<X, 16, 1, MODE> : H <= 1024 ? KERN<X, 16, 2, MODE>             \
+   : H <= 2048 ? KERN<X, 16, 4, MODE> : H <= 4096 ? KERN<X, 16, 8, MODE> : KERN<X, 32, 8, MODE>)
 
-static int ln_cpt(int64_t H) { return H <= 256 ? 8 : H <= 512 ? 16 : H <= 1024 ? 32 : H <= 2048 ? 8 : H <= 4096 ? 16 : 32; }
-static int ln_rows_per_block(int64_t H) { return H <= 1024 ? 8 : 1; }
+static int ln_cpt(int64_t H) { return H <= 256 ? 8 : H <= 4096 ? 16 : 32; }
+static int ln_rows_per_block(int64_t H) { return H <= 512 ? 8 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
 
 // Bytes of the ring.
 static size_t ln_ring(int mode, int stages, int tensors, int64_t H, int es) {
@@ -675,9 +665,11 @@ static LnBwdKernel ln_bwd_pick(int mode, int64_t H) {
 // Row groups of the backward's partial sums.
 static int ln_groups(int64_t T, int64_t H) {
   if (H > kLnMaxH) return (int)std::max<int64_t>(1, std::min<int64_t>(304, (T + 31) / 32));
-  // as many blocks as stay resident on 152 SMs, four passes each at least: a partial row costs like a pass
-  const int rows = 4 * ln_rows_per_block(H);
-  return (int)std::min<int64_t>(152 * ln_bwd_blocks(ln_cpt(H)), (T + rows - 1) / rows);
+  // as many blocks as stay resident on 152 SMs; above 64 of them four passes each at least, for a partial row costs
+  // about what a pass does
+  const int rows = ln_rows_per_block(H);
+  const int64_t fit = (T + rows - 1) / rows;
+  return (int)std::min<int64_t>(152 * ln_bwd_blocks(ln_cpt(H)), std::max<int64_t>(std::min<int64_t>(fit, 64), (fit + 3) / 4));
 }
 
 // How rows are read: see LnMode.  `in`: the row tensors read, `rest`: the other tensors that vectors would touch.
@@ -802,7 +794,7 @@ extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void
     const bool b16 = x_dtype == MOE_DT_BF16;
     const int es = b16 ? 2 : 4, mode = ln_mode(H, es, {dy, x, dres}, {dx, gamma}, {lddy, ldx, ldres});
     const LnBwdKernel k = b16 ? ln_bwd_pick<uint16_t>(mode, H) : ln_bwd_pick<float>(mode, H);
-    const size_t sums = H <= 1024 ? sizeof(float) * kLnThreads * ln_cpt(H) : 0;
+    const size_t sums = ln_rows_per_block(H) > 1 ? sizeof(float) * kLnThreads * ln_cpt(H) : 0;
     const size_t smem = std::max(ln_ring(mode, ln_stages(ln_bwd_blocks(ln_cpt(H)), 3, ln_cpt(H), es), 3, H, es), sums);
     if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem)) ||
         (rc = launch_pdl(k, dim3(a.G), dim3(kLnThreads), smem, st, "layer_norm_bwd", a, (int)(w_dtype == MOE_DT_BF16))))
