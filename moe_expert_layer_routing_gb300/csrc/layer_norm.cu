@@ -217,11 +217,14 @@ struct LnTile {
   static constexpr int GT = 32 * WPR;
   static constexpr int GROUPS = kLnThreads / GT;
   __device__ static int col(int v, int li) { return (v * GT + li) * VEC; }
-  __device__ static int group() { return threadIdx.x / GT; }
-  __device__ static int li() { return threadIdx.x % GT; }
+  // (told apart at compile time for a whole block: the division costs the row kernels registers they spill)
+  __device__ static int group() { return WPR == 8 ? 0 : threadIdx.x / GT; }
+  __device__ static int li() { return WPR == 8 ? threadIdx.x : threadIdx.x % GT; }
   __device__ static void sync() {  // the group
     if constexpr (WPR == 1)
       __syncwarp();
+    else if constexpr (WPR == 8)
+      __syncthreads();
     else
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group()), "n"(GT) : "memory");
   }
