@@ -313,6 +313,17 @@ __device__ __forceinline__ void ln_weights(const void* p, int bf16, int c, float
   }
 }
 
+// VEC consecutive fp32 values (16-byte stores when VEC > 1)
+template <int VEC>
+__device__ __forceinline__ void ln_store(float* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    p[0] = f[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  }
+}
+
 __device__ __forceinline__ float ln_warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -606,9 +617,7 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
       if constexpr (MODE != kLnDirect) cp_async_wait<0>();
       __syncthreads();
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sm[L::group() * (GT * CPT) + L::col(v, li) + i] = half ? ab[v][i] : ag[v][i];
+      for (int v = 0; v < NV; ++v) ln_store<VEC>(sm + L::group() * (GT * CPT) + L::col(v, li), half ? ab[v] : ag[v]);
       __syncthreads();
       for (int c = threadIdx.x; c < a.H; c += kLnThreads) {
         float q = 0.f;
@@ -621,12 +630,10 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = L::col(v, li);
-      if (c < a.H)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          a.part[(int64_t)blockIdx.x * a.H + c + i] = ag[v][i];
-          a.part[((int64_t)a.G + blockIdx.x) * a.H + c + i] = ab[v][i];
-        }
+      if (c < a.H) {
+        ln_store<VEC>(a.part + (int64_t)blockIdx.x * a.H + c, ag[v]);
+        ln_store<VEC>(a.part + ((int64_t)a.G + blockIdx.x) * a.H + c, ab[v]);
+      }
     }
   }
 }
@@ -668,11 +675,13 @@ static LnBwdKernel ln_bwd_pick(int mode, int64_t H) {
 // Row groups of the backward's partial sums.
 static int ln_groups(int64_t T, int64_t H) {
   if (H > kLnMaxH) return (int)std::max<int64_t>(1, std::min<int64_t>(304, (T + 31) / 32));
-  // as many blocks as stay resident on 152 SMs; above 64 of them four passes each at least, for a partial row costs
-  // about what a pass does
+  // A partial row costs about what a pass over a row does: a pass a block up to 64 blocks, two up to 256, four up to
+  // what stays resident on 152 SMs (512 x 4096: 9.7 us at 256 blocks, 11.2 at 128, 10.4 at 304; 1024 x 4096: 12.4 us
+  // at 256, 13.2 at 304).
   const int rows = ln_rows_per_block(H);
   const int64_t fit = (T + rows - 1) / rows;
-  return (int)std::min<int64_t>(152 * ln_bwd_blocks(ln_cpt(H)), std::max<int64_t>(std::min<int64_t>(fit, 64), (fit + 3) / 4));
+  const int64_t most = 152 * ln_bwd_blocks(ln_cpt(H));
+  return (int)std::min(most, std::max({std::min<int64_t>(fit, 64), std::min<int64_t>((fit + 1) / 2, 256), (fit + 3) / 4}));
 }
 
 // How rows are read: see LnMode.  `in`: the row tensors read, `rest`: the other tensors that vectors would touch.
