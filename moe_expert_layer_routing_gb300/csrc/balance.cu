@@ -104,12 +104,11 @@ __device__ __forceinline__ float lane_max(float v) {
   return v;
 }
 
-// e^(x - base) as 2^(x log2 e - base log2 e), b2 = base log2 e: one fused multiply-add and one exponential.  The
-// rounding of b2 is common to a row (it cancels in a probability and is below lse's own rounding).
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp_from(float x, float b2) {
+// e^(x - base): the difference first, so that logits of any magnitude keep it (a row of the type's lowest values
+// is a row of equal ones); results below 2^-126 are 0.
+__device__ __forceinline__ float exp_from(float x, float base) {
   float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x, kLog2e, -b2)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((x - base) * 1.4426950408889634f));
   return e;
 }
 
@@ -388,9 +387,22 @@ __global__ void __launch_bounds__(kBalThreads, NV <= 4 ? 3 : 1) router_fwd_kerne
     };
     int col[SLOTS];
     bool odd = false;
-    float m = -INFINITY;  // the row's maximum, or (top-K) one that differs from it in the dropped bits at most
+    // the tokens that need exact keys, done over
+    auto settle = [&]() {
+      const unsigned which_lanes = __ballot_sync(0xffffffffu, odd);
+      if (!which_lanes) return;
+      int ex[SLOTS];
+      topk_exact<NV, LANES, VEC, SLOTS>(row, a.E, a.K, sl, live, ex);
+      const unsigned mine = (LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u)) << (LANES * seg);
+      if (which_lanes & mine) {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) col[s] = ex[s];
+      }
+    };
+    float m = -INFINITY;  // the row's maximum
     if constexpr (TOPK) {
       odd = topk_packed<NV, LANES, SLOTS, HOW == kTopKList>(v, logit, a.E, a.K, sl, live, col);
+      settle();
       if (live && sl == 0) m = logit(col[0]);
       m = __shfl_sync(0xffffffffu, m, 0, LANES);
       if constexpr (VEC) {  // read again rather than kept through the selection: registers
@@ -402,11 +414,11 @@ __global__ void __launch_bounds__(kBalThreads, NV <= 4 ? 3 : 1) router_fwd_kerne
       for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
       m = lane_max<LANES>(m);
     }
-    const float base = m == -INFINITY ? 0.f : m, b2 = base * kLog2e;
+    const float base = m == -INFINITY ? 0.f : m;
     float total = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      v[j] = exp_from(v[j], b2);
+      v[j] = exp_from(v[j], base);
       total += v[j];
     }
     total = lane_sum<LANES>(total);
@@ -419,22 +431,14 @@ __global__ void __launch_bounds__(kBalThreads, NV <= 4 ? 3 : 1) router_fwd_kerne
       if (total != 0.f) z = fmaf(lse, lse, z);
     }
     if constexpr (TOPK) {
-      odd |= total != total;  // NaN or +inf among the logits
-      if (__any_sync(0xffffffffu, odd)) {
-        int ex[SLOTS];
-        topk_exact<NV, LANES, VEC, SLOTS>(row, a.E, a.K, sl, live, ex);
-        const unsigned mine = (LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u)) << (LANES * seg);
-        if (__ballot_sync(0xffffffffu, odd) & mine) {
-#pragma unroll
-          for (int s = 0; s < SLOTS; ++s) col[s] = ex[s];
-        }
-      }
+      odd = total != total;  // NaN or +inf among the logits
+      settle();
       float x[SLOTS], e[SLOTS], sum = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
         x[s] = live && s * LANES + sl < a.K ? logit(col[s]) : -INFINITY;
         if (x[s] == -INFINITY) col[s] = -1;  // a masked expert takes no slot
-        e[s] = exp_from(x[s], b2);
+        e[s] = exp_from(x[s], base);
         sum += e[s];
       }
       sum = lane_sum<LANES>(sum);
@@ -565,7 +569,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_reduce_kernel(const Balan
     }
     const float n = (float)max(seg_start(a, a.S + 1) - seg_start(a, 1), 1);
     a.loss[0] = a.alpha * (float)a.E / ((float)a.K * n) * lb;
-    a.loss[1] = a.beta / n * lz;
+    a.loss[1] = a.beta != 0.f ? a.beta / n * lz : 0.f;  // (lse^2 may be infinite)
   }
 }
 
@@ -602,12 +606,22 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
       for (int j = 0; j < N; ++j) b[j] = 0.f;
     }
     const bool none = lse == -INFINITY;  // nothing left by the mask, or a padding token
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = none ? 0.f : exp_from(v[j], lse);
+    // p = e^(l - lse) sums to 1 within lse's rounding, 2^-24 |lse|; where that shows, p is divided by its sum (finite
+    // masks in a whole row lose all of lse's fraction)
+    if (__any_sync(0xffffffffu, !none && !(fabsf(lse) < 16.f))) {
+      float total = 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) total += v[j];
+      total = lane_sum<LANES>(total);
+      const float inv = none ? 0.f : __fdividef(1.f, total);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] *= inv;
+    }
     float dot = 0.f;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] = none ? 0.f : exp_from(v[j], lse * kLog2e);
-      dot = fmaf(cnt[j], v[j], dot);
-    }
+    for (int j = 0; j < N; ++j) dot = fmaf(cnt[j], v[j], dot);
     dot = lane_sum<LANES>(dot);
     const float zt = none ? 0.f : wz * lse;
 #pragma unroll
@@ -786,6 +800,11 @@ static int router_entry(const char* who, bool topk, int mode, int renorm, const 
   if (T == 0) return stats ? balance_empty(E, num_seq, counts, prob_sum, loss, st) : MOE_OK;
   if (!logits || !ids || (topk && !scores)) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
   if (ld_logits < E) return fail(MOE_ERR_INVALID, "%s: row stride below E", who);
+  for (const void* p : {static_cast<const void*>(logits), static_cast<const void*>(seg_offsets),
+                        static_cast<const void*>(scores), static_cast<const void*>(ids), static_cast<const void*>(lse),
+                        static_cast<const void*>(counts), static_cast<const void*>(prob_sum),
+                        static_cast<const void*>(loss), static_cast<const void*>(status_dev)})
+    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(MOE_ERR_INVALID, "%s: tensors must be 4-byte aligned", who);
   const BalLayout L = bal_layout(T, K, E, num_seq);
   if (stats) {
     if (!workspace) return fail(MOE_ERR_INVALID, "%s: null pointer", who);
@@ -845,6 +864,12 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   if (T == 0) return status_dev ? cuda_check(cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st), "memset status") : MOE_OK;
   if (!logits || !lse || !counts || !dlogits) return fail(MOE_ERR_INVALID, "moe_balance_bwd: null pointer");
   if (ld_logits < E || (add && ld_add < E)) return fail(MOE_ERR_INVALID, "moe_balance_bwd: row stride below E");
+  for (const void* p : {static_cast<const void*>(logits), static_cast<const void*>(lse), static_cast<const void*>(counts),
+                        static_cast<const void*>(seg_offsets), static_cast<const void*>(dloss),
+                        static_cast<const void*>(add), static_cast<const void*>(dlogits),
+                        static_cast<const void*>(status_dev)})
+    if (reinterpret_cast<uintptr_t>(p) & 3)
+      return fail(MOE_ERR_INVALID, "moe_balance_bwd: tensors must be 4-byte aligned");
   const int lanes = bal_bwd_lanes(E), nv = (E + 4 * lanes - 1) / (4 * lanes);
   BalanceArgs a{};
   a.logits = logits;

@@ -176,6 +176,37 @@ def test_nan_and_infinite_logits():
     assert np64(plain["scores"])[2, 0] == np.inf and set(plain) == {"scores", "ids", "lse"}
 
 
+LOWEST = float(np.finfo(np.float32).min)
+
+
+@pytest.mark.parametrize("mask", [LOWEST, -1e9, -1e30])
+def test_finite_masks_and_huge_logits(mask):
+    """Experts masked with a large negative number instead of -inf, rows with nothing else (then uniform: the mask is a
+    value like any other), and logits so large that neighbours differ by more than e^88 of each other."""
+    mb = _mb()
+    T, E, K = 60, 24, 4
+    lg = _logits(T, E, 5, special=False)
+    lg[::3, 5:] = mask
+    lg[7] = mask
+    lg[8] = np.arange(E, dtype=np.float32)[::-1] * 3e6
+    lg[9] = 1e7 + np.arange(E, dtype=np.float32) * 3
+    lg[10] = -1e7 + np.arange(E, dtype=np.float32)[::-1]
+    out = mb.router_fwd(0, _dev(lg), K, alpha=A, beta=0.0)
+    g = mb.balance_bwd(_dev(lg), out["lse"], out["counts"], K, alpha=A, beta=0.0)
+    torch.cuda.synchronize()
+    ids = ob.topk(lg, K)
+    assert np.array_equal(out["ids"].cpu().numpy(), ids)
+    s = ob.scores(0, lg, ids)
+    tol = (E + 64 + 8 * 30) * U      # differences are exact or beyond e^-88 here: 30 covers the ordinary rows' range
+    assert np.all(np.abs(np64(out["scores"]) - s) <= tol * s + 1e-37)
+    ref = ob.losses(lg, ids, A, 0.0)
+    assert np.all(np.abs(np64(out["prob_sum"]) - ref["prob_sum"]) <= (T * U + tol) * ref["prob_sum"] + 1e-37)
+    assert abs(float(out["loss"][0]) - ref["loss"][0]) <= 2 * (T * U + tol) * ref["loss"][0] and float(out["loss"][1]) == 0.0
+    want = ob.gradient(lg, ref["counts"], K, A, 0.0)
+    lim = A * E / (K * T * T) * ref["counts"].max() * 2
+    assert np.all(np.abs(np64(g) - want) <= 4 * tol * lim)
+
+
 def test_bad_offsets_are_reported_and_stay_in_bounds():
     mb = _mb()
     T, E, K = 500, 16, 2

@@ -195,10 +195,10 @@ def test_accumulate_repeats_and_streams():
     assert torch.equal(b["dgamma"], ga) and torch.equal(b["dbeta"], ba)
 
 
-def test_residual_stream_updated_in_place():
+@pytest.mark.parametrize("T,H", [(5, 640), (700, 333), (2000, 2048)])
+def test_residual_stream_updated_in_place(T, H):
     """sum may be x or the residual themselves (C entry point)."""
     mb = _mb()
-    T, H = 5, 640
     x, r = _rand((T, H), torch.bfloat16, 1), _rand((T, H), torch.bfloat16, 2)
     gamma = torch.ones(H, device="cuda")
     ref = mb.layer_norm_fwd(x, gamma, gamma, residual=r)
