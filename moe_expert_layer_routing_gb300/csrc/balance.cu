@@ -25,7 +25,7 @@ namespace moebwd {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalStages = 2;
+constexpr int kBalStages = 2, kBalBwdStages = 2;
 
 struct BalanceArgs {
   const float* logits;
@@ -593,17 +593,61 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
     const int c = 4 * (LANES * (j >> 2) + sl) + (j & 3);
     cnt[j] = !pad && c < a.E ? (float)a.counts[(int64_t)(which - 1) * a.E + c] : 0.f;
   }
+  // VEC: logits and `add` come through a ring of rows by 16-byte asynchronous copies, each lane's own
+  extern __shared__ float4 ring[];
+  auto slot = [&](int stage, int tensor, int j) { return ring + ((stage * 2 + tensor) * NV + j) * kBalThreads + threadIdx.x; };
+  auto fetch = [&](int t, int stage) {
+    if constexpr (VEC) {
+      if (t < hi) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = 4 * (LANES * j + sl);
+          if (c < a.E) {
+            if (!pad) cp_async_16(smem_u32(slot(stage, 0, j)), a.logits + (int64_t)t * a.ld + c);
+            if (a.add) cp_async_16(smem_u32(slot(stage, 1, j)), a.add + (int64_t)t * a.ld_add + c);
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kBalBwdStages - 1; ++s) fetch(lo + (w + s * kBalWarps) * SEGS + seg, s);
+  float ahead = -INFINITY;  // lse of the next pass's token
+  {
+    const int t = lo + w * SEGS + seg;
+    if (t < hi && !pad) ahead = a.lse[t];
+  }
+  int stage = 0;
   for (int tb = lo + w * SEGS; tb < hi; tb += kBalWarps * SEGS) {
     const int t = tb + seg;
     const bool live = t < hi;
     float v[N], b[N];
-    const float lse = live && !pad ? a.lse[t] : -INFINITY;
-    load_row<NV, LANES, VEC>(a.logits + (int64_t)t * a.ld, a.E, sl, live && !pad, v);
-    if (a.add) {
-      load_row<NV, LANES, VEC>(a.add + (int64_t)t * a.ld_add, a.E, sl, live, b);
-    } else {
+    const float lse = ahead;
+    {
+      const int n = t + kBalWarps * SEGS;
+      ahead = n < hi && !pad ? a.lse[n] : -INFINITY;
+    }
+    if constexpr (VEC) {
+      fetch(t + (kBalBwdStages - 1) * kBalWarps * SEGS, stage == 0 ? kBalBwdStages - 1 : stage - 1);
+      cp_async_wait<kBalBwdStages - 1>();
 #pragma unroll
-      for (int j = 0; j < N; ++j) b[j] = 0.f;
+      for (int j = 0; j < NV; ++j) {
+        const bool in = live && 4 * (LANES * j + sl) < a.E;
+        const float4 f = in && !pad ? *slot(stage, 0, j) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        const float4 g = in && a.add ? *slot(stage, 1, j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[4 * j] = f.x; v[4 * j + 1] = f.y; v[4 * j + 2] = f.z; v[4 * j + 3] = f.w;
+        b[4 * j] = g.x; b[4 * j + 1] = g.y; b[4 * j + 2] = g.z; b[4 * j + 3] = g.w;
+      }
+      stage = stage + 1 == kBalBwdStages ? 0 : stage + 1;
+    } else {
+      load_row<NV, LANES, VEC>(a.logits + (int64_t)t * a.ld, a.E, sl, live && !pad, v);
+      if (a.add) {
+        load_row<NV, LANES, VEC>(a.add + (int64_t)t * a.ld_add, a.E, sl, live, b);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) b[j] = 0.f;
+      }
     }
     const bool none = lse == -INFINITY;  // nothing left by the mask, or a padding token
 #pragma unroll
@@ -645,14 +689,20 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
 // Lanes per token: 8 for up to 128 experts and K <= 8, 16 for up to 256 and K <= 16, else a warp (16 logits a lane;
 // 32 above 512 experts).
 static int bal_lanes(int K, int E) { return E <= 128 && K <= 8 ? 8 : E <= 256 && K <= 16 ? 16 : 32; }
-// The gradient keeps no keys and no slots: up to 32 logits a lane (131072 x 256 experts: 69 us, 76 us at 16 a lane).
-static int bal_bwd_lanes(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+// The gradient keeps no slots.
+static int bal_bwd_lanes(int E) { return E <= 128 ? 8 : E <= 256 ? 16 : 32; }
 
-// Tokens per chunk: one pass of a CTA's warps, more where that would be over four CTAs per SM.
-static int bal_chunk(int T, int lanes) {
+// Tokens per chunk, in passes of a CTA's warps.  Forward: one pass, more where the CTAs would not all be resident at
+// once (three on an SM): a CTA leaves E partial sums.  Gradient: two passes, more where the CTAs would be over three
+// times that (131072 x 256: 63.8 us, 66.7 us resident at once).
+static int64_t bal_passes(int T, int lanes, int64_t most) {
   const int step = kBalThreads / lanes;
-  const int64_t steps = ((int64_t)T + step - 1) / step, most = 3 * 152 - 8;
-  return (int)((steps + most - 1) / most) * step;
+  return (((int64_t)T + step - 1) / step + most - 1) / most;
+}
+static int bal_chunk(int T, int lanes) { return (int)bal_passes(T, lanes, 3 * 152 - 8) * (kBalThreads / lanes); }
+static int bal_bwd_chunk(int T, int lanes) {
+  return (int)std::max(bal_passes(T, lanes, 9 * 152 - 24), std::min<int64_t>(2, bal_passes(T, lanes, 3 * 152 - 8))) *
+         (kBalThreads / lanes);
 }
 
 static int bal_pieces(int T, int C, int S) { return (int)(((int64_t)T + C - 1) / C) + S + 1; }
@@ -730,9 +780,8 @@ static BalKernel bwd_kernel(int lanes, int nv) {
   if (lanes == 8)
     return nv <= 1   ? balance_bwd_kernel<1, 8, VEC>
            : nv <= 2 ? balance_bwd_kernel<2, 8, VEC>
-           : nv <= 4 ? balance_bwd_kernel<4, 8, VEC>
-                     : balance_bwd_kernel<8, 8, VEC>;
-  return lanes == 16 ? balance_bwd_kernel<8, 16, VEC> : balance_bwd_kernel<8, 32, VEC>;
+                     : balance_bwd_kernel<4, 8, VEC>;
+  return lanes == 16 ? balance_bwd_kernel<4, 16, VEC> : nv <= 4 ? balance_bwd_kernel<4, 32, VEC> : balance_bwd_kernel<8, 32, VEC>;
 }
 
 // Both forward entry points: the top-K (scores given) or the caller's ids, with or without the losses.
@@ -879,7 +928,7 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   a.E = E;
   a.off = seg_offsets;
   a.S = num_seq;
-  a.C = bal_chunk(T, lanes);
+  a.C = bal_bwd_chunk(T, lanes);
   a.pieces = bal_pieces(T, a.C, num_seq);
   a.alpha = alpha;
   a.beta = beta;
@@ -893,5 +942,11 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   const bool vec = E % 4 == 0 && ld_logits % 4 == 0 && (!add || ld_add % 4 == 0) &&
                    ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(add) |
                      reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
-  return launch_pdl((vec ? bwd_kernel<true>(lanes, nv) : bwd_kernel<false>(lanes, nv)), dim3(a.pieces), dim3(kBalThreads), 0, st, "balance_bwd", a);
+  const BalKernel kern = vec ? bwd_kernel<true>(lanes, nv) : bwd_kernel<false>(lanes, nv);
+  const int groups = nv <= 1 ? 1 : nv <= 2 && lanes == 8 ? 2 : nv <= 4 ? 4 : 8;
+  const size_t smem = vec ? sizeof(float4) * kBalBwdStages * 2 * groups * kBalThreads : 0;
+  if (smem > 40 * 1024 && (rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                                           "cudaFuncSetAttribute(balance_bwd)")))
+    return rc;
+  return launch_pdl(kern, dim3(a.pieces), dim3(kBalThreads), smem, st, "balance_bwd", a);
 }
