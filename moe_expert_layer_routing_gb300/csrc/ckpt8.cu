@@ -65,10 +65,27 @@ __device__ __forceinline__ int64_t sf_offset(int64_t bu, int tpb_shift, int tb, 
   return ((((bu << tpb_shift) + tb) * (I >> 5) + (f >> 5)) * 4 + g) * 32 + (f & 31);
 }
 
-// act(g) of the forward: SiLU(g) = g / (1 + e^-g), or GELU(g) = g Phi(g)
-__device__ __forceinline__ float glu_act(float g, int glu) {
-  if (glu == MOE_GLU_GEGLU) return g * (0.5f * (1.f + erff(g * 0.70710678118654752f)));
-  return __fdividef(g, 1.f + __expf(-g));
+// a = act(g) u scaled by sv, for two (gate, up) pairs: SiLU(g) = g / (1 + e^-g) in paired arithmetic, with the
+// exponential as 2^(-g log2 e) and the approximate reciprocal (2^-22 of the value each); or GELU(g) = g Phi(g).
+__device__ __forceinline__ uint32_t glu_pair(uint32_t gw, uint32_t uw, float sv, int glu) {
+  const uint64_t g = f2_pack(__uint_as_float(gw << 16), __uint_as_float(gw & 0xffff0000u));
+  const uint64_t u = f2_pack(__uint_as_float(uw << 16), __uint_as_float(uw & 0xffff0000u));
+  uint64_t act;
+  float x0, x1, y0, y1;
+  if (glu == MOE_GLU_GEGLU) {
+    f2_unpack(g, x0, x1);
+    act = f2_pack(x0 * (0.5f * (1.f + erff(x0 * 0.70710678118654752f))), x1 * (0.5f * (1.f + erff(x1 * 0.70710678118654752f))));
+  } else {
+    f2_unpack(f2_mul(g, f2_splat(-1.4426950408889634f)), x0, x1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(x0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(x1));
+    f2_unpack(f2_add(f2_pack(y0, y1), f2_splat(1.f)), x0, x1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(x0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(x1));
+    act = f2_mul(g, f2_pack(y0, y1));
+  }
+  f2_unpack(f2_mul(f2_mul(act, u), f2_splat(sv)), x0, x1);
+  return pack_bf16x2(x0, x1);
 }
 
 // Per half, max |x| over 32 words of two bf16 values each; a NaN or an infinity gives an exponent field of 255.
@@ -138,11 +155,7 @@ __device__ __forceinline__ void glu_tile(const GluArgs& p, int t, int f0, int64_
     }
     uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float a0 = glu_act(__uint_as_float(g[k] << 16), p.glu) * __uint_as_float(u[k] << 16);
-      const float a1 = glu_act(__uint_as_float(g[k] & 0xffff0000u), p.glu) * __uint_as_float(u[k] & 0xffff0000u);
-      o[k] = pack_bf16x2(sv * a0, sv * a1);
-    }
+    for (int k = 0; k < 4; ++k) o[k] = glu_pair(g[k], u[k], sv, p.glu);
     *reinterpret_cast<uint4*>(p.a + (r0 + r) * (int64_t)p.I + f0 + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
   }
   if (!p.q) return;
