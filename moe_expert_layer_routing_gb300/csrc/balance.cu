@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kBalThreads) balance_reduce_kernel(const Balan
   __shared__ int sc[kBalWarps][32];
   __shared__ bool last;
   pdl_wait();
-  pdl_trigger();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.x, col = blockIdx.y * 32 + lane, tiles = gridDim.y;
   const int b0 = seg_start(a, s + 1), b1 = seg_start(a, s + 2);

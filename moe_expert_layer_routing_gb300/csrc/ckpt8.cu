@@ -256,8 +256,7 @@ __global__ void __launch_bounds__(kGluThreads) ckpt8_unpack_kernel(const UnpackA
   constexpr int COLS = 2 * kGluFeat;
   __shared__ __align__(16) uint32_t code[COLS][kGluRows / 4];
   __shared__ __align__(16) float scale[4][COLS];
-  pdl_wait();
-  pdl_trigger();
+  pdl_wait();  // (no early trigger: blocks of a persistent successor waiting beside this kernel's last ones cost 3%)
   const uint32_t chunks = p.I / kGluFeat;
   const int t = (int)(blockIdx.x / chunks);
   const int f0 = (int)(blockIdx.x - t * chunks) * kGluFeat;

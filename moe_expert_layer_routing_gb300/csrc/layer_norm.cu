@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(kLnReduceThreads) ln_bwd_reduce_kernel(const f
                                                                          float* dbeta, int accumulate) {
   __shared__ float red[32][33];
   pdl_wait();
-  pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? dbeta : dgamma;
