@@ -431,8 +431,8 @@ int moe_balance_bwd(const float* logits, int64_t ld_logits, const float* lse, co
  *   [N,2,B/128,I/32,4,32] (128-slot tile, 32 features, 32-slot group, feature).  32 consecutive slots of one
  *   feature share byte = max(1, exponent field of their largest magnitude - 6); a code is
  *   round-to-nearest-even(v 2^(127-byte)) clamped to +-127 and stands for code 2^(byte-127), so a value is off
- *   by at most half a step, 1/128 of the group's largest magnitude (a step where the clamp acts; groups whose
- *   largest magnitude is under 2^-120 keep the step 2^-126).  A group holding a NaN or an infinity gets byte
+ *   by at most half a step, 1/128 of the group's largest magnitude (groups whose largest magnitude is under
+ *   2^-120 keep the step 2^-126).  A group holding a NaN or an infinity gets byte
  *   255 and reads as NaN (in moe_bwd NaN or infinite).  Slots of a 128-slot tile behind the expert's last row
  *   are zeros; tiles without a row are not written.
  * I a multiple of 64 (moe_bwd: of 128); tensors 16-byte aligned.  rows = 0: nothing is written. */
