@@ -17,7 +17,7 @@
 // 311 us (6.9 TB/s).  Three passes over each row with the caches' help had taken 747 and 1376 us.  Few rows are
 // bound by latency: 2.7 us (forward) and 5 us (backward, two kernels) for 1 to 64 rows.  Rows that are not whole
 // 16-byte pieces are bound by the shared-memory and store instructions of their single elements: fp32 32768 x 1111
-// at 3.2 to 3.7 TB/s, 16384 x 3001 at 5.1 to 5.9, bf16 (2-byte elements) 32768 x 3001 at 3.0 to 3.4 TB/s.
+// at 3.7 to 4.0 TB/s, 16384 x 3001 at 5.4, bf16 (2-byte elements) 32768 x 3001 at 3.6 to 3.8 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -348,7 +348,7 @@ __device__ __forceinline__ void LnStream<X, CPT, WPR, MODE, TENSORS>::read(int64
 }
 
 // Resident blocks (registers) and rows of the ring, as many as 192 KB an SM hold.
-__host__ __device__ constexpr int ln_fwd_blocks(int cpt, int es) { return cpt == 8 ? 4 : cpt == 16 ? 3 : es == 2 ? 2 : 1; }
+__host__ __device__ constexpr int ln_fwd_blocks(int cpt, int es) { return cpt == 8 ? 4 : cpt <= 16 ? 3 : es == 2 ? 2 : 1; }
 __host__ __device__ constexpr int ln_bwd_blocks(int cpt) { return cpt == 32 ? 1 : 2; }
 __host__ __device__ constexpr int ln_stages(int blocks, int tensors, int cpt, int es) {
   return 196608 / (blocks * tensors * kLnThreads * cpt * es) > 6 ? 6 : 196608 / (blocks * tensors * kLnThreads * cpt * es);
@@ -656,13 +656,22 @@ constexpr int kLnMaxH = 8192;
   (H <= 256 ? KERN<X, 8, 1, MODE> : H <= 512 ? KERN<X, 16, 1, MODE> : H <= 1024 ? KERN<X, 16, 2, MODE>             \
    : H <= 2048 ? KERN<X, 16, 4, MODE> : H <= 4096 ? KERN<X, 16, 8, MODE> : KERN<X, 32, 8, MODE>)
 
-static int ln_cpt(int64_t H) { return H <= 256 ? 8 : H <= 4096 ? 16 : 32; }
+// Shifted rows pay per element: 12 columns a thread where they reach (32768 x 3001 bf16: backward 267 -> 217 us,
+// forward 235 -> 209 us; 65536 x 333: 62 -> 54 and 51 -> 44 us).
+static bool ln_twelve(int64_t H, int mode) {
+  return mode == kLnShifted && ((H > 256 && H <= 384) || (H > 512 && H <= 768) || (H > 1024 && H <= 1536) || (H > 2048 && H <= 3072));
+}
+#define LN_PICK_SHIFTED(KERN, X)                                                                                   \
+  (!ln_twelve(H, kLnShifted) ? LN_PICK(KERN, X, kLnShifted) : H <= 384 ? KERN<X, 12, 1, kLnShifted>                \
+   : H <= 768 ? KERN<X, 12, 2, kLnShifted> : H <= 1536 ? KERN<X, 12, 4, kLnShifted> : KERN<X, 12, 8, kLnShifted>)
+
+static int ln_cpt(int64_t H, int mode) { return ln_twelve(H, mode) ? 12 : H <= 256 ? 8 : H <= 4096 ? 16 : 32; }
 static int ln_rows_per_block(int64_t H) { return H <= 512 ? 8 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
 
 // Bytes of the ring.
 static size_t ln_ring(int mode, int stages, int tensors, int64_t H, int es) {
   if (mode == kLnDirect) return 0;
-  if (mode == kLnVector) return (size_t)stages * tensors * kLnThreads * ln_cpt(H) * es;
+  if (mode == kLnVector) return (size_t)stages * tensors * kLnThreads * ln_cpt(H, mode) * es;
   return (size_t)stages * tensors * ln_rows_per_block(H) * ln_row_bytes((int)H, es);
 }
 
@@ -670,13 +679,13 @@ static size_t ln_ring(int mode, int stages, int tensors, int64_t H, int es) {
 template <typename X>
 static LnFwdKernel ln_fwd_pick(int mode, int64_t H) {
   return mode == kLnVector    ? LN_PICK(ln_fwd_kernel, X, kLnVector)
-         : mode == kLnShifted ? LN_PICK(ln_fwd_kernel, X, kLnShifted)
+         : mode == kLnShifted ? LN_PICK_SHIFTED(ln_fwd_kernel, X)
                               : LN_PICK(ln_fwd_kernel, X, kLnDirect);
 }
 template <typename X>
 static LnBwdKernel ln_bwd_pick(int mode, int64_t H) {
   return mode == kLnVector    ? LN_PICK(ln_bwd_kernel, X, kLnVector)
-         : mode == kLnShifted ? LN_PICK(ln_bwd_kernel, X, kLnShifted)
+         : mode == kLnShifted ? LN_PICK_SHIFTED(ln_bwd_kernel, X)
                               : LN_PICK(ln_bwd_kernel, X, kLnDirect);
 }
 
@@ -688,7 +697,7 @@ static int ln_groups(int64_t T, int64_t H) {
   // at 256, 13.2 at 304).
   const int rows = ln_rows_per_block(H);
   const int64_t fit = (T + rows - 1) / rows;
-  const int64_t most = 152 * ln_bwd_blocks(ln_cpt(H));
+  const int64_t most = 152 * ln_bwd_blocks(ln_cpt(H, kLnVector));  // (the same in every mode)
   return (int)std::min(most, std::max({std::min<int64_t>(fit, 64), std::min<int64_t>((fit + 1) / 2, 256), (fit + 3) / 4}));
 }
 
@@ -755,8 +764,8 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
   if (H <= kLnMaxH) {
     const int es = b16 ? 2 : 4, mode = ln_mode(H, es, {x, residual}, {y, sum, gamma, beta}, {ldx, ldr});
     const LnFwdKernel k = b16 ? ln_fwd_pick<uint16_t>(mode, H) : ln_fwd_pick<float>(mode, H);
-    const int blocks = ln_fwd_blocks(ln_cpt(H), es);
-    const size_t smem = ln_ring(mode, ln_stages(blocks, 2, ln_cpt(H), es), 2, H, es);
+    const int cpt = ln_cpt(H, mode), blocks = ln_fwd_blocks(cpt, es);
+    const size_t smem = ln_ring(mode, ln_stages(blocks, 2, cpt, es), 2, H, es);
     if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem))) return rc;
     const int rows = ln_rows_per_block(H);
     const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * blocks);
@@ -814,8 +823,9 @@ extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void
     const bool b16 = x_dtype == MOE_DT_BF16;
     const int es = b16 ? 2 : 4, mode = ln_mode(H, es, {dy, x, dres}, {dx, gamma}, {lddy, ldx, ldres});
     const LnBwdKernel k = b16 ? ln_bwd_pick<uint16_t>(mode, H) : ln_bwd_pick<float>(mode, H);
-    const size_t sums = ln_rows_per_block(H) > 1 ? sizeof(float) * kLnThreads * ln_cpt(H) : 0;
-    const size_t smem = std::max(ln_ring(mode, ln_stages(ln_bwd_blocks(ln_cpt(H)), 3, ln_cpt(H), es), 3, H, es), sums);
+    const int cpt = ln_cpt(H, mode);
+    const size_t sums = ln_rows_per_block(H) > 1 ? sizeof(float) * kLnThreads * cpt : 0;
+    const size_t smem = std::max(ln_ring(mode, ln_stages(ln_bwd_blocks(cpt), 3, cpt, es), 3, H, es), sums);
     if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem)) ||
         (rc = launch_pdl(k, dim3(a.G), dim3(kLnThreads), smem, st, "layer_norm_bwd", a, (int)(w_dtype == MOE_DT_BF16))))
       return rc;
