@@ -625,10 +625,10 @@ def ckpt8_sf_shape(N: int, I: int, block_size: int) -> tuple:
 
 
 def _meta_ptrs(route_meta, dev):
-    eo, bo, b2e = (route_meta[k] for k in ("expert_offsets", "block_offsets", "block_to_expert"))
-    E = eo.numel() - 1
+    eo, bo, b2e = route_meta["expert_offsets"], route_meta["block_offsets"], route_meta["block_to_expert"]
+    E, N = eo.numel() - 1, b2e.numel()
     return (_dense(eo, torch.int32, (E + 1,), "expert_offsets", dev), _dense(bo, torch.int32, (E + 1,), "block_offsets", dev),
-            _dense(b2e, torch.int32, (b2e.numel(),), "block_to_expert", dev), E, b2e.numel())
+            _dense(b2e, torch.int32, (N,), "block_to_expert", dev), E, N)
 
 
 def glu_fwd(h: torch.Tensor, route_meta: dict, block_size: int, glu: int = GLU_SWIGLU,
@@ -657,8 +657,10 @@ def glu_fwd(h: torch.Tensor, route_meta: dict, block_size: int, glu: int = GLU_S
     a = _new2(rows, I, torch.bfloat16)
     q = sf = None
     if checkpoint:
-        q = torch.empty(N, 2, I, block_size, dtype=torch.int8, device=dev)
-        sf = torch.empty(ckpt8_sf_shape(N, I, block_size), dtype=torch.uint8, device=dev)
+        q = _empty_strided((N, 2, I, block_size), (2 * I * block_size, I * block_size, block_size, 1), torch.int8)
+        per = 4 * I                                     # scale bytes of 128 slots
+        sf = _empty_strided(ckpt8_sf_shape(N, I, block_size),
+                            (2 * (block_size // 128) * per, (block_size // 128) * per, per, 128, 32, 1), torch.uint8)
     rc = lib().moe_glu_fwd(h.data_ptr(), ldh, rows, I, E, block_size, N, glu, gate_up_layout, eo, bo, b2e, sp, sip,
                            slots, a.data_ptr(), None if q is None else q.data_ptr(),
                            None if sf is None else sf.data_ptr(), st)

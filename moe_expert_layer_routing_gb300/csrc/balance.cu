@@ -811,12 +811,7 @@ static int launch_router(BalanceArgs a, bool topk, bool stats, const BalLayout& 
                       (vec ? sizeof(float4) * kBalStages * groups * kBalThreads : 0);
   const int how = !topk ? kIdsGiven : a.K <= 8 ? kTopKList : kTopKRounds;
   const BalKernel kern = vec ? fwd_kernel<true>(lanes, groups, how) : fwd_kernel<false>(lanes, groups, how);
-  int rc = MOE_OK;
-  if (smem > 40 * 1024 &&
-      (rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                       "cudaFuncSetAttribute(router_fwd)")))
-    return rc;
-  rc = launch_pdl(kern, dim3(a.pieces), dim3(kBalThreads), smem, st, "router_fwd", a);
+  const int rc = launch_pdl(kern, dim3(a.pieces), dim3(kBalThreads), smem, st, "router_fwd", a);
   if (rc || !stats) return rc;
   return launch_pdl(balance_reduce_kernel, dim3(a.S, (a.E + 31) / 32), dim3(kBalThreads), 0, st, "balance_reduce", a);
 }
@@ -953,8 +948,5 @@ extern "C" int moe_balance_bwd(const float* logits, int64_t ld_logits, const flo
   const BalKernel kern = vec ? bwd_kernel<true>(lanes, nv) : bwd_kernel<false>(lanes, nv);
   const int groups = nv <= 1 ? 1 : nv <= 2 && lanes == 8 ? 2 : nv <= 4 ? 4 : 8;
   const size_t smem = vec ? sizeof(float4) * kBalBwdStages * 2 * groups * kBalThreads : 0;
-  if (smem > 40 * 1024 && (rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                                           "cudaFuncSetAttribute(balance_bwd)")))
-    return rc;
   return launch_pdl(kern, dim3(a.pieces), dim3(kBalThreads), smem, st, "balance_bwd", a);
 }

@@ -371,9 +371,6 @@ extern "C" int moe_glu_fwd(const void* h, int64_t ldh, int64_t rows, int I, int 
   p.tpb_shift = tile_shift(block_size);
   p.items = (num_blocks << p.tpb_shift) * (I / kGluFeat);
   constexpr size_t smem = 2 * sizeof(uint32_t) * kGluRows * kGluFeat;
-  if ((rc = cuda_check(cudaFuncSetAttribute(glu_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                       "cudaFuncSetAttribute(glu_fwd)")))
-    return rc;
   return launch_pdl(glu_fwd_kernel, dim3((unsigned)std::min<int64_t>(p.items, kGluBlocks * device_sm_count())),
                     dim3(kGluThreads), smem, reinterpret_cast<cudaStream_t>(stream), "glu_fwd", p);
 }

@@ -1209,8 +1209,6 @@ int gemm_launch_instance(const GemmParams& p, const void* tmA, const void* tmB, 
                          cudaStream_t st) {
   using C = GemmCfg<MX, BN, EPI>;
   auto kern = gemm_kernel<MX, BN, EPI>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return cuda_check(e, "cudaFuncSetAttribute(gemm)");
   return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, "gemm launch",
                     *static_cast<const CUtensorMap*>(tmA), *static_cast<const CUtensorMap*>(tmB),
                     *static_cast<const CUtensorMap*>(tmC), p);

@@ -128,6 +128,38 @@ int fork_join(cudaStream_t st, const std::function<int(cudaStream_t)>& side, con
   return rc_side ? rc_side : rc_main;
 }
 
+// The dynamic shared memory that kernels were allowed on a device: a fixed table of (kernel, device) with linear
+// probing; a full table only means asking the driver every time.
+namespace {
+constexpr int kAllowed = 1024;
+struct Allowed {
+  std::atomic<uint64_t> key{0};  // kernel address * kMaxDevices + device
+  std::atomic<size_t> bytes{0};
+};
+Allowed g_allowed[kAllowed];
+}  // namespace
+
+int allow_smem(const void* kern, size_t bytes, bool again) {
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc) return rc;
+  Allowed* slot = nullptr;
+  if (dev >= 0 && dev < kMaxDevices) {
+    const uint64_t key = (uint64_t)reinterpret_cast<uintptr_t>(kern) * kMaxDevices + (uint64_t)dev;
+    uint64_t i = (key * 0x9E3779B97F4A7C15ull) >> 54;
+    for (int n = 0; n < 16 && !slot; ++n, i = (i + 1) % kAllowed) {
+      uint64_t seen = g_allowed[i].key.load(std::memory_order_acquire);
+      if (seen == 0 && g_allowed[i].key.compare_exchange_strong(seen, key)) seen = key;
+      if (seen == key) slot = &g_allowed[i];
+    }
+  }
+  if (slot && !again && slot->bytes.load(std::memory_order_acquire) >= bytes) return MOE_OK;
+  rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
+                  "shared memory of a kernel");
+  if (!rc && slot) slot->bytes.store(bytes, std::memory_order_release);
+  return rc;
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

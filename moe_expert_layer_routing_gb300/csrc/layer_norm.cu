@@ -715,13 +715,6 @@ static int ln_mode(int64_t H, int es, std::initializer_list<const void*> in, std
   return kLnVector;
 }
 
-// Shared memory above what every kernel may have (48 KB, the static part included).
-static int ln_smem(const void* kern, size_t bytes) {
-  if (bytes <= 40 * 1024) return MOE_OK;
-  return cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
-                    "cudaFuncSetAttribute(layer_norm)");
-}
-
 static int ln_check(const char* who, int kind, int x_dtype, int w_dtype, int64_t T, int64_t H) {
   if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) return fail(MOE_ERR_INVALID, "%s: bad kind", who);
   if ((x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F32) || (w_dtype != MOE_DT_BF16 && w_dtype != MOE_DT_F32))
@@ -766,7 +759,6 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
     const LnFwdKernel k = b16 ? ln_fwd_pick<uint16_t>(mode, H) : ln_fwd_pick<float>(mode, H);
     const int cpt = ln_cpt(H, mode), blocks = ln_fwd_blocks(cpt, es);
     const size_t smem = ln_ring(mode, ln_stages(blocks, 2, cpt, es), 2, H, es);
-    if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem))) return rc;
     const int rows = ln_rows_per_block(H);
     const int64_t grid = std::min<int64_t>((T + rows - 1) / rows, 152 * blocks);
     return launch_pdl(k, dim3((unsigned)grid), dim3(kLnThreads), smem, st, "layer_norm_fwd", a,
@@ -826,8 +818,7 @@ extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void
     const int cpt = ln_cpt(H, mode);
     const size_t sums = ln_rows_per_block(H) > 1 ? sizeof(float) * kLnThreads * cpt : 0;
     const size_t smem = std::max(ln_ring(mode, ln_stages(ln_bwd_blocks(cpt), 3, cpt, es), 3, H, es), sums);
-    if ((rc = ln_smem(reinterpret_cast<const void*>(k), smem)) ||
-        (rc = launch_pdl(k, dim3(a.G), dim3(kLnThreads), smem, st, "layer_norm_bwd", a, (int)(w_dtype == MOE_DT_BF16))))
+    if ((rc = launch_pdl(k, dim3(a.G), dim3(kLnThreads), smem, st, "layer_norm_bwd", a, (int)(w_dtype == MOE_DT_BF16))))
       return rc;
     return weights();
   }

@@ -157,8 +157,6 @@ int launch_linear_quant(const uint16_t* dY, const uint16_t* W, const uint16_t* X
   if (a.total > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "linear quantiser: too many tiles");
   const int grid = (int)std::min<int64_t>(a.total, (int64_t)kLinCtasPerSm * device_sm_count());
   auto k = fmt == MOE_FP8_E5M2 ? linear_quant_kernel<MOE_FP8_E5M2> : linear_quant_kernel<MOE_FP8_E4M3>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmemBytes);
-  if (e != cudaSuccess) return cuda_check(e, "linear quantiser attribute");
   return launch_pdl(k, dim3((unsigned)grid), dim3(256), kLinSmemBytes, st, "linear quantiser", a);
 }
 

@@ -27,6 +27,10 @@ int device_sm_count();
 size_t align_up(size_t v, size_t a);
 void count_launch();   // one kernel launched by this library
 int64_t option(int opt);  // current value of a MOE_OPT_* option
+// Lets a kernel have `bytes` of dynamic shared memory on the current device: the driver is asked once per kernel and
+// device (about 2 us a call) and the answer remembered, unless `again`.
+int allow_smem(const void* kern, size_t bytes, bool again = false);
+constexpr size_t kSmemAnyKernel = 40 * 1024;  // what every kernel may have beside its static part
 // Runs `side` on a library-owned second stream of the current device, ordered after the work already
 // enqueued on `st`, and `main` on `st` meanwhile; `st` then waits for the side work.  Returns the first
 // nonzero code (main is skipped when side failed).
@@ -55,7 +59,17 @@ int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = option(MOE_OPT_PDL) ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (smem > kSmemAnyKernel) {
+    const int rc = allow_smem(reinterpret_cast<const void*>(kern), smem);
+    if (rc) return rc;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaErrorInvalidValue && smem > kSmemAnyKernel) {  // what was remembered is gone with a reset device
+    cudaGetLastError();
+    const int rc = allow_smem(reinterpret_cast<const void*>(kern), smem, true);
+    if (rc) return rc;
+    e = cudaLaunchKernelEx(&cfg, kern, args...);
+  }
   count_launch();
   if (e != cudaSuccess) return cuda_check(e, what);
   return cuda_check(cudaGetLastError(), what);

@@ -391,8 +391,6 @@ static int prep_launch(const PrepArgs& a, int grid, cudaStream_t st) {
       return MOE_ERR_INVALID;
   }
   const int smem = prep_smem_bytes<MX>();
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_check(e, "prep attribute");
   return launch_pdl(k, dim3(grid), dim3(256), smem, st, "prep", a, tm_dgt, tm_xgt);
 }
 
