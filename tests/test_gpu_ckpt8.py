@@ -165,6 +165,8 @@ def _run(inp, mb, interleaved=0, glu=0, accumulate=False, **act):
     (260, 2, 6, 128, 256, 256, PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, {}),
     (260, 2, 6, 256, 384, 512, PREC_MXFP8, AFFINITY_ON_H, True, 1, 1, {}),
     (200, 2, 6, 128, 384, 128, PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, {"G1_TILE_N": 128, "G1_WARPS": 16}),
+    (260, 2, 6, 128, 256, 256, PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, {"G1_TILE_N": 256}),
+    (260, 2, 6, 128, 256, 128, PREC_BF16, AFFINITY_ON_H, False, 0, 0, {"G1_TILE_N": 128, "PDL": 0}),
 ])
 def test_moe_bwd_on_codes_is_bit_identical_to_their_values_in_bf16(T, K, E, H, I, B, precision, affinity, bias, glu, il,
                                                                    opts, set_option):

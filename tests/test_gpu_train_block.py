@@ -85,3 +85,42 @@ def test_backward_repeats_bit_for_bit():
     torch.cuda.synchronize()
     for k in a:
         assert torch.equal(a[k], b[k]), k
+
+
+def test_calls_captured_into_a_graph_replay_to_the_eager_results():
+    """Layer norm, router with its losses, their gradients, activation and read-back captured once; the replay reads the
+    inputs as they then are."""
+    ex = _example()
+    mb = ex.mb
+    T, H, E, K, I, B = 200, 320, 24, 3, 128, 128
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, dy, logits = rand(T, H).to(torch.bfloat16), rand(T, H).to(torch.bfloat16), rand(T, E)
+    h = rand(T * K, 2 * I).to(torch.bfloat16)
+    gamma = torch.ones(H, device="cuda")
+    seg = torch.tensor([0, 90, 200], dtype=torch.int32, device="cuda")
+    meta = mb.route_meta(mb.router_fwd(0, logits, K)["ids"], E, B)
+
+    def calls():
+        n = mb.layer_norm_fwd(x, gamma, gamma)
+        b = mb.layer_norm_bwd(dy, x, gamma, n["mean"], n["rstd"])
+        r = mb.router_fwd(0, logits, K, seg_offsets=seg, alpha=0.1, beta=0.1)
+        d = mb.balance_bwd(logits, r["lse"], r["counts"], K, seg_offsets=seg, alpha=0.1, beta=0.1)
+        g = mb.glu_fwd(h, meta, B)
+        u = mb.ckpt8_unpack(g["ckpt_q"], g["ckpt_sf"], meta, T * K)
+        return [n["y"], b["dx"], b["dgamma"], b["dbeta"], r["ids"], r["scores"], r["loss"], r["counts"], d, g["a"], u]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = calls()
+    for t in (x, dy, logits, h):
+        t.mul_(-0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(held, calls()):
+        assert torch.equal(a, b)
