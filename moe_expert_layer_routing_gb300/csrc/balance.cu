@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "moebwd_internal.h"
+#include "mx_device.cuh"
 #include "ptx.cuh"
 
 namespace moebwd {
@@ -225,7 +226,7 @@ __device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], Logit logi
     const int b = __float_as_int(v[j] + 0.f);
     // columns past E hold -inf, behind every logit: they are taken last (K <= E), or in a row with a NaN of negative
     // sign, which is done over
-    key[j] = ((uint32_t)(b ^ (b >> 31 | (int)0x80000000)) >> 1 & ~CM) | (CM - (uint32_t)c);
+    key[j] = ((uint32_t)(b ^ (b >> 31 | (int)0x80000000)) >> (LIST ? 0 : 1) & ~CM) | (CM - (uint32_t)c);
   }
   uint32_t mk[SLOTS] = {}, next[SLOTS] = {};
   uint32_t last, behind;  // the K-th key, and the largest of this lane's (LIST) or of all below it
@@ -260,10 +261,11 @@ __device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], Logit logi
     mk[0] = sl & 1 ? q1 : q0;
     next[0] = __shfl_down_sync(0xffffffffu, mk[0], 1, LANES);
     last = __shfl_sync(0xffffffffu, mk[0], K - 1, LANES);
-    behind = 0;
+    // the least last - 1 - key: as unsigned, keys from last on are far above those in the same leading bits
+    uint32_t below = 0xffffffffu;
 #pragma unroll
-    for (int j = 0; j < N; j += 2) behind = __vimax3_u32(behind, key[j] - last, key[j + 1] - last);
-    behind = behind >= 0x80000000u ? behind + last : 0u;
+    for (int j = 0; j < N; j += 2) below = __vimin3_u32(below, last - 1u - key[j], last - 1u - key[j + 1]);
+    behind = below <= CM ? last - 1u - below : 0u;
   } else {
     uint32_t m = 0x80000000u;
     last = 0;
@@ -424,17 +426,25 @@ __global__ void __launch_bounds__(kBalThreads, NV <= 4 ? 3 : 1) router_fwd_kerne
       m = lane_max<LANES>(m);
     }
     const float base = m == -INFINITY ? 0.f : m;
-    float total = 0.f;
+    const uint64_t nbase = f2_splat(-base), l2e = f2_splat(1.4426950408889634f);
+    uint64_t total2 = f2_splat(0.f);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] = exp_from(v[j], base);
-      total += v[j];
+    for (int j = 0; j < N; j += 2) {
+      float x0, x1;
+      f2_unpack(f2_mul(f2_add(f2_pack(v[j], v[j + 1]), nbase), l2e), x0, x1);
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j]) : "f"(x0));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j + 1]) : "f"(x1));
+      total2 = f2_add(total2, f2_pack(v[j], v[j + 1]));
     }
-    total = lane_sum<LANES>(total);
+    float total, total_hi;
+    f2_unpack(total2, total, total_hi);
+    total = lane_sum<LANES>(total + total_hi);
     const float inv = total != 0.f ? __fdividef(1.f, total) : 0.f;  // 0: every expert masked (or no token here)
     const float lse = base + logf(total);
+    const uint64_t inv2 = f2_splat(inv);
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
+    for (int j = 0; j < N; j += 2)
+      f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), inv2, f2_pack(acc[j], acc[j + 1])), acc[j], acc[j + 1]);
     if (sl == 0 && live) {
       if (a.lse) a.lse[t] = lse;
       if (total != 0.f) z = fmaf(lse, lse, z);
