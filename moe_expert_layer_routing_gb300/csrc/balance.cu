@@ -16,9 +16,9 @@
 // counts are one partial row, which a second kernel adds per sequence in a fixed order.
 //
 // The gradient is bound by HBM: 131072 x 256 with `add` moves 403 MB, 59 us at the measured copy rate; measured 63.5 us
-// (6.3 TB/s).  The forward reads 34 MB at 65536 x 128 (5.6 us) and is bound by the selection's integer arithmetic: about
-// 240 warp instructions a token, half of them minima, maxima and logic on the half-rate ALU pipe (busy 47% of the time,
-// issue slots 62%); measured 24 us with the losses (top-8), 10 us with the ids given, and 5 us for the reduction, whose
+// (6.3 TB/s).  The forward reads 34 MB at 65536 x 128 (5.6 us) and is bound by the selection's integer arithmetic: over
+// 200 warp instructions a token, half of them minima, maxima and logic on the half-rate ALU pipe (busy 47% of the time,
+// issue slots 62%); measured 23 us with the losses (top-8), 10 us with the ids given, and 5 us for the reduction, whose
 // chain of dependent steps is all latency.
 #include <cuda_runtime.h>
 
@@ -178,12 +178,13 @@ __device__ __noinline__ void topk_exact(const float* row, int E, int K, int sl, 
   }
 }
 
-// The same with unique 31-bit keys: a value's leading bits, then its column counted backwards (CB bits), so that the
-// larger key is the value to take and no search for columns follows.  True marks rows that need exact keys all the
-// same: values that differ in the dropped bits alone and came out of order, or might have at the end.
+// The same with unique keys of 32 bits (31 in rounds): a value's leading bits, then its column counted backwards, so
+// that the larger key is the value to take and no search for columns follows.  True marks rows that need exact keys all
+// the same: values that differ in the dropped bits alone and came out of order, or might have at the end.
 //
 // Measured at 65536 x 128 with the losses: exact keys with a search per round 42 us, rounds of packed keys 30 us, sorted
-// lists 26 us, and 23 us with the logits a pass ahead in shared memory and read again after the selection.
+// lists 26 us, 24 us with the logits a pass ahead in shared memory and read again after the selection, 23 us with the
+// softmax and its column sums in paired arithmetic.
 //
 // K <= 8 (LIST): a sorted list of the eight largest per lane (a sorting network of 19 comparators per 8 values), then
 // merged with the lists of the lanes 1, 2, 4, ... away: max(a_i, b_7-i) holds the eight largest of both and is
@@ -261,11 +262,12 @@ __device__ __forceinline__ bool topk_packed(const float (&v)[4 * NV], Logit logi
     mk[0] = sl & 1 ? q1 : q0;
     next[0] = __shfl_down_sync(0xffffffffu, mk[0], 1, LANES);
     last = __shfl_sync(0xffffffffu, mk[0], K - 1, LANES);
-    // the least last - 1 - key: as unsigned, keys from last on are far above those in the same leading bits
+    // the least last - 1 - key: as unsigned, keys from last on are far above those in the same leading bits, but where
+    // last itself has none of them set (a NaN of negative sign): there every key is looked at
     uint32_t below = 0xffffffffu;
 #pragma unroll
     for (int j = 0; j < N; j += 2) below = __vimin3_u32(below, last - 1u - key[j], last - 1u - key[j + 1]);
-    behind = below <= CM ? last - 1u - below : 0u;
+    behind = last <= CM ? last : below <= CM ? last - 1u - below : 0u;
   } else {
     uint32_t m = 0x80000000u;
     last = 0;
