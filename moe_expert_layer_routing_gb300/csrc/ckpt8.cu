@@ -323,7 +323,7 @@ static int ckpt8_check(const char* who, int64_t rows, int I, int E, int block_si
     return fail(MOE_ERR_UNSUPPORTED, "%s: block_size must be 128, 256, 512 or 1024", who);
   if (gate_up_layout != MOE_GATE_UP_CONCAT && gate_up_layout != MOE_GATE_UP_INTERLEAVED)
     return fail(MOE_ERR_INVALID, "%s: bad gate_up_layout", who);
-  if (num_blocks * (block_size / kGluRows) * (I / kGluFeat) > INT32_MAX)
+  if (num_blocks > INT32_MAX || num_blocks * (block_size / kGluRows) * (I / kGluFeat) > INT32_MAX)
     return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   return MOE_OK;
 }

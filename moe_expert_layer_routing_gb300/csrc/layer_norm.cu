@@ -750,6 +750,8 @@ extern "C" int layer_norm_fwd(int kind, const void* x, int64_t ldx, const void* 
     if ((rc = ln_aligned("layer_norm_fwd", p, x_dtype))) return rc;
   for (const void* p : {gamma, beta})
     if ((rc = ln_aligned("layer_norm_fwd", p, w_dtype))) return rc;
+  for (const float* p : {mean, rstd})
+    if ((rc = ln_aligned("layer_norm_fwd", p, MOE_DT_F32))) return rc;
   LnFwdArgs a{x, residual, gamma, beta, y, sum, kind == MOE_NORM_LAYER ? mean : nullptr, rstd, ldx, ldr, T, (int)H,
               kind == MOE_NORM_RMS, eps};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -785,6 +787,8 @@ extern "C" int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void
   if (rc) return rc;
   if (accumulate != 0 && accumulate != 1) return fail(MOE_ERR_INVALID, "layer_norm_bwd: accumulate must be 0 or 1");
   if (!dgamma) return fail(MOE_ERR_INVALID, "layer_norm_bwd: null pointer");
+  for (const float* p : {mean, rstd, static_cast<const float*>(dgamma), static_cast<const float*>(dbeta)})
+    if ((rc = ln_aligned("layer_norm_bwd", p, MOE_DT_F32))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) {  // sums over no rows
     if (accumulate) return MOE_OK;

@@ -155,3 +155,21 @@ def test_python_layer_refuses_cpu_tensors(lib):
         mb.router_fwd(0, x, 2)
     with pytest.raises(mb.MoeError):
         mb.balance_bwd(x, torch.zeros(4), torch.zeros(1, 8, dtype=torch.int32), 2)
+
+
+@pytest.mark.parametrize("kw", [dict(mean=A + 2), dict(rstd=A + 1)])
+def test_layer_norm_statistics_alignment(lib, kw):
+    for call, who in ((_ln_fwd, b"layer_norm_fwd"), (_ln_bwd, b"layer_norm_bwd")):
+        assert call(lib, **kw) == INVALID
+        assert who in lib.moe_last_error() and b"aligned" in lib.moe_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(dg=A + 2), dict(db=A + 3)])
+def test_layer_norm_weight_gradient_alignment(lib, kw):
+    assert _ln_bwd(lib, **kw) == INVALID
+    assert b"aligned" in lib.moe_last_error()
+
+
+def test_checkpoint_blocks_past_32_bits(lib):
+    assert _glu(lib, N=1 << 61) == UNSUPPORTED
+    assert b"too many tiles" in lib.moe_last_error()
