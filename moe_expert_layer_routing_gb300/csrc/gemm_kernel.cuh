@@ -320,7 +320,8 @@ __device__ __forceinline__ void group_bar(int id) {
 //   ds += <dA_raw, a>,  dA = s dA_raw,  dgate = dA up SiLU'(gate),  dup = dA SiLU(gate),  a' = s a
 // and write dh [P,2I] (row-major), dh^T [2I,P], a'^T [I,P] (bf16, or fp8 + scales).  The row-wise
 // MXFP8 groups of dh (32 features) span the 32/NC warps of a TMEM lane quarter: partial amax values
-// are exchanged through `xchg` ([slice][gate|up][32 lanes]) with a barrier over those warps.
+// are exchanged through `xchg` ([slice][gate|up][32 lanes]) with a barrier over those warps.  BF16 exchanges
+// nothing, and its warps run apart (a barrier per chunk cost G1 2% on 8-bit codes at 1024 rows an expert).
 // GENERIC with `ga` (this row's slot in a saved act(gate) checkpoint [N,I,B], feature stride B):
 // act(gate) is read from it, act'(gate) still computed from the pre-activation.
 // Padding rows produce zeros.
@@ -477,8 +478,8 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     // this warp's 16 (gate, up) pairs are the 32 consecutive columns 2*c0.. of dh: one MX group
     // (the layout is fixed per launch: a quarter's warps take the same branch and meet at the same
     // named barriers)
-    group_bar<32 * SUBS>(bar_id);
     if constexpr (MX) {
+      group_bar<32 * SUBS>(bar_id);
       const float am = fmaxf(amax_tree<NC>(dg), amax_tree<NC>(du));
       const uint32_t byte = e8m0_byte(__float_as_uint(am), AF);
       const float inv = e8m0_inv_scale(byte);
@@ -539,7 +540,6 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
       p.dh_sf[sf_tiled_offset(prow, I + i0, 2 * (int64_t)I)] = (uint8_t)bu;
     }
   } else {
-    group_bar<32 * SUBS>(bar_id);  // the amax exchange's barrier on the MXFP8 branch (its partner's reads)
     uint16_t* dh = static_cast<uint16_t*>(p.dh) + prow * (2 * (int64_t)I);
     auto pg = [&](int j) { return pack_bf16x2(dg[j], dg[j + 1]); };
     auto pu = [&](int j) { return pack_bf16x2(du[j], du[j + 1]); };
