@@ -324,12 +324,14 @@ __device__ __forceinline__ void group_bar(int id) {
 // nothing, and its warps run apart (a barrier per chunk cost G1 2% on 8-bit codes at 1024 rows an expert).
 // GENERIC with `ga` (this row's slot in a saved act(gate) checkpoint [N,I,B], feature stride B):
 // act(gate) is read from it, act'(gate) still computed from the pre-activation.
-// Padding rows produce zeros.
+// Padding rows produce zeros: their terms are computed from whatever the accumulator and the checkpoint hold there
+// and dropped at the end, in a branch that only tiles with padding take (G1 on codes 70.4 us at 1024 rows an expert
+// and, for MXFP8, 0.888 ms at 2048; with selects on every input 77.5 us and 0.955 ms).
 // CK8: the chunk holds int8 codes and the scale bytes of their 32-row groups (value code 2^(byte - 127)); a
 // TMEM lane quarter is one group, so a warp's NC features take their scales from one or two broadcast loads.
 // A code becomes a float by its bits in the mantissa of 2^23 and one paired subtraction, then one paired
-// multiplication (an integer-to-float conversion instead: G1 +2%).  The decoding costs G1 5% (BF16) to 12% (MXFP8
-// where the epilogue bounds it).
+// multiplication (an integer-to-float conversion instead: G1 +2%).  Against bf16 values the decoding costs G1 4% for
+// MXFP8, whose epilogue bounds it, and nothing for BF16, which reads half the bytes.
 template <bool MX, int NC, int AF, bool GENERIC, bool SHARED_TBUF, bool CK8>
 __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t taddr, int64_t prow, int m, int lane,
                                                  bool valid, float sv, int i0, int sub, const uint16_t* ck,
@@ -396,7 +398,6 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     for (int jj = 0; jj < NC; ++jj) {
       float g = ck_one(0, jj);
       float u = ck_one(1, jj);
-      if (!valid) g = u = 0.f;
       const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
       const float pdf = 0.39894228040143268f * __expf(-0.5f * g * g);
       float act = g * cdf;
@@ -410,7 +411,6 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     for (int jj = 0; jj < NC; ++jj) {
       float g = ck_one(0, jj);
       float u = ck_one(1, jj);
-      if (!valid) g = u = 0.f;
       const float sg = __fdividef(1.f, 1.f + __expf(-g));
       float sl = g * sg;
       sl = saved ? sa[jj] : sl;
@@ -424,7 +424,7 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     const uint64_t one2 = f2_splat(1.f), neg1 = f2_splat(-1.f), nl2e = f2_splat(-1.4426950408889634f);
 #pragma unroll
     for (int jj = 0; jj < NC; jj += 2) {
-      const uint64_t G = valid ? ck_two(0, jj) : f2_splat(0.f), U = valid ? ck_two(1, jj) : f2_splat(0.f);
+      const uint64_t G = ck_two(0, jj), U = ck_two(1, jj);
       float x0, x1;
       f2_unpack(f2_mul(G, nl2e), x0, x1);
       float e0, e1, s0, s1;
@@ -445,13 +445,17 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
   if constexpr (GENERIC) {
 #pragma unroll
     for (int jj = 0; jj < NC; ++jj) {
-      const float v = valid ? __uint_as_float(r[jj]) : 0.f;
+      const float v = __uint_as_float(r[jj]);
       const float a = ap[jj];
       ds_acc = fmaf(v, a, ds_acc);
       const float dA = sv * v;
       dg[jj] = dA * dg[jj];
       du[jj] = dA * du[jj];
       ap[jj] = (p.affinity_on_i || p.ap_s) ? sv * a : a;
+    }
+    if (!valid) {
+#pragma unroll
+      for (int jj = 0; jj < NC; ++jj) dg[jj] = du[jj] = ap[jj] = 0.f;
     }
   } else {
     const uint64_t sv2 = f2_splat(sv);
@@ -460,7 +464,7 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     uint64_t DS = f2_splat(0.f);
 #pragma unroll
     for (int jj = 0; jj < NC; jj += 2) {
-      const uint64_t V = valid ? f2_pack(__uint_as_float(r[jj]), __uint_as_float(r[jj + 1])) : f2_splat(0.f);
+      const uint64_t V = f2_pack(__uint_as_float(r[jj]), __uint_as_float(r[jj + 1]));
       const uint64_t A = f2_pack(ap[jj], ap[jj + 1]);
       DS = f2_fma(V, A, DS);
       const uint64_t DA = f2_mul(sv2, V);
@@ -471,6 +475,10 @@ __device__ __forceinline__ void epi_dswiglu_part(const GemmParams& p, uint32_t t
     float d0, d1;
     f2_unpack(DS, d0, d1);
     ds_acc += d0 + d1;
+    if (!valid) {
+#pragma unroll
+      for (int jj = 0; jj < NC; ++jj) dg[jj] = du[jj] = ap[jj] = 0.f;
+    }
   }
   const int c0 = i0 + sub * NC;  // first feature of this warp's columns
   const bool il = GENERIC && NC == 16 && p.interleaved;  // gate_i, up_i at columns 2i, 2i+1 (host: NC == 16)
