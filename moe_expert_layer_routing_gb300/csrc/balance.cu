@@ -16,8 +16,8 @@
 // counts are one partial row, which a second kernel adds per sequence in a fixed order.
 //
 // The gradient is bound by HBM: 131072 x 256 with `add` moves 403 MB, 59 us at the measured copy rate; measured 63.5 us
-// (6.3 TB/s).  The forward reads 34 MB at 65536 x 128 (5.6 us) and is bound by the selection's integer arithmetic: over
-// 200 warp instructions a token, half of them minima, maxima and logic on the half-rate ALU pipe (busy 47% of the time,
+// (6.3 TB/s).  The forward reads 34 MB at 65536 x 128 (5.6 us) and is bound by the selection's integer arithmetic: about
+// 230 warp instructions a token, half of them minima, maxima and logic on the half-rate ALU pipe (busy 47% of the time,
 // issue slots 62%); measured 23 us with the losses (top-8), 10 us with the ids given, and 5 us for the reduction, whose
 // chain of dependent steps is all latency.
 #include <cuda_runtime.h>
