@@ -71,15 +71,15 @@ __device__ __forceinline__ int seg_start(const BalanceArgs& a, int i) {
   return min(max(a.off[i - 1], 0), a.T);
 }
 
-// Segment and tokens [lo, hi) of piece p; false when the piece is empty.
+// Segment and tokens [lo, hi) of piece p; false when the piece is empty.  Every warp finds them with its 32 lanes: two
+// rounds up to 1023 sequences.
 __device__ __forceinline__ bool find_piece(const BalanceArgs& a, int p, int& seg, int& lo, int& hi) {
   int l = 0, h = a.S + 1;  // the last segment i whose first piece, start / C + i, is not behind p
   while (l < h) {
-    const int m = (l + h + 1) >> 1;
-    if (seg_start(a, m) / a.C + m <= p)
-      l = m;
-    else
-      h = m - 1;
+    const int step = (h - l + 31) >> 5, m = l + ((int)(threadIdx.x & 31) + 1) * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, m <= h && seg_start(a, m) / a.C + m <= p));
+    h = min(h, l + (c + 1) * step - 1);
+    l = min(l + c * step, h);
   }
   seg = l;
   const int64_t c0 = (int64_t)(p - l) * a.C;
