@@ -263,3 +263,34 @@ def test_empty_and_refusals():
                 lambda: mb.balance_bwd(lg, lse, cnt, 2, add=lg[:3])):
         with pytest.raises((mb.MoeError, RuntimeError)):
             bad()
+
+
+@pytest.mark.parametrize("S", [31, 33, 1023, 1500, 40000])
+def test_pieces_of_many_sequences(S):
+    """Sequences of 0 to 2 tokens between padding at both ends; more of them than tokens."""
+    mb = _mb()
+    T, E, K = 1300, 16, 2
+    rng = np.random.default_rng(S)
+    lg = _logits(T, E, S)
+    seg = np.sort(rng.integers(3, T - 4, S + 1)).astype(np.int64)
+    ids = ob.topk(lg, K, seg.tolist())
+    owner = np.searchsorted(seg, np.arange(T), side="right") - 1      # the last of the sequences that start there
+    owner[np.arange(T) >= seg[-1]] = -1
+    out = mb.router_fwd(0, _dev(lg), K, alpha=A, beta=B, seg_offsets=_t(seg.tolist()))
+    assert np.array_equal(out["ids"].cpu().numpy(), ids) and int(out["status"].item()) == 0
+    counts = np.zeros((S, E), np.int64)
+    for t in np.flatnonzero(owner >= 0):
+        for e in ids[t]:
+            if e >= 0:
+                counts[owner[t], e] += 1
+    assert np.array_equal(out["counts"].cpu().numpy(), counts)
+    got = np64(mb.balance_bwd(_dev(lg), out["lse"], out["counts"], K, seg_offsets=_t(seg.tolist()), alpha=A, beta=B))
+    lse = np64(out["lse"])
+    n, lens = int((owner >= 0).sum()), np.diff(seg)
+    for t in range(T):
+        if owner[t] < 0 or not np.isfinite(lse[t]):
+            assert not got[t].any()
+            continue
+        p, c = np.exp(lg[t].astype(np.float64) - np.logaddexp.reduce(lg[t].astype(np.float64))), counts[owner[t]]
+        bal, z = A * E / (K * n * lens[owner[t]]) * p, 2 * B / n * np.logaddexp.reduce(lg[t].astype(np.float64)) * p
+        assert np.all(np.abs(got[t] - (bal * (c - (c * p).sum()) + z)) <= 2 * _tol(lg, 0) * (bal * (c + (c * p).sum()) + np.abs(z)) + 1e-30)
