@@ -717,7 +717,7 @@ static int bal_bwd_lanes(int E) { return E <= 128 ? 8 : E <= 256 ? 16 : 32; }
 // times that (131072 x 256: 63.8 us, 66.7 us resident at once).
 static int64_t bal_passes(int T, int lanes, int64_t most) {
   const int step = kBalThreads / lanes;
-  return (((int64_t)T + step - 1) / step + most - 1) / most;
+  return std::max<int64_t>(1, (((int64_t)T + step - 1) / step + most - 1) / most);  // (no tokens: a chunk has a size)
 }
 static int bal_chunk(int T, int lanes) { return (int)bal_passes(T, lanes, 3 * 152 - 8) * (kBalThreads / lanes); }
 static int bal_bwd_chunk(int T, int lanes) {

@@ -173,3 +173,11 @@ def test_layer_norm_weight_gradient_alignment(lib, kw):
 def test_checkpoint_blocks_past_32_bits(lib):
     assert _glu(lib, N=1 << 61) == UNSUPPORTED
     assert b"too many tiles" in lib.moe_last_error()
+
+
+@pytest.mark.parametrize("K,E", [(2, 64), (1, 1), (8, 256), (64, 1024)])
+@pytest.mark.parametrize("S", [1, 2, 1000])
+def test_balance_workspace_of_an_empty_batch(lib, K, E, S):
+    """T = 0 is a valid problem, and its workspace size is asked for like any other's."""
+    size = lib.moe_balance_workspace_size
+    assert 0 < size(0, K, E, S) <= size(1, K, E, S)
