@@ -294,24 +294,26 @@ __device__ __forceinline__ uint4 ln_pack(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// VEC weights from column c on, in fp32 (16-byte loads when VEC > 1)
+// VEC weights from column c on, in fp32 (16-byte loads when VEC > 1).  Ordinary loads here and for mean and rstd: a
+// kernel starts while the one before it on the stream still runs, and the read-only path (__ldg) is only for memory
+// that nothing writes during the whole of a kernel.
 template <int VEC>
 __device__ __forceinline__ void ln_weights(const void* p, int bf16, int c, float (&f)[VEC]) {
   if constexpr (VEC == 1) {
-    f[0] = bf16 ? bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p) + c)) : __ldg(static_cast<const float*>(p) + c);
+    f[0] = bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[c]) : static_cast<const float*>(p)[c];
   } else if (!bf16) {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + i));
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + i);
       f[i] = w.x;
       f[i + 1] = w.y;
       f[i + 2] = w.z;
       f[i + 3] = w.w;
     }
   } else if constexpr (VEC == 8) {
-    ln_unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c)), f);
+    ln_unpack(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c), f);
   } else {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c));
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c);
     f[0] = __uint_as_float(w.x << 16);
     f[1] = __uint_as_float(w.x & 0xffff0000u);
     f[2] = __uint_as_float(w.y << 16);
@@ -539,8 +541,8 @@ __global__ void __launch_bounds__(kLnThreads, ln_bwd_blocks(CPT)) ln_bwd_kernel(
   float mu_next = 0.f, rs_next = 0.f;  // a row ahead, like the ring
   auto stats = [&](int64_t t) {
     if (t < a.T) {
-      mu_next = a.rms ? 0.f : __ldg(a.mean + t);
-      rs_next = __ldg(a.rstd + t);
+      mu_next = a.rms ? 0.f : a.mean[t];
+      rs_next = a.rstd[t];
     }
   };
   stats(t);

@@ -232,3 +232,44 @@ def test_empty_and_refusals():
                 lambda: mb.layer_norm_bwd(x, x, g, None, s)):
         with pytest.raises(mb.MoeError):
             bad()
+
+
+@pytest.mark.parametrize("T", [1, 7, 300])
+@pytest.mark.parametrize("H,shift", [(96, 0), (1111, 0), (2048, 0), (2048, 1)])
+def test_calls_back_to_back_on_reused_buffers(T, H, shift):
+    """A kernel may start before the one in front of it has written: forward and backward one right after the other on the
+    same statistics buffers, and a norm's output as the next norm's weights, with other inputs each time, give the
+    bits of calls that are waited for one by one."""
+    mb = _mb()
+    n = 40
+    lib, st = mb.lib(), torch.cuda.current_stream().cuda_stream
+    x, dy = ([_rand((T, H), torch.float32, 100 * k + i, None, shift) for i in range(n)] for k in (1, 2))
+    z = [_rand((1, H), torch.float32, 300 + i) for i in range(n)]
+    gamma = _rand((1, H), torch.float32, 4)[0]
+    size = max(lib.layer_norm_bwd_workspace_size(T, H), 256)
+
+    def run(wait):
+        new = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+        y, w, mean, rstd, m1, r1, ws = new(T, H), new(1, H), new(T), new(T), new(1), new(1), new(size // 4)
+        m2, r2 = new(T), new(T)
+        dx, dg, db, y2 = new(n, T, H), new(n, H), new(n, H), new(n, T, H)
+        torch.cuda.synchronize()
+        for i in range(n):
+            calls = [lambda: lib.layer_norm_fwd(0, x[i].data_ptr(), H, None, 0, gamma.data_ptr(), None, 1, 1, T, H, EPS,
+                                                y.data_ptr(), None, mean.data_ptr(), rstd.data_ptr(), st),
+                     lambda: lib.layer_norm_bwd(0, dy[i].data_ptr(), H, x[i].data_ptr(), H, gamma.data_ptr(), mean.data_ptr(),
+                                                rstd.data_ptr(), None, 0, 1, 1, T, H, dx[i].data_ptr(), dg[i].data_ptr(),
+                                                db[i].data_ptr(), 0, ws.data_ptr(), size, st),
+                     lambda: lib.layer_norm_fwd(0, z[i].data_ptr(), H, None, 0, gamma.data_ptr(), None, 1, 1, 1, H, EPS,
+                                                w.data_ptr(), None, m1.data_ptr(), r1.data_ptr(), st),
+                     lambda: lib.layer_norm_fwd(0, x[i].data_ptr(), H, None, 0, w.data_ptr(), w.data_ptr(), 1, 1, T, H, EPS,
+                                                y2[i].data_ptr(), None, m2.data_ptr(), r2.data_ptr(), st)]
+            for call in calls:
+                assert call() == 0
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return dx, dg, db, y2
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
