@@ -45,7 +45,8 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 // Launch with programmatic dependent launch (unless MOE_OPT_PDL is 0): the kernel's CTAs may be
 // scheduled while the previous kernel on the stream finishes; every kernel launched this way calls
 // pdl_wait() before it touches memory that earlier work wrote, and pdl_trigger() to let the next
-// kernel be scheduled early in turn.
+// kernel be scheduled early in turn.  What the previous kernel writes is thus written during this one's lifetime and
+// must be read with ordinary loads: no __ldg and no const __restrict__ parameters, which allow the read-only path.
 template <typename... KArgs, typename... Args>
 int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const char* what,
                Args... args) {

@@ -534,7 +534,7 @@ int launch_tile_row_slot(int64_t P, int B, const int32_t* num_tiles, const int32
 // (bn % 128 != 0): tile j's scales fill ceil(bn / 128) whole atoms, rows j*bn .. j*bn + bn - 1 in
 // order and the rest of the last atom zero.  The four scale bytes of one row inside an atom are
 // contiguous in both layouts, so each thread moves one 32-bit word.
-__global__ void __launch_bounds__(256) sf_retile_kernel(const uint32_t* __restrict__ src, int64_t R, int64_t C,
+__global__ void __launch_bounds__(256) sf_retile_kernel(const uint32_t* src, int64_t R, int64_t C,
                                                         int bn, int atoms, uint32_t* __restrict__ dst) {
   pdl_wait();  // results of the previous kernel on the stream
   pdl_trigger();
@@ -590,9 +590,9 @@ __device__ __forceinline__ uint2 quant_piece(const uint4 v, int fmt, uint32_t& b
                     fp8x4(d[4] * inv, d[5] * inv, d[6] * inv, d[7] * inv, fmt));
 }
 
-__global__ void __launch_bounds__(256) quant_rowwise_kernel(const uint16_t* __restrict__ in, int64_t src_rows,
+__global__ void __launch_bounds__(256) quant_rowwise_kernel(const uint16_t* in, int64_t src_rows,
                                                             int64_t rows, int64_t cols, int64_t ld,
-                                                            const int32_t* __restrict__ row_index, int fmt,
+                                                            const int32_t* row_index, int fmt,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
                                                             int tiled) {
   pdl_wait();  // results of the previous kernel on the stream

@@ -12,8 +12,8 @@
 
 namespace moebwd {
 
-__global__ void __launch_bounds__(256) dx_scatter_sum_kernel(const uint16_t* __restrict__ dx_exp,
-                                                             const int32_t* __restrict__ flat_tile_row, int K, int H,
+__global__ void __launch_bounds__(256) dx_scatter_sum_kernel(const uint16_t* dx_exp,
+                                                             const int32_t* flat_tile_row, int K, int H,
                                                              uint16_t* __restrict__ dx) {
   pdl_wait();  // results of the previous kernel on the stream
   pdl_trigger();
@@ -47,8 +47,8 @@ int launch_dx_scatter_sum(const uint16_t* dx_exp, const int32_t* flat_tile_row, 
   return launch_pdl(dx_scatter_sum_kernel, dim3(T), dim3(256), 0, st, "dx_scatter_sum", dx_exp, flat_tile_row, K, H, dx);
 }
 
-__global__ void ds_finalize_kernel(const float* __restrict__ ds_part, int nparts, const float* __restrict__ ds_bias,
-                                   const int32_t* __restrict__ flat_tile_row, int64_t TK, float* __restrict__ ds) {
+__global__ void ds_finalize_kernel(const float* ds_part, int nparts, const float* ds_bias,
+                                   const int32_t* flat_tile_row, int64_t TK, float* __restrict__ ds) {
   pdl_wait();  // results of the previous kernel on the stream
   pdl_trigger();
   const int64_t f = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -127,7 +127,7 @@ struct BiasJob {
 };
 
 template <int PARTS>
-__device__ __forceinline__ float bias_sum(const float* __restrict__ part, int64_t F, int64_t f, int t0, int t1) {
+__device__ __forceinline__ float bias_sum(const float* part, int64_t F, int64_t f, int t0, int t1) {
   float a0 = 0.f, a1 = 0.f;
   int t = t0;
   for (; t + 1 < t1; t += 2) {
@@ -145,7 +145,7 @@ __device__ __forceinline__ float bias_sum(const float* __restrict__ part, int64_
 }
 
 __global__ void __launch_bounds__(256) bias_parts_reduce_kernel(BiasJob j0, BiasJob j1,
-                                                                const int32_t* __restrict__ tile_offsets,
+                                                                const int32_t* tile_offsets,
                                                                 int accumulate) {
   pdl_wait();  // results of the previous kernel on the stream
   pdl_trigger();

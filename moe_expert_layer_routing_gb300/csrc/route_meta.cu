@@ -38,9 +38,9 @@ struct RouteFill {
   int nzero;
 };
 
-__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const int32_t* __restrict__ ids, int64_t TK,
+__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const int32_t* ids, int64_t TK,
                                                                     int K, int E,
-                                                                    const int32_t* __restrict__ num_valid,
+                                                                    const int32_t* num_valid,
                                                                     int32_t* __restrict__ chunk_counts,
                                                                     int32_t* status, RouteFill fill) {
   pdl_wait();  // results of the previous kernel on the stream
@@ -169,11 +169,11 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(int nchunks, int E, in
 }
 
 __global__ void __launch_bounds__(kRouteThreads) route_scatter_kernel(
-    const int32_t* __restrict__ ids, int64_t TK, int K, int E, int B, const int32_t* __restrict__ chunk_base,
-    const int32_t* __restrict__ expert_offsets, const int32_t* __restrict__ block_offsets,
-    const int32_t* __restrict__ tile_offsets, int32_t* x_gather_idx, int32_t* s_scatter_idx, int32_t* s_reverse,
+    const int32_t* ids, int64_t TK, int K, int E, int B, const int32_t* chunk_base,
+    const int32_t* expert_offsets, const int32_t* block_offsets,
+    const int32_t* tile_offsets, int32_t* x_gather_idx, int32_t* s_scatter_idx, int32_t* s_reverse,
     int32_t* token_position_to_id, int32_t* tile_row_flat, int32_t* flat_tile_row,
-    const int32_t* __restrict__ num_valid) {
+    const int32_t* num_valid) {
   pdl_wait();  // results of the previous kernel on the stream
   pdl_trigger();
   extern __shared__ int32_t sm[];
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_scatter_kernel(
 // concurrently running tiles read within a narrow window, so the K reads of a token row mostly hit
 // L2.  The order inside a bucket is arbitrary; it only changes the processing order.
 constexpr int kOrderBuckets = 4096;
-__global__ void __launch_bounds__(1024) tile_order_kernel(const int32_t* __restrict__ tile_row_flat,
-                                                          const int32_t* __restrict__ num_tiles, int T, int K,
+__global__ void __launch_bounds__(1024) tile_order_kernel(const int32_t* tile_row_flat,
+                                                          const int32_t* num_tiles, int T, int K,
                                                           int32_t* __restrict__ order) {
   pdl_wait();  // results of the previous kernel on the stream
   pdl_trigger();
