@@ -259,6 +259,15 @@ def quantize_weights(W: torch.Tensor, fmt: int = FP8_E4M3, stream=None):
     return mxfp8_quantize(W.reshape(E * R, C), QUANT_ROWWISE, fmt, None, SF_TILED, stream)
 
 
+def _check_status(t, device):
+    """Refuses a status word that the kernels on `device` cannot write: anything but one int32 there."""
+    if not t.is_cuda or t.dtype is not torch.int32 or t.numel() != 1:
+        raise MoeError(f"status must be a CUDA tensor of one int32, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    here = device.index if device.index is not None else torch.cuda.current_device()
+    if device.type != "cuda" or t.device.index != here:
+        raise MoeError(f"status is on {t.device}, which is not the operator's device")
+
+
 class MoeBwd:
     """One MoE backward problem bound to device buffers: outputs and workspace are allocated once,
     run() enqueues moe_bwd on the stream (no host synchronisation)."""
@@ -266,7 +275,10 @@ class MoeBwd:
     def __init__(self, *, T, H, I, E, K, block_size, precision=PREC_BF16, affinity=AFFINITY_ON_H,
                  fp8_act=FP8_E5M2, fp8_w=FP8_E4M3, has_bias=False, accumulate=False, act_src=ACT_CHECKPOINT,
                  ds_masked=False, glu=GLU_SWIGLU, gate_up_layout=GATE_UP_CONCAT, device="cuda", status=None):
-        """status: an int32 [1] CUDA tensor for the status word (None: one is made, 0 until the first run)."""
+        """status: an int32 [1] CUDA tensor on `device` for the status word (None: one is made, 0 until the first run)."""
+        self.device = torch.device(device)
+        if status is not None:
+            _check_status(status, self.device)
         self.a = MoeBwdArgs()
         self.a.glu = int(glu)
         self.a.gate_up_layout = int(gate_up_layout)
@@ -275,7 +287,6 @@ class MoeBwd:
         for k, v in dict(T=T, H=H, I=I, E=E, K=K, block_size=block_size, precision=precision,
                          affinity=affinity, fp8_act=fp8_act, fp8_w=fp8_w, has_bias=int(bool(has_bias))).items():
             setattr(self.a, k, int(v))
-        self.device = torch.device(device)
         size = lib().moe_bwd_workspace_size(ctypes.byref(self.a))
         if size == 0:
             raise MoeError(f"unsupported moe_bwd configuration: {lib().moe_last_error().decode()}")

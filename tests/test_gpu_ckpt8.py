@@ -221,3 +221,22 @@ def test_refusals():
         op.bind(**common, ckpt_q=q).run()
     with pytest.raises(mb.MoeError):
         mb.MoeBwd(**kw, act_src=3)
+
+
+def test_status_word_of_the_caller():
+    mb = _mb()
+    kw = dict(T=8, H=128, I=128, E=2, K=1, block_size=128)
+    for bad in (torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.uint8, device="cuda"),
+                torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")):
+        with pytest.raises(mb.MoeError, match="status"):
+            mb.MoeBwd(**kw, status=bad)
+    inp = _problem(200, 2, 6, 128, 256, 128, PREC_BF16, AFFINITY_ON_H)
+    c8, _ = _grouped(inp, mb, 0)
+    cfg = inp.cfg
+    word = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    op = mb.MoeBwd(T=cfg.T, H=cfg.H, I=cfg.I, E=cfg.E, K=cfg.K, block_size=cfg.block_size, act_src=mb.ACT_CHECKPOINT8,
+                   status=word)
+    op.bind(x=inp.x.cuda(), dout=inp.dout.cuda(), s=inp.s.cuda(), ids=inp.ids.cuda(), W1=inp.W1.cuda(), W2=inp.W2.cuda(),
+            ckpt_q=c8["ckpt_q"], ckpt_sf=c8["ckpt_sf"]).run()
+    torch.cuda.synchronize()
+    assert int(word.item()) == 0

@@ -181,3 +181,14 @@ def test_balance_workspace_of_an_empty_batch(lib, K, E, S):
     """T = 0 is a valid problem, and its workspace size is asked for like any other's."""
     size = lib.moe_balance_workspace_size
     assert 0 < size(0, K, E, S) <= size(1, K, E, S)
+
+
+def test_moe_bwd_refuses_a_status_word_it_cannot_write(lib):
+    """Before anything is allocated, so without a device too."""
+    import torch
+    import moe_expert_layer_routing_gb300 as mb
+    kw = dict(T=8, H=128, I=128, E=2, K=1, block_size=128)
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32),
+                torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(mb.MoeError, match="status must be a CUDA tensor of one int32"):
+            mb.MoeBwd(**kw, status=bad)
