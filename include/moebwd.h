@@ -435,7 +435,8 @@ int moe_balance_bwd(const float* logits, int64_t ld_logits, const float* lse, co
  *   2^-120 keep the step 2^-126).  A group holding a NaN or an infinity gets byte
  *   255 and reads as NaN (in moe_bwd NaN or infinite).  Slots of a 128-slot tile behind the expert's last row
  *   are zeros; tiles without a row are not written.
- * I a multiple of 64 (moe_bwd: of 128); tensors 16-byte aligned.  rows = 0: nothing is written. */
+ * I a multiple of 64 (moe_bwd: of 128); tensors 16-byte aligned, metadata and scores 4-byte.  rows = 0: nothing is
+ * written. */
 int moe_glu_fwd(const void* h, int64_t ldh, int64_t rows, int I, int E, int block_size, int64_t num_blocks, int glu,
                 int gate_up_layout, const int32_t* expert_offsets, const int32_t* block_offsets,
                 const int32_t* block_to_expert, const float* s, const int32_t* s_scatter_idx, int64_t num_slots,

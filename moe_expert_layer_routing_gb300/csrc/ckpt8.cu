@@ -25,6 +25,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "moebwd_internal.h"
 #include "mx_device.cuh"
@@ -328,6 +329,14 @@ static int ckpt8_check(const char* who, int64_t rows, int I, int E, int block_si
   return MOE_OK;
 }
 
+// Routing metadata and scores: single 4-byte elements.
+static int ckpt8_aligned(const char* who, std::initializer_list<const void*> meta) {
+  for (const void* p : meta)
+    if (reinterpret_cast<uintptr_t>(p) & 3)
+      return fail(MOE_ERR_INVALID, "%s: routing metadata and scores must be 4-byte aligned", who);
+  return MOE_OK;
+}
+
 }  // namespace moebwd
 
 using namespace moebwd;
@@ -350,6 +359,7 @@ extern "C" int moe_glu_fwd(const void* h, int64_t ldh, int64_t rows, int I, int 
   if (ldh < 2 * (int64_t)I || ldh % 8) return fail(MOE_ERR_INVALID, "moe_glu_fwd: row stride of h must be a multiple of 8, at least 2I");
   for (const void* q : {h, static_cast<const void*>(a), static_cast<const void*>(ckpt_q), static_cast<const void*>(ckpt_sf)})
     if (reinterpret_cast<uintptr_t>(q) & 15) return fail(MOE_ERR_INVALID, "moe_glu_fwd: tensors must be 16-byte aligned");
+  if ((rc = ckpt8_aligned("moe_glu_fwd", {expert_offsets, block_offsets, block_to_expert, s, s_scatter_idx}))) return rc;
   GluArgs p{};
   p.h = static_cast<const uint16_t*>(h);
   p.ldh = ldh;
@@ -388,6 +398,7 @@ extern "C" int moe_ckpt8_unpack(const int8_t* ckpt_q, const uint8_t* ckpt_sf, in
   if (ldh < 2 * (int64_t)I || ldh % 8) return fail(MOE_ERR_INVALID, "moe_ckpt8_unpack: row stride of h must be a multiple of 8, at least 2I");
   for (const void* q : {static_cast<const void*>(ckpt_q), static_cast<const void*>(ckpt_sf), static_cast<const void*>(h)})
     if (reinterpret_cast<uintptr_t>(q) & 15) return fail(MOE_ERR_INVALID, "moe_ckpt8_unpack: tensors must be 16-byte aligned");
+  if ((rc = ckpt8_aligned("moe_ckpt8_unpack", {expert_offsets, block_offsets, block_to_expert}))) return rc;
   UnpackArgs p{ckpt_q, ckpt_sf, static_cast<uint16_t*>(h), ldh, rows, expert_offsets, block_offsets, block_to_expert, I,
                block_size, E, gate_up_layout == MOE_GATE_UP_INTERLEAVED, tile_shift(block_size)};
   const int64_t grid = (num_blocks << p.tpb_shift) * (I / kGluFeat);

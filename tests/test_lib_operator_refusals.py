@@ -192,3 +192,15 @@ def test_moe_bwd_refuses_a_status_word_it_cannot_write(lib):
                 torch.zeros(0, dtype=torch.int32)):
         with pytest.raises(mb.MoeError, match="status must be a CUDA tensor of one int32"):
             mb.MoeBwd(**kw, status=bad)
+
+
+@pytest.mark.parametrize("which", range(5))
+def test_checkpoint_metadata_alignment(lib, which):
+    """Offsets, block table, scores and their index that are not on a 4-byte boundary are refused on the host."""
+    p = [A] * 5
+    p[which] = A + 2
+    assert lib.moe_glu_fwd(A, 256, 4, 128, 2, 128, 3, 0, 0, *p, 4, A, A, A, None) == INVALID
+    assert b"moe_glu_fwd" in lib.moe_last_error() and b"4-byte" in lib.moe_last_error()
+    if which < 3:
+        assert lib.moe_ckpt8_unpack(A, A, 4, 128, 2, 128, 3, 0, *p[:3], A, 256, None) == INVALID
+        assert b"moe_ckpt8_unpack" in lib.moe_last_error() and b"4-byte" in lib.moe_last_error()
