@@ -390,8 +390,8 @@ size_t moe_balance_workspace_size(int T, int K, int E, int num_seq);
  *   loss (device) fp32 [2]: alpha sum_s (n_s/n) sum_e (E counts_se / (K n_s)) (prob_sum_se / n_s)   (balance)
  *                           beta / n sum_t lse_t^2                                               (z)
  * A token with every expert masked counts in n_s and adds nothing else.
- * status_dev (device, nullable) int32 [1]: reset, then MOE_STATUS_BAD_SEGMENTS for bad offsets (checked with
- * the losses; outputs then invalid, no access leaves its buffer).
+ * status_dev (device, nullable) int32 [1]: reset, then MOE_STATUS_BAD_SEGMENTS for bad offsets, with or without the
+ * losses (outputs are then invalid and may be left unwritten, no access leaves its buffer).
  * 1 <= K <= E <= 1024, K <= 64.  Sums in fp32 in a fixed order (bit-reproducible).  T = 0: counts, prob_sum
  * and loss are zeroed, nothing else is written.  The workspace is only needed with the losses. */
 int moe_router_fwd(int mode, int renorm, const float* logits, int64_t ld_logits, int T, int K, int E,

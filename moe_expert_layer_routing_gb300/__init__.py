@@ -556,7 +556,8 @@ def _balance_outputs(T, K, E, S, dev):
 def router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False, seg_offsets=None, alpha: float = 0.0,
                beta: float = 0.0, balance: bool = True, stream=None) -> dict:
     """moe_router_fwd: top-K of fp32 logits [T, E] (dense rows of any stride).  Returns scores [T, K], ids [T, K],
-    lse [T] and, unless balance is False, counts and prob_sum [num_seq, E], loss [2] = (balance, z) and status."""
+    lse [T] and, unless balance is False, counts and prob_sum [num_seq, E], loss [2] = (balance, z).  With the losses or
+    with seg_offsets also status, int32 [1]: STATUS_BAD_SEGMENTS for bad offsets (the results are then invalid)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return router_fwd(mode, logits, K, renorm, seg_offsets, alpha, beta, balance)
@@ -576,6 +577,9 @@ def router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False, se
         counts, prob, loss, status, ws = _balance_outputs(T, K, E, S, dev)
         out.update(counts=counts, prob_sum=prob, loss=loss, status=status)
         p = [counts.data_ptr(), prob.data_ptr(), loss.data_ptr(), status.data_ptr()]
+    elif off is not None:
+        out["status"] = _new1(1, torch.int32)
+        p[3] = out["status"].data_ptr()
     rc = lib().moe_router_fwd(mode, int(renorm), logits.data_ptr(), ld, T, K, E, off, S, alpha, beta,
                               scores.data_ptr(), ids.data_ptr(), out["lse"].data_ptr(), *p,
                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st)

@@ -294,3 +294,18 @@ def test_pieces_of_many_sequences(S):
         p, c = np.exp(lg[t].astype(np.float64) - np.logaddexp.reduce(lg[t].astype(np.float64))), counts[owner[t]]
         bal, z = A * E / (K * n * lens[owner[t]]) * p, 2 * B / n * np.logaddexp.reduce(lg[t].astype(np.float64)) * p
         assert np.all(np.abs(got[t] - (bal * (c - (c * p).sum()) + z)) <= 2 * _tol(lg, 0) * (bal * (c + (c * p).sum()) + np.abs(z)) + 1e-30)
+
+
+BAD_SEGMENTS = ([0, 300, 200, 500], [-5, 500], [0, 509], [500, 0], [400, 100, 450, 2])
+
+
+def test_selection_without_losses_reports_bad_offsets():
+    mb = _mb()
+    lg = _dev(_logits(500, 16, 4))
+    for seg in BAD_SEGMENTS:
+        out = mb.router_fwd(0, lg, 2, seg_offsets=_t(seg), balance=False)
+        assert int(out["status"].item()) == mb.STATUS_BAD_SEGMENTS, seg
+    good = mb.router_fwd(0, lg, 2, seg_offsets=_t([0, 100, 500]), balance=False)
+    assert int(good["status"].item()) == 0 and set(good) == {"scores", "ids", "lse", "status"}
+    none = mb.router_fwd(0, torch.empty(0, 16, device="cuda"), 2, seg_offsets=_t([0, 0]), balance=False)
+    assert int(none["status"].item()) == 0
