@@ -97,7 +97,7 @@ def main():
         grads = block.backward((diff / T).to(torch.bfloat16), saved)
         block.update(grads, lr=0.02)
         if step % 5 == 0 or step == a.steps - 1:
-            assert int(grads["status"].item()) == 0
+            assert int(grads["status"].item()) == 0 and int(saved["route"]["status"].item()) == 0
             print(f"step {step:3d}  loss {0.5 * diff.square().sum().item() / T:10.4f}  balance {aux[0].item():.5f}  z {aux[1].item():.5f}")
 
 

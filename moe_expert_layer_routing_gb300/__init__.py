@@ -611,12 +611,13 @@ def balance_fwd(logits: torch.Tensor, ids: torch.Tensor, seg_offsets=None, alpha
 
 
 def balance_bwd(logits: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor, K: int, seg_offsets=None,
-                alpha: float = 0.0, beta: float = 0.0, dloss=None, add=None, stream=None) -> torch.Tensor:
+                alpha: float = 0.0, beta: float = 0.0, dloss=None, add=None, stream=None, status=None) -> torch.Tensor:
     """moe_balance_bwd: gradient of dloss[0] * balance + dloss[1] * z by the logits [T, E], plus `add` (e.g.
-    router_bwd's result).  lse and counts are the forward's."""
+    router_bwd's result).  lse and counts are the forward's.  status: an int32 [1] CUDA tensor that the call sets to 0, or
+    to STATUS_BAD_SEGMENTS for bad offsets (the result is then invalid; the forward's status reports the same offsets)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return balance_bwd(logits, lse, counts, K, seg_offsets, alpha, beta, dloss, add)
+            return balance_bwd(logits, lse, counts, K, seg_offsets, alpha, beta, dloss, add, None, status)
     if logits.dim() != 2:
         raise MoeError("logits must be [T, E]")
     T, E = logits.shape
@@ -626,10 +627,11 @@ def balance_bwd(logits: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor, K
     off, S = _segments(seg_offsets, dev)
     lp, cp = _dense(lse, torch.float32, (T,), "lse", dev), _dense(counts, torch.int32, (S, E), "counts", dev)
     dl = _dense(dloss, torch.float32, (2,), "dloss", dev)
+    sp = _dense(status, torch.int32, (1,), "status", dev)
     st = _here(dev)
     out = _new2(T, E, torch.float32)
     rc = lib().moe_balance_bwd(logits.data_ptr(), ld, lp, cp, T, K, E, off, S, alpha, beta, dl,
-                               None if add is None else add.data_ptr(), ld_add, out.data_ptr(), None, st)
+                               None if add is None else add.data_ptr(), ld_add, out.data_ptr(), sp, st)
     _check(rc, "moe_balance_bwd")
     return out
 

@@ -309,3 +309,26 @@ def test_selection_without_losses_reports_bad_offsets():
     assert int(good["status"].item()) == 0 and set(good) == {"scores", "ids", "lse", "status"}
     none = mb.router_fwd(0, torch.empty(0, 16, device="cuda"), 2, seg_offsets=_t([0, 0]), balance=False)
     assert int(none["status"].item()) == 0
+
+
+def test_gradient_reports_bad_offsets():
+    mb = _mb()
+    T, E, K = 500, 16, 2
+    lg = _dev(_logits(T, E, 4))
+    f = mb.router_fwd(0, lg, K, alpha=A, beta=B)
+    word = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    for seg in BAD_SEGMENTS:
+        counts = torch.ones(len(seg) - 1, E, dtype=torch.int32, device="cuda")
+        mb.balance_bwd(lg, f["lse"], counts, K, seg_offsets=_t(seg), alpha=A, beta=B, status=word)
+        assert int(word.item()) == mb.STATUS_BAD_SEGMENTS, seg
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for kw in (dict(), dict(seg_offsets=_t([0, T])), dict(stream=side)):
+        word.fill_(77)
+        torch.cuda.synchronize()
+        d = mb.balance_bwd(lg, f["lse"], f["counts"], K, alpha=A, beta=B, status=word, **kw)
+        torch.cuda.synchronize()
+        assert int(word.item()) == 0 and torch.equal(d, mb.balance_bwd(lg, f["lse"], f["counts"], K, alpha=A, beta=B))
+    for bad in (word.cpu(), word.float(), torch.zeros(2, dtype=torch.int32, device="cuda")):
+        with pytest.raises(mb.MoeError, match="status"):
+            mb.balance_bwd(lg, f["lse"], f["counts"], K, alpha=A, beta=B, status=bad)
