@@ -687,9 +687,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalanceA
 #pragma unroll
     for (int j = 0; j < N; ++j) dot = fmaf(cnt[j], v[j], dot);
     dot = lane_sum<LANES>(dot);
-    const float zt = none ? 0.f : wz * lse;
+    const float wt = none ? 0.f : wb, zt = none ? 0.f : wz * lse;  // (the loss's gradient may be infinite)
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = fmaf(v[j], fmaf(wb, cnt[j] - dot, zt), b[j]);
+    for (int j = 0; j < N; ++j) v[j] = fmaf(v[j], fmaf(wt, cnt[j] - dot, zt), b[j]);
     if (!live) continue;
     float* out = a.dlogits + (int64_t)t * a.E;
 #pragma unroll

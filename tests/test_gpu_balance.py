@@ -332,3 +332,23 @@ def test_gradient_reports_bad_offsets():
     for bad in (word.cpu(), word.float(), torch.zeros(2, dtype=torch.int32, device="cuda")):
         with pytest.raises(mb.MoeError, match="status"):
             mb.balance_bwd(lg, f["lse"], f["counts"], K, alpha=A, beta=B, status=bad)
+
+
+@pytest.mark.parametrize("E", [24, 64, 200, 1000, 33])
+@pytest.mark.parametrize("dl", [(float("inf"), 1.0), (1.0, float("-inf")), (float("nan"), float("nan"))])
+def test_loss_gradients_that_are_not_finite_stay_out_of_padding(E, dl):
+    """Padding tokens and tokens with every expert masked get `add` alone, or 0, whatever the losses' gradient is (an
+    overflow of a scaled loss must not reach what takes no part)."""
+    mb = _mb()
+    T, K = 80, 3
+    lg = _logits(T, E, 3, special=False)
+    lg[20] = -np.inf
+    seg = _t([10, 40, 40, 60])
+    f = mb.router_fwd(0, _dev(lg), K, seg_offsets=seg, alpha=A, beta=B)
+    base = torch.from_numpy(np.random.default_rng(1).standard_normal((T, E)).astype(np.float32)).cuda()
+    out_of_it = torch.tensor([t < 10 or t >= 60 or t == 20 for t in range(T)], device="cuda")
+    for add in (None, base):
+        d = mb.balance_bwd(_dev(lg), f["lse"], f["counts"], K, seg_offsets=seg, alpha=A, beta=B, add=add,
+                           dloss=torch.tensor(dl, device="cuda"))
+        assert torch.equal(d[out_of_it], torch.zeros_like(d[out_of_it]) if add is None else add[out_of_it])
+        assert not torch.isfinite(d[~out_of_it]).all()
