@@ -240,3 +240,103 @@ def test_status_word_of_the_caller():
             ckpt_q=c8["ckpt_q"], ckpt_sf=c8["ckpt_sf"]).run()
     torch.cuda.synchronize()
     assert int(word.item()) == 0
+
+
+def _padding(inp, mb):
+    """[N, B]: slots of the block layout that no row has."""
+    cfg = inp.cfg
+    meta = mb.route_meta(inp.ids.cuda(), cfg.E, cfg.block_size)
+    slot = torch.from_numpy(_slots(meta, inp.ids.numpy(), cfg.E, cfg.block_size)).cuda()
+    N = meta["block_to_expert"].numel()
+    free = torch.ones(N * cfg.block_size, dtype=torch.bool, device="cuda")
+    free[slot] = False
+    return free.reshape(N, cfg.block_size)
+
+
+@pytest.mark.parametrize("precision,affinity,bias,glu,il,I,B,names,opts", [
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 0, 256, 128, ("gate_act_ckpt",), {}),
+    (PREC_BF16, AFFINITY_ON_I, False, 1, 1, 384, 256, ("gate_act_ckpt", "intermediate_ckpt"), {}),
+    (PREC_BF16, AFFINITY_ON_H, True, 0, 0, 256, 256, ("intermediate_ckpt", "down_proj_act_ckpt"), {}),
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 0, 256, 128, ("down_proj_act_ckpt", "gate_act_ckpt"), {"MN_OPERANDS": 0}),
+    (PREC_BF16, AFFINITY_ON_I, False, 0, 0, 128, 512, ("scaled_intermediate_ckpt",), {}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, 384, 128, ("gate_act_ckpt",), {}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 1, 1, 256, 256, ("gate_act_ckpt", "scaled_intermediate_ckpt"), {}),
+    (PREC_MXFP8, AFFINITY_ON_I, True, 0, 0, 256, 128, ("intermediate_ckpt",), {}),
+    (PREC_MXFP8, AFFINITY_ON_H, False, 0, 0, 256, 256, ("intermediate_ckpt", "down_proj_act_ckpt"), {}),
+])
+def test_codes_with_saved_factors(precision, affinity, bias, glu, il, I, B, names, opts, set_option):
+    """The forward's other saved values beside the codes, as beside a bf16 checkpoint of the codes' values: the same bits."""
+    mb = _mb()
+    for k, v in opts.items():
+        set_option(k, v)
+    inp = _problem(260, 2, 6, 128, I, B, precision, affinity, bias)
+    c8, ckpt = _grouped(inp, mb, il)
+    keep = ~_padding(inp, mb)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    saved = {}
+    for n in names:
+        if n == "down_proj_act_ckpt":
+            v = torch.randn(keep.shape[0], B, inp.cfg.H, generator=gen, device="cuda") * keep[..., None]
+        else:
+            v = torch.randn(keep.shape[0], I, B, generator=gen, device="cuda") * keep[:, None]
+        saved[n] = v.to(torch.bfloat16)
+    got = _run(inp, mb, il, glu, ckpt_q=c8["ckpt_q"], ckpt_sf=c8["ckpt_sf"], **saved)
+    ref = _run(inp, mb, il, glu, ckpt=ckpt, **saved)
+    plain = _run(inp, mb, il, glu, ckpt_q=c8["ckpt_q"], ckpt_sf=c8["ckpt_sf"])
+    for k in ("dx", "dW1", "dW2", "ds", "db1", "db2"):
+        if ref[k] is not None:
+            assert torch.isfinite(ref[k]).all() and torch.equal(got[k], ref[k]), k
+    assert not torch.equal(got["dW2"], plain["dW2"])          # the saved values are what was used
+
+
+@pytest.mark.parametrize("precision,affinity,bias,glu,il,I,B,gate_act,opts", [
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 0, 256, 128, False, {}),
+    (PREC_BF16, AFFINITY_ON_I, True, 0, 0, 384, 256, False, {}),
+    (PREC_BF16, AFFINITY_ON_H, True, 1, 0, 256, 128, False, {}),
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 1, 256, 512, False, {}),
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 0, 256, 128, True, {}),
+    (PREC_BF16, AFFINITY_ON_H, True, 0, 0, 256, 256, False, {"MN_OPERANDS": 0}),
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 0, 256, 128, False, {"G1_GATHER": 1}),
+    (PREC_BF16, AFFINITY_ON_H, False, 0, 0, 256, 128, False, {"G1_GATHER": 0}),
+    (PREC_MXFP8, AFFINITY_ON_I, True, 0, 0, 384, 128, False, {}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, 256, 256, False, {}),
+    (PREC_MXFP8, AFFINITY_ON_H, False, 1, 1, 384, 512, False, {}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, 256, 128, True, {}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, 384, 128, False, {"G1_GATHER": 1}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, 384, 128, False, {"G1_GATHER": 0}),
+    (PREC_MXFP8, AFFINITY_ON_I, False, 0, 0, 256, 128, False, {"G1_WARPS": 16, "G1_TILE_N": 128}),
+])
+def test_what_lies_in_padding_slots_does_not_matter(precision, affinity, bias, glu, il, I, B, gate_act, opts, set_option):
+    """NaN and infinities in a bf16 checkpoint's padding slots (a caller's uninitialised memory), any codes behind the last
+    row and scale byte 255 (NaN) for groups without a row: the bits of the zero-padded run."""
+    mb = _mb()
+    for k, v in opts.items():
+        set_option(k, v)
+    inp = _problem(260, 2, 6, 128, I, B, precision, affinity, bias)
+    c8, ckpt = _grouped(inp, mb, il)
+    free = _padding(inp, mb)
+    N = free.shape[0]
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    junk = torch.randint(0, 3, ckpt.shape, generator=gen, device="cuda")
+    junk = torch.tensor([float("nan"), float("inf"), float("-inf")], device="cuda")[junk].to(torch.bfloat16)
+    at = free[:, None, None, :].expand_as(ckpt)
+    bad_ckpt = torch.where(at, junk, ckpt)
+    codes = torch.randint(-128, 128, ckpt.shape, generator=gen, device="cuda").to(torch.int8)
+    bad_q = torch.where(at, codes, c8["ckpt_q"])
+    no_row = free.reshape(N, B // 128, 4, 32).all(-1)[:, None, :, None, :, None].expand_as(c8["ckpt_sf"])
+    bad_sf = torch.where(no_row, torch.full_like(c8["ckpt_sf"], 255), c8["ckpt_sf"])
+    saved, bad_saved = {}, {}
+    if gate_act:
+        v = torch.randn(N, I, B, generator=gen, device="cuda").to(torch.bfloat16)
+        saved["gate_act_ckpt"] = torch.where(free[:, None], torch.zeros_like(v), v)
+        bad_saved["gate_act_ckpt"] = torch.where(free[:, None], junk[:, 0], v)
+    ref = _run(inp, mb, il, glu, ckpt=ckpt, **saved)
+    got = _run(inp, mb, il, glu, ckpt=bad_ckpt, **bad_saved)
+    got8 = _run(inp, mb, il, glu, ckpt_q=bad_q, ckpt_sf=bad_sf, **bad_saved)
+    for k in ("dx", "dW1", "dW2", "ds", "db1", "db2"):
+        if ref[k] is not None:
+            assert torch.isfinite(ref[k]).all() and torch.equal(got[k], ref[k]), k
+            if not opts.get("G1_WARPS"):      # (sixteen warps on the bf16 checkpoint alone: ds in another order)
+                assert torch.equal(got8[k], ref[k]), k
+            else:
+                assert torch.isfinite(got8[k]).all(), k

@@ -273,3 +273,37 @@ def test_calls_back_to_back_on_reused_buffers(T, H, shift):
 
     for a, b in zip(run(False), run(True)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,pad,shift", [(700, 8200, 0, 0), (333, 12288, 8, 0), (97, 16385, 0, 1), (40, 32768, 0, 0)])
+def test_many_wide_rows(dtype, T, H, pad, shift):
+    """Above 8192 columns: several row groups, several rows a warp of a group, column tiles that end inside 32."""
+    test_many_rows(dtype, T, H, pad, shift)
+
+
+@pytest.mark.parametrize("H", [8200, 1024])
+def test_root_mean_square_over_many_rows(H):
+    """The form without a mean: dx and dgamma against automatic differentiation of its formula in float64; dgamma added to
+    an earlier result."""
+    mb = _mb()
+    T = 650
+    x, dy, dres = (_rand((T, H), torch.float32, k) for k in (1, 5, 6))
+    gamma = _rand((1, H), torch.float32, 3)[0]
+    f = mb.layer_norm_fwd(x, gamma, None, eps=EPS, kind=1)
+    b = mb.layer_norm_bwd(dy, x, gamma, None, f["rstd"], dres=dres, kind=1)
+    x64, g64 = x.double().requires_grad_(), gamma.double().requires_grad_()
+    y = x64 * (x64.square().mean(-1, keepdim=True) + EPS).rsqrt() * g64
+    (y * dy.double()).sum().backward()
+    grow = (4 * H + 64) * U * 2
+    y, d = y.detach(), x64.grad + dres.double()
+    xh = x.double() * f["rstd"].double()[:, None]
+    assert torch.all((f["y"].double() - y).abs() <= grow * xh.abs() * gamma.abs().double() + U * y.abs())
+    w = (dy.double() * gamma).abs()
+    parts = f["rstd"].double()[:, None] * (w + xh.abs() * (w * xh.abs()).mean(1, keepdim=True))
+    assert torch.all((b["dx"].double() - d).abs() <= grow * (parts + dres.double().abs()) + U * d.abs())
+    size = (dy.double().abs() * xh.abs()).sum(0)
+    assert torch.all((b["dgamma"].double() - g64.grad).abs() <= (2 * (T + 64) * U + grow) * size)
+    before = b["dgamma"].clone()
+    mb.layer_norm_bwd(dy, x, gamma, None, f["rstd"], dres=dres, kind=1, accumulate_into=b)
+    assert b["dbeta"] is None and torch.equal(b["dgamma"], before + before)
