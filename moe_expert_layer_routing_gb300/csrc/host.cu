@@ -129,7 +129,8 @@ int fork_join(cudaStream_t st, const std::function<int(cudaStream_t)>& side, con
 }
 
 // The dynamic shared memory that kernels were allowed on a device: a fixed table of (kernel, device) with linear
-// probing; a full table only means asking the driver every time.
+// probing; a full table only means asking the driver every time.  An allowance is only ever raised, under a lock: a
+// thread that set a smaller one behind another's back would make the other's launch fail.
 namespace {
 constexpr int kAllowed = 1024;
 struct Allowed {
@@ -137,6 +138,7 @@ struct Allowed {
   std::atomic<size_t> bytes{0};
 };
 Allowed g_allowed[kAllowed];
+std::mutex g_allowed_mu;
 }  // namespace
 
 int allow_smem(const void* kern, size_t bytes, bool again) {
@@ -154,6 +156,12 @@ int allow_smem(const void* kern, size_t bytes, bool again) {
     }
   }
   if (slot && !again && slot->bytes.load(std::memory_order_acquire) >= bytes) return MOE_OK;
+  std::lock_guard<std::mutex> lock(g_allowed_mu);
+  if (slot) {
+    const size_t had = slot->bytes.load(std::memory_order_acquire);
+    if (!again && had >= bytes) return MOE_OK;
+    bytes = bytes > had ? bytes : had;
+  }
   rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
                   "shared memory of a kernel");
   if (!rc && slot) slot->bytes.store(bytes, std::memory_order_release);
