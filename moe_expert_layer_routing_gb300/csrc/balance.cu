@@ -16,10 +16,14 @@
 // counts are one partial row, which a second kernel adds per sequence in a fixed order.
 //
 // The gradient is bound by HBM: 131072 x 256 with `add` moves 403 MB, 59 us at the measured copy rate; measured 62.4 us
-// (6.5 TB/s).  The forward reads 34 MB at 65536 x 128 (5.6 us) and is bound by the selection's integer arithmetic: about
-// 230 warp instructions a token, half of them minima, maxima and logic on the half-rate ALU pipe (busy 47% of the time,
-// issue slots 62%); measured 23 us with the losses (top-8), 10 us with the ids given, and 5 us for the reduction, whose
-// chain of dependent steps is all latency.
+// (6.5 TB/s).  The forward reads 34 MB at 65536 x 128 (5.6 us) and takes 23 us with the losses (top-8), 10 us with the ids
+// given, and 5 us for the reduction, whose chain of dependent steps is all latency.  It is bound by the selection: about
+// 230 warp instructions a token, half of them minima, maxima and logic on the half-rate ALU pipe.  Neither that pipe (busy
+// 48% of the time) nor the issue slots (61%) are full: with 80 registers three blocks are resident, 29% of an SM's warps,
+// and the dependent steps of a token's merges wait for one another.  Top-16 and top-32 in rounds: 56 and 137 us a call.
+//
+// Exponentials and quotients are the approximate instructions (2^-22 of the value): scores, sums and losses come out 6e-8
+// to 7e-8 from float64, where expf and a division give 5e-8 to 6e-8.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -186,9 +190,10 @@ __device__ __noinline__ void topk_exact(const float* row, int E, int K, int sl, 
 // lists 26 us, 24 us with the logits a pass ahead in shared memory and read again after the selection, 23 us with the
 // softmax and its column sums in paired arithmetic.
 //
-// K <= 8 (LIST): a sorted list of the eight largest per lane (a sorting network of 19 comparators per 8 values), then
-// merged with the lists of the lanes 1, 2, 4, ... away: max(a_i, b_7-i) holds the eight largest of both and is
-// bitonic, twelve comparators sort it.  log2(LANES) dependent shuffle steps, all comparators of a level independent.
+// K <= 8 (LIST): a sorted list of the eight largest per lane (a sorting network of 19 comparators in six layers per 8
+// values, the fewest there can be: Knuth, The Art of Computer Programming, volume 3, section 5.3.4), then merged with the
+// lists of the lanes 1, 2, 4, ... away: max(a_i, b_7-i) holds the eight largest of both and is bitonic, and the twelve
+// comparators of Batcher's bitonic merge sort it.  log2(LANES) dependent shuffle steps, all comparators of a level independent.
 // K > 8: rounds of one maximum.  "Smaller than the last" is a subtraction: key - m as unsigned is 2^31 or more
 // exactly for the keys below m.
 __device__ __forceinline__ void sort_desc(uint32_t& a, uint32_t& b) {
@@ -714,7 +719,8 @@ static int bal_bwd_lanes(int E) { return E <= 128 ? 8 : E <= 256 ? 16 : 32; }
 
 // Tokens per chunk, in passes of a CTA's warps.  Forward: one pass, more where the CTAs would not all be resident at
 // once (three on an SM): a CTA leaves E partial sums.  Gradient: two passes, more where the CTAs would be over three
-// times that (131072 x 256: 63.8 us, 66.7 us resident at once).
+// times that (131072 x 256: 63.8 us, 66.7 us resident at once).  8 blocks of each wave on 152 SMs (24 of three) are left
+// for what cutting at sequence boundaries adds: there are up to S + 1 more pieces than chunks.
 static int64_t bal_passes(int T, int lanes, int64_t most) {
   const int step = kBalThreads / lanes;
   return std::max<int64_t>(1, (((int64_t)T + step - 1) / step + most - 1) / most);  // (no tokens: a chunk has a size)

@@ -9,9 +9,10 @@
 //   Every value code 2^(byte - 127) has 7 significant bits: bf16 holds it exactly.
 //
 // Bound by HBM: at 131072 rows x I = 1024 the forward moves 1.08 GB (159 us at the measured copy rate) and the read-back
-// 0.81 GB (120 us).  Measured 177 us (6.1 TB/s) and 119 us (6.8 TB/s).  In moe_bwd the codes take 33/64 of the bf16
-// checkpoint's bytes and cost G1's epilogue their decoding: G1 +5% (BF16, 64 experts), +8% and +12% (MXFP8), the whole
-// pass +2 to +4%.
+// 0.81 GB (120 us).  Measured 177 us (6.1 TB/s) and 119 us (6.8 TB/s); GeGLU's erff takes the forward to 248 us, bound by
+// its arithmetic.  In moe_bwd the codes take 33/64 of the bf16 checkpoint's bytes; what their decoding costs G1 stands at
+// its epilogue (gemm_kernel.cuh), and the whole pass takes 1 to 3% longer (BF16, 64 experts: 2.76 -> 2.79 to 2.84 ms;
+// MXFP8, 128 experts: 3.33 -> 3.37 ms).
 //
 // Layout: codes int8 [N, 2, I, B], the bf16 checkpoint's; scale bytes [N, 2, B/128, I/32, 4, 32], so that the
 // 32 features x 128 rows of a GEMM epilogue's chunk have their bytes in 128 consecutive ones, those of one
@@ -72,7 +73,8 @@ __device__ __forceinline__ int64_t sf_offset(int64_t bu, int tpb_shift, int tb, 
 }
 
 // a = act(g) u scaled by sv, for two (gate, up) pairs: SiLU(g) = g / (1 + e^-g) in paired arithmetic, with the
-// exponential as 2^(-g log2 e) and the approximate reciprocal (2^-22 of the value each); or GELU(g) = g Phi(g).
+// exponential as 2^(-g log2 e) and the approximate reciprocal (2^-22 of the value each, and |g| 2^-24 from rounding the
+// exponent: far below the rounding to bf16 that follows; one value at a time 184 instead of 177 us); or GELU(g) = g Phi(g).
 __device__ __forceinline__ uint32_t glu_pair(uint32_t gw, uint32_t uw, float sv, int glu) {
   const uint64_t g = f2_pack(__uint_as_float(gw << 16), __uint_as_float(gw & 0xffff0000u));
   const uint64_t u = f2_pack(__uint_as_float(uw << 16), __uint_as_float(uw & 0xffff0000u));

@@ -14,10 +14,12 @@
 //
 // Bound by HBM: 65536 x 4096 bf16 with residual / skip gradient moves 2.15 GB each way, 317 us at the measured copy
 // rate of 6.78 TB/s.  Measured: forward 344 us (6.3 TB/s: equal reads and writes), backward with the weight gradients
-// 311 us (6.9 TB/s).  Three passes over each row with the caches' help had taken 747 and 1376 us.  Few rows are
-// bound by latency: 2.7 us (forward) and 5 us (backward, two kernels) for 1 to 64 rows.  Rows that are not whole
-// 16-byte pieces are bound by the shared-memory and store instructions of their single elements: fp32 32768 x 1111
-// at 3.7 to 4.0 TB/s, 16384 x 3001 at 5.4, bf16 (2-byte elements) 32768 x 3001 at 3.6 to 3.8 TB/s.
+// 311 us (6.9 TB/s).  Three passes over each row with the caches' help had taken 747 and 1376 us, and rows above 8192
+// columns still go that way: 16384 x 16384 bf16 without residual or skip gradient 453 us (2.4 TB/s) and 1125 us (1.4
+// TB/s), bound by single-element accesses and the repeated reads.  Few rows are bound by latency: 2.7 us (forward) and
+// 5 us (backward, two kernels) for 1 to 64 rows.  Rows that are not whole 16-byte pieces are bound by the shared-memory
+// and store instructions of their single elements: fp32 32768 x 1111 at 3.7 to 4.0 TB/s, 16384 x 3001 at 5.4, bf16
+// (2-byte elements) 32768 x 3001 at 3.6 to 3.8 TB/s with residual and skip gradient, 2.1 and 3.1 TB/s without.
 #include <cuda_runtime.h>
 
 #include <algorithm>

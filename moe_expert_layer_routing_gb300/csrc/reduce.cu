@@ -1,6 +1,9 @@
 // Reductions after the grouped GEMMs:
 //   dx_scatter_sum   dx[t] = sum_k dx_expanded[row(t,k)]   (sonic-moe _token_broadcast_backward),
-//                    fp32 accumulation in ascending k, 16-byte vector loads, one CTA per token row
+//                    fp32 accumulation in ascending k, 16-byte vector loads, one CTA per token row.  The rows are
+//                    bf16, as G2 stored them: with dh (an operand of the matrix instruction) and dx itself three
+//                    roundings, dx 2.9e-3 from float64 where one rounding is 1.7e-3.  fp32 rows would give 2.4e-3
+//                    and double the bytes that G2 writes and this kernel reads
 //   ds_finalize      ds[f] = sum of the dA-epilogue partials of its row + <dout_t, b2_e>
 //                    (gemm_dgated colvec_reduce and db2_and_ds_kernel)
 //   segment_rowsum   db[e, j] = sum over the tile rows of expert e of buf[j, p] (* w_p)
