@@ -214,9 +214,10 @@ typedef struct MoeBwdArgs {
   const void* gate_up_ckpt; /* (device) bf16 [N,2,I,B] gate/up pre-activation checkpoint in the
                                block layout of moe_route_meta (N = moe_num_blocks_bound):
                                gate of the j-th row of expert e at [blk,0,:,b], up at [blk,1,:,b],
-                               slot blk*B + b = block_offsets[e]*B + j. */
+                               slot blk*B + b = block_offsets[e]*B + j; slots of no row may hold anything. */
 
-  void* dx;     /* (device) bf16 [T,H] */
+  void* dx;     /* (device) bf16 [T,H]: the sum over a token's slots in fp32, of slot rows kept in bf16 between the
+                   GEMMs (BF16 precision: three roundings with dh's, 2.9e-3 from float64) */
   void* dW1;    /* (device) bf16 [E,H,2I] */
   void* dW2;    /* (device) bf16 [E,I,H] */
   float* ds;    /* (device) fp32 [T,K] */
@@ -229,8 +230,9 @@ typedef struct MoeBwdArgs {
   int accumulate;         /* [BW] accumulation / grad-init: 0 overwrites dW1, dW2, db1, db2; 1 adds this
                              pass's gradients to their current contents (bf16 adds for dW, fp32 for db).
                              dx and ds are always overwritten. */
-  int act_src;            /* MOE_ACT_CHECKPOINT (gate_up_ckpt read) or MOE_ACT_RECOMPUTE (gate_up_ckpt
-                             unused, may be NULL; the fields below are read) */
+  int act_src;            /* MOE_ACT_CHECKPOINT (gate_up_ckpt read), MOE_ACT_CHECKPOINT8 (gate_up_ckpt_q and _sf
+                             read) or MOE_ACT_RECOMPUTE (the fields below are read); gate_up_ckpt is unused, may
+                             be NULL, with the last two */
   const void* W1t;        /* (device) RECOMPUTE, BF16: bf16 [E,2I,H], W1 with each expert's block
                              transposed, rows [gate | up] (row j of expert e = column j of the
                              concat-layout W1[e], whatever gate_up_layout) */
