@@ -483,6 +483,39 @@ int layer_norm_bwd(int kind, const void* dy, int64_t lddy, const void* x, int64_
                    size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Gated feed-forward block                                                                     */
+/* ------------------------------------------------------------------------------------------ */
+
+/* Bytes of workspace ffn_fwd needs. */
+size_t ffn_fwd_workspace_size(int64_t T, int64_t H, int64_t I);
+
+/* A dense gated feed-forward block (the shared expert beside the routed ones, moe_bwd's experts without routing):
+ *   h = x W1 + b1,  a = act(gate) * up,  out = a W2 + b2
+ * x (device) bf16 [T,H], row stride ldx (a multiple of 8); W1 bf16 [H,2I], its columns (and those of b1, h) by
+ * gate_up_layout; W2 bf16 [I,H]; b1 [2I], b2 [H] bf16, nullable.  h (device, nullable) bf16 [T,2I]: the pre-activations,
+ * which ffn_bwd reads; NULL where no gradient is wanted.  out (device) bf16 [T,H] dense.
+ * Products accumulate in fp32; a is rounded to bf16 between the two (from the unrounded h), h and out once.
+ * status_dev (device, nullable) int32 [1]: MOE_STATUS_TIMEOUT is OR-ed in (never reset here); outputs then invalid.
+ * H and I multiples of 8, tensors 16-byte aligned, outputs apart from the inputs.  T = 0 writes nothing. */
+int ffn_fwd(const void* x, int64_t ldx, const void* W1, const void* b1, const void* W2, const void* b2, int64_t T, int64_t H,
+            int64_t I, int glu, int gate_up_layout, void* h, void* out, int32_t* status_dev, void* workspace,
+            size_t workspace_bytes, moe_stream_t stream);
+
+/* Bytes of workspace ffn_bwd needs; bias: db1 and db2 wanted. */
+size_t ffn_bwd_workspace_size(int64_t T, int64_t H, int64_t I, int bias);
+
+/* Gradients of ffn_fwd, h being the pre-activations it saved:
+ *   da = dout W2^T, dh = (da up act'(gate), da act(gate)),  dx = dh W1^T,  dW1 = x^T dh,  dW2 = a^T dout,
+ *   db1 = sum_t dh,  db2 = sum_t dout
+ * dout, x (device) bf16 [T,H] with row strides (multiples of 8).  dx, dW1 [H,2I], dW2 [I,H] (device) bf16 dense; db1 [2I],
+ * db2 [H] (device, both or neither) fp32, db1 from the unrounded dh.  dh and a (recomputed from h) are rounded to bf16
+ * between the products, as in moe_bwd.  accumulate = 1 adds to dW1, dW2 (bf16 adds), db1 and db2 (fp32); dx is always
+ * overwritten.  Sums in a fixed order (bit-reproducible).  T = 0: dW and db are zeroed, or left as they are with accumulate. */
+int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t ldx, const void* h, const void* W1, const void* W2,
+            int64_t T, int64_t H, int64_t I, int glu, int gate_up_layout, void* dx, void* dW1, void* dW2, float* db1,
+            float* db2, int accumulate, int32_t* status_dev, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Instrumentation                                                                             */
 /* ------------------------------------------------------------------------------------------ */
 
@@ -561,6 +594,9 @@ enum {
                                 the caller's stream sees both results as before); the persistent CTAs of
                                 one GEMM fill the SMs the other's last wave leaves idle.  0: both on the
                                 caller's stream, one after the other */
+  MOE_OPT_FFN_TILES,         /* ffn_fwd, tiles of a projection: 0 automatic (default: weight-major tiles split along the
+                                contraction where 256 x 256 pair tiles would leave SMs without work), 1 always
+                                weight-major tiles, 2 always pair tiles */
   MOE_NUM_OPTIONS
 };
 /* Set an option; value -1 restores its default.  MOE_ERR_INVALID for an unknown option or value. */

@@ -36,11 +36,13 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_num_blocks_bound", "moe_route_
             "linear_bwd", "moe_profile_enable", "moe_profile_read", "moe_kernel_launches",
             "moe_route_meta_noalloc", "moe_router_bwd", "moe_set_option", "moe_get_option",
             "moe_balance_workspace_size", "moe_router_fwd", "moe_balance_fwd", "moe_balance_bwd", "moe_glu_fwd",
-            "moe_ckpt8_unpack", "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd"]
+            "moe_ckpt8_unpack", "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd",
+            "ffn_fwd_workspace_size", "ffn_fwd", "ffn_bwd_workspace_size", "ffn_bwd"]
 
 # library options (moe_set_option)
 OPTIONS = ["WAIT_LIMIT_NS", "PAIR_GEMMS", "PAIR_TILE_N", "G1_TILE_N", "G2_TILE_N", "G3_TILE_N", "G4_TILE_N",
-           "PREP_TILE_ORDER", "G1_GATHER", "G1_WARPS", "PDL", "MN_OPERANDS", "LINEAR_CONCURRENT"]
+           "PREP_TILE_ORDER", "G1_GATHER", "G1_WARPS", "PDL", "MN_OPERANDS", "LINEAR_CONCURRENT",
+           "FFN_TILES"]
 
 STAGES = ["route", "prep", "G1_dA_dswiglu", "G3_dW2", "G2_dx_expanded", "G4_dW1", "reduce", "G0_recompute_h"]
 
@@ -111,6 +113,10 @@ def lib():
         "layer_norm_bwd_workspace_size": ([i64, i64], sz),
         "layer_norm_bwd": ([i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, i32, i32, i64, i64, vp, vp, vp, i32, vp, sz,
                             vp], i32),
+        "ffn_fwd_workspace_size": ([i64, i64, i64], sz),
+        "ffn_fwd": ([vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp], i32),
+        "ffn_bwd_workspace_size": ([i64, i64, i64, i32], sz),
+        "ffn_bwd": ([vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -704,6 +710,70 @@ def ckpt8_unpack(ckpt_q: torch.Tensor, ckpt_sf: torch.Tensor, route_meta: dict, 
     rc = lib().moe_ckpt8_unpack(qp, sp, rows, I, E, B, Nb, gate_up_layout, eo, bo, b2e, h.data_ptr(), 2 * I, st)
     _check(rc, "moe_ckpt8_unpack")
     return h
+
+
+def _ffn_sizes(x, W1, W2, what):
+    if x.dim() != 2 or W1.dim() != 2 or W2.dim() != 2 or W1.shape[1] % 2:
+        raise MoeError(f"{what}: x must be [T, H], W1 [H, 2I], W2 [I, H]")
+    return x.shape[0], x.shape[1], W1.shape[1] // 2, x.device
+
+
+def ffn_fwd(x, W1, W2, b1=None, b2=None, glu: int = GLU_SWIGLU, gate_up_layout: int = GATE_UP_CONCAT, save: bool = True,
+            status=None, stream=None) -> dict:
+    """ffn_fwd: the gated feed-forward block out = act(gate) * up W2 + b2 with (gate, up) = x W1 + b1 on bf16 rows x [T, H]
+    (dense rows of any stride that is a multiple of 8), W1 [H, 2I], W2 [I, H], b1 [2I], b2 [H].  Returns out [T, H] and,
+    unless save is False, h [T, 2I], the pre-activations that ffn_bwd takes.  status: an int32 [1] CUDA tensor that
+    STATUS_TIMEOUT is OR-ed into."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ffn_fwd(x, W1, W2, b1, b2, glu, gate_up_layout, save, status)
+    T, H, I, dev = _ffn_sizes(x, W1, W2, "ffn_fwd")
+    bf = torch.bfloat16
+    ldx = _rows(x, bf, (T, H), "x", dev)
+    w1, w2 = _dense(W1, bf, (H, 2 * I), "W1", dev), _dense(W2, bf, (I, H), "W2", dev)
+    p1, p2 = _dense(b1, bf, (2 * I,), "b1", dev), _dense(b2, bf, (H,), "b2", dev)
+    sp = _dense(status, torch.int32, (1,), "status", dev)
+    st = _here(dev)
+    out = _new2(T, H, bf)
+    h = _new2(T, 2 * I, bf) if save else None
+    ws = _new1(max(lib().ffn_fwd_workspace_size(T, H, I), 256), torch.uint8)
+    rc = lib().ffn_fwd(x.data_ptr(), ldx, w1, p1, w2, p2, T, H, I, glu, gate_up_layout, None if h is None else h.data_ptr(),
+                       out.data_ptr(), sp, ws.data_ptr(), ws.numel(), st)
+    _check(rc, "ffn_fwd")
+    return dict(out=out, h=h)
+
+
+def ffn_bwd(dout, x, h, W1, W2, bias: bool = False, glu: int = GLU_SWIGLU, gate_up_layout: int = GATE_UP_CONCAT,
+            accumulate_into=None, status=None, stream=None) -> dict:
+    """ffn_bwd: gradients of ffn_fwd from its saved pre-activations h.  Returns dx [T, H], dW1, dW2 in bf16 and, with bias,
+    db1, db2 in fp32.  accumulate_into: an earlier result whose dW1, dW2, db1 and db2 are added to in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ffn_bwd(dout, x, h, W1, W2, bias, glu, gate_up_layout, accumulate_into, status)
+    T, H, I, dev = _ffn_sizes(x, W1, W2, "ffn_bwd")
+    bf, f32 = torch.bfloat16, torch.float32
+    ldx, ldd = _rows(x, bf, (T, H), "x", dev), _rows(dout, bf, (T, H), "dout", dev)
+    hp = _dense(h, bf, (T, 2 * I), "h", dev)
+    w1, w2 = _dense(W1, bf, (H, 2 * I), "W1", dev), _dense(W2, bf, (I, H), "W2", dev)
+    sp = _dense(status, torch.int32, (1,), "status", dev)
+    st = _here(dev)
+    dx = _new2(T, H, bf)
+    if accumulate_into is not None:
+        dW1, dW2, db1, db2 = (accumulate_into[k] for k in ("dW1", "dW2", "db1", "db2"))
+        _dense(dW1, bf, (H, 2 * I), "dW1", dev), _dense(dW2, bf, (I, H), "dW2", dev)
+        _dense(db1, f32, (2 * I,), "db1", dev), _dense(db2, f32, (H,), "db2", dev)
+        if bias != (db1 is not None):
+            raise MoeError("ffn_bwd: accumulate_into was made with another `bias`")
+    else:
+        dW1, dW2 = _new2(H, 2 * I, bf), _new2(I, H, bf)
+        db1, db2 = (_new1(2 * I, f32), _new1(H, f32)) if bias else (None, None)
+    ws = _new1(max(lib().ffn_bwd_workspace_size(T, H, I, int(bias)), 256), torch.uint8)
+    rc = lib().ffn_bwd(dout.data_ptr(), ldd, x.data_ptr(), ldx, hp, w1, w2, T, H, I, glu, gate_up_layout, dx.data_ptr(),
+                       dW1.data_ptr(), dW2.data_ptr(), None if db1 is None else db1.data_ptr(),
+                       None if db2 is None else db2.data_ptr(), int(accumulate_into is not None), sp, ws.data_ptr(), ws.numel(),
+                       st)
+    _check(rc, "ffn_bwd")
+    return dict(dx=dx, dW1=dW1, dW2=dW2, db1=db1, db2=db2)
 
 
 class LinearBwd:

@@ -55,6 +55,7 @@ static const int64_t kOptDefault[MOE_NUM_OPTIONS] = {
     1,                      // MOE_OPT_PDL
     1,                      // MOE_OPT_MN_OPERANDS
     1,                      // MOE_OPT_LINEAR_CONCURRENT
+    0,                      // MOE_OPT_FFN_TILES (automatic)
 };
 static std::once_flag g_opt_once;
 static void opt_init() {
@@ -82,6 +83,7 @@ static bool option_value_ok(int o, int64_t v) {
     case MOE_OPT_PDL:
     case MOE_OPT_MN_OPERANDS:
     case MOE_OPT_LINEAR_CONCURRENT: return v == 0 || v == 1;
+    case MOE_OPT_FFN_TILES: return v >= 0 && v <= 2;
     case MOE_OPT_G1_WARPS: return v == 0 || v == 8 || v == 16;
     default: return false;
   }
