@@ -340,10 +340,11 @@ extern "C" int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t 
     alignas(64) FfnParams P{};
     add_problem(P, T, I, cdiv(I, 256), H, false, false);
     if (!operand(&P.map[0], dout, T, H, lddout, false) || !operand(&P.map[1], W2, I, H, H, false) ||
-        !gate_up_slabs(&P.map[2], h, T, I, inter) || !gate_up_slabs(&P.map[4], dh, T, I, inter) || !slabs(&P.map[6], a, T, I, I))
+        !gate_up_slabs(&P.map[2], h, T, I, inter) || !gate_up_slabs(&P.map[4], dh, T, I, inter))
       return MOE_ERR_INVALID;
-    for (int i = 7; i < kFfnMaps; ++i) P.map[i] = P.map[0];
+    for (int i = 6; i < kFfnMaps; ++i) P.map[i] = P.map[0];
     P.glu = glu; P.interleaved = inter;
+    P.a_out = static_cast<uint16_t*>(a);
     P.db1_part = part1;
     P.zero_counter = counter;
     P.status = status_dev;

@@ -13,8 +13,11 @@
 // no operand is ever copied or transposed.  Sizes off the tile are zero-filled and clipped by the tensor maps.
 //
 // Roles, as in the grouped pair kernel: warp 0 TMA producer (the leader claims tiles and publishes them to both CTAs' rings),
-// warp 1 MMA issue (leader), warps 2-9 epilogue.  The epilogue's two halves (warps 2-5: columns 0-127 of the accumulator,
-// warps 6-9: 128-255, one row of a 32-row quarter a lane) have staging buffers and barriers of their own and never meet.
+// warp 1 MMA issue (leader), warps 2-17 epilogue.  The epilogue's two halves (warps 2-9: columns 0-127 of the accumulator,
+// warps 10-17: 128-255) have staging buffers and barriers of their own and never meet; within a half, two groups of four
+// warps take alternate 32-column pieces, one row of a 32-row quarter a lane.  The epilogues are bound by dependent
+// steps, not by issue: sixteen warps instead of eight (and paired fp32 arithmetic) took the whole of one tile's kFfnDGlu
+// from 27 to %DG us, kFfnGlu from 17 to %GL us.
 // Every wait is bounded; a timeout raises MOE_STATUS_TIMEOUT and the abort flags of both CTAs.
 #pragma once
 #include "gemm_pair_kernel.cuh"
@@ -35,12 +38,13 @@ struct FfnProblem {
 constexpr int kFfnMaps = 9;
 struct FfnParams {
   // kFfnStore: A, B, C of problem i at 3 i.  kFfnGlu: x, Wg, Wu, a, h (gate part), h (up part).
-  // kFfnDGlu: dout, W2, h (gate), h (up), dh (gate), dh (up), a.  Interleaved columns: one matrix, the two parts the same.
+  // kFfnDGlu: dout, W2, h (gate), h (up), dh (gate), dh (up).  Interleaved columns: one matrix, the two parts the same.
   CUtensorMap map[kFfnMaps];
   FfnProblem prob[3];
   int nprob;
   int glu, interleaved, save;
   const uint16_t* b1;     // kFfnGlu: [2I] or null
+  uint16_t* a_out;        // kFfnDGlu: a [T, I]
   float* db1_part;        // kFfnDGlu: [4 * 128-row tiles, 2I] column sums, or null
   int32_t* tile_counter;  // null: tiles in turn; else zero before the launch, dynamic claims
   int32_t* zero_counter;  // set to 0 for the next kernel
@@ -53,11 +57,11 @@ struct FfnCfg {
   static constexpr int BN = 256, BKE = 64;
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int BUF_BYTES = 128 * 128;  // a slab of 128 rows x 64 bf16 columns, 128-byte swizzle
-  // staging slabs of each half: one of C; two to alternate (a, gate, up); gate, up and a at once
-  static constexpr int BUFS = EPI == kFfnStore ? 1 : EPI == kFfnGlu ? 2 : 3;
-  static constexpr int STAGES = EPI == kFfnStore ? 6 : EPI == kFfnGlu ? 5 : 4;
+  // staging slabs of each half: one of C; two to alternate (a, gate, up); gate and up
+  static constexpr int BUFS = EPI == kFfnStore ? 1 : 2;
+  static constexpr int STAGES = EPI == kFfnStore ? 6 : 5;
   static constexpr int RING = 4;
-  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARPS = 16;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int BAR_BYTES = 512;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 2 * BUFS * BUF_BYTES + BAR_BYTES;
@@ -89,14 +93,14 @@ __device__ __forceinline__ FfnTile ffn_decode(const FfnParams& P, int t, int ran
   return ti;
 }
 
-// Barrier over the 128 threads of one epilogue half, and the form that ORs a predicate over them.
-__device__ __forceinline__ void half_bar(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+// Barrier over the 256 threads of one epilogue half, and the form that ORs a predicate over them.
+__device__ __forceinline__ void half_bar(int half) { asm volatile("bar.sync %0, 256;" ::"r"(1 + half) : "memory"); }
 __device__ __forceinline__ bool half_bar_any(int half, bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %2, 0;\n\t"
-      "bar.red.or.pred q, %1, 128, p;\n\t"
+      "bar.red.or.pred q, %1, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(1 + half), "r"((uint32_t)pred)
@@ -131,23 +135,46 @@ __device__ __forceinline__ float glu_value(int glu, float g, float u) {
   if (glu == MOE_GLU_SWIGLU) return g * ffn_sigmoid(g) * u;
   return g * (0.5f * (1.f + erff(g * 0.70710678118654752f))) * u;
 }
-// act(g) and act'(g)
-__device__ __forceinline__ void glu_terms(int glu, float g, float& act, float& slope) {
-  if (glu == MOE_GLU_SWIGLU) {
-    const float s = ffn_sigmoid(g);
-    act = g * s;
-    slope = s * (1.f + g * (1.f - s));
+// Two features' act(g) and act'(g), in paired fp32 arithmetic where the formula allows.
+__device__ __forceinline__ void glu_terms2(int glu, uint64_t G, uint64_t& act, uint64_t& slope) {
+  float g0, g1;
+  if (glu == MOE_GLU_SWIGLU) {  // s = sigma(g): g s and s (1 + g (1 - s))
+    float e0, e1, s0, s1;
+    f2_unpack(f2_mul(G, f2_splat(-1.4426950408889634f)), g0, g1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(g0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(g1));
+    f2_unpack(f2_add(f2_pack(e0, e1), f2_splat(1.f)), g0, g1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(g0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(g1));
+    const uint64_t S = f2_pack(s0, s1);
+    act = f2_mul(G, S);
+    slope = f2_mul(S, f2_fma(G, f2_fma(S, f2_splat(-1.f), f2_splat(1.f)), f2_splat(1.f)));
   } else {
-    const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-    act = g * cdf;
-    slope = cdf + g * (0.39894228040143268f * __expf(-0.5f * g * g));
+    f2_unpack(G, g0, g1);
+    const float c0 = 0.5f * (1.f + erff(g0 * 0.70710678118654752f)), c1 = 0.5f * (1.f + erff(g1 * 0.70710678118654752f));
+    act = f2_pack(g0 * c0, g1 * c1);
+    slope = f2_pack(c0 + g0 * (0.39894228040143268f * __expf(-0.5f * g0 * g0)),
+                    c1 + g1 * (0.39894228040143268f * __expf(-0.5f * g1 * g1)));
   }
 }
 
-// Sum over the warp's 32 rows of each of 32 columns; lane j gets column j's sum.  Halving exchange: 31 shuffles.
-__device__ __forceinline__ float column_sums32(float (&v)[32], int lane) {
+// Two fp32 values rounded to bf16, in one instruction.
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return to_bf16x2(lo, hi);
+}
+
+// Sums over the warp's 32 rows of 8 columns: lanes j, j + 8, j + 16 and j + 24 get column j's.  Three halving exchanges,
+// then two whole ones: 9 shuffles.
+__device__ __forceinline__ float column_sums8(float (&v)[8], int lane) {
 #pragma unroll
-  for (int w = 16; w >= 1; w >>= 1) {
+  for (int w = 4; w >= 1; w >>= 1) {
     const bool hi = lane & w;
 #pragma unroll
     for (int j = 0; j < w; ++j) {
@@ -156,7 +183,8 @@ __device__ __forceinline__ float column_sums32(float (&v)[32], int lane) {
       v[j] = keep + __shfl_xor_sync(0xffffffffu, send, w);
     }
   }
-  return v[0];
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 template <int EPI>
@@ -360,11 +388,12 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
       mbar_wait_drain(done, 0, P.status);
     }
   } else {
-    // ---------------- epilogue warps 2..9 (both CTAs) ----------------
+    // ---------------- epilogue warps 2..17 (both CTAs) ----------------
     const int q = warp & 3;
     const int m = 32 * q + lane;
-    const int half = (warp - 2) >> 2;
-    const bool elect = (warp == 2 || warp == 6) && lane == 0;
+    const int half = (warp - 2) >> 3;
+    const int sub = ((warp - 2) >> 2) & 1;
+    const bool elect = (warp == 2 || warp == 10) && lane == 0;
     uint8_t* buf = smBuf + half * C::BUFS * C::BUF_BYTES;
     const uint32_t row_off = (uint32_t)m * 128;
     const uint32_t sw = (uint32_t)(m & 7);
@@ -429,14 +458,15 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
       };
 
       if constexpr (EPI == kFfnStore) {
-        uint32_t pk[2][32];
+        uint32_t pk[2][16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int sl = 0; sl < 2; ++sl) {
           uint32_t r[32];
-          tmem_ld_32x32b_x32(taddr + half * 128 + c * 32, r);
+          const int c0 = half * 128 + sl * 64 + sub * 32;
+          tmem_ld_32x32b_x32(taddr + c0, r);
           tmem_ld_wait_32(r);
           if (pr.bias) {
-            const int n0 = ti.nt * 256 + half * 128 + c * 32;
+            const int n0 = ti.nt * 256 + c0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               if (n0 + 8 * j >= pr.N) break;  // N is a multiple of 8
@@ -450,8 +480,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
             }
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            pk[c >> 1][(c & 1) * 16 + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          for (int j = 0; j < 16; ++j) pk[sl][j] = to_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
         }
         release();
 #pragma unroll
@@ -460,8 +489,8 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           if (elect) bulk_wait_read_all();
           half_bar(half);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *piece(0, j) = make_uint4(pk[sl][4 * j], pk[sl][4 * j + 1], pk[sl][4 * j + 2], pk[sl][4 * j + 3]);
+          for (int j = 0; j < 4; ++j)
+            *piece(0, 4 * sub + j) = make_uint4(pk[sl][4 * j], pk[sl][4 * j + 1], pk[sl][4 * j + 2], pk[sl][4 * j + 3]);
           fence_proxy_async_smem();
           half_bar(half);
           if (elect && ti.valid && n0 < pr.N) {
@@ -473,15 +502,16 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           }
         }
       } else if constexpr (EPI == kFfnGlu) {
-        // 64 features of this half: pa their a, ph_[0], ph_[1] the 64-column slabs of h
-        uint32_t pa[32], hw[2][32];
+        // 64 features of this half, 32 of them here: pa their a; hw their gate and up (interleaved: 64 columns of h)
+        uint32_t pa[16], hw[32];
         const int f0 = ti.nt * 128 + half * 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 features at a time
+        for (int c = 0; c < 2; ++c) {  // 16 features at a time
+          const int k = sub * 32 + c * 16;
           float g[16], u[16];
           if (P.interleaved) {
             uint32_t r[32];
-            tmem_ld_32x32b_x32(taddr + half * 128 + c * 32, r);
+            tmem_ld_32x32b_x32(taddr + half * 128 + 2 * k, r);
             tmem_ld_wait_32(r);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -490,8 +520,8 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
             }
           } else {
             uint32_t rg[16], ru[16];
-            tmem_ld_32x32b_x16(taddr + half * 64 + c * 16, rg);
-            tmem_ld_32x32b_x16(taddr + 128 + half * 64 + c * 16, ru);
+            tmem_ld_32x32b_x16(taddr + half * 64 + k, rg);
+            tmem_ld_32x32b_x16(taddr + 128 + half * 64 + k, ru);
             tmem_ld_wait_regs<16>(rg);
             tmem_ld_wait_regs<16>(ru);
 #pragma unroll
@@ -503,7 +533,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           if (P.b1) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int f = f0 + c * 16 + 8 * j;
+              const int f = f0 + k + 8 * j;
               if (f >= pr.N) break;  // N = I is a multiple of 8
               const uint16_t* pg = P.interleaved ? P.b1 + 2 * f : P.b1 + f;
               const uint16_t* pu = P.interleaved ? P.b1 + 2 * f + 8 : P.b1 + pr.N + f;
@@ -527,22 +557,22 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            pa[8 * c + j] = pack_bf16x2(glu_value(P.glu, g[2 * j], u[2 * j]), glu_value(P.glu, g[2 * j + 1], u[2 * j + 1]));
+            pa[8 * c + j] = to_bf16x2(glu_value(P.glu, g[2 * j], u[2 * j]), glu_value(P.glu, g[2 * j + 1], u[2 * j + 1]));
             if (P.interleaved) {
-              hw[c >> 1][(c & 1) * 16 + 2 * j] = pack_bf16x2(g[2 * j], u[2 * j]);
-              hw[c >> 1][(c & 1) * 16 + 2 * j + 1] = pack_bf16x2(g[2 * j + 1], u[2 * j + 1]);
+              hw[16 * c + 2 * j] = to_bf16x2(g[2 * j], u[2 * j]);
+              hw[16 * c + 2 * j + 1] = to_bf16x2(g[2 * j + 1], u[2 * j + 1]);
             } else {
-              hw[0][8 * c + j] = pack_bf16x2(g[2 * j], g[2 * j + 1]);
-              hw[1][8 * c + j] = pack_bf16x2(u[2 * j], u[2 * j + 1]);
+              hw[8 * c + j] = to_bf16x2(g[2 * j], g[2 * j + 1]);
+              hw[16 + 8 * c + j] = to_bf16x2(u[2 * j], u[2 * j + 1]);
             }
           }
         }
         release();
-        auto put = [&](const uint32_t (&w)[32], const CUtensorMap* map, int col, int cols) {
+        // `fill` writes this thread's pieces of a slab, which then goes to columns `col` ..
+        auto put = [&](auto fill, const CUtensorMap* map, int col, int cols) {
           if (elect) bulk_wait_read<1>();  // the slab before the last has been read: this buffer is free
           half_bar(half);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) *piece(slot, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          fill();
           fence_proxy_async_smem();
           half_bar(half);
           if (elect) {
@@ -551,19 +581,36 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           }
           slot ^= 1;
         };
-        put(pa, &P.map[3], f0, pr.N);
+        put([&]() {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *piece(slot, 4 * sub + j) = make_uint4(pa[4 * j], pa[4 * j + 1], pa[4 * j + 2], pa[4 * j + 3]);
+        }, &P.map[3], f0, pr.N);
         if (P.save) {
-          if (P.interleaved) {
-            put(hw[0], &P.map[4], 2 * f0, 2 * pr.N);
-            put(hw[1], &P.map[5], 2 * f0 + 64, 2 * pr.N);
-          } else {
-            put(hw[0], &P.map[4], f0, pr.N);
-            put(hw[1], &P.map[5], f0, pr.N);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const int col = P.interleaved ? 2 * f0 + 64 * part : f0;
+            put([&]() {
+              if (P.interleaved) {  // a slab is one group's 32 features
+                if (sub == part) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    *piece(slot, j) = make_uint4(hw[4 * j], hw[4 * j + 1], hw[4 * j + 2], hw[4 * j + 3]);
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  *piece(slot, 4 * sub + j) = make_uint4(hw[16 * part + 4 * j], hw[16 * part + 4 * j + 1],
+                                                         hw[16 * part + 4 * j + 2], hw[16 * part + 4 * j + 3]);
+              }
+            }, &P.map[4 + part], col, P.interleaved ? 2 * pr.N : pr.N);
           }
         }
       } else {
         bool gone = false;
-#pragma unroll
+        const bool mine = row0 + m < pr.M;
+        uint16_t* a_row = P.a_out + (int64_t)(row0 + m) * pr.N;
+#pragma unroll 1
         for (int sl = 0; sl < 2; ++sl) {
           const int f0 = ti.nt * 256 + half * 128 + sl * 64;
           if (sl == 1 && elect) {
@@ -580,60 +627,60 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
             break;
           }
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {  // 32 features
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(taddr + half * 128 + sl * 64 + c * 32, r);
-            tmem_ld_wait_32(r);
+          for (int c = 0; c < 2; ++c) {  // 16 features at a time
+            const int k = sub * 32 + c * 16;
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(taddr + half * 128 + sl * 64 + k, r);
+            tmem_ld_wait_regs<16>(r);
             if (sl == 1 && c == 1) release();
-            float dg[32], du[32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // 8 features: 16 bytes of gate and of up, or 32 interleaved
-              // interleaved: columns 2 f .. of features 32 c + 8 j .. : slab c, pieces 2 j and 2 j + 1
-              uint4* p0 = P.interleaved ? piece(c, 2 * j) : piece(0, 4 * c + j);
-              uint4* p1 = P.interleaved ? piece(c, 2 * j + 1) : piece(1, 4 * c + j);
+            for (int j = 0; j < 2; ++j) {  // 8 features: 16 bytes of gate and of up, or 32 interleaved
+              const int f = f0 + k + 8 * j;
+              const int i0 = 2 * c + j;  // eighth of the group's 32 features
+              uint4* p0 = P.interleaved ? piece(sub, 2 * i0) : piece(0, 4 * sub + i0);
+              uint4* p1 = P.interleaved ? piece(sub, 2 * i0 + 1) : piece(1, 4 * sub + i0);
               const uint4 x = *p0, y = *p1;
               const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-              float a[8];
+              uint32_t wa[4], wg[4], wu[4];
+              float dg[8], du[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float g, u;
+              for (int i = 0; i < 4; ++i) {  // features 2 i and 2 i + 1
+                const uint64_t G = P.interleaved ? f2_pack(bf_lo(w[2 * i]), bf_lo(w[2 * i + 1])) : f2_pack(bf_lo(w[i]), bf_hi(w[i]));
+                const uint64_t Up = P.interleaved ? f2_pack(bf_hi(w[2 * i]), bf_hi(w[2 * i + 1]))
+                                                  : f2_pack(bf_lo(w[4 + i]), bf_hi(w[4 + i]));
+                uint64_t act, slope;
+                glu_terms2(P.glu, G, act, slope);
+                const uint64_t da = f2_pack(__uint_as_float(r[8 * j + 2 * i]), __uint_as_float(r[8 * j + 2 * i + 1]));
+                wa[i] = to_bf16x2(f2_mul(act, Up));
+                f2_unpack(f2_mul(f2_mul(da, Up), slope), dg[2 * i], dg[2 * i + 1]);
+                f2_unpack(f2_mul(da, act), du[2 * i], du[2 * i + 1]);
                 if (P.interleaved) {
-                  g = bf_lo(w[i]);
-                  u = bf_hi(w[i]);
+                  wg[i] = to_bf16x2(dg[2 * i], du[2 * i]);
+                  wu[i] = to_bf16x2(dg[2 * i + 1], du[2 * i + 1]);
                 } else {
-                  g = (i & 1) ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
-                  u = (i & 1) ? bf_hi(w[4 + (i >> 1)]) : bf_lo(w[4 + (i >> 1)]);
+                  wg[i] = to_bf16x2(dg[2 * i], dg[2 * i + 1]);
+                  wu[i] = to_bf16x2(du[2 * i], du[2 * i + 1]);
                 }
-                float act, slope;
-                glu_terms(P.glu, g, act, slope);
-                const float da = __uint_as_float(r[8 * j + i]);
-                a[i] = act * u;
-                dg[8 * j + i] = da * u * slope;
-                du[8 * j + i] = da * act;
               }
-              const float* G = dg + 8 * j;
-              const float* U = du + 8 * j;
               if (P.interleaved) {
-                *p0 = make_uint4(pack_bf16x2(G[0], U[0]), pack_bf16x2(G[1], U[1]), pack_bf16x2(G[2], U[2]),
-                                 pack_bf16x2(G[3], U[3]));
-                *p1 = make_uint4(pack_bf16x2(G[4], U[4]), pack_bf16x2(G[5], U[5]), pack_bf16x2(G[6], U[6]),
-                                 pack_bf16x2(G[7], U[7]));
+                *p0 = make_uint4(wg[0], wu[0], wg[1], wu[1]);
+                *p1 = make_uint4(wg[2], wu[2], wg[3], wu[3]);
               } else {
-                *p0 = make_uint4(pack_bf16x2(G[0], G[1]), pack_bf16x2(G[2], G[3]), pack_bf16x2(G[4], G[5]),
-                                 pack_bf16x2(G[6], G[7]));
-                *p1 = make_uint4(pack_bf16x2(U[0], U[1]), pack_bf16x2(U[2], U[3]), pack_bf16x2(U[4], U[5]),
-                                 pack_bf16x2(U[6], U[7]));
+                *p0 = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+                *p1 = make_uint4(wu[0], wu[1], wu[2], wu[3]);
               }
-              *piece(2, 4 * c + j) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                                                pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
-            }
-            if (P.db1_part) {  // sums of the unrounded values over this warp's 32 rows
-              const float sg = column_sums32(dg, lane), su = column_sums32(du, lane);
-              const int f = f0 + c * 32 + lane;
-              if (ti.valid && f < pr.N) {
-                float* dst = P.db1_part + ((int64_t)ti.mt * 4 + q) * 2 * pr.N;
-                dst[P.interleaved ? 2 * f : f] = sg;
-                dst[P.interleaved ? 2 * f + 1 : pr.N + f] = su;
+              // a straight from registers: a lane's 32 bytes (both j) fill a sector, and no slab is needed for it
+              if (mine && f < pr.N) *reinterpret_cast<uint4*>(a_row + f) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+              if (P.db1_part) {  // sums of the unrounded values over this warp's 32 rows
+                const float sg = column_sums8(dg, lane), su = column_sums8(du, lane);
+                if (ti.valid && f < pr.N && lane < 16) {
+                  float* dst = P.db1_part + ((int64_t)ti.mt * 4 + q) * 2 * pr.N;
+                  const int fl = f + (lane & 7);
+                  if (lane < 8)
+                    dst[P.interleaved ? 2 * fl : fl] = sg;
+                  else
+                    dst[P.interleaved ? 2 * fl + 1 : pr.N + fl] = su;
+                }
               }
             }
           }
@@ -644,7 +691,6 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
             tma_store_2d(&P.map[4], buf, c, row0);
             if (!P.interleaved || c + 64 < 2 * pr.N)
               tma_store_2d(&P.map[5], buf + C::BUF_BYTES, P.interleaved ? c + 64 : c, row0);
-            tma_store_2d(&P.map[6], buf + 2 * C::BUF_BYTES, f0, row0);
             bulk_commit();
           }
         }

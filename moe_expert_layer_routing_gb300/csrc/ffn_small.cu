@@ -13,6 +13,7 @@
 // own start), so that only the activations' arrival is left on its critical path.
 #include <cuda.h>
 #include <algorithm>
+#include <type_traits>
 
 #include "ffn_kernel.cuh"
 #include "ffn.h"
@@ -33,7 +34,7 @@ struct SmallParams {
   uint64_t wait_ns;
 };
 
-constexpr int kSmallThreads = 192;
+constexpr int kSmallThreads = 320;  // producer, MMA issue, eight warps that empty the accumulator; all of them sum
 constexpr int kSmallABytes = 128 * 128;
 constexpr int kSmallMaxStages = 8;
 
@@ -46,7 +47,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
   return v;
 }
 
-template <bool GLU>
+template <bool GLU, int SPLIT>
 __global__ void __launch_bounds__(kSmallThreads, 1) ffn_small_kernel(const __grid_constant__ SmallParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -60,9 +61,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ffn_small_kernel(const __gri
   float* part = reinterpret_cast<float*>(stages);  // [nt][128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t split;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
-  const uint32_t rank = cluster_ctarank();
+  constexpr uint32_t split = SPLIT;
+  const uint32_t rank = SPLIT > 1 ? cluster_ctarank() : 0;
   const int tile = blockIdx.x / split;
   const int t0 = blockIdx.y * P.nt;
   const int kb0 = (int)((int64_t)P.nk * rank / split);
@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ffn_small_kernel(const __gri
   pdl_wait();  // every thread: outputs (and the bias) belong to earlier work until here
   __syncthreads();  // the products are in TMEM, no copy is in flight
   tc_fence_after();
-  if (warp >= 2) {  // lane quarter `warp & 3`: weight columns 32 q + lane, one token a TMEM column
-    const int q = warp & 3;
+  if (warp >= 2) {  // lane quarter `warp & 3`: weight columns 32 q + lane, one token a TMEM column; two warps a quarter
+    const int q = warp & 3, sub = (warp - 2) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16);
-    for (int c = 0; c < P.nt; c += 16) {
+    for (int c = 16 * sub; c < P.nt; c += 32) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(taddr + c, r);
       tmem_ld_wait_regs<16>(r);
@@ -166,77 +166,90 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ffn_small_kernel(const __gri
     }
   }
   tc_fence_before();
-  cluster_sync_all();  // every CTA's partial tile is complete
+  if (SPLIT > 1)
+    cluster_sync_all();  // every CTA's partial tile is complete
+  else
+    __syncthreads();
 
-  // 8 output columns of one token a thread; the cluster's CTAs take turns
-  const int pieces = GLU ? 8 : 16;
+  // 4 output columns of one token a thread: a warp reads whole rows of partial tiles; the cluster's CTAs take turns
+  constexpr int kPieces = GLU ? 16 : 32, V = GLU ? 8 : 4;
   const int tokens = P.T - t0 < P.nt ? P.T - t0 : P.nt;
-  for (int i = (int)rank * kSmallThreads + threadIdx.x; i < tokens * pieces; i += (int)split * kSmallThreads) {
-    const int tok = i / pieces, pc = i - tok * pieces;
-    // floats of the tile row: with GLU 16 of them (gate 8 pc .. and up 64 + 8 pc .., or interleaved 16 pc ..)
-    const int o0 = GLU && P.interleaved ? 16 * pc : 8 * pc;
-    const int o1 = GLU && !P.interleaved ? 64 + 8 * pc : o0 + 8;
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  for (int i = (int)rank * kSmallThreads + threadIdx.x; i < tokens * kPieces; i += (int)split * kSmallThreads) {
+    const int tok = i / kPieces, pc = i % kPieces;
+    // floats of the tile row: with GLU 8 of them (gate 4 pc .. and up 64 + 4 pc .., or interleaved 8 pc ..)
+    const int o0 = GLU && P.interleaved ? 8 * pc : 4 * pc;
+    const int o1 = GLU && !P.interleaved ? 64 + 4 * pc : o0 + 4;
+    float v[V];
+    float4 f[SPLIT][V / 4];
     const uint32_t base = smem_u32(part + tok * 128);
-    for (uint32_t r = 0; r < split; ++r) {
-      const uint32_t pb = mapa_shared(base, r);
 #pragma unroll
-      for (int j = 0; j < (GLU ? 4 : 2); ++j) {
-        const float4 f = ld_cluster_f4(pb + 4 * ((j < 2 ? o0 : o1) + 4 * (j & 1)));
-        v[4 * j] += f.x;
-        v[4 * j + 1] += f.y;
-        v[4 * j + 2] += f.z;
-        v[4 * j + 3] += f.w;
+    for (uint32_t r = 0; r < split; ++r) {
+      const uint32_t pb = SPLIT > 1 ? mapa_shared(base, r) : base;
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j)
+        f[r][j] = SPLIT > 1 ? ld_cluster_f4(pb + 4 * (j ? o1 : o0))
+                            : *reinterpret_cast<const float4*>(part + tok * 128 + (j ? o1 : o0));
+    }
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      v[4 * j] = f[0][j].x;
+      v[4 * j + 1] = f[0][j].y;
+      v[4 * j + 2] = f[0][j].z;
+      v[4 * j + 3] = f[0][j].w;
+#pragma unroll
+      for (uint32_t r = 1; r < split; ++r) {
+        v[4 * j] += f[r][j].x;
+        v[4 * j + 1] += f[r][j].y;
+        v[4 * j + 2] += f[r][j].z;
+        v[4 * j + 3] += f[r][j].w;
       }
     }
-    const int col = tile * (GLU ? 64 : 128) + 8 * pc;
+    const int col = tile * (GLU ? 64 : 128) + 4 * pc;
     if (col >= P.N) continue;  // N is a multiple of 8
     const int64_t row = t0 + tok;
-    auto add8 = [&](float* d, const uint16_t* b) {
-      const uint4 x = *reinterpret_cast<const uint4*>(b);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[2 * j] += bf_lo(w[j]);
-        d[2 * j + 1] += bf_hi(w[j]);
-      }
+    auto add4 = [&](float* d, const uint16_t* b) {
+      const uint2 x = *reinterpret_cast<const uint2*>(b);
+      d[0] += bf_lo(x.x);
+      d[1] += bf_hi(x.x);
+      d[2] += bf_lo(x.y);
+      d[3] += bf_hi(x.y);
     };
-    auto pack8 = [](const float* d) {
-      return make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7]));
-    };
+    auto pack4 = [](const float* d) { return make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])); };
     if constexpr (GLU) {
       if (P.bias) {
-        add8(v, P.bias + (P.interleaved ? 2 * col : col));
-        add8(v + 8, P.bias + (P.interleaved ? 2 * col + 8 : P.N + col));
+        add4(v, P.bias + (P.interleaved ? 2 * col : col));
+        add4(v + 4, P.bias + (P.interleaved ? 2 * col + 4 : P.N + col));
       }
-      float a[8];
+      float a[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        a[j] = P.interleaved ? glu_value(P.glu, v[2 * j], v[2 * j + 1]) : glu_value(P.glu, v[j], v[8 + j]);
-      *reinterpret_cast<uint4*>(P.out + row * P.N + col) = pack8(a);
+      for (int j = 0; j < 4; ++j)
+        a[j] = P.interleaved ? glu_value(P.glu, v[2 * j], v[2 * j + 1]) : glu_value(P.glu, v[j], v[4 + j]);
+      *reinterpret_cast<uint2*>(P.out + row * P.N + col) = pack4(a);
       if (P.h) {
         uint16_t* h = P.h + row * 2 * P.N;
-        *reinterpret_cast<uint4*>(h + (P.interleaved ? 2 * col : col)) = pack8(v);
-        *reinterpret_cast<uint4*>(h + (P.interleaved ? 2 * col + 8 : P.N + col)) = pack8(v + 8);
+        *reinterpret_cast<uint2*>(h + (P.interleaved ? 2 * col : col)) = pack4(v);
+        *reinterpret_cast<uint2*>(h + (P.interleaved ? 2 * col + 4 : P.N + col)) = pack4(v + 4);
       }
     } else {
-      if (P.bias) add8(v, P.bias + col);
-      *reinterpret_cast<uint4*>(P.out + row * P.N + col) = pack8(v);
+      if (P.bias) add4(v, P.bias + col);
+      *reinterpret_cast<uint2*>(P.out + row * P.N + col) = pack4(v);
     }
   }
   __syncwarp();
-  cluster_sync_all();  // no CTA leaves while a peer may still read its partial tile
+  if (SPLIT > 1)
+    cluster_sync_all();  // no CTA leaves while a peer may still read its partial tile
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, tmem_cols);
   }
 }
 
-template <bool GLU>
-int launch_small(const SmallParams& P, int tiles, int token_tiles, int split, cudaStream_t st) {
-  auto kern = ffn_small_kernel<GLU>;
+template <bool GLU, int SPLIT>
+int launch_small(const SmallParams& P, int tiles, int token_tiles, cudaStream_t st) {
+  auto kern = ffn_small_kernel<GLU, SPLIT>;
+  constexpr int split = SPLIT;
   const size_t smem = 2048 + std::max<size_t>((size_t)P.stages * (kSmallABytes + P.nt * 128), (size_t)P.nt * 512);
   int rc = allow_smem(reinterpret_cast<const void*>(kern), kSmemLimit);
   if (rc) return rc;
@@ -300,8 +313,17 @@ int launch_ffn_small(bool glu_kernel, const SmallPlan& pl, const FfnSmallArgs& a
   P.h = a.h;
   P.status = a.status;
   P.wait_ns = (uint64_t)option(MOE_OPT_WAIT_LIMIT_NS);
-  return glu_kernel ? launch_small<true>(P, (int)pl.tiles, (int)pl.token_tiles, pl.split, st)
-                    : launch_small<false>(P, (int)pl.tiles, (int)pl.token_tiles, pl.split, st);
+  auto go = [&](auto s) {
+    constexpr int S = decltype(s)::value;
+    return glu_kernel ? launch_small<true, S>(P, (int)pl.tiles, (int)pl.token_tiles, st)
+                      : launch_small<false, S>(P, (int)pl.tiles, (int)pl.token_tiles, st);
+  };
+  switch (pl.split) {
+    case 1: return go(std::integral_constant<int, 1>());
+    case 2: return go(std::integral_constant<int, 2>());
+    case 4: return go(std::integral_constant<int, 4>());
+    default: return go(std::integral_constant<int, 8>());
+  }
 }
 
 }  // namespace moebwd
