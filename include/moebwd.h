@@ -516,6 +516,25 @@ int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t ldx, const 
             float* db2, int accumulate, int32_t* status_dev, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Dropout                                                                                      */
+/* ------------------------------------------------------------------------------------------ */
+
+/* y = residual + keep x / (1 - p): dropout of a branch on its way to the residual stream, its mask never stored.
+ * keep(t,j) of row t and column j: word j % 4 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
+ * easy as 1, 2, 3", SC'11) on the counter (j / 4, t, offset low, offset high) under the key (seed low, seed high) is at
+ * least min(round(p 2^32), 2^32 - 1).  offset_dev (device, nullable) int64 [1] is added to offset: a captured call
+ * draws another mask at each replay.  Calls that are to be independent take different offsets (or seeds), a
+ * backward its forward's.
+ * x, residual (device, residual nullable) dtype [T,H] with row strides; y (device) dtype [T,H] dense; it may be x or residual
+ * itself when that is dense.  0 <= p < 1; a dropped value is 0 whatever x holds.  fp32 arithmetic, y rounded once. */
+int dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, int64_t T, int64_t H, double p,
+                uint64_t seed, uint64_t offset, const int64_t* offset_dev, void* y, moe_stream_t stream);
+
+/* dx = keep dy / (1 - p) (the residual's gradient is dy itself).  dx may be dy when that is dense. */
+int dropout_bwd(const void* dy, int64_t lddy, int dtype, int64_t T, int64_t H, double p, uint64_t seed, uint64_t offset,
+                const int64_t* offset_dev, void* dx, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Instrumentation                                                                             */
 /* ------------------------------------------------------------------------------------------ */
 

@@ -37,7 +37,8 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_num_blocks_bound", "moe_route_
             "moe_route_meta_noalloc", "moe_router_bwd", "moe_set_option", "moe_get_option",
             "moe_balance_workspace_size", "moe_router_fwd", "moe_balance_fwd", "moe_balance_bwd", "moe_glu_fwd",
             "moe_ckpt8_unpack", "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd",
-            "ffn_fwd_workspace_size", "ffn_fwd", "ffn_bwd_workspace_size", "ffn_bwd"]
+            "ffn_fwd_workspace_size", "ffn_fwd", "ffn_bwd_workspace_size", "ffn_bwd",
+            "dropout_fwd", "dropout_bwd"]
 
 # library options (moe_set_option)
 OPTIONS = ["WAIT_LIMIT_NS", "PAIR_GEMMS", "PAIR_TILE_N", "G1_TILE_N", "G2_TILE_N", "G3_TILE_N", "G4_TILE_N",
@@ -82,6 +83,7 @@ def lib():
         raise MoeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    f64, u64 = ctypes.c_double, ctypes.c_uint64
     sig = {
         "moe_last_error": ([], ctypes.c_char_p),
         "moe_version": ([], ctypes.c_char_p),
@@ -117,6 +119,8 @@ def lib():
         "ffn_fwd": ([vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp], i32),
         "ffn_bwd_workspace_size": ([i64, i64, i64, i32], sz),
         "ffn_bwd": ([vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp], i32),
+        "dropout_fwd": ([vp, i64, vp, i64, i32, i64, i64, f64, u64, u64, vp, vp, vp], i32),
+        "dropout_bwd": ([vp, i64, i32, i64, i64, f64, u64, u64, vp, vp, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -774,6 +778,53 @@ def ffn_bwd(dout, x, h, W1, W2, bias: bool = False, glu: int = GLU_SWIGLU, gate_
                        st)
     _check(rc, "ffn_bwd")
     return dict(dx=dx, dW1=dW1, dW2=dW2, db1=db1, db2=db2)
+
+
+def _dropout_args(x, seed, offset, what):
+    if x.dim() != 2 or x.dtype not in _DT:
+        raise MoeError(f"{what}: rows must be bfloat16 or float32 [T, H]")
+    at = 0
+    dev = x.device
+    p = None
+    if isinstance(offset, torch.Tensor):
+        p = _dense(offset, torch.int64, (1,), "offset", dev)
+    else:
+        at = offset
+    if not 0 <= seed < 1 << 64 or not 0 <= at < 1 << 64:
+        raise MoeError(f"{what}: seed and offset must be in [0, 2^64)")
+    return x.shape[0], x.shape[1], dev, at, p
+
+
+def dropout_fwd(x, p: float, seed: int, offset=0, residual=None, stream=None) -> torch.Tensor:
+    """dropout_fwd: residual + keep * x / (1 - p) on bf16 or fp32 rows [T, H] (dense rows of any stride).  The mask is a
+    function of (seed, offset, row, column); offset: an int, or an int64 [1] CUDA tensor that is read when the call runs
+    (captured calls then draw a new mask whenever it has changed).  The backward takes the same seed and offset."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dropout_fwd(x, p, seed, offset, residual)
+    T, H, dev, at, op = _dropout_args(x, seed, offset, "dropout_fwd")
+    ldx = _rows(x, x.dtype, (T, H), "x", dev)
+    ldr = 0 if residual is None else _rows(residual, x.dtype, (T, H), "residual", dev)
+    st = _here(dev)
+    y = _new2(T, H, x.dtype)
+    rc = lib().dropout_fwd(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, _DT[x.dtype], T, H, p,
+                           seed, at, op, y.data_ptr(), st)
+    _check(rc, "dropout_fwd")
+    return y
+
+
+def dropout_bwd(dy, p: float, seed: int, offset=0, stream=None) -> torch.Tensor:
+    """dropout_bwd: gradient of dropout_fwd by x (the residual's is dy itself), from the forward's seed and offset."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dropout_bwd(dy, p, seed, offset)
+    T, H, dev, at, op = _dropout_args(dy, seed, offset, "dropout_bwd")
+    ld = _rows(dy, dy.dtype, (T, H), "dy", dev)
+    st = _here(dev)
+    dx = _new2(T, H, dy.dtype)
+    rc = lib().dropout_bwd(dy.data_ptr(), ld, _DT[dy.dtype], T, H, p, seed, at, op, dx.data_ptr(), st)
+    _check(rc, "dropout_bwd")
+    return dx
 
 
 class LinearBwd:

@@ -141,8 +141,12 @@ int launch_pair(FfnParams& P, cudaStream_t st) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// operand [rows, K] (box 128 rows x 64) or [K, rows] (box 64 x 64)
+// operand [rows, K] (box 128 rows x 64) or [K, rows]: 64 x 128 in one copy where its columns are whole groups of 64, else
+// two boxes of 64 x 64.  One producer thread issues every copy, and with three or four a k-block its issue bounds the
+// kernel.
+int mn_of(int64_t cols) { return cols % 64 ? 1 : 2; }
 bool operand(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, bool mn) {
+  if (mn && mn_of(cols) == 2) return make_tmap_groups(m, p, (uint64_t)rows, (uint64_t)cols, (uint64_t)ld * 2, 64, 2);
   return make_tmap_2d(m, p, 2, (uint64_t)rows, (uint64_t)cols, (uint64_t)ld * 2, mn ? 64 : 128, 64);
 }
 // a matrix moved in slabs of 128 rows x 64 columns
@@ -156,7 +160,7 @@ bool gate_up_slabs(CUtensorMap* m, const void* p, int64_t rows, int64_t I, bool 
                      : slabs(m, b, rows, I, 2 * I) && slabs(m + 1, b + I, rows, I, 2 * I);
 }
 
-void add_problem(FfnParams& P, int64_t rows, int64_t cols, int64_t n_tiles, int64_t K, bool a_mn, bool b_mn) {
+void add_problem(FfnParams& P, int64_t rows, int64_t cols, int64_t n_tiles, int64_t K, int a_mn, int b_mn) {
   FfnProblem& p = P.prob[P.nprob];
   const int64_t before = P.nprob ? P.prob[P.nprob - 1].end : 0;
   p.n_tiles = (int)n_tiles;
@@ -169,12 +173,15 @@ void add_problem(FfnParams& P, int64_t rows, int64_t cols, int64_t n_tiles, int6
   ++P.nprob;
 }
 
-// Whether a projection runs on ffn_small_kernel: where its 256 x 256 pair tiles would leave more than half of the SMs
-// without work.
-bool few_tiles(int64_t T, int64_t columns) {
+// Whether a projection of T rows runs on ffn_small_kernel (tiles as `plan` says) or on pair tiles.  Pair tiles: 7.5 us of
+// launch, latency and epilogue, 0.36 a k-block in each wave of tiles (fitted like small_plan's estimate).  Measured on both
+// sides of the border, H 2048, I 1024, forward: T 777 35 us against 40, T 2048 26 against 34, T 4096 78 against 60.
+bool use_small(const SmallPlan& plan, int64_t T, int64_t col_tiles, int64_t K, int sms) {
   const int64_t how = option(MOE_OPT_FFN_TILES);
+  if (plan.token_tiles > 65535) return false;  // the grid's second dimension
   if (how) return how == 1;
-  return cdiv(T, 256) * cdiv(columns, 256) * 4 <= device_sm_count();
+  const int64_t waves = cdiv(cdiv(T, 256) * col_tiles, std::max(1, sms / 2));
+  return plan.us < 7.5f + 0.36f * (float)(waves * cdiv(K, 64));
 }
 
 int check_common(const char* who, int64_t T, int64_t H, int64_t I, int glu, int layout) {
@@ -219,15 +226,16 @@ extern "C" int ffn_fwd(const void* x, int64_t ldx, const void* W1, const void* b
   const bool inter = gate_up_layout == MOE_GATE_UP_INTERLEAVED;
   const int sms = device_sm_count();
 
-  if (few_tiles(T, 2 * I)) {
+  const SmallPlan up = small_plan(T, I, H, 64, sms), down = small_plan(T, H, I, 128, sms);
+  if (use_small(up, T, cdiv(I, 128), H, sms)) {
     FfnSmallArgs s{};
     s.W = W1; s.ldw = 2 * I; s.x = x; s.ldx = ldx; s.T = T; s.K = H; s.N = I;
     s.glu = glu; s.interleaved = inter; s.bias = static_cast<const uint16_t*>(b1);
     s.out = a; s.h = static_cast<uint16_t*>(h); s.status = status_dev;
-    rc = launch_ffn_small(true, small_plan(T, I, H, 64, sms), s, st);
+    rc = launch_ffn_small(true, up, s, st);
   } else {
     alignas(64) FfnParams P{};
-    add_problem(P, T, I, cdiv(I, 128), H, false, true);
+    add_problem(P, T, I, cdiv(I, 128), H, 0, mn_of(inter ? 2 * I : I));
     const uint16_t* w = static_cast<const uint16_t*>(W1);
     bool ok = operand(&P.map[0], x, T, H, ldx, false);
     ok = ok && (inter ? operand(&P.map[1], w, H, 2 * I, 2 * I, true) && operand(&P.map[2], w, H, 2 * I, 2 * I, true)
@@ -243,16 +251,16 @@ extern "C" int ffn_fwd(const void* x, int64_t ldx, const void* W1, const void* b
   }
   if (rc) return rc;
 
-  if (few_tiles(T, H)) {
+  if (use_small(down, T, cdiv(H, 256), I, sms)) {
     FfnSmallArgs s{};
     s.W = W2; s.ldw = H; s.x = a; s.ldx = I; s.T = T; s.K = I; s.N = H;
     s.early = 1;  // the first projection's kernel lets this one start once all that went before is complete
     s.bias = static_cast<const uint16_t*>(b2);
     s.out = static_cast<uint16_t*>(out); s.status = status_dev;
-    return launch_ffn_small(false, small_plan(T, H, I, 128, sms), s, st);
+    return launch_ffn_small(false, down, s, st);
   }
   alignas(64) FfnParams P{};
-  add_problem(P, T, H, cdiv(H, 256), I, false, true);
+  add_problem(P, T, H, cdiv(H, 256), I, 0, mn_of(H));
   P.prob[0].bias = static_cast<const uint16_t*>(b2);
   if (!operand(&P.map[0], a, T, I, I, false) || !operand(&P.map[1], W2, I, H, H, true) || !slabs(&P.map[2], out, T, H, H))
     return MOE_ERR_INVALID;
@@ -338,7 +346,7 @@ extern "C" int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t 
   }
   {
     alignas(64) FfnParams P{};
-    add_problem(P, T, I, cdiv(I, 256), H, false, false);
+    add_problem(P, T, I, cdiv(I, 256), H, 0, 0);
     if (!operand(&P.map[0], dout, T, H, lddout, false) || !operand(&P.map[1], W2, I, H, H, false) ||
         !gate_up_slabs(&P.map[2], h, T, I, inter) || !gate_up_slabs(&P.map[4], dh, T, I, inter))
       return MOE_ERR_INVALID;
@@ -355,18 +363,18 @@ extern "C" int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t 
     alignas(64) FfnParams P{};
     auto weights = [&]() {
       const int i = 3 * P.nprob;
-      add_problem(P, H, 2 * I, cdiv(2 * I, 256), T, true, true);
+      add_problem(P, H, 2 * I, cdiv(2 * I, 256), T, mn_of(H), mn_of(2 * I));
       P.prob[P.nprob - 1].accumulate = accumulate;
       bool ok = operand(&P.map[i], x, T, H, ldx, true) && operand(&P.map[i + 1], dh, T, 2 * I, 2 * I, true) &&
                 slabs(&P.map[i + 2], dW1, H, 2 * I, 2 * I);
-      add_problem(P, I, H, cdiv(H, 256), T, true, true);
+      add_problem(P, I, H, cdiv(H, 256), T, mn_of(I), mn_of(H));
       P.prob[P.nprob - 1].accumulate = accumulate;
       return ok && operand(&P.map[i + 3], a, T, I, I, true) && operand(&P.map[i + 4], dout, T, H, lddout, true) &&
              slabs(&P.map[i + 5], dW2, I, H, H);
     };
     auto rows = [&]() {
       const int i = 3 * P.nprob;
-      add_problem(P, T, H, cdiv(H, 256), 2 * I, false, false);
+      add_problem(P, T, H, cdiv(H, 256), 2 * I, 0, 0);
       return operand(&P.map[i], dh, T, 2 * I, 2 * I, false) && operand(&P.map[i + 1], W1, H, 2 * I, 2 * I, false) &&
              slabs(&P.map[i + 2], dx, T, H, H);
     };

@@ -8,6 +8,7 @@ namespace moebwd {
 struct SmallPlan {
   int nt, split;
   int64_t tiles, token_tiles;
+  float us;  // estimate
 };
 SmallPlan small_plan(int64_t T, int64_t columns, int64_t K, int per_tile, int sms);
 

@@ -30,7 +30,7 @@ struct FfnProblem {
   int end;              // tiles of this problem and those before it
   int n_tiles, nk;      // column tiles; k-blocks of 64
   int M, N;             // rows, and columns of the output (kFfnGlu, kFfnDGlu: features)
-  int a_mn, b_mn;       // operand stored [K, rows]
+  int a_mn, b_mn;       // operand stored [K, rows]: 1 its map is 2D, 2 in groups of 64 columns (see make_tmap_groups)
   int accumulate;       // add to the output
   const uint16_t* bias; // [N] or null
 };
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
         const CUtensorMap* mb = &P.map[EPI == kFfnStore ? 3 * ti.p + 1 : EPI == kFfnGlu ? 1 + (int)rank : 1];
         const int a_row = ti.mt * 128;
         const int b_col = EPI == kFfnGlu && !P.interleaved ? ti.nt * 128 : ti.nt * 256 + 128 * (int)rank;
-        const bool a_mn = EPI == kFfnStore && pr.a_mn;
-        const bool b_mn = EPI == kFfnGlu || (EPI == kFfnStore && pr.b_mn);
+        const int a_mn = EPI == kFfnStore ? pr.a_mn : 0;
+        const int b_mn = EPI == kFfnDGlu ? 0 : pr.b_mn;
         bool ok = true;
         for (int kb = 0; kb < ti.nk; ++kb) {
           if (!pair_wait(&empty[s], ph ^ 1u, P.status, abort_flag, peer_abort, P.wait_ns)) {
@@ -302,13 +302,18 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
           const uint32_t fb = lead_full + (uint32_t)(s * 8);
           const int kc = kb * C::BKE;
-          if (a_mn) {  // 64 x 64 boxes, 8 KB apart along the rows
+          // [K, rows]: two tiles of 64 rows, 8 KB apart
+          if (a_mn == 2) {
+            tma_load_3d_pair(smA + s * C::A_BYTES, ma, fb, 0, kc, a_row / 64);
+          } else if (a_mn) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) tma_load_2d_pair(smA + s * C::A_BYTES + j * 8192, ma, fb, a_row + 64 * j, kc);
           } else {
             tma_load_2d_pair(smA + s * C::A_BYTES, ma, fb, kc, a_row);
           }
-          if (b_mn) {
+          if (b_mn == 2) {
+            tma_load_3d_pair(smB + s * C::B_BYTES, mb, fb, 0, kc, b_col / 64);
+          } else if (b_mn) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) tma_load_2d_pair(smB + s * C::B_BYTES + j * 8192, mb, fb, b_col + 64 * j, kc);
           } else {

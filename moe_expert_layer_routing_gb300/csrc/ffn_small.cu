@@ -275,15 +275,29 @@ int launch_small(const SmallParams& P, int tiles, int token_tiles, cudaStream_t 
 
 }  // namespace
 
+// Microseconds of one projection on this kernel, fitted on one GB300 (T 1 .. 2048, K 768 .. 4096, weights in L2) within 15%:
+// launch and load latency 2.5; 0.27 a k-block, whatever the token tile (with 16 tokens the issue of copies and
+// products, with 256 the tensor core); emptying the accumulator 1 per 64 tokens; meeting in the cluster 1.1, with 8 CTAs
+// 1.8.  Clusters need their SMs in one GPC, so the larger ones fill fewer of the 152: 8 CTAs with more than one token
+// tile's shared memory each ran in two waves from 128 CTAs on (21.7 us where 4 took 10.1), and are not offered.
 SmallPlan small_plan(int64_t T, int64_t columns, int64_t K, int per_tile, int sms) {
-  SmallPlan pl;
-  pl.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  pl.tiles = (columns + per_tile - 1) / per_tile;
-  pl.token_tiles = (T + pl.nt - 1) / pl.nt;
-  const int64_t nk = (K + 63) / 64;
-  pl.split = 1;
-  while (pl.split < 8 && 2 * pl.split <= nk && pl.tiles * pl.token_tiles * pl.split * 2 <= sms) pl.split *= 2;
-  return pl;
+  SmallPlan best;
+  best.us = 1e30f;
+  const int64_t tiles = (columns + per_tile - 1) / per_tile, nk = (K + 63) / 64;
+  for (int nt = 16; nt <= 256; nt *= 2) {
+    if (nt < T && nt < 128) continue;  // one token tile, or tiles of 128 or 256
+    const int64_t token_tiles = (T + nt - 1) / nt;
+    for (int split = 1; split <= (nt == 16 ? 8 : 4); split *= 2) {
+      if (split > nk) break;
+      const int64_t room = split == 1 ? sms : split == 2 ? sms - 8 : sms - 16;
+      const int64_t waves = (tiles * token_tiles * split + room - 1) / room;
+      const float us = (float)waves * (2.5f + 0.0156f * nt + (split == 1 ? 0.f : split == 8 ? 1.8f : 1.1f) +
+                                       0.27f * (float)((nk + split - 1) / split));
+      if (us < best.us) best = SmallPlan{nt, split, tiles, token_tiles, us};
+    }
+    if (nt >= T) break;
+  }
+  return best;
 }
 
 int launch_ffn_small(bool glu_kernel, const SmallPlan& pl, const FfnSmallArgs& a, cudaStream_t st) {

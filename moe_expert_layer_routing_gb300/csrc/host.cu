@@ -215,6 +215,30 @@ bool make_tmap_2d(void* out_tmap, const void* base, int elem_bytes, uint64_t row
   return true;
 }
 
+bool make_tmap_groups(void* out_tmap, const void* base, uint64_t rows, uint64_t cols, uint64_t row_pitch_bytes,
+                      uint32_t box_rows, uint32_t box_groups) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) {
+    fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
+    return false;
+  }
+  CUtensorMap* m = static_cast<CUtensorMap*>(out_tmap);
+  std::memset(m, 0, sizeof(*m));
+  const cuuint64_t dims[3] = {64, rows, cols / 64};
+  const cuuint64_t strides[2] = {row_pitch_bytes, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_groups};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    fail(MOE_ERR_INVALID, "cuTensorMapEncodeTiled failed (%d): rows=%llu cols=%llu pitch=%llu in groups of 64", (int)r,
+         (unsigned long long)rows, (unsigned long long)cols, (unsigned long long)row_pitch_bytes);
+    return false;
+  }
+  return true;
+}
+
 }  // namespace moebwd
 
 extern "C" const char* moe_last_error(void) { return moebwd::g_err; }

@@ -82,6 +82,11 @@ bool make_tmap_2d(void* out_tmap /* CUtensorMap* */, const void* base, int elem_
                   uint64_t cols, uint64_t row_pitch_bytes, uint32_t box_rows, uint32_t box_cols,
                   bool swizzle128 = true);
 
+// 3D tensor map of a row-major [rows, cols] bf16 matrix, cols a multiple of 64, as [cols / 64][rows][64]: a box of
+// box_rows rows x 64 columns x box_groups column groups lands as that many 128-byte-swizzled tiles one behind another.
+bool make_tmap_groups(void* out_tmap, const void* base, uint64_t rows, uint64_t cols, uint64_t row_pitch_bytes,
+                      uint32_t box_rows, uint32_t box_groups);
+
 // ------------------------------------------------------------------------------------------
 // routing (route_meta.cu)
 // ------------------------------------------------------------------------------------------
