@@ -26,16 +26,15 @@ struct DropArgs {
   const void *x, *r;
   void* y;
   int64_t ldx, ldr, T;
-  int H, segs;  // segments of a row
+  int H, segs, iters;  // segments of a row, 32-piece steps of a segment
   uint32_t thr;
   float scale;
   uint64_t seed, offset;
   const int64_t* offset_dev;
 };
 
-// Keep bits of the four columns of counter (c0, c1, c2, c3).
-__device__ __forceinline__ uint32_t philox_keep(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1,
-                                                uint32_t thr) {
+// The four words of counter (c0, c1, c2, c3).
+__device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
@@ -44,7 +43,10 @@ __device__ __forceinline__ uint32_t philox_keep(uint32_t c0, uint32_t c1, uint32
     c1 = (uint32_t)p1;
     c3 = (uint32_t)p0;
   }
-  return (uint32_t)(c0 >= thr) | (uint32_t)(c1 >= thr) << 1 | (uint32_t)(c2 >= thr) << 2 | (uint32_t)(c3 >= thr) << 3;
+  return make_uint4(c0, c1, c2, c3);
+}
+__device__ __forceinline__ uint32_t keep_bits(const uint4& w, uint32_t thr) {
+  return (uint32_t)(w.x >= thr) | (uint32_t)(w.y >= thr) << 1 | (uint32_t)(w.z >= thr) << 2 | (uint32_t)(w.w >= thr) << 3;
 }
 
 __device__ __forceinline__ float dr_ld(const float* p) { return *p; }
@@ -74,10 +76,10 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[16 / sizeof(E)]) {
 }
 
 // E: float or uint16_t (bf16).  SAME: every row of x (and r) lies at its y row's offset within 16 bytes, so that all move in
-// aligned pieces; else their elements are loaded one by one.
-template <typename E, int ITERS, bool RES, bool SAME>
+// aligned pieces; else their elements are loaded one by one.  A warp walks `iters` steps of 32 pieces, four at a time.
+template <typename E, bool RES, bool SAME>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
-  constexpr int N = 16 / sizeof(E);
+  constexpr int N = 16 / sizeof(E), B = 4;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -93,28 +95,17 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
     const E* r = RES ? static_cast<const E*>(a.r) + t * a.ldr : nullptr;
     // columns in front of the first aligned piece of y
     const int shift = (int)((N - (reinterpret_cast<uintptr_t>(y) / sizeof(E)) % N) % N);
-    const int first = seg * 32 * ITERS + lane;  // this lane's first piece: columns shift + N first ..
+    const int first = seg * 32 * a.iters + lane;  // this lane's first piece: columns shift + N first ..
     // keep bits of columns N k .. N k + N - 1
     auto bits = [&](int k) {
       uint32_t m = 0;
 #pragma unroll
       for (int g = 0; g < N / 4; ++g)
-        m |= philox_keep((uint32_t)(k * (N / 4) + g), (uint32_t)t, o0, o1, k0, k1, a.thr) << (4 * g);
+        m |= keep_bits(philox((uint32_t)(k * (N / 4) + g), (uint32_t)t, o0, o1, k0, k1), a.thr) << (4 * g);
       return m;
     };
-    uint4 vx[ITERS], vr[ITERS];
-    if constexpr (SAME) {
-#pragma unroll
-      for (int i = 0; i < ITERS; ++i) {
-        const int c = shift + N * (first + 32 * i);
-        if (c + N <= a.H) {
-          vx[i] = *reinterpret_cast<const uint4*>(x + c);
-          if constexpr (RES) vr[i] = *reinterpret_cast<const uint4*>(r + c);
-        }
-      }
-    }
     uint32_t m = bits(first);
-    if (first < 32 && shift) {  // the row's head, element by element (all lanes of segment 0 are here)
+    if (seg == 0 && shift) {  // the row's head, element by element
       const uint32_t m0 = __shfl_sync(0xffffffffu, m, 0);
       if (lane < shift && lane < a.H) {
         float v = (m0 >> lane & 1) ? dr_ld(x + lane) * a.scale : 0.f;
@@ -122,51 +113,118 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
         dr_st(y + lane, v);
       }
     }
+    for (int i0 = 0; i0 < a.iters; i0 += B) {
+      uint4 vx[B], vr[B];
+      if constexpr (SAME) {
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-      const int k = first + 32 * i;
-      const int c = shift + N * k;
-      if (c - N * lane >= a.H) break;  // the same for the whole warp
-      uint32_t next = 0, keep = m;
-      if (i + 1 < ITERS || shift) next = bits(k + 32);
-      if (shift) {
-        const uint32_t beside = __shfl_down_sync(0xffffffffu, m, 1), over = __shfl_sync(0xffffffffu, next, 0);
-        keep = (m | (lane == 31 ? over : beside) << N) >> shift;
-      }
-      m = next;
-      if (c + N <= a.H) {
-        float f[N], s[N];
-        if constexpr (SAME) {
-          unpack16<E>(vx[i], f);
-          if constexpr (RES) unpack16<E>(vr[i], s);
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            f[j] = dr_ld(x + c + j);
-            if constexpr (RES) s[j] = dr_ld(r + c + j);
+        for (int i = 0; i < B; ++i) {
+          const int c = shift + N * (first + 32 * (i0 + i));
+          if (c + N <= a.H) {
+            vx[i] = *reinterpret_cast<const uint4*>(x + c);
+            if constexpr (RES) vr[i] = *reinterpret_cast<const uint4*>(r + c);
           }
         }
+      }
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          f[j] = (keep >> j & 1) ? f[j] * a.scale : 0.f;  // a dropped infinity or NaN is gone
-          if constexpr (RES) f[j] += s[j];
+      for (int i = 0; i < B; ++i) {
+        const int k = first + 32 * (i0 + i);
+        const int c = shift + N * k;
+        if (i0 + i >= a.iters || c - N * lane >= a.H) break;  // the same for the whole warp
+        const uint32_t next = bits(k + 32);
+        uint32_t keep = m;
+        if (shift) {  // a piece straddles two groups of N columns: the second one's bits are the next lane's
+          const uint32_t beside = __shfl_down_sync(0xffffffffu, m, 1), over = __shfl_sync(0xffffffffu, next, 0);
+          keep = (m | (lane == 31 ? over : beside) << N) >> shift;
         }
-        *reinterpret_cast<uint4*>(y + c) = pack16<E>(f);
-      } else {
-        for (int j = 0; c + j < a.H && j < N; ++j) {
-          float v = (keep >> j & 1) ? dr_ld(x + c + j) * a.scale : 0.f;
-          if constexpr (RES) v += dr_ld(r + c + j);
-          dr_st(y + c + j, v);
+        m = next;
+        if (c + N <= a.H) {
+          float f[N], s[N];
+          if constexpr (SAME) {
+            unpack16<E>(vx[i], f);
+            if constexpr (RES) unpack16<E>(vr[i], s);
+          } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+              f[j] = dr_ld(x + c + j);
+              if constexpr (RES) s[j] = dr_ld(r + c + j);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            f[j] = (keep >> j & 1) ? f[j] * a.scale : 0.f;  // a dropped infinity or NaN is gone
+            if constexpr (RES) f[j] += s[j];
+          }
+          *reinterpret_cast<uint4*>(y + c) = pack16<E>(f);
+        } else {
+          for (int j = 0; c + j < a.H && j < N; ++j) {
+            float v = (keep >> j & 1) ? dr_ld(x + c + j) * a.scale : 0.f;
+            if constexpr (RES) v += dr_ld(r + c + j);
+            dr_st(y + c + j, v);
+          }
         }
       }
     }
   }
 }
 
-template <typename E, int ITERS>
-int launch(const DropArgs& a, bool same, int64_t blocks, cudaStream_t st) {
-  auto k = a.r ? (same ? dropout_kernel<E, ITERS, true, true> : dropout_kernel<E, ITERS, true, false>)
-               : (same ? dropout_kernel<E, ITERS, false, true> : dropout_kernel<E, ITERS, false, false>);
+// The same for rows of whole 16-byte pieces that all start on a 16-byte boundary: a piece is one or two generator groups, whose
+// words select the values directly.
+template <typename E, int ITERS, bool RES>
+__global__ void __launch_bounds__(256) dropout_whole_kernel(const DropArgs a) {
+  constexpr int N = 16 / sizeof(E);
+  pdl_wait();
+  pdl_trigger();
+  const uint64_t off = a.offset + (a.offset_dev ? (uint64_t)*a.offset_dev : 0);
+  const uint32_t k0 = (uint32_t)a.seed, k1 = (uint32_t)(a.seed >> 32);
+  const uint32_t o0 = (uint32_t)off, o1 = (uint32_t)(off >> 32);
+  const int64_t units = a.T * a.segs;
+  const uint64_t scale = f2_splat(a.scale);
+  for (int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); unit < units; unit += (int64_t)gridDim.x * 8) {
+    const int64_t t = unit / a.segs;
+    const int first = (int)(unit - t * a.segs) * 32 * ITERS + (threadIdx.x & 31);
+    const E* x = static_cast<const E*>(a.x) + t * a.ldx;
+    const E* r = RES ? static_cast<const E*>(a.r) + t * a.ldr : nullptr;
+    E* y = static_cast<E*>(a.y) + t * a.H;
+    uint4 vx[ITERS], vr[ITERS];
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      const int c = N * (first + 32 * i);
+      if (c < a.H) {
+        vx[i] = *reinterpret_cast<const uint4*>(x + c);
+        if constexpr (RES) vr[i] = *reinterpret_cast<const uint4*>(r + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      const int c = N * (first + 32 * i);
+      if (c >= a.H) break;
+      float f[N], s[N];
+      unpack16<E>(vx[i], f);
+      if constexpr (RES) unpack16<E>(vr[i], s);
+#pragma unroll
+      for (int g = 0; g < N / 4; ++g) {
+        const uint4 w = philox((uint32_t)(c / 4 + g), (uint32_t)t, o0, o1, k0, k1);
+        const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {  // a dropped infinity or NaN is gone
+          const uint64_t v = f2_pack(word[j] >= a.thr ? f[4 * g + j] : 0.f, word[j + 1] >= a.thr ? f[4 * g + j + 1] : 0.f);
+          if constexpr (RES)
+            f2_unpack(f2_fma(v, scale, f2_pack(s[4 * g + j], s[4 * g + j + 1])), f[4 * g + j], f[4 * g + j + 1]);
+          else
+            f2_unpack(f2_mul(v, scale), f[4 * g + j], f[4 * g + j + 1]);
+        }
+      }
+      *reinterpret_cast<uint4*>(y + c) = pack16<E>(f);
+    }
+  }
+}
+
+template <typename E>
+int launch(const DropArgs& a, bool same, bool whole, bool deep, int64_t blocks, cudaStream_t st) {
+  auto k = whole ? (deep ? (a.r ? dropout_whole_kernel<E, 4, true> : dropout_whole_kernel<E, 4, false>)
+                         : (a.r ? dropout_whole_kernel<E, 1, true> : dropout_whole_kernel<E, 1, false>))
+           : a.r ? (same ? dropout_kernel<E, true, true> : dropout_kernel<E, true, false>)
+                 : (same ? dropout_kernel<E, false, true> : dropout_kernel<E, false, false>);
   return launch_pdl(k, dim3((unsigned)blocks), dim3(256), 0, st, "dropout", a);
 }
 
@@ -187,20 +245,24 @@ int dropout(const char* who, const void* x, int64_t ldx, const void* r, int64_t 
   const int n = 16 / es;
   auto beside = [&](uintptr_t p0, int64_t ld) { return (p0 - ay) % 16 == 0 && (T == 1 || (ld - H) % n == 0); };
   const bool same = beside(ax, ldx) && (!r || beside(ar, ldr));
+  const bool whole = same && ay % 16 == 0 && H % n == 0;
   DropArgs a{};
   a.x = x; a.r = r; a.y = y; a.ldx = ldx; a.ldr = ldr; a.T = T; a.H = (int)H;
   a.thr = (uint32_t)std::min(4294967295.0, std::floor(p * 4294967296.0 + 0.5));
   a.scale = (float)(1.0 / (1.0 - p));
   a.seed = seed; a.offset = offset; a.offset_dev = offset_dev;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Four pieces a lane where that still gives every SM its warps, else one (7 x 2048 bf16: more lanes at work).
+  // Whole rows: four pieces a lane where that still gives every SM its warps, else one (7 x 2048 bf16: more lanes at
+  // work).  Rows off the 16-byte boundary: segments as long as that allows, since each begins with a step of the generator more
+  // (fp32 16411 x 1111: 32 us with whole rows, 34 with segments of four steps).
   const int sms = device_sm_count();
-  const int64_t pieces = (H + n - 1) / n;
-  const bool deep = T * ((pieces + 127) / 128) >= (int64_t)sms * 32;
-  a.segs = (int)((pieces + (deep ? 127 : 31)) / (deep ? 128 : 32));
-  const int64_t blocks = std::min<int64_t>((T * a.segs + 7) / 8, (int64_t)sms * 64);
-  if (dtype == MOE_DT_F32) return deep ? launch<float, 4>(a, same, blocks, st) : launch<float, 1>(a, same, blocks, st);
-  return deep ? launch<uint16_t, 4>(a, same, blocks, st) : launch<uint16_t, 1>(a, same, blocks, st);
+  const int64_t steps = ((H + n - 1) / n + 31) / 32, want = (int64_t)sms * 32;
+  const bool deep = T * ((steps + 3) / 4) >= want;
+  const int64_t most = std::min(steps, (want + T - 1) / T);
+  a.iters = whole ? (deep ? 4 : 1) : (int)((steps + most - 1) / most);
+  a.segs = (int)((steps + a.iters - 1) / a.iters);
+  const int64_t blocks = std::min<int64_t>((T * a.segs + 7) / 8, 1 << 30);
+  return dtype == MOE_DT_F32 ? launch<float>(a, same, whole, deep, blocks, st) : launch<uint16_t>(a, same, whole, deep, blocks, st);
 }
 
 }  // namespace
