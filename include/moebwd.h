@@ -535,6 +535,41 @@ int dropout_bwd(const void* dy, int64_t lddy, int dtype, int64_t T, int64_t H, d
                 const int64_t* offset_dev, void* dx, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Low-rank adapters                                                                            */
+/* ------------------------------------------------------------------------------------------ */
+
+/* Bytes of workspace adapter_fwd (backward 0) or adapter_bwd (1) needs on the current device. */
+size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, int backward);
+
+/* Low-rank adapters of many requests beside a shared projection: token t of adapter a adds to its row of the projection's
+ * output (base)
+ *   u_t = A_a x_t,  y_t = base_t + scale_a B_a^T u_t
+ * and a token without an adapter keeps it.
+ * x (device) bf16 [T,H], row stride ldx; A bf16 [n,r,H], B bf16 [n,r,N]: r rows of features each, dense; scale (device,
+ * nullable: ones) fp32 [n]; base (device, nullable: zeros) bf16 [T,N], row stride ldbase; y (device) bf16 [T,N] dense; it
+ * may be base itself when that is dense.  u (device, nullable) fp32 [T,r]: the backward's, zeros for tokens without one.
+ * expert_offsets [n+1], x_gather_idx [T], s_reverse_scatter_idx [T] (device): moe_route_meta's for ids [T,1] (-1: none) and
+ *   E = n.  Offsets are clamped to [0,T] and indices outside it skipped: wrong metadata gives wrong rows, no access
+ *   leaves its buffer.
+ * Sums in fp32 in a fixed order (bit-reproducible); scale_a u is rounded to bf16 as the second product's operand, y once.
+ * H and N multiples of 8 (the row strides too), r <= 128, n <= 1024, tensors 16-byte aligned.  T = 0 writes nothing. */
+int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base, int64_t ldbase,
+                const int32_t* expert_offsets, const int32_t* x_gather_idx, const int32_t* s_reverse_scatter_idx, int64_t T,
+                int64_t H, int64_t N, int64_t n, int64_t r, void* y, float* u, void* workspace, size_t workspace_bytes,
+                moe_stream_t stream);
+
+/* Gradients of adapter_fwd, u being its:
+ *   v_t = scale_a B_a dy_t,  dx_t = base_t + A_a^T v_t,  dA_a = sum_t v_t x_t^T,  dB_a = sum_t scale_a u_t dy_t^T
+ * base (device, nullable: zeros) bf16 [T,H]: the shared projection's own gradient (linear_bwd's dX); dx may be base itself
+ * when that is dense (the gradient of the forward's base is dy).  dx [T,H], dA [n,r,H], dB [n,r,N] (device) bf16 dense; adapters without a token get zeros.
+ * v and scale_a u are rounded to bf16 as operands, results once.  accumulate = 1 adds to dA and dB (one rounding).  T = 0: dA
+ * and dB are zeroed, or left as they are with accumulate. */
+int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* u, const void* A, const void* B,
+                const float* scale, const void* base, int64_t ldbase, const int32_t* expert_offsets, const int32_t* x_gather_idx,
+                const int32_t* s_reverse_scatter_idx, int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, void* dx, void* dA,
+                void* dB, int accumulate, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Instrumentation                                                                             */
 /* ------------------------------------------------------------------------------------------ */
 

@@ -38,7 +38,7 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_num_blocks_bound", "moe_route_
             "moe_balance_workspace_size", "moe_router_fwd", "moe_balance_fwd", "moe_balance_bwd", "moe_glu_fwd",
             "moe_ckpt8_unpack", "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd",
             "ffn_fwd_workspace_size", "ffn_fwd", "ffn_bwd_workspace_size", "ffn_bwd",
-            "dropout_fwd", "dropout_bwd"]
+            "dropout_fwd", "dropout_bwd", "adapter_workspace_size", "adapter_fwd", "adapter_bwd"]
 
 # library options (moe_set_option)
 OPTIONS = ["WAIT_LIMIT_NS", "PAIR_GEMMS", "PAIR_TILE_N", "G1_TILE_N", "G2_TILE_N", "G3_TILE_N", "G4_TILE_N",
@@ -121,6 +121,9 @@ def lib():
         "ffn_bwd": ([vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp], i32),
         "dropout_fwd": ([vp, i64, vp, i64, i32, i64, i64, f64, u64, u64, vp, vp, vp], i32),
         "dropout_bwd": ([vp, i64, i32, i64, i64, f64, u64, u64, vp, vp, vp], i32),
+        "adapter_workspace_size": ([i64] * 5 + [i32], sz),
+        "adapter_fwd": ([vp, i64, vp, vp, vp, vp, i64, vp, vp, vp] + [i64] * 5 + [vp, vp, vp, sz, vp], i32),
+        "adapter_bwd": ([vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp] + [i64] * 5 + [vp, vp, vp, i32, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -825,6 +828,69 @@ def dropout_bwd(dy, p: float, seed: int, offset=0, stream=None) -> torch.Tensor:
     rc = lib().dropout_bwd(dy.data_ptr(), ld, _DT[dy.dtype], T, H, p, seed, at, op, dx.data_ptr(), st)
     _check(rc, "dropout_bwd")
     return dx
+
+
+def _adapter_args(x, A, B, route_meta, scale, what):
+    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise MoeError(f"{what}: x must be [T, H], A [n, r, H], B [n, r, N]")
+    (T, H), (n, r, N), dev = x.shape, B.shape, x.device
+    bf, i32 = torch.bfloat16, torch.int32
+    ldx = _rows(x, bf, (T, H), "x", dev)
+    p = (_dense(A, bf, (n, r, H), "A", dev), _dense(B, bf, (n, r, N), "B", dev), _dense(scale, torch.float32, (n,), "scale", dev))
+    m = (_dense(route_meta["expert_offsets"], i32, (n + 1,), "expert_offsets", dev),
+         _dense(route_meta["x_gather_idx"], i32, (T,), "x_gather_idx", dev),
+         _dense(route_meta["s_reverse_scatter_idx"], i32, (T,), "s_reverse_scatter_idx", dev))
+    return T, H, N, n, r, dev, ldx, p, m
+
+
+def adapter_fwd(x, A, B, route_meta: dict, scale=None, base=None, out=None, save: bool = True, stream=None) -> dict:
+    """adapter_fwd: y = base + scale_a B_a^T (A_a x) for the rows of x [T, H] (bf16) that have an adapter, base (or 0) for the
+    others.  A [n, r, H], B [n, r, N] bf16, scale fp32 [n].  route_meta: route_meta(ids [T, 1], n, ...)'s dict, id -1
+    for a row without an adapter.  base [T, N] bf16: the shared projection's output; out: a dense [T, N] tensor to write, which
+    may be base (None: a new one).  Returns y and, unless save is False, u [T, r] in fp32, which adapter_bwd takes."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return adapter_fwd(x, A, B, route_meta, scale, base, out, save)
+    T, H, N, n, r, dev, ldx, p, m = _adapter_args(x, A, B, route_meta, scale, "adapter_fwd")
+    ldb = 0 if base is None else _rows(base, x.dtype, (T, N), "base", dev)
+    yp = _dense(out, x.dtype, (T, N), "out", dev)
+    st = _here(dev)
+    y = _new2(T, N, x.dtype) if out is None else out
+    u = _new2(T, r, torch.float32) if save else None
+    ws = _new1(max(lib().adapter_workspace_size(T, H, N, n, r, 0), 256), torch.uint8)
+    rc = lib().adapter_fwd(x.data_ptr(), ldx, *p, None if base is None else base.data_ptr(), ldb, *m, T, H, N, n, r,
+                           y.data_ptr() if yp is None else yp, None if u is None else u.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    _check(rc, "adapter_fwd")
+    return dict(y=y, u=u)
+
+
+def adapter_bwd(dy, x, u, A, B, route_meta: dict, scale=None, base=None, out=None, accumulate_into=None, stream=None) -> dict:
+    """adapter_bwd: gradients of adapter_fwd from its u.  base [T, H] bf16: the shared projection's own dX (e.g. linear_bwd's), to
+    which the adapters' is added in dx; out as in adapter_fwd.  Returns dx [T, H], dA, dB (bf16; zeros for adapters without a
+    row).  accumulate_into: an earlier result whose dA and dB are added to in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return adapter_bwd(dy, x, u, A, B, route_meta, scale, base, out, accumulate_into)
+    T, H, N, n, r, dev, ldx, p, m = _adapter_args(x, A, B, route_meta, scale, "adapter_bwd")
+    bf = torch.bfloat16
+    ldd = _rows(dy, bf, (T, N), "dy", dev)
+    up = _dense(u, torch.float32, (T, r), "u", dev)
+    ldb = 0 if base is None else _rows(base, bf, (T, H), "base", dev)
+    op = _dense(out, bf, (T, H), "out", dev)
+    st = _here(dev)
+    dx = _new2(T, H, bf) if out is None else out
+    if accumulate_into is not None:
+        dA, dB = accumulate_into["dA"], accumulate_into["dB"]
+        _dense(dA, bf, (n, r, H), "dA", dev), _dense(dB, bf, (n, r, N), "dB", dev)
+    else:
+        dA = _empty_strided((n, r, H), (r * H, H, 1), bf)
+        dB = _empty_strided((n, r, N), (r * N, N, 1), bf)
+    ws = _new1(max(lib().adapter_workspace_size(T, H, N, n, r, 1), 256), torch.uint8)
+    rc = lib().adapter_bwd(dy.data_ptr(), ldd, x.data_ptr(), ldx, up, *p, None if base is None else base.data_ptr(), ldb, *m, T, H,
+                           N, n, r, dx.data_ptr() if op is None else op, dA.data_ptr(), dB.data_ptr(),
+                           int(accumulate_into is not None), ws.data_ptr(), ws.numel(), st)
+    _check(rc, "adapter_bwd")
+    return dict(dx=dx, dA=dA, dB=dB)
 
 
 class LinearBwd:
