@@ -24,11 +24,7 @@
 namespace moebwd {
 namespace {
 
-constexpr int kRows = 64;      // tokens of a tile
-constexpr int kChunk = 128;    // features of a pipeline stage
-constexpr int kThreads = 128;  // four warps: 16 tokens each (shrink, expand), 32 features each (grad)
-constexpr int kStages = 3;
-constexpr int kMaxSplit = 16;
+constexpr int kThreads = 256;  // eight warps
 constexpr int kMaxPer = 1024;  // rows of a gradient tile at most
 
 struct Groups {
@@ -89,59 +85,104 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte of 16-byte piece `c` of row `row` in a tile of 256-byte rows: eight rows at one piece fall into eight bank groups.
-__device__ __forceinline__ uint32_t at256(int row, int c) { return (uint32_t)(row * 256 + ((c ^ (row & 7)) << 4)); }
-// The same for rows of RP bf16 numbers.
+// Byte of 16-byte piece `c` of row `row` in a tile of PITCH-byte rows (PITCH >= 128): eight rows at one piece fall into
+// eight bank groups.  Moving from piece c to c ^ d is an exclusive or of the byte with d << 4.
+template <int PITCH>
+__device__ __forceinline__ uint32_t at(int row, int c) {
+  return (uint32_t)(row * PITCH + ((c ^ (row & 7)) << 4));
+}
+// The same for rows of RP bf16 numbers (32 bytes and more).
 template <int RP>
 __device__ __forceinline__ uint32_t at_rank(int row, int c) {
   constexpr int mask = RP / 8 < 8 ? RP / 8 - 1 : 7;
   return (uint32_t)(row * RP * 2 + ((c ^ (row & mask)) << 4));
 }
 
+__device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------------------------------
-// shrink: part[split, row, :] = x[token(row), its features] W_a^T
+// shrink: w_t = W_a x_t, and from it v = c_a w (bf16, by grouped row), u = w (fp32, by token), su = c_a u_in (bf16)
 // ------------------------------------------------------------------------------------------
 struct ShrinkArgs {
   Groups g;
-  const uint16_t* x;  // [T, K], row stride ld
-  const uint16_t* W;  // [n, R, K]
-  float* part;        // [splits, T, RP]
+  const uint16_t* x;   // [T, K], row stride ld
+  const uint16_t* W;   // [n, R, K]
+  const float* scale;  // [n] or null
+  uint16_t* v;         // [T, RP]
+  float* u;            // [T, R] or null
+  const float* u_in;   // [T, R] with su [T, RP], or null
+  uint16_t* su;
   int64_t ld;
-  int K, R, splits;
+  int K, R;
 };
 
+// A tile of tokens by all r rows, its contraction split over a cluster whose partial tiles meet in distributed shared memory,
+// summed in rank order.  Ranks up to 32: 64 tokens, stages of 128 features, two groups of four warps take a stage's
+// halves; above: 128 tokens (their W tile is as large as the tokens'), stages of 64 features.  A thread copies the same
+// four rows' pieces in every stage, so that a copy costs two additions beside it: the address arithmetic, not the products
+// or the bytes, bound the form that computed each address (rank 64, 8192 x 4096: 30 us, now 25 us).
 template <int RP>
+struct ShrinkCfg {
+  static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PITCH = KC * 2, PIECES = KC / 8;
+  static constexpr int HALVES = 512 / (ROWS * 4);  // groups of warps that share a row's contraction
+  static constexpr int STAGES = RP <= 64 ? 4 : 3;
+  static constexpr int X = ROWS * PITCH, STAGE = X + RP * PITCH;
+  static constexpr int PART = HALVES * ROWS * RP * 4;
+  static constexpr int SMEM = STAGES * STAGE > PART ? STAGES * STAGE : PART;
+};
+
+template <int RP, int SPLIT>
 __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkArgs p) {
+  using C = ShrinkCfg<RP>;
   extern __shared__ __align__(256) uint8_t smem[];
-  __shared__ int tok[kRows];
-  constexpr int kStage = (kRows + RP) * 256;
+  __shared__ int tok[C::ROWS];
   pdl_wait();
   pdl_trigger();
+  const uint32_t rank = SPLIT > 1 ? cluster_ctarank() : 0;
   Tile t;
-  if (!find_tile(p.g, blockIdx.x, kRows, t)) return;
+  // the whole cluster works on one tile, so that all of it leaves here or none
+  if (!find_tile(p.g, blockIdx.x / SPLIT, C::ROWS, t)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < kRows) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
+  if (tid < C::ROWS) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
   __syncthreads();
-  const int chunks = (p.K + kChunk - 1) / kChunk;
-  const int c0 = (int)((int64_t)chunks * blockIdx.y / p.splits), c1 = (int)((int64_t)chunks * (blockIdx.y + 1) / p.splits);
-  const uint16_t* W = p.W + (int64_t)t.a * p.R * p.K;
+  const int chunks = (p.K + C::KC - 1) / C::KC;
+  const int c0 = (int)((int64_t)chunks * rank / SPLIT), c1 = (int)((int64_t)chunks * (rank + 1) / SPLIT);
   const uint32_t base = smem_u32(smem);
-  const int pc = tid & 15;  // this thread's 16-byte piece of every row it copies
+  const int pc = tid % C::PIECES, r0 = tid / C::PIECES;
+  constexpr int STEP = kThreads / C::PIECES;        // rows of one pass of copies
+  constexpr int WN = (RP + STEP - 1) / STEP;        // passes over W's rows
+  const uint16_t* xs[4];
+  uint32_t xb[4], xd[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = r0 + STEP * i, tk = tok[row];
+    xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)c0 * C::KC;
+    xb[i] = tk < 0 ? 0u : 16u;
+    xd[i] = row < ((t.rows + 15) & ~15) ? base + at<C::PITCH>(row, pc) : 0u;  // rows that no warp reads are not filled
+  }
+  const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)c0 * C::KC;
   auto load = [&](int c) {
-    const uint32_t s = base + (uint32_t)((c - c0) % kStages) * kStage;
-    const int k = c * kChunk + 8 * pc;
+    const int k = c * C::KC + 8 * pc;
     const uint32_t in = k < p.K ? 16u : 0u;  // K is a multiple of 8
+    const uint32_t st = (uint32_t)((c - c0) % C::STAGES) * C::STAGE;
+    const int64_t o = (int64_t)(c - c0) * C::KC;
 #pragma unroll
-    for (int i = 0; i < kRows / 8; ++i) {
-      const int row = (tid >> 4) + 8 * i, tk = tok[row];
-      if (row < ((t.rows + 15) & ~15))  // tiles of 16 rows that no warp reads are not filled
-        cp_async_16_zfill(s + at256(row, pc), tk >= 0 && in ? p.x + (int64_t)tk * p.ld + k : p.x, tk >= 0 ? in : 0u);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (xd[i]) cp_async_16_zfill(xd[i] + st, in ? xs[i] + o : p.x, xb[i] & in);
 #pragma unroll
-    for (int i = 0; i < RP / 8; ++i) {
-      const int row = (tid >> 4) + 8 * i;
-      const bool ok = row < p.R && in;
-      cp_async_16_zfill(s + kRows * 256 + at256(row, pc), ok ? W + (int64_t)row * p.K + k : p.W, ok ? 16u : 0u);
+    for (int i = 0; i < WN; ++i) {
+      const int row = r0 + STEP * i;
+      if (RP % STEP == 0 || row < RP) {
+        const bool ok = row < p.R && in;
+        cp_async_16_zfill(base + st + C::X + at<C::PITCH>(row, pc), ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
+      }
     }
   };
   float acc[RP / 8][4];
@@ -149,25 +190,30 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
   for (int i = 0; i < RP / 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  for (int i = 0; i < kStages - 1; ++i) {
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) {
     if (c0 + i < c1) load(c0 + i);
     cp_async_commit();
   }
+  const int rg = C::HALVES == 2 ? warp & 3 : warp, half = C::HALVES == 2 ? warp >> 2 : 0;
+  constexpr int KK = C::KC / 16 / C::HALVES;
+  const uint32_t aoff = base + at<C::PITCH>(rg * 16 + (lane & 15), 2 * KK * half + (lane >> 4));
+  const uint32_t boff = base + C::X + at<C::PITCH>((lane & 7) + ((lane >> 4) << 3), 2 * KK * half + ((lane >> 3) & 1));
   for (int c = c0; c < c1; ++c) {
-    cp_async_wait<kStages - 2>();
+    cp_async_wait<C::STAGES - 2>();
     __syncthreads();  // stage c has landed for everyone, and everyone is done with the stage refilled now
-    if (c + kStages - 1 < c1) load(c + kStages - 1);
+    if (c + C::STAGES - 1 < c1) load(c + C::STAGES - 1);
     cp_async_commit();
-    if (warp * 16 < t.rows) {
-      const uint32_t s = base + (uint32_t)((c - c0) % kStages) * kStage;
+    if (rg * 16 < t.rows) {
+      const uint32_t st = (uint32_t)((c - c0) % C::STAGES) * C::STAGE;
 #pragma unroll
-      for (int kk = 0; kk < kChunk / 16; ++kk) {
+      for (int kk = 0; kk < KK; ++kk) {
         uint32_t a[4];
-        ldsm4(a, s + at256(warp * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+        ldsm4(a, (aoff + st) ^ (uint32_t)(kk << 5));
 #pragma unroll
         for (int nb = 0; nb < RP / 16; ++nb) {
           uint32_t b[4];
-          ldsm4(b, s + kRows * 256 + at256(nb * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+          ldsm4(b, ((boff + st) ^ (uint32_t)(kk << 5)) + nb * 16 * C::PITCH);
           mma16816(acc[2 * nb], a, b[0], b[1]);
           mma16816(acc[2 * nb + 1], a, b[2], b[3]);
         }
@@ -175,51 +221,89 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
     }
   }
   cp_async_wait<0>();
+  __syncthreads();  // the partial tiles overlay the stages
+  float* part = reinterpret_cast<float*>(smem);  // [halves][rows][RP]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int row = warp * 16 + (lane >> 2) + 8 * h;
-    if (row >= t.rows) continue;
-    float* out = p.part + ((int64_t)blockIdx.y * p.g.T + t.r0 + row) * RP + 2 * (lane & 3);
+    float* out = part + (half * C::ROWS + rg * 16 + (lane >> 2) + 8 * h) * RP + 2 * (lane & 3);
 #pragma unroll
     for (int i = 0; i < RP / 8; ++i) *reinterpret_cast<float2*>(out + 8 * i) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
   }
+  if (SPLIT > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  const float scale = p.scale ? p.scale[t.a] : 1.f;
+  for (int i = (int)rank * kThreads + tid; i < t.rows * (RP / 4); i += SPLIT * kThreads) {
+    const int row = i / (RP / 4), c = 4 * (i % (RP / 4));
+    float4 f[SPLIT * C::HALVES];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k)
+#pragma unroll
+      for (int h = 0; h < C::HALVES; ++h) {
+        const float* q = part + (h * C::ROWS + row) * RP + c;
+        f[k * C::HALVES + h] = SPLIT > 1 ? ld_peer_f4(mapa_shared(smem_u32(q), (uint32_t)k)) : *reinterpret_cast<const float4*>(q);
+      }
+    float4 s = f[0];
+#pragma unroll
+    for (int k = 1; k < SPLIT * C::HALVES; ++k) {
+      s.x += f[k].x;
+      s.y += f[k].y;
+      s.z += f[k].z;
+      s.w += f[k].w;
+    }
+    const int tk = tok[row];
+    const int64_t o = (int64_t)(t.r0 + row) * RP + c;
+    *reinterpret_cast<uint2*>(p.v + o) = make_uint2(pack_bf16x2(s.x * scale, s.y * scale), pack_bf16x2(s.z * scale, s.w * scale));
+    const float w[4] = {s.x, s.y, s.z, s.w};
+    if (p.u && tk >= 0)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < p.R) p.u[(int64_t)tk * p.R + c + j] = w[j];
+    if (p.su) {
+      float z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = tk >= 0 && c + j < p.R ? p.u_in[(int64_t)tk * p.R + c + j] * scale : 0.f;
+      *reinterpret_cast<uint2*>(p.su + o) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+    }
+  }
+  __syncwarp();
+  if (SPLIT > 1) cluster_sync_all();  // no CTA leaves while a peer may still read its partial tile
 }
 
 // ------------------------------------------------------------------------------------------
-// expand: out[token] = base[token] + v W_a, v = c_a sum over the splits
+// expand: out[token] = base[token] + v W_a
 // ------------------------------------------------------------------------------------------
 struct ExpandArgs {
   Groups g;
-  const float* part;     // [splits, T, RP]
-  const float* scale;    // [n] or null
+  const uint16_t* v;     // [T, RP] by grouped row
   const uint16_t* W;     // [n, R, N]
   const uint16_t* base;  // [T, N], row stride ldb, or null
   uint16_t* out;         // [T, N] dense
   const int32_t* back;   // [T] token -> grouped row, negative: none
-  float* u;              // [T, R] unscaled sums by token, or null
-  uint16_t* v;           // [T, RP] bf16 v by grouped row, or null
-  const float* u_in;     // [T, R] with su [T, RP]: bf16 c_a u_in by grouped row, or null
-  uint16_t* su;
+  float* u;              // [T, R] zeros for tokens without an adapter, or null
   int64_t ldb;
-  int N, R, splits, cols, col_blocks, slots;  // columns of a block (a multiple of 128)
+  int N, R, per, col_blocks, slots;  // rows of a tile (at most kExpandRows)
 };
+constexpr int kExpandRows = 256;
 
-// A tile's 64 tokens x `cols` columns, 128 at a time.  The columns of W are permuted within 32 on their way to shared memory
-// so that a thread's four 8-column matrix tiles give it 8 neighbouring columns: base and out move in 16-byte pieces,
-// four lanes to 64 bytes of a row, with no pass through shared memory.
+// A tile of up to 256 tokens x 128 columns.  W's 128 columns and the tile's v stay in shared memory; then the warps go on
+// alone, 16 tokens x 64 columns at a time with the next piece's base already on its way.  The columns of W are
+// permuted within 32 on their way to shared memory so that a thread's four 8-column matrix tiles give it 8 neighbouring
+// columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a row, with no pass through shared memory.
 template <int RP>
-__global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const ExpandArgs p) {
+__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_kernel(const ExpandArgs p) {
   extern __shared__ __align__(256) uint8_t smem[];
-  uint8_t* sW = smem;
-  uint8_t* sV = smem + RP * 256;
-  __shared__ int tok[kRows];
+  uint8_t* sW = smem;              // [RP][128], permuted
+  uint8_t* sV = smem + RP * 256;   // [per][RP]
+  __shared__ int tok[kExpandRows];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int work = p.slots * p.col_blocks;
   if ((int)blockIdx.x >= work) {  // 64 tokens: rows without an adapter keep their base
-    const int64_t t0 = ((int64_t)blockIdx.x - work) * kRows;
-    for (int i = warp; i < kRows; i += 4) {
+    const int64_t t0 = ((int64_t)blockIdx.x - work) * 64;
+    for (int i = warp; i < 64; i += 8) {
       const int64_t t = t0 + i;
       if (t >= p.g.T || p.back[t] >= 0) continue;
       if (p.u)
@@ -232,111 +316,94 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const ExpandAr
     return;
   }
   Tile t;
-  const int slot = blockIdx.x / p.col_blocks, block = blockIdx.x % p.col_blocks;
-  if (!find_tile(p.g, slot, kRows, t)) return;
-  if (tid < kRows) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
+  const int slot = blockIdx.x / p.col_blocks, n0 = (blockIdx.x % p.col_blocks) * 128;
+  if (!find_tile(p.g, slot, p.per, t)) return;
+  if (tid < t.rows) tok[tid] = token_of(p.g, t.r0 + tid);
+  const int padded = (t.rows + 15) & ~15;
+  const uint32_t bw = smem_u32(sW), bv = smem_u32(sV);
+  for (int i = tid; i < padded * (RP / 8); i += kThreads) {
+    const int row = i / (RP / 8), c = i % (RP / 8);
+    const bool ok = row < t.rows;
+    cp_async_16_zfill(bv + at_rank<RP>(row, c), ok ? p.v + (int64_t)(t.r0 + row) * RP + 8 * c : p.v, ok ? 16u : 0u);
+  }
+  cp_async_commit();
+  const uint16_t* W = p.W + (int64_t)t.a * p.R * p.N;
+#pragma unroll
+  for (int i = 0; i < RP / 16; ++i) {
+    const int row = (tid >> 4) + 16 * i, pc = tid & 15;
+    const int c = n0 + 8 * pc;
+    const uint4 w = row < p.R && c < p.N ? *reinterpret_cast<const uint4*>(W + (int64_t)row * p.N + c) : make_uint4(0, 0, 0, 0);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    // columns 8 pc + 2 j, + 1 of group pc / 4: columns 2 (pc % 4), + 1 of that group's matrix tile j
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(sW + at<256>(row, (pc & 12) + j) + 4 * (pc & 3)) = ww[j];
+  }
+  cp_async_wait<0>();
   __syncthreads();
-  const float scale = p.scale ? p.scale[t.a] : 1.f;
-  for (int i = tid; i < kRows * RP / 4; i += kThreads) {
-    const int row = i / (RP / 4), c = 4 * (i % (RP / 4));
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < t.rows) {
-      const float* q = p.part + (int64_t)(t.r0 + row) * RP + c;
-      for (int k = 0; k < p.splits; ++k) {
-        const float4 f = *reinterpret_cast<const float4*>(q + (int64_t)k * p.g.T * RP);
-        s.x += f.x;
-        s.y += f.y;
-        s.z += f.z;
-        s.w += f.w;
+  const int qr = lane >> 2, qc = lane & 3;
+  const int pieces = padded / 16 * 2;  // 16 tokens x 64 columns; a warp takes both halves of a group of tokens
+  uint4 b[2][2], bn[2][2];
+  int64_t rows[2], rn[2];
+  auto fetch = [&](int piece, int64_t (&r)[2], uint4 (&q)[2][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = (piece >> 1) * 16 + qr + 8 * h;
+      r[h] = piece < pieces && row < t.rows ? tok[row] : -1;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int c = n0 + 64 * (piece & 1) + 32 * g + 8 * qc;
+        q[h][g] = p.base && r[h] >= 0 && c < p.N ? *reinterpret_cast<const uint4*>(p.base + r[h] * p.ldb + c) : make_uint4(0, 0, 0, 0);
       }
     }
-    const uint2 w = make_uint2(pack_bf16x2(s.x * scale, s.y * scale), pack_bf16x2(s.z * scale, s.w * scale));
-    *reinterpret_cast<uint2*>(sV + at_rank<RP>(row, c >> 3) + (c & 4) * 2) = w;
-    if (block == 0 && row < t.rows) {
-      const int tk = tok[row];
-      const float f[4] = {s.x, s.y, s.z, s.w};
-      if (p.u && tk >= 0)
+  };
+  const uint32_t woff = bw + at<256>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4);
+  int piece = 2 * warp;
+  fetch(piece, rows, b);
+  while (piece < pieces) {
+    const int next = piece & 1 ? piece + 15 : piece + 1;
+    fetch(next, rn, bn);
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    const uint32_t wp = woff ^ (uint32_t)((piece & 1) << 7);
+#pragma unroll
+    for (int kk = 0; kk < RP / 16; ++kk) {
+      uint32_t a[4];
+      ldsm4(a, bv + at_rank<RP>((piece >> 1) * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t w[4];
+        ldsm4t(w, (wp ^ (uint32_t)(np << 5)) + kk * 16 * 256);
+        mma16816(acc[2 * np], a, w[0], w[1]);
+        mma16816(acc[2 * np + 1], a, w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (rows[h] < 0) continue;
+      uint16_t* out = p.out + rows[h] * p.N;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int c = n0 + 64 * (piece & 1) + 32 * g + 8 * qc;
+        if (c >= p.N) continue;
+        const uint32_t o[4] = {b[h][g].x, b[h][g].y, b[h][g].z, b[h][g].w};
+        uint32_t r[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (c + j < p.R) p.u[(int64_t)tk * p.R + c + j] = f[j];
-      if (p.v) *reinterpret_cast<uint2*>(p.v + (int64_t)(t.r0 + row) * RP + c) = w;
-      if (p.su) {
-        float z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = tk >= 0 && c + j < p.R ? p.u_in[(int64_t)tk * p.R + c + j] * scale : 0.f;
-        *reinterpret_cast<uint2*>(p.su + (int64_t)(t.r0 + row) * RP + c) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+          r[j] = pack_bf16x2(__uint_as_float(o[j] << 16) + acc[4 * g + j][2 * h],
+                             __uint_as_float(o[j] & 0xFFFF0000u) + acc[4 * g + j][2 * h + 1]);
+        *reinterpret_cast<uint4*>(out + c) = make_uint4(r[0], r[1], r[2], r[3]);
       }
     }
-  }
-  const uint16_t* W = p.W + (int64_t)t.a * p.R * p.N;
-  const uint32_t bw = smem_u32(sW), bv = smem_u32(sV);
-  const int n1 = min(p.N, (block + 1) * p.cols);
-  const int qr = lane >> 2, qc = lane & 3;
-  int64_t rows[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = warp * 16 + qr + 8 * h;
-    rows[h] = row < t.rows ? tok[row] : -1;
-  }
-  for (int n0 = block * p.cols; n0 < n1; n0 += 128) {
-    uint4 b[2][4];  // base: two rows, four groups of 32 columns
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int c = n0 + 32 * g + 8 * qc;
-        b[h][g] = p.base && rows[h] >= 0 && c < n1 ? *reinterpret_cast<const uint4*>(p.base + rows[h] * p.ldb + c)
-                                                  : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i) {
-      const int row = (tid >> 4) + 8 * i, pc = tid & 15;
-      const int c = n0 + 8 * pc;
-      const uint4 w = row < p.R && c < p.N ? *reinterpret_cast<const uint4*>(W + (int64_t)row * p.N + c) : make_uint4(0, 0, 0, 0);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      // columns 8 pc + 2 j, + 1 of group pc / 4: columns 2 (pc % 4), + 1 of that group's matrix tile j
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint32_t*>(sW + at256(row, (pc & 12) + j) + 4 * (pc & 3)) = ww[j];
+    for (int h = 0; h < 2; ++h) {
+      rows[h] = rn[h];
+      b[h][0] = bn[h][0];
+      b[h][1] = bn[h][1];
     }
-    __syncthreads();
-    if (warp * 16 < t.rows) {
-      float acc[16][4];
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < RP / 16; ++kk) {
-        uint32_t a[4];
-        ldsm4(a, bv + at_rank<RP>(warp * 16 + (lane & 15), 2 * kk + (lane >> 4)));
-#pragma unroll
-        for (int np = 0; np < 8; ++np) {
-          uint32_t w[4];
-          ldsm4t(w, bw + at256(kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * np + (lane >> 4)));
-          mma16816(acc[2 * np], a, w[0], w[1]);
-          mma16816(acc[2 * np + 1], a, w[2], w[3]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (rows[h] < 0) continue;
-        uint16_t* out = p.out + rows[h] * p.N;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = n0 + 32 * g + 8 * qc;
-          if (c >= n1) continue;
-          const uint32_t o[4] = {b[h][g].x, b[h][g].y, b[h][g].z, b[h][g].w};
-          uint32_t r[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            r[j] = pack_bf16x2(__uint_as_float(o[j] << 16) + acc[4 * g + j][2 * h],
-                               __uint_as_float(o[j] & 0xFFFF0000u) + acc[4 * g + j][2 * h + 1]);
-          *reinterpret_cast<uint4*>(out + c) = make_uint4(r[0], r[1], r[2], r[3]);
-        }
-      }
-    }
-    __syncthreads();  // sW is read
+    piece = next;
   }
 }
 
@@ -349,7 +416,7 @@ struct GradProblem {
   uint16_t* dW;       // [n, R, K]
   float* part;        // [2 (T / per + 1), R, K]
   int64_t ld;
-  int K, blocks;      // blocks of 128 features
+  int K, blocks;      // blocks of 256 features
 };
 struct GradArgs {
   Groups g;
@@ -361,38 +428,50 @@ struct GradArgs {
 // such adapters' first rows, and any two other tiles, are more than `per` rows apart, so that no two share a place.
 __device__ __forceinline__ int part_of(int r0, int per, int index) { return 2 * (r0 / per) + (index == 0 ? 1 : 0); }
 
+// All r rows by 256 features (32 a warp) over up to `per` tokens, 32 tokens a stage.
 template <int RP>
-__global__ void __launch_bounds__(kThreads) adapter_grad_kernel(const GradArgs p) {
+struct GradCfg {
+  static constexpr int ROWS = 32, STAGES = RP <= 64 ? 5 : 4;
+  static constexpr int X = ROWS * 512, STAGE = X + ROWS * RP * 2;
+};
+template <int RP>
+__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kernel(const GradArgs p) {
+  using C = GradCfg<RP>;
   extern __shared__ __align__(256) uint8_t smem[];
   __shared__ int tok[kMaxPer];
-  constexpr int kStage = kRows * 256 + kRows * RP * 2;
   pdl_wait();
   pdl_trigger();
   Tile t;
   if (!find_tile(p.g, blockIdx.y, p.per, t)) return;
   const GradProblem& q = p.pr[(int)blockIdx.x < p.pr[0].blocks ? 0 : 1];
-  const int n0 = ((int)blockIdx.x < p.pr[0].blocks ? (int)blockIdx.x : (int)blockIdx.x - p.pr[0].blocks) * 128;
+  const int n0 = ((int)blockIdx.x < p.pr[0].blocks ? (int)blockIdx.x : (int)blockIdx.x - p.pr[0].blocks) * 256;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = smem_u32(smem);
-  for (int i = tid; i < t.rows; i += kThreads) tok[i] = token_of(p.g, t.r0 + i);
+  const int steps = (t.rows + C::ROWS - 1) / C::ROWS;
+  for (int i = tid; i < steps * C::ROWS; i += kThreads) tok[i] = i < t.rows ? token_of(p.g, t.r0 + i) : -1;
   __syncthreads();
-  const int steps = (t.rows + kRows - 1) / kRows;
-  const int pc = tid & 15;
-  const uint32_t in = n0 + 8 * pc < q.K ? 16u : 0u;
-  auto load = [&](int s) {
-    const uint32_t st = base + (uint32_t)(s % kStages) * kStage;
-    const int r = s * kRows;
+  // copies: pieces of 16 bytes, a warp a row of 512; v's rows one behind another
+  const uint32_t in = n0 + 8 * lane < q.K ? 16u : 0u;
+  const uint16_t* xcol = q.x + (in ? n0 + 8 * lane : 0);
+  uint32_t xd[4];
 #pragma unroll
-    for (int i = 0; i < kRows / 8; ++i) {
-      const int row = (tid >> 4) + 8 * i;
-      const int tk = r + row < t.rows ? tok[r + row] : -1;
-      cp_async_16_zfill(st + at256(row, pc), tk >= 0 && in ? q.x + (int64_t)tk * q.ld + n0 + 8 * pc : q.x, tk >= 0 ? in : 0u);
+  for (int i = 0; i < 4; ++i) xd[i] = base + at<512>(warp + 8 * i, lane);
+  constexpr int VN = (C::ROWS * RP / 8 + kThreads - 1) / kThreads;
+  auto load = [&](int s) {
+    const uint32_t st = (uint32_t)(s % C::STAGES) * C::STAGE;
+    const int r = s * C::ROWS;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tk = tok[r + warp + 8 * i];
+      cp_async_16_zfill(xd[i] + st, xcol + (int64_t)(tk < 0 ? 0 : tk) * q.ld, tk < 0 ? 0u : in);
     }
-    for (int i = tid; i < kRows * RP / 8; i += kThreads) {
-      const int row = i / (RP / 8), c = i % (RP / 8);
-      const bool ok = r + row < t.rows;
-      cp_async_16_zfill(st + kRows * 256 + at_rank<RP>(row, c), ok ? q.v + (int64_t)(t.r0 + r + row) * RP + 8 * c : q.v,
-                        ok ? 16u : 0u);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const int e = tid + i * kThreads, row = e / (RP / 8), c = e % (RP / 8);
+      if (e < C::ROWS * RP / 8) {
+        const bool ok = r + row < t.rows;
+        cp_async_16_zfill(base + st + C::X + at_rank<RP>(row, c), ok ? q.v + (int64_t)(t.r0 + r + row) * RP + 8 * c : q.v, ok ? 16u : 0u);
+      }
     }
   };
   float acc[RP / 16][4][4];
@@ -402,26 +481,28 @@ __global__ void __launch_bounds__(kThreads) adapter_grad_kernel(const GradArgs p
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
-  for (int i = 0; i < kStages - 1; ++i) {
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) {
     if (i < steps) load(i);
     cp_async_commit();
   }
+  const uint32_t xo = base + at<512>((lane & 7) + (((lane >> 3) & 1) << 3), warp * 4 + (lane >> 4));
+  const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
   for (int s = 0; s < steps; ++s) {
-    cp_async_wait<kStages - 2>();
+    cp_async_wait<C::STAGES - 2>();
     __syncthreads();
-    if (s + kStages - 1 < steps) load(s + kStages - 1);
+    if (s + C::STAGES - 1 < steps) load(s + C::STAGES - 1);
     cp_async_commit();
-    const uint32_t st = base + (uint32_t)(s % kStages) * kStage;
+    const uint32_t st = (uint32_t)(s % C::STAGES) * C::STAGE;
 #pragma unroll
-    for (int kk = 0; kk < kRows / 16; ++kk) {
+    for (int kk = 0; kk < C::ROWS / 16; ++kk) {
       uint32_t b[2][4];
 #pragma unroll
-      for (int np = 0; np < 2; ++np)
-        ldsm4t(b[np], st + at256(kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), warp * 4 + 2 * np + (lane >> 4)));
+      for (int np = 0; np < 2; ++np) ldsm4t(b[np], ((xo + st) ^ (uint32_t)(np << 5)) + kk * 16 * 512);
 #pragma unroll
       for (int mt = 0; mt < RP / 16; ++mt) {
         uint32_t a[4];
-        ldsm4t(a, st + kRows * 256 + at_rank<RP>(kk * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * mt + ((lane >> 3) & 1)));
+        ldsm4t(a, base + st + C::X + at_rank<RP>(kk * 16 + vr, 2 * mt + vc));
 #pragma unroll
         for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
       }
@@ -469,10 +550,13 @@ __global__ void __launch_bounds__(256) adapter_reduce_kernel(const GradArgs p) {
   const int64_t size = (int64_t)p.R * q.K;
   const int tiles = count <= 0 ? 0 : (count + p.per - 1) / p.per;
   uint16_t* dW = q.dW + a * size;
+  const int place = part_of(o0, p.per, 1);  // of tile 0 one more; each tile further 2
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * 1024) {  // K is a multiple of 8
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* src = q.part + (int64_t)place * size + i;
+#pragma unroll 4
     for (int k = 0; k < tiles; ++k) {
-      const float4 f = *reinterpret_cast<const float4*>(q.part + part_of(o0 + k * p.per, p.per, k) * size + i);
+      const float4 f = *reinterpret_cast<const float4*>(src + (2 * k + (k == 0)) * size);
       s.x += f.x;
       s.y += f.y;
       s.z += f.z;
@@ -497,38 +581,67 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 int64_t slots_of(int64_t T, int64_t n, int64_t per) { return T / per + n; }
 
-// CTAs along the contraction: enough for six an SM, no more than its chunks.
-int splits_of(int64_t T, int64_t n, int64_t K, int sms) {
-  const int64_t tiles = cdiv(T, kRows) + std::min<int64_t>(n, T) - 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(cdiv(K, kChunk), kMaxSplit), 6 * sms / std::max<int64_t>(tiles, 1)));
-}
 int grad_rows(int64_t T) { return T <= 4096 ? 256 : T <= 8192 ? 512 : kMaxPer; }
+// tiles of `per` rows that T tokens of n adapters come to, about
+int64_t tiles_of(int64_t T, int64_t n, int64_t per) { return cdiv(T, per) + (std::min<int64_t>(n, T) - 1) / 2; }
 
+template <int RP, int SPLIT>
+int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
+  using C = ShrinkCfg<RP>;
+  auto kern = adapter_shrink_kernel<RP, SPLIT>;
+  const dim3 grid((unsigned)(slots_of(a.g.T, a.g.n, C::ROWS) * SPLIT));
+  if constexpr (SPLIT == 1) {
+    return launch_pdl(kern, grid, dim3(kThreads), C::SMEM, st, "adapter shrink", a);
+  } else {
+    const int rc = allow_smem(reinterpret_cast<const void*>(kern), C::SMEM);
+    if (rc) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = SPLIT;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = option(MOE_OPT_PDL) ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    count_launch();
+    if (e != cudaSuccess) return cuda_check(e, "adapter shrink");
+    return cuda_check(cudaGetLastError(), "adapter shrink");
+  }
+}
+// CTAs along the contraction: as many as two resident CTAs an SM have room for (longer CTAs pay their start once).
 template <int RP>
-int run_shrink(const ShrinkArgs& a, cudaStream_t st) {
-  return launch_pdl(adapter_shrink_kernel<RP>, dim3((unsigned)slots_of(a.g.T, a.g.n, kRows), (unsigned)a.splits), dim3(kThreads),
-                    (size_t)kStages * (kRows + RP) * 256, st, "adapter shrink", a);
+int run_shrink(const ShrinkArgs& a, int sms, cudaStream_t st) {
+  using C = ShrinkCfg<RP>;
+  const int64_t tiles = tiles_of(a.g.T, a.g.n, C::ROWS), chunks = cdiv(a.K, C::KC);
+  const auto fits = [&](int s) { return tiles * s <= 2 * sms && chunks >= s; };
+  return fits(8) ? launch_shrink<RP, 8>(a, st) : fits(4) ? launch_shrink<RP, 4>(a, st) : fits(2) ? launch_shrink<RP, 2>(a, st)
+                                                                                              : launch_shrink<RP, 1>(a, st);
 }
 template <int RP>
 int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
-  a.slots = (int)slots_of(a.g.T, a.g.n, kRows);
-  // 512 columns a CTA share the summation of a tile's r numbers; fewer where that leaves SMs without work
-  const int64_t tiles = cdiv(a.g.T, kRows) + std::min<int64_t>(a.g.n, a.g.T) - 1;
-  a.cols = 512;
-  while (a.cols > 128 && tiles * cdiv(a.N, a.cols) < 4 * sms) a.cols /= 2;
-  a.col_blocks = (int)cdiv(a.N, a.cols);
-  const int64_t blocks = (int64_t)a.slots * a.col_blocks + cdiv(a.g.T, kRows);
+  // 256 tokens a CTA share W's columns; fewer where that leaves SMs without work
+  a.col_blocks = (int)cdiv(a.N, 128);
+  a.per = kExpandRows;
+  while (a.per > 64 && tiles_of(a.g.T, a.g.n, a.per) * a.col_blocks < 4 * sms) a.per /= 2;
+  a.slots = (int)slots_of(a.g.T, a.g.n, a.per);
+  const int64_t blocks = (int64_t)a.slots * a.col_blocks + cdiv(a.g.T, 64);
   if (blocks > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "adapter: too many tiles");
-  return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)blocks), dim3(kThreads), RP * 256 + kRows * RP * 2, st,
+  return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)blocks), dim3(kThreads), (size_t)RP * 256 + (size_t)a.per * RP * 2, st,
                     "adapter expand", a);
 }
 template <int RP>
 int run_grad(const GradArgs& a, cudaStream_t st) {
   int rc = launch_pdl(adapter_grad_kernel<RP>, dim3((unsigned)(a.pr[0].blocks + a.pr[1].blocks), (unsigned)slots_of(a.g.T, a.g.n, a.per)),
-                      dim3(kThreads), (size_t)kStages * (kRows * 256 + kRows * RP * 2), st, "adapter gradient", a);
+                      dim3(kThreads), (size_t)GradCfg<RP>::STAGES * GradCfg<RP>::STAGE, st, "adapter gradient", a);
   if (rc) return rc;
   const int64_t most = (int64_t)a.R * std::max(a.pr[0].K, a.pr[1].K);
-  return launch_pdl(adapter_reduce_kernel, dim3((unsigned)std::min<int64_t>(cdiv(most, 1024), 64), (unsigned)a.g.n, 2), dim3(256), 0,
+  return launch_pdl(adapter_reduce_kernel, dim3((unsigned)std::min<int64_t>(cdiv(most, 1024), 512), (unsigned)a.g.n, 2), dim3(256), 0,
                     st, "adapter gradient sums", a);
 }
 template <typename F>
@@ -542,9 +655,9 @@ int by_rank(int rp, F&& f) {
 }
 
 struct Layout {
-  size_t part, v, su, grad0, grad1, total;
+  size_t v, su, grad0, grad1, total;
 };
-Layout layout(int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, bool backward, int sms) {
+Layout layout(int64_t T, int64_t H, int64_t N, int64_t r, bool backward) {
   Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -553,9 +666,8 @@ Layout layout(int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, bool backwa
     return at;
   };
   const int rp = padded_rank(r);
-  L.part = take((size_t)splits_of(T, n, backward ? N : H, sms) * T * rp * 4);
+  L.v = take((size_t)T * rp * 2);
   if (backward) {
-    L.v = take((size_t)T * rp * 2);
     L.su = take((size_t)T * rp * 2);
     const size_t places = 2 * (size_t)(T / grad_rows(T) + 1);
     L.grad0 = take(places * r * H * 4);
@@ -583,7 +695,7 @@ using namespace moebwd;
 
 extern "C" size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, int backward) {
   if (T <= 0 || H <= 0 || N <= 0 || n <= 0 || r <= 0 || r > 128) return 0;
-  return layout(T, H, N, n, r, backward != 0, device_sm_count()).total;
+  return layout(T, H, N, r, backward != 0).total;
 }
 
 extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base,
@@ -603,21 +715,21 @@ extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void
     return fail(MOE_ERR_INVALID, "adapter_fwd: metadata, scales and u must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_ERR_INVALID, "adapter_fwd: workspace must be 256-byte aligned");
   const int sms = device_sm_count();
-  const Layout L = layout(T, H, N, n, r, false, sms);
+  const Layout L = layout(T, H, N, r, false);
   if (workspace_bytes < L.total) return fail(MOE_ERR_INVALID, "adapter_fwd: workspace too small (%zu < %zu)", workspace_bytes, L.total);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Groups g{expert_offsets, x_gather_idx, (int)n, (int)T};
-  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.part);
   ShrinkArgs s{};
-  s.g = g; s.x = static_cast<const uint16_t*>(x); s.ld = ldx; s.W = static_cast<const uint16_t*>(A); s.part = part;
-  s.K = (int)H; s.R = (int)r; s.splits = splits_of(T, n, H, sms);
+  s.g = g; s.x = static_cast<const uint16_t*>(x); s.ld = ldx; s.W = static_cast<const uint16_t*>(A); s.scale = scale;
+  s.v = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + L.v); s.u = u;
+  s.K = (int)H; s.R = (int)r;
   ExpandArgs e{};
-  e.g = g; e.part = part; e.scale = scale; e.W = static_cast<const uint16_t*>(B);
+  e.g = g; e.v = s.v; e.W = static_cast<const uint16_t*>(B);
   e.base = static_cast<const uint16_t*>(base); e.ldb = ldbase; e.out = static_cast<uint16_t*>(y); e.back = s_reverse_scatter_idx;
-  e.u = u; e.N = (int)N; e.R = (int)r; e.splits = s.splits;
+  e.u = u; e.N = (int)N; e.R = (int)r;
   return by_rank(padded_rank(r), [&](auto k) {
     constexpr int RP = decltype(k)::value;
-    const int rc1 = run_shrink<RP>(s, st);
+    const int rc1 = run_shrink<RP>(s, sms, st);
     return rc1 ? rc1 : run_expand<RP>(e, sms, st);
   });
 }
@@ -650,28 +762,27 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
     return fail(MOE_ERR_INVALID, "adapter_bwd: metadata, scales and u must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_ERR_INVALID, "adapter_bwd: workspace must be 256-byte aligned");
   const int sms = device_sm_count();
-  const Layout L = layout(T, H, N, n, r, true, sms);
+  const Layout L = layout(T, H, N, r, true);
   if (workspace_bytes < L.total) return fail(MOE_ERR_INVALID, "adapter_bwd: workspace too small (%zu < %zu)", workspace_bytes, L.total);
   char* ws = static_cast<char*>(workspace);
   const Groups g{expert_offsets, x_gather_idx, (int)n, (int)T};
   ShrinkArgs s{};
-  s.g = g; s.x = static_cast<const uint16_t*>(dy); s.ld = lddy; s.W = static_cast<const uint16_t*>(B);
-  s.part = reinterpret_cast<float*>(ws + L.part);
-  s.K = (int)N; s.R = (int)r; s.splits = splits_of(T, n, N, sms);
+  s.g = g; s.x = static_cast<const uint16_t*>(dy); s.ld = lddy; s.W = static_cast<const uint16_t*>(B); s.scale = scale;
+  s.v = reinterpret_cast<uint16_t*>(ws + L.v); s.u_in = u; s.su = reinterpret_cast<uint16_t*>(ws + L.su);
+  s.K = (int)N; s.R = (int)r;
   ExpandArgs e{};
-  e.g = g; e.part = s.part; e.scale = scale; e.W = static_cast<const uint16_t*>(A);
+  e.g = g; e.v = s.v; e.W = static_cast<const uint16_t*>(A);
   e.base = static_cast<const uint16_t*>(base); e.ldb = ldbase; e.out = static_cast<uint16_t*>(dx); e.back = s_reverse_scatter_idx;
-  e.v = reinterpret_cast<uint16_t*>(ws + L.v); e.u_in = u; e.su = reinterpret_cast<uint16_t*>(ws + L.su);
-  e.N = (int)H; e.R = (int)r; e.splits = s.splits;
+  e.N = (int)H; e.R = (int)r;
   GradArgs d{};
   d.g = g; d.R = (int)r; d.per = grad_rows(T); d.accumulate = accumulate;
-  d.pr[0] = GradProblem{static_cast<const uint16_t*>(x), e.v, static_cast<uint16_t*>(dA), reinterpret_cast<float*>(ws + L.grad0), ldx,
-                        (int)H, (int)cdiv(H, 128)};
-  d.pr[1] = GradProblem{static_cast<const uint16_t*>(dy), e.su, static_cast<uint16_t*>(dB), reinterpret_cast<float*>(ws + L.grad1), lddy,
-                        (int)N, (int)cdiv(N, 128)};
+  d.pr[0] = GradProblem{static_cast<const uint16_t*>(x), s.v, static_cast<uint16_t*>(dA), reinterpret_cast<float*>(ws + L.grad0), ldx,
+                        (int)H, (int)cdiv(H, 256)};
+  d.pr[1] = GradProblem{static_cast<const uint16_t*>(dy), s.su, static_cast<uint16_t*>(dB), reinterpret_cast<float*>(ws + L.grad1), lddy,
+                        (int)N, (int)cdiv(N, 256)};
   return by_rank(padded_rank(r), [&](auto k) {
     constexpr int RP = decltype(k)::value;
-    int rc1 = run_shrink<RP>(s, st);
+    int rc1 = run_shrink<RP>(s, sms, st);
     if (!rc1) rc1 = run_expand<RP>(e, sms, st);
     return rc1 ? rc1 : run_grad<RP>(d, st);
   });
