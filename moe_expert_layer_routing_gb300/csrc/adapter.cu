@@ -25,7 +25,7 @@ namespace moebwd {
 namespace {
 
 constexpr int kThreads = 256;  // eight warps
-constexpr int kMaxPer = 1024;  // rows of a gradient tile at most
+constexpr int kMaxPer = 2048;  // rows of a gradient range at most
 
 struct Groups {
   const int32_t* off;  // [n + 1]
@@ -79,7 +79,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -131,7 +131,8 @@ struct ShrinkArgs {
 template <int RP>
 struct ShrinkCfg {
   static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PITCH = KC * 2, PIECES = KC / 8;
-  static constexpr int HALVES = 512 / (ROWS * 4);  // groups of warps that share a row's contraction
+  static constexpr int MT = RP == 64 ? 2 : 1;               // 16-token tiles of a warp, which share what it reads of W
+  static constexpr int HALVES = 8 * 16 * MT / ROWS;         // groups of warps that share a row's contraction
   static constexpr int STAGES = RP <= 64 ? 4 : 3;
   static constexpr int X = ROWS * PITCH, STAGE = X + RP * PITCH;
   static constexpr int PART = HALVES * ROWS * RP * 4;
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
     const int row = r0 + STEP * i, tk = tok[row];
     xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)c0 * C::KC;
     xb[i] = tk < 0 ? 0u : 16u;
-    xd[i] = row < ((t.rows + 15) & ~15) ? base + at<C::PITCH>(row, pc) : 0u;  // rows that no warp reads are not filled
+    xd[i] = row < ((t.rows + 16 * C::MT - 1) & ~(16 * C::MT - 1)) ? base + at<C::PITCH>(row, pc) : 0u;  // rows that no warp reads are not filled
   }
   const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)c0 * C::KC;
   auto load = [&](int c) {
@@ -185,11 +186,13 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
       }
     }
   };
-  float acc[RP / 8][4];
+  float acc[C::MT][RP / 8][4];
 #pragma unroll
-  for (int i = 0; i < RP / 8; ++i)
+  for (int m = 0; m < C::MT; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int i = 0; i < RP / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) {
     if (c0 + i < c1) load(c0 + i);
@@ -197,25 +200,29 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
   }
   const int rg = C::HALVES == 2 ? warp & 3 : warp, half = C::HALVES == 2 ? warp >> 2 : 0;
   constexpr int KK = C::KC / 16 / C::HALVES;
-  const uint32_t aoff = base + at<C::PITCH>(rg * 16 + (lane & 15), 2 * KK * half + (lane >> 4));
+  const uint32_t aoff = base + at<C::PITCH>(rg * 16 * C::MT + (lane & 15), 2 * KK * half + (lane >> 4));
   const uint32_t boff = base + C::X + at<C::PITCH>((lane & 7) + ((lane >> 4) << 3), 2 * KK * half + ((lane >> 3) & 1));
   for (int c = c0; c < c1; ++c) {
     cp_async_wait<C::STAGES - 2>();
     __syncthreads();  // stage c has landed for everyone, and everyone is done with the stage refilled now
     if (c + C::STAGES - 1 < c1) load(c + C::STAGES - 1);
     cp_async_commit();
-    if (rg * 16 < t.rows) {
+    if (rg * 16 * C::MT < t.rows) {
       const uint32_t st = (uint32_t)((c - c0) % C::STAGES) * C::STAGE;
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        uint32_t a[4];
-        ldsm4(a, (aoff + st) ^ (uint32_t)(kk << 5));
+        uint32_t a[C::MT][4];
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m) ldsm4(a[m], ((aoff + st) ^ (uint32_t)(kk << 5)) + m * 16 * C::PITCH);
 #pragma unroll
         for (int nb = 0; nb < RP / 16; ++nb) {
           uint32_t b[4];
           ldsm4(b, ((boff + st) ^ (uint32_t)(kk << 5)) + nb * 16 * C::PITCH);
-          mma16816(acc[2 * nb], a, b[0], b[1]);
-          mma16816(acc[2 * nb + 1], a, b[2], b[3]);
+#pragma unroll
+          for (int m = 0; m < C::MT; ++m) {
+            mma16816(acc[m][2 * nb], a[m], b[0], b[1]);
+            mma16816(acc[m][2 * nb + 1], a[m], b[2], b[3]);
+          }
         }
       }
     }
@@ -224,10 +231,11 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
   __syncthreads();  // the partial tiles overlay the stages
   float* part = reinterpret_cast<float*>(smem);  // [halves][rows][RP]
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float* out = part + (half * C::ROWS + rg * 16 + (lane >> 2) + 8 * h) * RP + 2 * (lane & 3);
+  for (int h = 0; h < 2 * C::MT; ++h) {
+    float* out = part + (half * C::ROWS + rg * 16 * C::MT + (lane >> 2) + 8 * h) * RP + 2 * (lane & 3);
 #pragma unroll
-    for (int i = 0; i < RP / 8; ++i) *reinterpret_cast<float2*>(out + 8 * i) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+    for (int i = 0; i < RP / 8; ++i)
+      *reinterpret_cast<float2*>(out + 8 * i) = make_float2(acc[h >> 1][i][2 * (h & 1)], acc[h >> 1][i][2 * (h & 1) + 1]);
   }
   if (SPLIT > 1)
     cluster_sync_all();
@@ -283,127 +291,202 @@ struct ExpandArgs {
   const int32_t* back;   // [T] token -> grouped row, negative: none
   float* u;              // [T, R] zeros for tokens without an adapter, or null
   int64_t ldb;
-  int N, R, per, col_blocks, slots;  // rows of a tile (at most kExpandRows)
+  int N, R, per, shift, col_blocks;  // rows of a tile: 2^shift, at most kExpandRows
 };
 constexpr int kExpandRows = 256;
 
-// A tile of up to 256 tokens x 128 columns.  W's 128 columns and the tile's v stay in shared memory; then the warps go on
-// alone, 16 tokens x 64 columns at a time with the next piece's base already on its way.  The columns of W are
-// permuted within 32 on their way to shared memory so that a thread's four 8-column matrix tiles give it 8 neighbouring
-// columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a row, with no pass through shared memory.
+// Tiles of 2^shift rows before each adapter's, first[0 .. n]; the number of all is returned.  All 256 threads call it.
+__device__ __forceinline__ int tile_table(const Groups& g, int shift, int* first, int* warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, each = (g.n + kThreads - 1) / kThreads, a0 = tid * each;
+  const int round = (1 << shift) - 1;
+  int mine = 0;
+  for (int i = a0; i < a0 + each && i < g.n; ++i) {
+    const int c = clamp_row(g.off[i + 1], g.T) - clamp_row(g.off[i], g.T);
+    first[i] = mine;
+    mine += c > 0 ? (c + round) >> shift : 0;
+  }
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) warp_sum[tid >> 5] = sum;
+  __syncthreads();
+  int before = sum - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < (tid >> 5)) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  for (int i = a0; i < a0 + each && i < g.n; ++i) first[i] += before;
+  if (tid == 0) first[g.n] = all;
+  __syncthreads();
+  return all;
+}
+
+// One wave of CTAs shares out the pieces of work (a tile of up to 256 tokens x 128 columns, a tile's pieces one behind
+// another) in equal, contiguous parts.  The tile's v stays in shared memory; W's columns come in two buffers, the next
+// piece's while this one is worked on.  A warp goes through its tokens, 16 x 64 columns at a time, with the next
+// ones' base already on its way, across pieces too.  (A CTA a piece, 7 waves of them, started anew each time: 16384 x 4096,
+// rank 16: %E0 us, now %E1.)  The columns of W are permuted within 32 on their way to shared memory so that a thread's four
+// 8-column matrix tiles give it 8 neighbouring columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a
+// row, with no pass through shared memory.
+// What the kernel reads before pdl_wait, and the rows without an adapter that it writes there, belong to the caller: whatever wrote
+// or read them is complete before the shrink kernel lets this one start.
 template <int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_kernel(const ExpandArgs p) {
   extern __shared__ __align__(256) uint8_t smem[];
-  uint8_t* sW = smem;              // [RP][128], permuted
-  uint8_t* sV = smem + RP * 256;   // [per][RP]
-  __shared__ int tok[kExpandRows];
-  pdl_wait();
-  pdl_trigger();
+  uint8_t* sW = smem;                  // 2 x [RP][128], permuted
+  uint8_t* sV = smem + 2 * RP * 256;   // [per][RP]
+  __shared__ int tok[kExpandRows], first[kMaxExperts + 1], warp_sum[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int work = p.slots * p.col_blocks;
-  if ((int)blockIdx.x >= work) {  // 64 tokens: rows without an adapter keep their base
-    const int64_t t0 = ((int64_t)blockIdx.x - work) * 64;
-    for (int i = warp; i < 64; i += 8) {
-      const int64_t t = t0 + i;
-      if (t >= p.g.T || p.back[t] >= 0) continue;
+  const int64_t me = blockIdx.x, all = gridDim.x;
+  // rows without an adapter keep their base
+  const int t1 = (int)(p.g.T * (me + 1) / all);
+  for (int t0 = (int)(p.g.T * me / all) + 32 * warp; t0 < t1; t0 += kThreads) {
+    const bool mine = t0 + lane < t1 && p.back[t0 + lane] < 0;
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, mine); left; left &= left - 1) {
+      const int64_t t = t0 + __ffs(left) - 1;
       if (p.u)
         for (int c = lane; c < p.R; c += 32) p.u[t * p.R + c] = 0.f;
       if (p.base == p.out) continue;
-      for (int c = 8 * lane; c < p.N; c += 256)
-        *reinterpret_cast<uint4*>(p.out + t * p.N + c) =
-            p.base ? *reinterpret_cast<const uint4*>(p.base + t * p.ldb + c) : make_uint4(0, 0, 0, 0);
+      for (int c = 8 * lane; c < p.N; c += 8 * 256) {
+        uint4 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          q[i] = p.base && c + 256 * i < p.N ? *reinterpret_cast<const uint4*>(p.base + t * p.ldb + c + 256 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + 256 * i < p.N) *reinterpret_cast<uint4*>(p.out + t * p.N + c + 256 * i) = q[i];
+      }
     }
-    return;
   }
-  Tile t;
-  const int slot = blockIdx.x / p.col_blocks, n0 = (blockIdx.x % p.col_blocks) * 128;
-  if (!find_tile(p.g, slot, p.per, t)) return;
-  if (tid < t.rows) tok[tid] = token_of(p.g, t.r0 + tid);
-  const int padded = (t.rows + 15) & ~15;
+  const int found = tile_table(p.g, p.shift, first, warp_sum), most = (p.g.T >> p.shift) + p.g.n;  // wrong offsets may name more
+  const int64_t units = (int64_t)(found < most ? found : most) * p.col_blocks;
+  int64_t unit = units * me / all;
+  const int64_t end = units * (me + 1) / all;
   const uint32_t bw = smem_u32(sW), bv = smem_u32(sV);
-  for (int i = tid; i < padded * (RP / 8); i += kThreads) {
-    const int row = i / (RP / 8), c = i % (RP / 8);
-    const bool ok = row < t.rows;
-    cp_async_16_zfill(bv + at_rank<RP>(row, c), ok ? p.v + (int64_t)(t.r0 + row) * RP + 8 * c : p.v, ok ? 16u : 0u);
+  const int qr = lane >> 2, qc = lane & 3, half = warp & 1, g0 = warp >> 1;
+  const uint32_t woff = bw + (at<256>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4) ^ (uint32_t)(half << 7));
+  bool waited = false;
+  int tile = (int)(unit / p.col_blocks), cb = (int)(unit - (int64_t)tile * p.col_blocks);
+  for (; unit < end; ++tile, cb = 0) {
+    int a = 0;  // the last adapter whose first tile is at or before this one
+    for (int hi = p.g.n; hi - a > 1;) {
+      const int mid = (a + hi) >> 1;
+      if (first[mid] <= tile) a = mid; else hi = mid;
+    }
+    const int o1 = clamp_row(p.g.off[a + 1], p.g.T);
+    const int64_t r0 = clamp_row(p.g.off[a], p.g.T) + ((int64_t)(tile - first[a]) << p.shift);
+    const int rows = (int)(o1 - r0 < p.per ? o1 - r0 : p.per), padded = (rows + 15) & ~15;
+    __syncthreads();  // everyone is done with the last tile's
+    if (tid < rows) tok[tid] = token_of(p.g, (int)r0 + tid);
+    const uint16_t* W = p.W + (int64_t)a * p.R * p.N + (int64_t)(tid >> 4) * p.N + 8 * (tid & 15);
+    uint4 w[RP / 16];
+    auto load_w = [&](int block) {
+      const bool in = block * 128 + 8 * (tid & 15) < p.N;
+#pragma unroll
+      for (int i = 0; i < RP / 16; ++i)
+        w[i] = in && (tid >> 4) + 16 * i < p.R ? *reinterpret_cast<const uint4*>(W + (int64_t)16 * i * p.N + block * 128)
+                                               : make_uint4(0, 0, 0, 0);
+    };
+    auto store_w = [&](int buffer) {
+#pragma unroll
+      for (int i = 0; i < RP / 16; ++i) {
+        const int row = (tid >> 4) + 16 * i, pc = tid & 15;
+        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        // columns 8 pc + 2 j, + 1 of group pc / 4: columns 2 (pc % 4), + 1 of that group's matrix tile j
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(sW + buffer * RP * 256 + at<256>(row, (pc & 12) + j) + 4 * (pc & 3)) = ww[j];
+      }
+    };
+    uint4 b[2][2];
+    int next[2];
+    auto fetch = [&](int block, int group) {
+      const int c = block * 128 + 64 * half + 8 * qc;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = group * 16 + qr + 8 * h;
+        next[h] = row < rows ? tok[row] : -1;
+        const uint16_t* src = p.base + next[h] * p.ldb + c;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          b[h][g] = p.base && next[h] >= 0 && c + 32 * g < p.N ? *reinterpret_cast<const uint4*>(src + 32 * g) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    load_w(cb);
+    __syncthreads();  // tok
+    fetch(cb, g0);
+    store_w(0);
+    if (!waited) {
+      pdl_wait();  // v
+      pdl_trigger();
+      waited = true;
+    }
+    for (int i = tid; i < padded * (RP / 8); i += kThreads) {
+      const int row = i / (RP / 8), c = i % (RP / 8);
+      const bool ok = row < rows;
+      cp_async_16_zfill(bv + at_rank<RP>(row, c), ok ? p.v + (r0 + row) * RP + 8 * c : p.v, ok ? 16u : 0u);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    int buffer = 0;
+    for (; unit < end && cb < p.col_blocks; ++unit, ++cb, buffer ^= 1) {
+      const bool more = unit + 1 < end && cb + 1 < p.col_blocks;
+      if (more) load_w(cb + 1);
+      const uint32_t wp = woff + buffer * RP * 256;
+      for (int group = g0; group * 16 < rows; group += 4) {
+        const bool last = (group + 4) * 16 >= rows;
+        float acc[8][4];  // starts from the base
+        int row[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          row[h] = next[h];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t o[4] = {b[h][g].x, b[h][g].y, b[h][g].z, b[h][g].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[4 * g + j][2 * h] = __uint_as_float(o[j] << 16);
+              acc[4 * g + j][2 * h + 1] = __uint_as_float(o[j] & 0xFFFF0000u);
+            }
+          }
+        }
+        if (!last || more) fetch(last ? cb + 1 : cb, last ? g0 : group + 4);
+#pragma unroll
+        for (int kk = 0; kk < RP / 16; ++kk) {
+          uint32_t f[4];
+          ldsm4(f, bv + at_rank<RP>(group * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+          for (int np = 0; np < 4; ++np) {
+            uint32_t q[4];
+            ldsm4t(q, (wp ^ (uint32_t)(np << 5)) + kk * 16 * 256);
+            mma16816(acc[2 * np], f, q[0], q[1]);
+            mma16816(acc[2 * np + 1], f, q[2], q[3]);
+          }
+        }
+        const int c = cb * 128 + 64 * half + 8 * qc;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (row[h] < 0) continue;
+          uint16_t* out = p.out + (int64_t)row[h] * p.N + c;
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            if (c + 32 * g < p.N)
+              *reinterpret_cast<uint4*>(out + 32 * g) =
+                  make_uint4(pack_bf16x2(acc[4 * g][2 * h], acc[4 * g][2 * h + 1]), pack_bf16x2(acc[4 * g + 1][2 * h], acc[4 * g + 1][2 * h + 1]),
+                             pack_bf16x2(acc[4 * g + 2][2 * h], acc[4 * g + 2][2 * h + 1]), pack_bf16x2(acc[4 * g + 3][2 * h], acc[4 * g + 3][2 * h + 1]));
+        }
+      }
+      if (more) store_w(buffer ^ 1);
+      __syncthreads();
+    }
   }
-  cp_async_commit();
-  const uint16_t* W = p.W + (int64_t)t.a * p.R * p.N;
-#pragma unroll
-  for (int i = 0; i < RP / 16; ++i) {
-    const int row = (tid >> 4) + 16 * i, pc = tid & 15;
-    const int c = n0 + 8 * pc;
-    const uint4 w = row < p.R && c < p.N ? *reinterpret_cast<const uint4*>(W + (int64_t)row * p.N + c) : make_uint4(0, 0, 0, 0);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    // columns 8 pc + 2 j, + 1 of group pc / 4: columns 2 (pc % 4), + 1 of that group's matrix tile j
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(sW + at<256>(row, (pc & 12) + j) + 4 * (pc & 3)) = ww[j];
-  }
-  cp_async_wait<0>();
-  __syncthreads();
-  const int qr = lane >> 2, qc = lane & 3;
-  const int pieces = padded / 16 * 2;  // 16 tokens x 64 columns; a warp takes both halves of a group of tokens
-  uint4 b[2][2], bn[2][2];
-  int64_t rows[2], rn[2];
-  auto fetch = [&](int piece, int64_t (&r)[2], uint4 (&q)[2][2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = (piece >> 1) * 16 + qr + 8 * h;
-      r[h] = piece < pieces && row < t.rows ? tok[row] : -1;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int c = n0 + 64 * (piece & 1) + 32 * g + 8 * qc;
-        q[h][g] = p.base && r[h] >= 0 && c < p.N ? *reinterpret_cast<const uint4*>(p.base + r[h] * p.ldb + c) : make_uint4(0, 0, 0, 0);
-      }
-    }
-  };
-  const uint32_t woff = bw + at<256>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4);
-  int piece = 2 * warp;
-  fetch(piece, rows, b);
-  while (piece < pieces) {
-    const int next = piece & 1 ? piece + 15 : piece + 1;
-    fetch(next, rn, bn);
-    float acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    const uint32_t wp = woff ^ (uint32_t)((piece & 1) << 7);
-#pragma unroll
-    for (int kk = 0; kk < RP / 16; ++kk) {
-      uint32_t a[4];
-      ldsm4(a, bv + at_rank<RP>((piece >> 1) * 16 + (lane & 15), 2 * kk + (lane >> 4)));
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t w[4];
-        ldsm4t(w, (wp ^ (uint32_t)(np << 5)) + kk * 16 * 256);
-        mma16816(acc[2 * np], a, w[0], w[1]);
-        mma16816(acc[2 * np + 1], a, w[2], w[3]);
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (rows[h] < 0) continue;
-      uint16_t* out = p.out + rows[h] * p.N;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int c = n0 + 64 * (piece & 1) + 32 * g + 8 * qc;
-        if (c >= p.N) continue;
-        const uint32_t o[4] = {b[h][g].x, b[h][g].y, b[h][g].z, b[h][g].w};
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          r[j] = pack_bf16x2(__uint_as_float(o[j] << 16) + acc[4 * g + j][2 * h],
-                             __uint_as_float(o[j] & 0xFFFF0000u) + acc[4 * g + j][2 * h + 1]);
-        *reinterpret_cast<uint4*>(out + c) = make_uint4(r[0], r[1], r[2], r[3]);
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      rows[h] = rn[h];
-      b[h][0] = bn[h][0];
-      b[h][1] = bn[h][1];
-    }
-    piece = next;
+  if (!waited) {
+    pdl_wait();
+    pdl_trigger();
   }
 }
 
@@ -414,26 +497,42 @@ struct GradProblem {
   const uint16_t* x;  // [T, K], row stride ld
   const uint16_t* v;  // [T, RP] by grouped row
   uint16_t* dW;       // [n, R, K]
-  float* part;        // [2 (T / per + 1), R, K]
+  float* part;        // [2 ranges, R, K]
   int64_t ld;
   int K, blocks;      // blocks of 256 features
 };
 struct GradArgs {
   Groups g;
   GradProblem pr[2];
-  int R, per, accumulate;
+  int R, ranges, accumulate;
 };
 
-// Partial sums of adapters with more than `per` rows: tile `index` at grouped row r0 goes to 2 (r0 / per) + (index == 0).  Two
-// such adapters' first rows, and any two other tiles, are more than `per` rows apart, so that no two share a place.
-__device__ __forceinline__ int part_of(int r0, int per, int index) { return 2 * (r0 / per) + (index == 0 ? 1 : 0); }
+// The grouped rows are cut into `ranges` equal parts of `per` rows (a multiple of 32) whatever the adapters.  An adapter whose rows
+// lie in one part is summed there; of any other each part holds a partial sum: at place 2 part + 1 for the one that has the
+// adapter's first row (the part's last adapter), at 2 part for the others (the part's first), so that no two share one.
+__device__ __forceinline__ int rows_of_range(const Groups& g, int ranges, int& rows) {
+  rows = clamp_row(g.off[g.n], g.T);
+  const int per = ((rows + ranges - 1) / ranges + 31) & ~31;
+  return per > 32 ? per : 32;
+}
 
-// All r rows by 256 features (32 a warp) over up to `per` tokens, 32 tokens a stage.
+// All r rows by 256 features (32 a warp) over a range of tokens, 32 of one adapter a stage.  Equal ranges for a whole wave of
+// CTAs: with tiles of one adapter's rows, which are uneven and do not fill the waves, 16384 x (4096 + 4096) at rank 64 took %G0 us, now %G1.
 template <int RP>
 struct GradCfg {
   static constexpr int ROWS = 32, STAGES = RP <= 64 ? 5 : 4;
   static constexpr int X = ROWS * 512, STAGE = X + ROWS * RP * 2;
 };
+struct Segment {
+  int a, r, end;  // adapter, next row, row behind the adapter's last in the range
+};
+__device__ __forceinline__ void next_segment(const Groups& g, int hi, Segment& s) {
+  while (s.end <= s.r && s.r < hi) {  // the last adapter takes what wrong offsets leave over
+    ++s.a;
+    const int o1 = s.a + 1 < g.n ? clamp_row(g.off[s.a + 1], g.T) : hi;
+    s.end = o1 < hi ? o1 : hi;
+  }
+}
 template <int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kernel(const GradArgs p) {
   using C = GradCfg<RP>;
@@ -441,37 +540,52 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
   __shared__ int tok[kMaxPer];
   pdl_wait();
   pdl_trigger();
-  Tile t;
-  if (!find_tile(p.g, blockIdx.y, p.per, t)) return;
+  int rows;
+  const int per = rows_of_range(p.g, p.ranges, rows);
+  const int64_t from = (int64_t)blockIdx.y * per;
+  if (from >= rows) return;
+  const int lo = (int)from, hi = rows - lo < per ? rows : lo + per;
   const GradProblem& q = p.pr[(int)blockIdx.x < p.pr[0].blocks ? 0 : 1];
   const int n0 = ((int)blockIdx.x < p.pr[0].blocks ? (int)blockIdx.x : (int)blockIdx.x - p.pr[0].blocks) * 256;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = smem_u32(smem);
-  const int steps = (t.rows + C::ROWS - 1) / C::ROWS;
-  for (int i = tid; i < steps * C::ROWS; i += kThreads) tok[i] = i < t.rows ? token_of(p.g, t.r0 + i) : -1;
-  __syncthreads();
-  // copies: pieces of 16 bytes, a warp a row of 512; v's rows one behind another
+  for (int i = tid; i < hi - lo; i += kThreads) tok[i] = token_of(p.g, lo + i);
+  // the adapter of the range's first row: the last that begins at or before it
+  int at_or_before = 0;
+  for (int i0 = 0; i0 < p.g.n; i0 += kThreads)
+    at_or_before += __syncthreads_count(i0 + tid < p.g.n && clamp_row(p.g.off[i0 + tid < p.g.n ? i0 + tid : 0], p.g.T) <= lo);
+  Segment put{at_or_before > 0 ? at_or_before - 2 : -1, lo, lo};
+  next_segment(p.g, hi, put);
+  Segment get = put;
+  // copies: pieces of 16 bytes, a warp a row of 512, four rows; v's rows one behind another
   const uint32_t in = n0 + 8 * lane < q.K ? 16u : 0u;
   const uint16_t* xcol = q.x + (in ? n0 + 8 * lane : 0);
-  uint32_t xd[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) xd[i] = base + at<512>(warp + 8 * i, lane);
-  constexpr int VN = (C::ROWS * RP / 8 + kThreads - 1) / kThreads;
-  auto load = [&](int s) {
-    const uint32_t st = (uint32_t)(s % C::STAGES) * C::STAGE;
-    const int r = s * C::ROWS;
+  const int64_t ld = q.ld;
+  const uint32_t xd = base + at<512>(4 * warp, lane);
+  constexpr int VN = (C::ROWS * RP / 8 + kThreads - 1) / kThreads, VSTEP = kThreads / (RP / 8);  // rows of one pass
+  const int v0 = tid / (RP / 8);
+  const uint16_t* vcol = q.v + (int64_t)v0 * RP + 8 * (tid % (RP / 8));
+  const uint32_t vd = base + C::X + at_rank<RP>(v0, tid % (RP / 8));  // VSTEP is a multiple of 8
+  auto load = [&](uint32_t st) {  // the next rows, at most 32 of one adapter
+    const int count = put.end - put.r;
+    const int* tk = tok + (put.r - lo) + 4 * warp;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int tk = tok[r + warp + 8 * i];
-      cp_async_16_zfill(xd[i] + st, xcol + (int64_t)(tk < 0 ? 0 : tk) * q.ld, tk < 0 ? 0u : in);
+      const int t = 4 * warp + i < count ? tk[i] : -1;
+      cp_async_16_zfill((xd ^ (uint32_t)(i << 4)) + i * 512 + st, xcol + (int64_t)(t < 0 ? 0 : t) * ld, t < 0 ? 0u : in);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
-      const int e = tid + i * kThreads, row = e / (RP / 8), c = e % (RP / 8);
-      if (e < C::ROWS * RP / 8) {
-        const bool ok = r + row < t.rows;
-        cp_async_16_zfill(base + st + C::X + at_rank<RP>(row, c), ok ? q.v + (int64_t)(t.r0 + r + row) * RP + 8 * c : q.v, ok ? 16u : 0u);
+      const int row = v0 + i * VSTEP;
+      if (VSTEP * (i + 1) <= C::ROWS || row < C::ROWS) {
+        const bool ok = row < count;
+        cp_async_16_zfill(vd + i * VSTEP * RP * 2 + st, vcol + (int64_t)(ok ? put.r + i * VSTEP : 0) * RP, ok ? 16u : 0u);
       }
+    }
+    put.r += C::ROWS;
+    if (put.r >= put.end) {
+      put.r = put.end;
+      next_segment(p.g, hi, put);
     }
   };
   float acc[RP / 16][4][4];
@@ -483,17 +597,17 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
       for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) {
-    if (i < steps) load(i);
+    if (put.r < hi) load(i * C::STAGE);
     cp_async_commit();
   }
   const uint32_t xo = base + at<512>((lane & 7) + (((lane >> 3) & 1) << 3), warp * 4 + (lane >> 4));
   const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
-  for (int s = 0; s < steps; ++s) {
+  uint32_t st = 0, st_put = (C::STAGES - 1) * C::STAGE;
+  while (get.r < hi) {
     cp_async_wait<C::STAGES - 2>();
     __syncthreads();
-    if (s + C::STAGES - 1 < steps) load(s + C::STAGES - 1);
+    if (put.r < hi) load(st_put);
     cp_async_commit();
-    const uint32_t st = (uint32_t)(s % C::STAGES) * C::STAGE;
 #pragma unroll
     for (int kk = 0; kk < C::ROWS / 16; ++kk) {
       uint32_t b[2][4];
@@ -507,56 +621,64 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
         for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
       }
     }
-  }
-  cp_async_wait<0>();
-  const bool whole = t.count <= p.per;
-  float* part = whole ? nullptr : q.part + (int64_t)part_of(t.r0, p.per, t.index) * p.R * q.K;
-  uint16_t* dW = q.dW + (int64_t)t.a * p.R * q.K;
+    st = st == (C::STAGES - 1) * C::STAGE ? 0 : st + C::STAGE;
+    st_put = st_put == (C::STAGES - 1) * C::STAGE ? 0 : st_put + C::STAGE;
+    get.r += C::ROWS;
+    if (get.r < get.end) continue;
+    get.r = get.end;
+    // the adapter's last rows of this range
+    const bool starts = clamp_row(p.g.off[get.a], p.g.T) >= lo, ends = clamp_row(p.g.off[get.a + 1], p.g.T) <= hi;
+    const bool whole = starts && ends;
+    float* part = whole ? nullptr : q.part + (int64_t)(2 * (int)blockIdx.y + (starts ? 1 : 0)) * p.R * q.K;
+    uint16_t* dW = q.dW + (int64_t)get.a * p.R * q.K;
 #pragma unroll
-  for (int mt = 0; mt < RP / 16; ++mt)
+    for (int mt = 0; mt < RP / 16; ++mt)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = mt * 16 + (lane >> 2) + 8 * h;
-      if (m >= p.R) continue;
+      for (int h = 0; h < 2; ++h) {
+        const int m = mt * 16 + (lane >> 2) + 8 * h;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = n0 + warp * 32 + 8 * j + 2 * (lane & 3);
-        if (c >= q.K) continue;
-        float f0 = acc[mt][j][2 * h], f1 = acc[mt][j][2 * h + 1];
-        const int64_t o = (int64_t)m * q.K + c;
-        if (!whole) {
-          *reinterpret_cast<float2*>(part + o) = make_float2(f0, f1);
-        } else {
-          uint32_t* d = reinterpret_cast<uint32_t*>(dW + o);
-          if (p.accumulate) {
-            f0 += __uint_as_float(*d << 16);
-            f1 += __uint_as_float(*d & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) {
+          const int c = n0 + warp * 32 + 8 * j + 2 * (lane & 3);
+          float f0 = acc[mt][j][2 * h], f1 = acc[mt][j][2 * h + 1];
+          acc[mt][j][2 * h] = acc[mt][j][2 * h + 1] = 0.f;
+          if (m >= p.R || c >= q.K) continue;
+          const int64_t o = (int64_t)m * q.K + c;
+          if (!whole) {
+            *reinterpret_cast<float2*>(part + o) = make_float2(f0, f1);
+          } else {
+            uint32_t* d = reinterpret_cast<uint32_t*>(dW + o);
+            if (p.accumulate) {
+              f0 += __uint_as_float(*d << 16);
+              f1 += __uint_as_float(*d & 0xFFFF0000u);
+            }
+            *d = pack_bf16x2(f0, f1);
           }
-          *d = pack_bf16x2(f0, f1);
         }
       }
-    }
+    next_segment(p.g, hi, get);
+  }
+  cp_async_wait<0>();
 }
 
-// Sums of the partial tiles of an adapter with more than `per` rows, in order; zeros for one without rows.
+// Sums of the partial tiles of an adapter whose rows lie in several ranges, in order; zeros for one without rows.
 __global__ void __launch_bounds__(256) adapter_reduce_kernel(const GradArgs p) {
   pdl_wait();
   pdl_trigger();
   const GradProblem& q = p.pr[blockIdx.z];
   const int a = blockIdx.y;
-  const int o0 = clamp_row(p.g.off[a], p.g.T), o1 = clamp_row(p.g.off[a + 1], p.g.T);
-  const int count = o1 - o0;
-  if ((count > 0 && count <= p.per) || (count <= 0 && p.accumulate)) return;
+  int rows;
+  const int per = rows_of_range(p.g, p.ranges, rows);
+  const int o0 = clamp_row(p.g.off[a], rows), o1 = clamp_row(p.g.off[a + 1], rows);
+  const bool none = o1 <= o0;
+  const int s0 = o0 / per, s1 = none ? s0 : (o1 - 1) / per;
+  if (none ? p.accumulate != 0 : s0 == s1) return;
   const int64_t size = (int64_t)p.R * q.K;
-  const int tiles = count <= 0 ? 0 : (count + p.per - 1) / p.per;
   uint16_t* dW = q.dW + a * size;
-  const int place = part_of(o0, p.per, 1);  // of tile 0 one more; each tile further 2
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * 1024) {  // K is a multiple of 8
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* src = q.part + (int64_t)place * size + i;
 #pragma unroll 4
-    for (int k = 0; k < tiles; ++k) {
-      const float4 f = *reinterpret_cast<const float4*>(src + (2 * k + (k == 0)) * size);
+    for (int k = none ? s1 + 1 : s0; k <= s1; ++k) {
+      const float4 f = *reinterpret_cast<const float4*>(q.part + (2 * (int64_t)k + (k == s0)) * size + i);
       s.x += f.x;
       s.y += f.y;
       s.z += f.z;
@@ -581,7 +703,11 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 int64_t slots_of(int64_t T, int64_t n, int64_t per) { return T / per + n; }
 
-int grad_rows(int64_t T) { return T <= 4096 ? 256 : T <= 8192 ? 512 : kMaxPer; }
+// Parts of the rows in the gradient: one wave of CTAs, but 64 rows a part at least and kMaxPer at most.
+int grad_ranges(int64_t T, int64_t H, int64_t N, int rp, int sms) {
+  const int64_t wave = (rp <= 64 ? 2 : 1) * sms / (cdiv(H, 256) + cdiv(N, 256));
+  return (int)std::max(cdiv(T, kMaxPer), std::min(wave, cdiv(T, 64)));
+}
 // tiles of `per` rows that T tokens of n adapters come to, about
 int64_t tiles_of(int64_t T, int64_t n, int64_t per) { return cdiv(T, per) + (std::min<int64_t>(n, T) - 1) / 2; }
 
@@ -625,19 +751,19 @@ int run_shrink(const ShrinkArgs& a, int sms, cudaStream_t st) {
 }
 template <int RP>
 int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
-  // 256 tokens a CTA share W's columns; fewer where that leaves SMs without work
+  // 256 tokens share W's columns; fewer where that leaves a CTA less than a few pieces of work to even out
+  const int64_t wave = (RP <= 64 ? 2 : 1) * sms;
   a.col_blocks = (int)cdiv(a.N, 128);
-  a.per = kExpandRows;
-  while (a.per > 64 && tiles_of(a.g.T, a.g.n, a.per) * a.col_blocks < 4 * sms) a.per /= 2;
-  a.slots = (int)slots_of(a.g.T, a.g.n, a.per);
-  const int64_t blocks = (int64_t)a.slots * a.col_blocks + cdiv(a.g.T, 64);
-  if (blocks > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "adapter: too many tiles");
-  return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)blocks), dim3(kThreads), (size_t)RP * 256 + (size_t)a.per * RP * 2, st,
-                    "adapter expand", a);
+  a.shift = 8;
+  while (a.shift > 6 && tiles_of(a.g.T, a.g.n, 1 << a.shift) * a.col_blocks < 6 * wave) --a.shift;
+  a.per = 1 << a.shift;
+  const int64_t most = std::max(slots_of(a.g.T, a.g.n, a.per) * a.col_blocks, cdiv(a.g.T, 8));
+  return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)std::min(wave, most)), dim3(kThreads),
+                    (size_t)2 * RP * 256 + (size_t)a.per * RP * 2, st, "adapter expand", a);
 }
 template <int RP>
 int run_grad(const GradArgs& a, cudaStream_t st) {
-  int rc = launch_pdl(adapter_grad_kernel<RP>, dim3((unsigned)(a.pr[0].blocks + a.pr[1].blocks), (unsigned)slots_of(a.g.T, a.g.n, a.per)),
+  int rc = launch_pdl(adapter_grad_kernel<RP>, dim3((unsigned)(a.pr[0].blocks + a.pr[1].blocks), (unsigned)a.ranges),
                       dim3(kThreads), (size_t)GradCfg<RP>::STAGES * GradCfg<RP>::STAGE, st, "adapter gradient", a);
   if (rc) return rc;
   const int64_t most = (int64_t)a.R * std::max(a.pr[0].K, a.pr[1].K);
@@ -657,7 +783,7 @@ int by_rank(int rp, F&& f) {
 struct Layout {
   size_t v, su, grad0, grad1, total;
 };
-Layout layout(int64_t T, int64_t H, int64_t N, int64_t r, bool backward) {
+Layout layout(int64_t T, int64_t H, int64_t N, int64_t r, bool backward, int sms) {
   Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -669,7 +795,7 @@ Layout layout(int64_t T, int64_t H, int64_t N, int64_t r, bool backward) {
   L.v = take((size_t)T * rp * 2);
   if (backward) {
     L.su = take((size_t)T * rp * 2);
-    const size_t places = 2 * (size_t)(T / grad_rows(T) + 1);
+    const size_t places = 2 * (size_t)grad_ranges(T, H, N, rp, sms);
     L.grad0 = take(places * r * H * 4);
     L.grad1 = take(places * r * N * 4);
   }
@@ -695,7 +821,7 @@ using namespace moebwd;
 
 extern "C" size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, int backward) {
   if (T <= 0 || H <= 0 || N <= 0 || n <= 0 || r <= 0 || r > 128) return 0;
-  return layout(T, H, N, r, backward != 0).total;
+  return layout(T, H, N, r, backward != 0, device_sm_count()).total;
 }
 
 extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base,
@@ -715,7 +841,7 @@ extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void
     return fail(MOE_ERR_INVALID, "adapter_fwd: metadata, scales and u must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_ERR_INVALID, "adapter_fwd: workspace must be 256-byte aligned");
   const int sms = device_sm_count();
-  const Layout L = layout(T, H, N, r, false);
+  const Layout L = layout(T, H, N, r, false, sms);
   if (workspace_bytes < L.total) return fail(MOE_ERR_INVALID, "adapter_fwd: workspace too small (%zu < %zu)", workspace_bytes, L.total);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Groups g{expert_offsets, x_gather_idx, (int)n, (int)T};
@@ -762,7 +888,7 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
     return fail(MOE_ERR_INVALID, "adapter_bwd: metadata, scales and u must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_ERR_INVALID, "adapter_bwd: workspace must be 256-byte aligned");
   const int sms = device_sm_count();
-  const Layout L = layout(T, H, N, r, true);
+  const Layout L = layout(T, H, N, r, true, sms);
   if (workspace_bytes < L.total) return fail(MOE_ERR_INVALID, "adapter_bwd: workspace too small (%zu < %zu)", workspace_bytes, L.total);
   char* ws = static_cast<char*>(workspace);
   const Groups g{expert_offsets, x_gather_idx, (int)n, (int)T};
@@ -775,7 +901,7 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
   e.base = static_cast<const uint16_t*>(base); e.ldb = ldbase; e.out = static_cast<uint16_t*>(dx); e.back = s_reverse_scatter_idx;
   e.N = (int)H; e.R = (int)r;
   GradArgs d{};
-  d.g = g; d.R = (int)r; d.per = grad_rows(T); d.accumulate = accumulate;
+  d.g = g; d.R = (int)r; d.ranges = grad_ranges(T, H, N, padded_rank(r), sms); d.accumulate = accumulate;
   d.pr[0] = GradProblem{static_cast<const uint16_t*>(x), s.v, static_cast<uint16_t*>(dA), reinterpret_cast<float*>(ws + L.grad0), ldx,
                         (int)H, (int)cdiv(H, 256)};
   d.pr[1] = GradProblem{static_cast<const uint16_t*>(dy), s.su, static_cast<uint16_t*>(dB), reinterpret_cast<float*>(ws + L.grad1), lddy,
