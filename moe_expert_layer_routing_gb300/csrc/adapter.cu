@@ -72,6 +72,9 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
                : "r"(a)
                : "memory");
 }
+__device__ __forceinline__ void ld_shared_v4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -295,6 +298,12 @@ struct ExpandArgs {
 };
 constexpr int kExpandRows = 256;
 
+template <int RP>
+struct ExpandCfg {
+  static constexpr int DEPTH = RP <= 32 ? 4 : RP <= 64 ? 3 : 4;  // pieces of base of a warp on their way or in work, 2 KB each
+  static size_t smem(int per) { return (size_t)2 * RP * 256 + (size_t)per * RP * 2 + (size_t)8 * DEPTH * 2048; }
+};
+
 // Tiles of 2^shift rows before each adapter's, first[0 .. n]; the number of all is returned.  All 256 threads call it.
 __device__ __forceinline__ int tile_table(const Groups& g, int shift, int* first, int* warp_sum) {
   const int tid = threadIdx.x, lane = tid & 31, each = (g.n + kThreads - 1) / kThreads, a0 = tid * each;
@@ -336,9 +345,11 @@ __device__ __forceinline__ int tile_table(const Groups& g, int shift, int* first
 // or read them is complete before the shrink kernel lets this one start.
 template <int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_kernel(const ExpandArgs p) {
+  using C = ExpandCfg<RP>;
   extern __shared__ __align__(256) uint8_t smem[];
   uint8_t* sW = smem;                  // 2 x [RP][128], permuted
   uint8_t* sV = smem + 2 * RP * 256;   // [per][RP]
+  // then base: [warp][slot][piece of 16 bytes][lane]
   __shared__ int tok[kExpandRows], first[kMaxExperts + 1], warp_sum[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t me = blockIdx.x, all = gridDim.x;
@@ -369,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
   const uint32_t bw = smem_u32(sW), bv = smem_u32(sV);
   const int qr = lane >> 2, qc = lane & 3, half = warp & 1, g0 = warp >> 1;
   const uint32_t woff = bw + (at<256>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4) ^ (uint32_t)(half << 7));
+  const uint32_t slots = bv + p.per * RP * 2 + (uint32_t)(warp * C::DEPTH * 2048 + lane * 16);
+  const uint32_t voff = bv + at_rank<RP>(lane & 15, lane >> 4);
   bool waited = false;
   int tile = (int)(unit / p.col_blocks), cb = (int)(unit - (int64_t)tile * p.col_blocks);
   for (; unit < end; ++tile, cb = 0) {
@@ -381,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
     const int64_t r0 = clamp_row(p.g.off[a], p.g.T) + ((int64_t)(tile - first[a]) << p.shift);
     const int rows = (int)(o1 - r0 < p.per ? o1 - r0 : p.per), padded = (rows + 15) & ~15;
     __syncthreads();  // everyone is done with the last tile's
-    if (tid < rows) tok[tid] = token_of(p.g, (int)r0 + tid);
+    tok[tid] = tid < rows ? token_of(p.g, (int)r0 + tid) : -1;
     const uint16_t* W = p.W + (int64_t)a * p.R * p.N + (int64_t)(tid >> 4) * p.N + 8 * (tid & 15);
     uint4 w[RP / 16];
     auto load_w = [&](int block) {
@@ -401,23 +414,32 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
         for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(sW + buffer * RP * 256 + at<256>(row, (pc & 12) + j) + 4 * (pc & 3)) = ww[j];
       }
     };
-    uint4 b[2][2];
-    int next[2];
-    auto fetch = [&](int block, int group) {
-      const int c = block * 128 + 64 * half + 8 * qc;
+    // the warp's pieces in order: (block, group); this thread's 64 bytes of a piece's base go to its own slot
+    int fb = cb, fg = g0, fslot = 0;
+    const int fb_end = p.col_blocks - cb < end - unit ? p.col_blocks : cb + (int)(end - unit);
+    auto fetch = [&]() {
+      if (p.base && fg * 16 < rows && fb < fb_end) {
+        const int c = fb * 128 + 64 * half + 8 * qc;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = group * 16 + qr + 8 * h;
-        next[h] = row < rows ? tok[row] : -1;
-        const uint16_t* src = p.base + next[h] * p.ldb + c;
+        for (int h = 0; h < 2; ++h) {
+          const int t = tok[fg * 16 + qr + 8 * h];
+          const uint16_t* src = p.base + (t < 0 ? 0 : t) * p.ldb;
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
-          b[h][g] = p.base && next[h] >= 0 && c + 32 * g < p.N ? *reinterpret_cast<const uint4*>(src + 32 * g) : make_uint4(0, 0, 0, 0);
+          for (int g = 0; g < 2; ++g) {
+            const bool ok = t >= 0 && c + 32 * g < p.N;
+            cp_async_16_zfill(slots + (uint32_t)(fslot * 4 + 2 * h + g) * 512, ok ? src + c + 32 * g : p.base, ok ? 16u : 0u);
+          }
+        }
       }
+      cp_async_commit();
+      fslot = fslot == C::DEPTH - 1 ? 0 : fslot + 1;
+      fg += 4;
+      if (fg * 16 >= rows) fg = g0, ++fb;
     };
     load_w(cb);
     __syncthreads();  // tok
-    fetch(cb, g0);
+#pragma unroll
+    for (int i = 0; i < C::DEPTH - 1; ++i) fetch();
     store_w(0);
     if (!waited) {
       pdl_wait();  // v
@@ -432,33 +454,32 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
     cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
-    int buffer = 0;
+    int buffer = 0, slot = 0;
     for (; unit < end && cb < p.col_blocks; ++unit, ++cb, buffer ^= 1) {
       const bool more = unit + 1 < end && cb + 1 < p.col_blocks;
       if (more) load_w(cb + 1);
       const uint32_t wp = woff + buffer * RP * 256;
       for (int group = g0; group * 16 < rows; group += 4) {
-        const bool last = (group + 4) * 16 >= rows;
+        cp_async_wait<C::DEPTH - 2>();
         float acc[8][4];  // starts from the base
-        int row[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          row[h] = next[h];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const uint32_t o[4] = {b[h][g].x, b[h][g].y, b[h][g].z, b[h][g].w};
+            uint32_t o[4] = {0, 0, 0, 0};
+            if (p.base) ld_shared_v4(o, slots + (uint32_t)(slot * 4 + 2 * h + g) * 512);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               acc[4 * g + j][2 * h] = __uint_as_float(o[j] << 16);
               acc[4 * g + j][2 * h + 1] = __uint_as_float(o[j] & 0xFFFF0000u);
             }
           }
-        }
-        if (!last || more) fetch(last ? cb + 1 : cb, last ? g0 : group + 4);
+        slot = slot == C::DEPTH - 1 ? 0 : slot + 1;
+        fetch();
 #pragma unroll
         for (int kk = 0; kk < RP / 16; ++kk) {
           uint32_t f[4];
-          ldsm4(f, bv + at_rank<RP>(group * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+          ldsm4(f, (voff + group * 32 * RP) ^ (uint32_t)(kk << 5));
 #pragma unroll
           for (int np = 0; np < 4; ++np) {
             uint32_t q[4];
@@ -470,8 +491,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
         const int c = cb * 128 + 64 * half + 8 * qc;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (row[h] < 0) continue;
-          uint16_t* out = p.out + (int64_t)row[h] * p.N + c;
+          const int t = tok[group * 16 + qr + 8 * h];
+          if (t < 0) continue;
+          uint16_t* out = p.out + (int64_t)t * p.N + c;
 #pragma unroll
           for (int g = 0; g < 2; ++g)
             if (c + 32 * g < p.N)
@@ -601,22 +623,23 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
     cp_async_commit();
   }
   const uint32_t xo = base + at<512>((lane & 7) + (((lane >> 3) & 1) << 3), warp * 4 + (lane >> 4));
-  const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+  const uint32_t vo = base + C::X + at_rank<RP>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
   uint32_t st = 0, st_put = (C::STAGES - 1) * C::STAGE;
   while (get.r < hi) {
     cp_async_wait<C::STAGES - 2>();
     __syncthreads();
     if (put.r < hi) load(st_put);
     cp_async_commit();
+    const uint32_t xs[2] = {xo + st, (xo + st) ^ 32u}, vs = vo + st;
 #pragma unroll
     for (int kk = 0; kk < C::ROWS / 16; ++kk) {
       uint32_t b[2][4];
 #pragma unroll
-      for (int np = 0; np < 2; ++np) ldsm4t(b[np], ((xo + st) ^ (uint32_t)(np << 5)) + kk * 16 * 512);
+      for (int np = 0; np < 2; ++np) ldsm4t(b[np], xs[np] + kk * 16 * 512);
 #pragma unroll
       for (int mt = 0; mt < RP / 16; ++mt) {
         uint32_t a[4];
-        ldsm4t(a, base + st + C::X + at_rank<RP>(kk * 16 + vr, 2 * mt + vc));
+        ldsm4t(a, (vs ^ (uint32_t)(mt << 5)) + kk * 32 * RP);
 #pragma unroll
         for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
       }
@@ -754,12 +777,12 @@ int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
   // 256 tokens share W's columns; fewer where that leaves a CTA less than a few pieces of work to even out
   const int64_t wave = (RP <= 64 ? 2 : 1) * sms;
   a.col_blocks = (int)cdiv(a.N, 128);
-  a.shift = 8;
+  a.shift = RP == 64 ? 7 : 8;  // two CTAs' shared memory on an SM
   while (a.shift > 6 && tiles_of(a.g.T, a.g.n, 1 << a.shift) * a.col_blocks < 6 * wave) --a.shift;
   a.per = 1 << a.shift;
   const int64_t most = std::max(slots_of(a.g.T, a.g.n, a.per) * a.col_blocks, cdiv(a.g.T, 8));
   return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)std::min(wave, most)), dim3(kThreads),
-                    (size_t)2 * RP * 256 + (size_t)a.per * RP * 2, st, "adapter expand", a);
+                    ExpandCfg<RP>::smem(a.per), st, "adapter expand", a);
 }
 template <int RP>
 int run_grad(const GradArgs& a, cudaStream_t st) {
