@@ -57,10 +57,16 @@ __global__ void __launch_bounds__(256) column_part_kernel(const uint16_t* in, in
   }
 }
 
+// Rows up to which the bias gradient of the output is summed by column_reduce_kernel from the matrix itself: one launch less
+// (333 rows: 40 us a backward pass without, 34 us with it; at 1024 rows a thread adds 32 numbers).
+constexpr int64_t kDirectRows = 1024;
+
 struct SumJob {
   const float* part;
   int64_t rows, cols;
   float* out;
+  const uint16_t* in;  // a bf16 matrix of row stride ld in place of part, or null
+  int64_t ld;
 };
 // out[c] (+)= sum over the rows of part[:, c]: 32 columns a block, 32 threads a column, fixed order
 __global__ void __launch_bounds__(1024) column_reduce_kernel(SumJob j0, SumJob j1, int blocks0, int accumulate) {
@@ -71,8 +77,15 @@ __global__ void __launch_bounds__(1024) column_reduce_kernel(SumJob j0, SumJob j
   pdl_wait();
   pdl_trigger();
   float s = 0.f;
-  if (c < j.cols)
-    for (int64_t r = g; r < j.rows; r += 32) s += j.part[r * j.cols + c];
+  if (c < j.cols) {
+    if (j.in) {
+#pragma unroll 8
+      for (int64_t r = g; r < j.rows; r += 32) s += __uint_as_float((uint32_t)j.in[r * j.ld + c] << 16);
+    } else {
+#pragma unroll 4
+      for (int64_t r = g; r < j.rows; r += 32) s += j.part[r * j.cols + c];
+    }
+  }
   acc[g][threadIdx.x & 31] = s;
   __syncthreads();
   if (g == 0 && c < j.cols) {
@@ -286,7 +299,7 @@ BwdLayout bwd_layout(int64_t T, int64_t H, int64_t I, bool bias) {
   L.dh = take((size_t)T * I * 4);
   L.counter = take(4);
   L.part1 = take(bias ? (size_t)cdiv(T, 128) * 4 * 2 * I * 4 : 0);
-  L.part2 = take(bias ? (size_t)cdiv(T, kSumRows) * H * 4 : 0);
+  L.part2 = take(bias && T > kDirectRows ? (size_t)cdiv(T, kSumRows) * H * 4 : 0);
   L.total = off;
   return L;
 }
@@ -338,7 +351,8 @@ extern "C" int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t 
   float* part2 = db1 ? reinterpret_cast<float*>(ws + L.part2) : nullptr;
   const bool inter = gate_up_layout == MOE_GATE_UP_INTERLEAVED;
 
-  if (db2) {
+  const bool direct = T <= kDirectRows;
+  if (db2 && !direct) {
     if (cdiv(T, kSumRows) > 65535) return fail(MOE_ERR_UNSUPPORTED, "ffn_bwd: too many rows for the bias gradients");
     rc = launch_pdl(column_part_kernel, dim3((unsigned)cdiv(H, 256), (unsigned)cdiv(T, kSumRows)), dim3(256), 0, st, "column sums",
                     static_cast<const uint16_t*>(dout), lddout, T, H, part2);
@@ -384,7 +398,8 @@ extern "C" int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t 
     if ((rc = launch_pair<kFfnStore>(P, st))) return rc;
   }
   if (!db1) return MOE_OK;
-  const SumJob j1{part1, cdiv(T, 128) * 4, 2 * I, db1}, j2{part2, cdiv(T, kSumRows), H, db2};
+  const SumJob j1{part1, cdiv(T, 128) * 4, 2 * I, db1, nullptr, 0};
+  const SumJob j2{part2, direct ? T : cdiv(T, kSumRows), H, db2, direct ? static_cast<const uint16_t*>(dout) : nullptr, lddout};
   const int blocks0 = (int)cdiv(2 * I, 32);
   return launch_pdl(column_reduce_kernel, dim3((unsigned)(blocks0 + cdiv(H, 32))), dim3(1024), 0, st, "bias gradients", j1, j2,
                     blocks0, accumulate);
