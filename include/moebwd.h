@@ -551,12 +551,13 @@ size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_
  * expert_offsets [n+1], x_gather_idx [T], s_reverse_scatter_idx [T] (device): moe_route_meta's for ids [T,1] (-1: none) and
  *   E = n.  Offsets are clamped to [0,T] and indices outside it skipped: wrong metadata gives wrong rows, no access
  *   leaves its buffer.
+ * status_dev (device, nullable) int32 [1]: MOE_STATUS_TIMEOUT is OR-ed in (never reset here); outputs then invalid.
  * Sums in fp32 in a fixed order (bit-reproducible); scale_a u is rounded to bf16 as the second product's operand, y once.
  * H and N multiples of 8 (the row strides too), r <= 128, n <= 1024, tensors 16-byte aligned.  T = 0 writes nothing. */
 int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base, int64_t ldbase,
                 const int32_t* expert_offsets, const int32_t* x_gather_idx, const int32_t* s_reverse_scatter_idx, int64_t T,
-                int64_t H, int64_t N, int64_t n, int64_t r, void* y, float* u, void* workspace, size_t workspace_bytes,
-                moe_stream_t stream);
+                int64_t H, int64_t N, int64_t n, int64_t r, void* y, float* u, int32_t* status_dev, void* workspace,
+                size_t workspace_bytes, moe_stream_t stream);
 
 /* Gradients of adapter_fwd, u being its:
  *   v_t = scale_a B_a dy_t,  dx_t = base_t + A_a^T v_t,  dA_a = sum_t v_t x_t^T,  dB_a = sum_t scale_a u_t dy_t^T
@@ -567,7 +568,7 @@ int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const 
 int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* u, const void* A, const void* B,
                 const float* scale, const void* base, int64_t ldbase, const int32_t* expert_offsets, const int32_t* x_gather_idx,
                 const int32_t* s_reverse_scatter_idx, int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, void* dx, void* dA,
-                void* dB, int accumulate, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+                void* dB, int accumulate, int32_t* status_dev, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
 /* Instrumentation                                                                             */

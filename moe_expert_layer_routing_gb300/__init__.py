@@ -123,8 +123,8 @@ def lib():
         "dropout_fwd": ([vp, i64, vp, i64, i32, i64, i64, f64, u64, u64, vp, vp, vp], i32),
         "dropout_bwd": ([vp, i64, i32, i64, i64, f64, u64, u64, vp, vp, vp], i32),
         "adapter_workspace_size": ([i64] * 5 + [i32], sz),
-        "adapter_fwd": ([vp, i64, vp, vp, vp, vp, i64, vp, vp, vp] + [i64] * 5 + [vp, vp, vp, sz, vp], i32),
-        "adapter_bwd": ([vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp] + [i64] * 5 + [vp, vp, vp, i32, vp, sz, vp], i32),
+        "adapter_fwd": ([vp, i64, vp, vp, vp, vp, i64, vp, vp, vp] + [i64] * 5 + [vp, vp, vp, vp, sz, vp], i32),
+        "adapter_bwd": ([vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp] + [i64] * 5 + [vp, vp, vp, i32, vp, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -853,41 +853,46 @@ def _adapter_args(x, A, B, route_meta, scale, what):
     return T, H, N, n, r, dev, ldx, p, m
 
 
-def adapter_fwd(x, A, B, route_meta: dict, scale=None, base=None, out=None, save: bool = True, stream=None) -> dict:
+def adapter_fwd(x, A, B, route_meta: dict, scale=None, base=None, out=None, save: bool = True, status=None,
+                stream=None) -> dict:
     """adapter_fwd: y = base + scale_a B_a^T (A_a x) for the rows of x [T, H] (bf16) that have an adapter, base (or 0) for the
     others.  A [n, r, H], B [n, r, N] bf16, scale fp32 [n].  route_meta: route_meta(ids [T, 1], n, ...)'s dict, id -1
     for a row without an adapter.  base [T, N] bf16: the shared projection's output; out: a dense [T, N] tensor to write, which
-    may be base (None: a new one).  Returns y and, unless save is False, u [T, r] in fp32, which adapter_bwd takes."""
+    may be base (None: a new one).  Returns y and, unless save is False, u [T, r] in fp32, which adapter_bwd takes.
+    status: an int32 [1] CUDA tensor that STATUS_TIMEOUT is OR-ed into."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return adapter_fwd(x, A, B, route_meta, scale, base, out, save)
+            return adapter_fwd(x, A, B, route_meta, scale, base, out, save, status)
     T, H, N, n, r, dev, ldx, p, m = _adapter_args(x, A, B, route_meta, scale, "adapter_fwd")
     ldb = 0 if base is None else _rows(base, x.dtype, (T, N), "base", dev)
     yp = _dense(out, x.dtype, (T, N), "out", dev)
+    sp = _dense(status, torch.int32, (1,), "status", dev)
     st = _here(dev)
     y = _new2(T, N, x.dtype) if out is None else out
     u = _new2(T, r, torch.float32) if save else None
     size = _ws_bytes("adapter_workspace_size", dev.index, T, H, N, n, r, 0)
     ws = _new1(size, torch.uint8)
     rc = lib().adapter_fwd(x.data_ptr(), ldx, *p, None if base is None else base.data_ptr(), ldb, *m, T, H, N, n, r,
-                           y.data_ptr() if yp is None else yp, None if u is None else u.data_ptr(), ws.data_ptr(), size, st)
+                           y.data_ptr() if yp is None else yp, None if u is None else u.data_ptr(), sp, ws.data_ptr(), size, st)
     _check(rc, "adapter_fwd")
     return dict(y=y, u=u)
 
 
-def adapter_bwd(dy, x, u, A, B, route_meta: dict, scale=None, base=None, out=None, accumulate_into=None, stream=None) -> dict:
+def adapter_bwd(dy, x, u, A, B, route_meta: dict, scale=None, base=None, out=None, accumulate_into=None, status=None,
+                stream=None) -> dict:
     """adapter_bwd: gradients of adapter_fwd from its u.  base [T, H] bf16: the shared projection's own dX (e.g. linear_bwd's), to
     which the adapters' is added in dx; out as in adapter_fwd.  Returns dx [T, H], dA, dB (bf16; zeros for adapters without a
-    row).  accumulate_into: an earlier result whose dA and dB are added to in place."""
+    row).  accumulate_into: an earlier result whose dA and dB are added to in place.  status as in adapter_fwd."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return adapter_bwd(dy, x, u, A, B, route_meta, scale, base, out, accumulate_into)
+            return adapter_bwd(dy, x, u, A, B, route_meta, scale, base, out, accumulate_into, status)
     T, H, N, n, r, dev, ldx, p, m = _adapter_args(x, A, B, route_meta, scale, "adapter_bwd")
     bf = torch.bfloat16
     ldd = _rows(dy, bf, (T, N), "dy", dev)
     up = _dense(u, torch.float32, (T, r), "u", dev)
     ldb = 0 if base is None else _rows(base, bf, (T, H), "base", dev)
     op = _dense(out, bf, (T, H), "out", dev)
+    sp = _dense(status, torch.int32, (1,), "status", dev)
     st = _here(dev)
     dx = _new2(T, H, bf) if out is None else out
     if accumulate_into is not None:
@@ -900,7 +905,7 @@ def adapter_bwd(dy, x, u, A, B, route_meta: dict, scale=None, base=None, out=Non
     ws = _new1(size, torch.uint8)
     rc = lib().adapter_bwd(dy.data_ptr(), ldd, x.data_ptr(), ldx, up, *p, None if base is None else base.data_ptr(), ldb, *m, T, H,
                            N, n, r, dx.data_ptr() if op is None else op, dA.data_ptr(), dB.data_ptr(),
-                           int(accumulate_into is not None), ws.data_ptr(), size, st)
+                           int(accumulate_into is not None), sp, ws.data_ptr(), size, st)
     _check(rc, "adapter_bwd")
     return dict(dx=dx, dA=dA, dB=dB)
 

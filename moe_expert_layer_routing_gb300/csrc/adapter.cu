@@ -18,8 +18,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ptx.cuh"
-#include "mx_device.cuh"
+#include "gemm_kernel.cuh"
 
 namespace moebwd {
 namespace {
@@ -66,40 +65,79 @@ __device__ __forceinline__ int token_of(const Groups& g, int row) {
   return t >= 0 && t < g.T ? t : -1;
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
 __device__ __forceinline__ void ld_shared_v4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Byte of 16-byte piece `c` of row `row` in a tile of PITCH-byte rows (PITCH >= 128): eight rows at one piece fall into
 // eight bank groups.  Moving from piece c to c ^ d is an exclusive or of the byte with d << 4.
 template <int PITCH>
 __device__ __forceinline__ uint32_t at(int row, int c) {
   return (uint32_t)(row * PITCH + ((c ^ (row & 7)) << 4));
 }
-// The same for rows of RP bf16 numbers (32 bytes and more).
-template <int RP>
-__device__ __forceinline__ uint32_t at_rank(int row, int c) {
-  constexpr int mask = RP / 8 < 8 ? RP / 8 - 1 : 7;
-  return (uint32_t)(row * RP * 2 + ((c ^ (row & mask)) << 4));
-}
+struct Waits {
+  int32_t* status;
+  uint64_t ns;
+};
+
+// The stages of a kernel whose threads copy operands with cp.async and one of which issues the products: a barrier a stage that
+// its products arrive on, and the accumulator's TMEM.  All threads call the members; the issuing one commits in between.
+// A wait that runs out is reported in the caller's status word, and every thread leaves the loop at its next barrier.
+template <int STAGES>
+struct PipeShared {
+  uint64_t done[STAGES];
+  uint32_t slot;
+  int abort_flag;
+};
+template <int STAGES>
+struct Pipe {
+  PipeShared<STAGES>& sh;
+  uint32_t at = 0, free = 0, parity = 0;  // stage in work, stage to refill; bit s: parity of stage s's next completion
+  bool begun = false, fail = false;
+  __device__ explicit Pipe(PipeShared<STAGES>& s) : sh(s) {}
+  __device__ __forceinline__ uint32_t start(uint32_t cols) {
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) mbar_init(&sh.done[s], 1);
+      sh.abort_flag = 0;
+      fence_mbar_init();
+    }
+    if (threadIdx.x >> 5 == 1) {
+      tmem_alloc(&sh.slot, cols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return sh.slot;
+  }
+  __device__ __forceinline__ void commit() { mma_commit(&sh.done[at]); }
+  __device__ __forceinline__ void wait(uint32_t s, const Waits& w) {
+    if (!mbar_wait_bounded(&sh.done[s], (parity >> s) & 1u, w.status, &sh.abort_flag, w.ns)) fail = true;
+  }
+  // Waits for the products of the stage before the one just committed, which `free` then names.
+  __device__ __forceinline__ void advance(const Waits& w) {
+    free = at == 0 ? STAGES - 1 : at - 1;
+    if (begun) {
+      wait(free, w);
+      parity ^= 1u << free;
+    }
+    begun = true;
+    at = at == STAGES - 1 ? 0 : at + 1;
+  }
+  // Waits for all products committed.
+  __device__ __forceinline__ void settle(const Waits& w) {
+    const uint32_t last = at == 0 ? STAGES - 1 : at - 1;
+    wait(last, w);
+    if (fail) mbar_wait_drain(&sh.done[last], (parity >> last) & 1u, w.status);
+  }
+  // Behind a barrier after the last use of the TMEM.
+  __device__ __forceinline__ void end(uint32_t tmem, uint32_t cols) {
+    if (threadIdx.x >> 5 == 1) {
+      tc_fence_after();
+      tmem_dealloc(tmem, cols);
+    }
+  }
+};
 
 __device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
   float4 v;
@@ -123,60 +161,61 @@ struct ShrinkArgs {
   const float* u_in;   // [T, R] with su [T, RP], or null
   uint16_t* su;
   int64_t ld;
-  int K, R;
+  int K, R, per;  // rows of a tile, at most ShrinkCfg::ROWS
+  Waits w;
 };
 
 // A tile of tokens by all r rows, its contraction split over a cluster whose partial tiles meet in distributed shared memory,
-// summed in rank order.  Ranks up to 32: 64 tokens, stages of 128 features, two groups of four warps take a stage's
-// halves; above: 128 tokens (their W tile is as large as the tokens'), stages of 64 features.  A thread copies the same
-// four rows' pieces in every stage, so that a copy costs two additions beside it: the address arithmetic, not the products
-// or the bytes, bound the form that computed each address (rank 64, 8192 x 4096: 30 us, now 25 us).
+// summed in rank order.  Stages of 64 features: asynchronous copies gather the tokens' 128-byte rows into the swizzled
+// K-major layout, one thread issues the tile's products (128 tokens x r), the accumulator stays in TMEM.  The form
+// whose warps multiplied from registers spent its time on operand loads and their latency (rank 64, 16384 x 4096: 38 us,
+// now %S64); a thread copies the same four rows' pieces in every stage, so that a copy costs two additions beside it.
 template <int RP>
 struct ShrinkCfg {
-  static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PITCH = KC * 2, PIECES = KC / 8;
-  static constexpr int MT = RP == 64 ? 2 : 1;               // 16-token tiles of a warp, which share what it reads of W
-  static constexpr int HALVES = 8 * 16 * MT / ROWS;         // groups of warps that share a row's contraction
-  static constexpr int STAGES = RP <= 64 ? 4 : 3;
-  static constexpr int X = ROWS * PITCH, STAGE = X + RP * PITCH;
-  static constexpr int PART = HALVES * ROWS * RP * 4;
-  static constexpr int SMEM = STAGES * STAGE > PART ? STAGES * STAGE : PART;
+  static constexpr int ROWS = 128, X = ROWS * 128, STAGE = X + RP * 128;
+  static constexpr int STAGES = RP <= 32 ? 5 : RP <= 64 ? 4 : 3;
+  static constexpr int TMEM = RP < 32 ? 32 : RP;
+  static constexpr int PITCH = RP + 4;  // floats of a partial row: 16-byte pieces of 8 rows in 8 bank groups
+  static constexpr int SMEM = 1024 + STAGES * STAGE;
+  static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "the partial tile overlays the stages");
 };
 
 template <int RP, int SPLIT>
-__global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const ShrinkArgs p) {
   using C = ShrinkCfg<RP>;
-  extern __shared__ __align__(256) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int tok[C::ROWS];
+  __shared__ PipeShared<C::STAGES> pipe_shared;
+  Pipe<C::STAGES> pipe(pipe_shared);
   pdl_wait();
-  pdl_trigger();
   const uint32_t rank = SPLIT > 1 ? cluster_ctarank() : 0;
   Tile t;
   // the whole cluster works on one tile, so that all of it leaves here or none
-  if (!find_tile(p.g, blockIdx.x / SPLIT, C::ROWS, t)) return;
+  if (!find_tile(p.g, blockIdx.x / SPLIT, p.per, t)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < C::ROWS) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
-  __syncthreads();
-  const int chunks = (p.K + C::KC - 1) / C::KC;
-  const int c0 = (int)((int64_t)chunks * rank / SPLIT), c1 = (int)((int64_t)chunks * (rank + 1) / SPLIT);
+  const uint32_t tmem = pipe.start(C::TMEM);
+  pdl_trigger();  // after the allocation: the next kernel cannot take the TMEM that this one is still to get
+  const int chunks = (p.K + 63) / 64;
+  const int mine = (chunks - (int)rank + SPLIT - 1) / SPLIT;  // chunks rank, rank + SPLIT, ...: the cluster reads a row's neighbours together
   const uint32_t base = smem_u32(smem);
-  const int pc = tid % C::PIECES, r0 = tid / C::PIECES;
-  constexpr int STEP = kThreads / C::PIECES;        // rows of one pass of copies
+  const int pc = tid & 7, r0 = tid >> 3;
+  constexpr int STEP = kThreads / 8;                // rows of one pass of copies
   constexpr int WN = (RP + STEP - 1) / STEP;        // passes over W's rows
   const uint16_t* xs[4];
   uint32_t xb[4], xd[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = r0 + STEP * i, tk = tok[row];
-    xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)c0 * C::KC;
+    xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)rank * 64;
     xb[i] = tk < 0 ? 0u : 16u;
-    xd[i] = row < ((t.rows + 16 * C::MT - 1) & ~(16 * C::MT - 1)) ? base + at<C::PITCH>(row, pc) : 0u;  // rows that no warp reads are not filled
+    xd[i] = row < t.rows ? base + at<128>(row, pc) : 0u;  // other rows only reach their own sums, which nobody reads
   }
-  const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)c0 * C::KC;
-  auto load = [&](int c) {
-    const int k = c * C::KC + 8 * pc;
-    const uint32_t in = k < p.K ? 16u : 0u;  // K is a multiple of 8
-    const uint32_t st = (uint32_t)((c - c0) % C::STAGES) * C::STAGE;
-    const int64_t o = (int64_t)(c - c0) * C::KC;
+  const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)rank * 64;
+  auto load = [&](int c, uint32_t st) {
+    const int64_t o = (int64_t)c * (64 * SPLIT);
+    const uint32_t in = (int)rank * 64 + o + 8 * pc < p.K ? 16u : 0u;  // K is a multiple of 8
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (xd[i]) cp_async_16_zfill(xd[i] + st, in ? xs[i] + o : p.x, xb[i] & in);
@@ -185,79 +224,62 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkAr
       const int row = r0 + STEP * i;
       if (RP % STEP == 0 || row < RP) {
         const bool ok = row < p.R && in;
-        cp_async_16_zfill(base + st + C::X + at<C::PITCH>(row, pc), ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
+        cp_async_16_zfill(base + st + C::X + at<128>(row, pc), ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
       }
     }
   };
-  float acc[C::MT][RP / 8][4];
-#pragma unroll
-  for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) {
-    if (c0 + i < c1) load(c0 + i);
+    if (i < mine) load(i, i * C::STAGE);
     cp_async_commit();
   }
-  const int rg = C::HALVES == 2 ? warp & 3 : warp, half = C::HALVES == 2 ? warp >> 2 : 0;
-  constexpr int KK = C::KC / 16 / C::HALVES;
-  const uint32_t aoff = base + at<C::PITCH>(rg * 16 * C::MT + (lane & 15), 2 * KK * half + (lane >> 4));
-  const uint32_t boff = base + C::X + at<C::PITCH>((lane & 7) + ((lane >> 4) << 3), 2 * KK * half + ((lane >> 3) & 1));
-  for (int c = c0; c < c1; ++c) {
+  constexpr uint32_t idesc = idesc_bf16(128, RP);
+  for (int c = 0; c < mine; ++c) {
     cp_async_wait<C::STAGES - 2>();
-    __syncthreads();  // stage c has landed for everyone, and everyone is done with the stage refilled now
-    if (c + C::STAGES - 1 < c1) load(c + C::STAGES - 1);
-    cp_async_commit();
-    if (rg * 16 * C::MT < t.rows) {
-      const uint32_t st = (uint32_t)((c - c0) % C::STAGES) * C::STAGE;
+    fence_proxy_async_smem();
+    if (__syncthreads_or(pipe.fail)) break;  // stage c has landed for everyone
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t a0 = base + pipe.at * C::STAGE;
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t a[C::MT][4];
-#pragma unroll
-        for (int m = 0; m < C::MT; ++m) ldsm4(a[m], ((aoff + st) ^ (uint32_t)(kk << 5)) + m * 16 * C::PITCH);
-#pragma unroll
-        for (int nb = 0; nb < RP / 16; ++nb) {
-          uint32_t b[4];
-          ldsm4(b, ((boff + st) ^ (uint32_t)(kk << 5)) + nb * 16 * C::PITCH);
-#pragma unroll
-          for (int m = 0; m < C::MT; ++m) {
-            mma16816(acc[m][2 * nb], a[m], b[0], b[1]);
-            mma16816(acc[m][2 * nb + 1], a[m], b[2], b[3]);
-          }
-        }
-      }
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16(tmem, kmajor_sw128_desc(a0 + kk * 32), kmajor_sw128_desc(a0 + C::X + kk * 32), idesc, (c > 0 || kk > 0) ? 1u : 0u);
+      pipe.commit();
     }
+    pipe.advance(p.w);  // the products of the step before are done with the stage refilled now
+    if (c + C::STAGES - 1 < mine) load(c + C::STAGES - 1, pipe.free * C::STAGE);
+    cp_async_commit();
   }
   cp_async_wait<0>();
+  if (pipe.begun) pipe.settle(p.w);
   __syncthreads();  // the partial tiles overlay the stages
-  float* part = reinterpret_cast<float*>(smem);  // [halves][rows][RP]
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(smem);  // [rows][PITCH]
+  for (int c = 16 * (warp >> 2); c < RP; c += 32) {
+    uint32_t r[16];
+    tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, r);
+    tmem_ld_wait_regs<16>(r);
+    float* out = part + (32 * (warp & 3) + lane) * C::PITCH + c;
 #pragma unroll
-  for (int h = 0; h < 2 * C::MT; ++h) {
-    float* out = part + (half * C::ROWS + rg * 16 * C::MT + (lane >> 2) + 8 * h) * RP + 2 * (lane & 3);
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i)
-      *reinterpret_cast<float2*>(out + 8 * i) = make_float2(acc[h >> 1][i][2 * (h & 1)], acc[h >> 1][i][2 * (h & 1) + 1]);
+    for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(out + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
   }
+  tc_fence_before();
   if (SPLIT > 1)
     cluster_sync_all();
   else
     __syncthreads();
+  pipe.end(tmem, C::TMEM);
   const float scale = p.scale ? p.scale[t.a] : 1.f;
   for (int i = (int)rank * kThreads + tid; i < t.rows * (RP / 4); i += SPLIT * kThreads) {
     const int row = i / (RP / 4), c = 4 * (i % (RP / 4));
-    float4 f[SPLIT * C::HALVES];
+    float4 f[SPLIT];
+    const float* q = part + row * C::PITCH + c;
 #pragma unroll
     for (int k = 0; k < SPLIT; ++k)
-#pragma unroll
-      for (int h = 0; h < C::HALVES; ++h) {
-        const float* q = part + (h * C::ROWS + row) * RP + c;
-        f[k * C::HALVES + h] = SPLIT > 1 ? ld_peer_f4(mapa_shared(smem_u32(q), (uint32_t)k)) : *reinterpret_cast<const float4*>(q);
-      }
+      f[k] = SPLIT > 1 ? ld_peer_f4(mapa_shared(smem_u32(q), (uint32_t)k)) : *reinterpret_cast<const float4*>(q);
     float4 s = f[0];
 #pragma unroll
-    for (int k = 1; k < SPLIT * C::HALVES; ++k) {
+    for (int k = 1; k < SPLIT; ++k) {
       s.x += f[k].x;
       s.y += f[k].y;
       s.z += f[k].z;
@@ -295,13 +317,15 @@ struct ExpandArgs {
   float* u;              // [T, R] zeros for tokens without an adapter, or null
   int64_t ldb;
   int N, R, per, shift, col_blocks;  // rows of a tile: 2^shift, at most kExpandRows
+  Waits w;
 };
-constexpr int kExpandRows = 256;
+constexpr int kExpandRows = 128;
 
 template <int RP>
 struct ExpandCfg {
-  static constexpr int DEPTH = RP <= 32 ? 4 : RP <= 64 ? 3 : 4;  // pieces of base of a warp on their way or in work, 2 KB each
-  static size_t smem(int per) { return (size_t)2 * RP * 256 + (size_t)per * RP * 2 + (size_t)8 * DEPTH * 2048; }
+  static constexpr int DEPTH = RP == 64 ? 3 : 4;  // 16 tokens x 64 columns of base of a warp on their way, 2 KB each
+  static constexpr int V = 16384 * (RP <= 64 ? 1 : 2), W = RP * 256;
+  static constexpr int SMEM = 1024 + V + 2 * W + 8 * DEPTH * 2048;
 };
 
 // Tiles of 2^shift rows before each adapter's, first[0 .. n]; the number of all is returned.  All 256 threads call it.
@@ -334,25 +358,26 @@ __device__ __forceinline__ int tile_table(const Groups& g, int shift, int* first
   return all;
 }
 
-// One wave of CTAs shares out the pieces of work (a tile of up to 256 tokens x 128 columns, a tile's pieces one behind
-// another) in equal, contiguous parts.  The tile's v stays in shared memory; W's columns come in two buffers, the next
-// piece's while this one is worked on.  A warp goes through its tokens, 16 x 64 columns at a time, with the next
-// ones' base already on its way, across pieces too.  (A CTA a piece, 7 waves of them, started anew each time: 16384 x 4096,
-// rank 16: %E0 us, now %E1.)  The columns of W are permuted within 32 on their way to shared memory so that a thread's four
-// 8-column matrix tiles give it 8 neighbouring columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a
-// row, with no pass through shared memory.
+// One wave of CTAs shares out the pieces of work (a tile of up to 128 tokens x 128 columns, a tile's pieces one behind
+// another) in equal, contiguous parts.  (A CTA a piece, 7 waves of them, started anew each time: 16384 x 4096, rank 16,
+// %E0 us, now %E1.)  The product of the next piece runs on the tensor core, tokens x columns into one half of the TMEM, while the warps
+// add this one's to the base: the tile's v stays in shared memory (K-major), W's columns come in two buffers (MN-major), and
+// every warp has a few pieces of base on their way.  (Products from registers took as long as the memory beside them: rank 64
+// %M0 us, now %M1.)  The columns of W are permuted within 32 on their way to shared memory so that the four 8-column tiles of
+// a TMEM load give a thread 8 neighbouring columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a row.
 // What the kernel reads before pdl_wait, and the rows without an adapter that it writes there, belong to the caller: whatever wrote
 // or read them is complete before the shrink kernel lets this one start.
 template <int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_kernel(const ExpandArgs p) {
   using C = ExpandCfg<RP>;
-  extern __shared__ __align__(256) uint8_t smem[];
-  uint8_t* sW = smem;                  // 2 x [RP][128], permuted
-  uint8_t* sV = smem + 2 * RP * 256;   // [per][RP]
-  // then base: [warp][slot][piece of 16 bytes][lane]
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int tok[kExpandRows], first[kMaxExperts + 1], warp_sum[kThreads / 32];
+  __shared__ PipeShared<2> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t me = blockIdx.x, all = gridDim.x;
+  Pipe<2> pipe(sh);
+  const uint32_t tmem = pipe.start(2 * 128);
   // rows without an adapter keep their base
   const int t1 = (int)(p.g.T * (me + 1) / all);
   for (int t0 = (int)(p.g.T * me / all) + 32 * warp; t0 < t1; t0 += kThreads) {
@@ -377,14 +402,31 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
   const int64_t units = (int64_t)(found < most ? found : most) * p.col_blocks;
   int64_t unit = units * me / all;
   const int64_t end = units * (me + 1) / all;
-  const uint32_t bw = smem_u32(sW), bv = smem_u32(sV);
-  const int qr = lane >> 2, qc = lane & 3, half = warp & 1, g0 = warp >> 1;
-  const uint32_t woff = bw + (at<256>((lane & 7) + (((lane >> 3) & 1) << 3), lane >> 4) ^ (uint32_t)(half << 7));
-  const uint32_t slots = bv + p.per * RP * 2 + (uint32_t)(warp * C::DEPTH * 2048 + lane * 16);
-  const uint32_t voff = bv + at_rank<RP>(lane & 15, lane >> 4);
-  bool waited = false;
+  const uint32_t bv = smem_u32(smem), bw = bv + C::V;
+  const uint32_t slots = bw + 2 * C::W + (uint32_t)(warp * C::DEPTH * 2048 + lane * 16);
+  const int qr = lane >> 2, qc = lane & 3, half = warp >> 2, first_row = 32 * (warp & 3);
+  constexpr uint32_t idesc = idesc_bf16(128, 128, 0, 1);
+  bool waited = false, stop = false;
+  uint32_t issued = 0, k = 0;  // pieces whose product was issued, pieces done
+  // everyone has stored its part of piece `issued`'s W (and v); one thread issues its product
+  auto product = [&]() {
+    fence_proxy_async_smem();
+    tc_fence_before();  // this thread's loads of the half that is overwritten
+    if (__syncthreads_or(pipe.fail)) return false;
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t w0 = bw + (issued & 1) * C::W;
+#pragma unroll
+      for (int kk = 0; kk < RP / 16; ++kk)
+        mma_bf16(tmem + (issued & 1) * 128, kmajor_sw128_desc(bv + (kk >> 2) * 16384 + (kk & 3) * 32),
+                 mnmajor_sw128_desc(w0 + kk * 2048, RP * 128), idesc, kk > 0 ? 1u : 0u);
+      mma_commit(&sh.done[issued & 1]);
+    }
+    ++issued;
+    return true;
+  };
   int tile = (int)(unit / p.col_blocks), cb = (int)(unit - (int64_t)tile * p.col_blocks);
-  for (; unit < end; ++tile, cb = 0) {
+  for (; unit < end && !stop; ++tile, cb = 0) {
     int a = 0;  // the last adapter whose first tile is at or before this one
     for (int hi = p.g.n; hi - a > 1;) {
       const int mid = (a + hi) >> 1;
@@ -392,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
     }
     const int o1 = clamp_row(p.g.off[a + 1], p.g.T);
     const int64_t r0 = clamp_row(p.g.off[a], p.g.T) + ((int64_t)(tile - first[a]) << p.shift);
-    const int rows = (int)(o1 - r0 < p.per ? o1 - r0 : p.per), padded = (rows + 15) & ~15;
+    const int rows = (int)(o1 - r0 < p.per ? o1 - r0 : p.per);
     __syncthreads();  // everyone is done with the last tile's
-    tok[tid] = tid < rows ? token_of(p.g, (int)r0 + tid) : -1;
+    if (tid < kExpandRows) tok[tid] = tid < rows ? token_of(p.g, (int)r0 + tid) : -1;
     const uint16_t* W = p.W + (int64_t)a * p.R * p.N + (int64_t)(tid >> 4) * p.N + 8 * (tid & 15);
     uint4 w[RP / 16];
     auto load_w = [&](int block) {
@@ -404,25 +446,26 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
         w[i] = in && (tid >> 4) + 16 * i < p.R ? *reinterpret_cast<const uint4*>(W + (int64_t)16 * i * p.N + block * 128)
                                                : make_uint4(0, 0, 0, 0);
     };
-    auto store_w = [&](int buffer) {
+    auto store_w = [&](uint32_t buffer) {
 #pragma unroll
       for (int i = 0; i < RP / 16; ++i) {
         const int row = (tid >> 4) + 16 * i, pc = tid & 15;
         const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        // columns 8 pc + 2 j, + 1 of group pc / 4: columns 2 (pc % 4), + 1 of that group's matrix tile j
+        // columns 8 pc + 2 j, + 1 of group pc / 4 of 32: columns 2 (pc % 4), + 1 of that group's tile j
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(sW + buffer * RP * 256 + at<256>(row, (pc & 12) + j) + 4 * (pc & 3)) = ww[j];
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint32_t*>(smem + C::V + buffer * C::W + (pc >> 3) * RP * 128 + at<128>(row, (pc & 4) + j) + 4 * (pc & 3)) = ww[j];
       }
     };
-    // the warp's pieces in order: (block, group); this thread's 64 bytes of a piece's base go to its own slot
-    int fb = cb, fg = g0, fslot = 0;
-    const int fb_end = p.col_blocks - cb < end - unit ? p.col_blocks : cb + (int)(end - unit);
+    // the warp's 16 tokens x 64 columns in order: (block, m); this thread's 64 bytes of them go to its own slot
+    int fb = cb, fm = 0, fslot = 0;
+    const int fb_end = first_row >= rows ? cb : p.col_blocks - cb < end - unit ? p.col_blocks : cb + (int)(end - unit);
     auto fetch = [&]() {
-      if (p.base && fg * 16 < rows && fb < fb_end) {
+      if (p.base && fb < fb_end) {
         const int c = fb * 128 + 64 * half + 8 * qc;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int t = tok[fg * 16 + qr + 8 * h];
+          const int t = tok[first_row + 16 * fm + qr + 8 * h];
           const uint16_t* src = p.base + (t < 0 ? 0 : t) * p.ldb;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -433,83 +476,86 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
       }
       cp_async_commit();
       fslot = fslot == C::DEPTH - 1 ? 0 : fslot + 1;
-      fg += 4;
-      if (fg * 16 >= rows) fg = g0, ++fb;
+      fm ^= 1;
+      fb += fm == 0;
     };
     load_w(cb);
     __syncthreads();  // tok
 #pragma unroll
-    for (int i = 0; i < C::DEPTH - 1; ++i) fetch();
-    store_w(0);
+    for (int i = 0; i < C::DEPTH; ++i) fetch();
+    store_w(issued & 1);
     if (!waited) {
       pdl_wait();  // v
       pdl_trigger();
       waited = true;
     }
-    for (int i = tid; i < padded * (RP / 8); i += kThreads) {
+    for (int i = tid; i < rows * (RP / 8); i += kThreads) {  // rows behind them only reach sums that nobody reads
       const int row = i / (RP / 8), c = i % (RP / 8);
-      const bool ok = row < rows;
-      cp_async_16_zfill(bv + at_rank<RP>(row, c), ok ? p.v + (r0 + row) * RP + 8 * c : p.v, ok ? 16u : 0u);
+      cp_async_16(bv + (c >> 3) * 16384 + at<128>(row, c & 7), p.v + (r0 + row) * RP + 8 * c);
     }
     cp_async_commit();
     cp_async_wait<0>();
-    __syncthreads();
-    int buffer = 0, slot = 0;
-    for (; unit < end && cb < p.col_blocks; ++unit, ++cb, buffer ^= 1) {
-      const bool more = unit + 1 < end && cb + 1 < p.col_blocks;
-      if (more) load_w(cb + 1);
-      const uint32_t wp = woff + buffer * RP * 256;
-      for (int group = g0; group * 16 < rows; group += 4) {
-        cp_async_wait<C::DEPTH - 2>();
-        float acc[8][4];  // starts from the base
+    stop = !product();
+    if (unit + 1 < end && cb + 1 < p.col_blocks) load_w(cb + 1);
+    int slot = 0;
+    for (; unit < end && cb < p.col_blocks && !stop; ++unit, ++cb, ++k) {
+      if (unit + 1 < end && cb + 1 < p.col_blocks) {
+        store_w(issued & 1);  // piece k - 1, whose buffer it is, is done
+        stop = !product();
+        if (stop) break;
+        if (unit + 2 < end && cb + 2 < p.col_blocks) load_w(cb + 2);
+      }
+      if (!mbar_wait_bounded(&sh.done[k & 1], (k >> 1) & 1u, p.w.status, &sh.abort_flag, p.w.ns)) pipe.fail = true;
+      if (first_row >= rows) continue;
+      tc_fence_after();
+      cp_async_wait<C::DEPTH - 2>();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int m = 0; m < 2; ++m) {
+        uint32_t r[2][16];
+        const uint32_t taddr = tmem + ((uint32_t)(first_row + 16 * m) << 16) + (k & 1) * 128 + 64 * half;
+        tmem_ld_16x256b_x4(taddr, r[0]);
+        tmem_ld_16x256b_x4(taddr + 32, r[1]);
+        uint32_t o[2][2][4] = {};
+        if (p.base) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t o[4] = {0, 0, 0, 0};
-            if (p.base) ld_shared_v4(o, slots + (uint32_t)(slot * 4 + 2 * h + g) * 512);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[4 * g + j][2 * h] = __uint_as_float(o[j] << 16);
-              acc[4 * g + j][2 * h + 1] = __uint_as_float(o[j] & 0xFFFF0000u);
-            }
-          }
-        slot = slot == C::DEPTH - 1 ? 0 : slot + 1;
-        fetch();
-#pragma unroll
-        for (int kk = 0; kk < RP / 16; ++kk) {
-          uint32_t f[4];
-          ldsm4(f, (voff + group * 32 * RP) ^ (uint32_t)(kk << 5));
-#pragma unroll
-          for (int np = 0; np < 4; ++np) {
-            uint32_t q[4];
-            ldsm4t(q, (wp ^ (uint32_t)(np << 5)) + kk * 16 * 256);
-            mma16816(acc[2 * np], f, q[0], q[1]);
-            mma16816(acc[2 * np + 1], f, q[2], q[3]);
-          }
+            for (int g = 0; g < 2; ++g) ld_shared_v4(o[h][g], slots + (uint32_t)(slot * 4 + 2 * h + g) * 512);
         }
+        slot = slot == C::DEPTH - 1 ? 0 : slot + 1;
+        tmem_ld_wait_regs<16>(r[0]);
+        tmem_ld_wait_regs<16>(r[1]);
         const int c = cb * 128 + 64 * half + 8 * qc;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int t = tok[group * 16 + qr + 8 * h];
+          const int t = tok[first_row + 16 * m + qr + 8 * h];
           if (t < 0) continue;
           uint16_t* out = p.out + (int64_t)t * p.N + c;
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
-            if (c + 32 * g < p.N)
-              *reinterpret_cast<uint4*>(out + 32 * g) =
-                  make_uint4(pack_bf16x2(acc[4 * g][2 * h], acc[4 * g][2 * h + 1]), pack_bf16x2(acc[4 * g + 1][2 * h], acc[4 * g + 1][2 * h + 1]),
-                             pack_bf16x2(acc[4 * g + 2][2 * h], acc[4 * g + 2][2 * h + 1]), pack_bf16x2(acc[4 * g + 3][2 * h], acc[4 * g + 3][2 * h + 1]));
+          for (int g = 0; g < 2; ++g) {
+            if (c + 32 * g >= p.N) continue;
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y[j] = pack_bf16x2(__uint_as_float(o[h][g][j] << 16) + __uint_as_float(r[g][4 * j + 2 * h]),
+                                 __uint_as_float(o[h][g][j] & 0xFFFF0000u) + __uint_as_float(r[g][4 * j + 2 * h + 1]));
+            *reinterpret_cast<uint4*>(out + 32 * g) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
+        __syncwarp();
+        fetch();
       }
-      if (more) store_w(buffer ^ 1);
-      __syncthreads();
     }
   }
   if (!waited) {
     pdl_wait();
     pdl_trigger();
   }
+  cp_async_wait<0>();
+  if (stop && issued) mbar_wait_drain(&sh.done[(issued - 1) & 1], ((issued - 1) >> 1) & 1u, p.w.status);
+  tc_fence_before();
+  __syncthreads();
+  pipe.end(tmem, 2 * 128);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -527,6 +573,7 @@ struct GradArgs {
   Groups g;
   GradProblem pr[2];
   int R, ranges, accumulate;
+  Waits w;
 };
 
 // The grouped rows are cut into `ranges` equal parts of `per` rows (a multiple of 32) whatever the adapters.  An adapter whose rows
@@ -538,12 +585,18 @@ __device__ __forceinline__ int rows_of_range(const Groups& g, int ranges, int& r
   return per > 32 ? per : 32;
 }
 
-// All r rows by 256 features (32 a warp) over a range of tokens, 32 of one adapter a stage.  Equal ranges for a whole wave of
-// CTAs: with tiles of one adapter's rows, which are uneven and do not fill the waves, 16384 x (4096 + 4096) at rank 64 took %G0 us, now %G1.
+// All r rows by 256 features over a range of tokens, 32 of one adapter a stage, as features x r on the tensor core: x and v
+// are MN-major operands (a token's features are contiguous, the sum runs over tokens), gathered by asynchronous copies into the
+// swizzled layout, one thread issues the products, two accumulators of 128 features stay in TMEM until the adapter changes.
+// Equal ranges make a whole wave of CTAs: with tiles of one adapter's rows, which are uneven and do not fill the
+// waves, and products from registers 16384 x (4096 + 4096) at rank 64 took %G0 us, now %G1.
 template <int RP>
 struct GradCfg {
-  static constexpr int ROWS = 32, STAGES = RP <= 64 ? 5 : 4;
-  static constexpr int X = ROWS * 512, STAGE = X + ROWS * RP * 2;
+  static constexpr int ROWS = 32, GROUP = ROWS * 128;  // 64 features (or ranks) of all tokens of a stage
+  static constexpr int X = 4 * GROUP, STAGE = X + (RP <= 64 ? 1 : 2) * GROUP;
+  static constexpr int STAGES = RP <= 64 ? 5 : 4;
+  static constexpr int TMEM = 2 * RP;
+  static constexpr int SMEM = 1024 + STAGES * STAGE;
 };
 struct Segment {
   int a, r, end;  // adapter, next row, row behind the adapter's last in the range
@@ -556,12 +609,14 @@ __device__ __forceinline__ void next_segment(const Groups& g, int hi, Segment& s
   }
 }
 template <int RP>
-__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kernel(const GradArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArgs p) {
   using C = GradCfg<RP>;
-  extern __shared__ __align__(256) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int tok[kMaxPer];
+  __shared__ PipeShared<C::STAGES> pipe_shared;
+  Pipe<C::STAGES> pipe(pipe_shared);
   pdl_wait();
-  pdl_trigger();
   int rows;
   const int per = rows_of_range(p.g, p.ranges, rows);
   const int64_t from = (int64_t)blockIdx.y * per;
@@ -576,32 +631,34 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
   int at_or_before = 0;
   for (int i0 = 0; i0 < p.g.n; i0 += kThreads)
     at_or_before += __syncthreads_count(i0 + tid < p.g.n && clamp_row(p.g.off[i0 + tid < p.g.n ? i0 + tid : 0], p.g.T) <= lo);
+  const uint32_t tmem = pipe.start(C::TMEM);
+  pdl_trigger();  // after the allocation, as in the shrink kernel
   Segment put{at_or_before > 0 ? at_or_before - 2 : -1, lo, lo};
   next_segment(p.g, hi, put);
   Segment get = put;
-  // copies: pieces of 16 bytes, a warp a row of 512, four rows; v's rows one behind another
+  // copies: a warp a token's 256 features, four tokens; v's rows one behind another
   const uint32_t in = n0 + 8 * lane < q.K ? 16u : 0u;
   const uint16_t* xcol = q.x + (in ? n0 + 8 * lane : 0);
   const int64_t ld = q.ld;
-  const uint32_t xd = base + at<512>(4 * warp, lane);
-  constexpr int VN = (C::ROWS * RP / 8 + kThreads - 1) / kThreads, VSTEP = kThreads / (RP / 8);  // rows of one pass
-  const int v0 = tid / (RP / 8);
-  const uint16_t* vcol = q.v + (int64_t)v0 * RP + 8 * (tid % (RP / 8));
-  const uint32_t vd = base + C::X + at_rank<RP>(v0, tid % (RP / 8));  // VSTEP is a multiple of 8
+  const uint32_t xd = base + (lane >> 3) * C::GROUP + at<128>(4 * warp, lane & 7);
+  constexpr int PIECES = RP / 8, VSTEP = kThreads / PIECES, VN = (C::ROWS + VSTEP - 1) / VSTEP;  // v rows of one pass, passes
+  const int v0 = tid / PIECES, vc = tid % PIECES;
+  const uint16_t* vcol = q.v + (int64_t)v0 * RP + 8 * vc;
+  const uint32_t vd = base + C::X + (vc >> 3) * C::GROUP + at<128>(v0, vc & 7);  // VSTEP is a multiple of 8
   auto load = [&](uint32_t st) {  // the next rows, at most 32 of one adapter
     const int count = put.end - put.r;
     const int* tk = tok + (put.r - lo) + 4 * warp;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 4 * warp + i < count ? tk[i] : -1;
-      cp_async_16_zfill((xd ^ (uint32_t)(i << 4)) + i * 512 + st, xcol + (int64_t)(t < 0 ? 0 : t) * ld, t < 0 ? 0u : in);
+      cp_async_16_zfill((xd ^ (uint32_t)(i << 4)) + i * 128 + st, xcol + (int64_t)(t < 0 ? 0 : t) * ld, t < 0 ? 0u : in);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int row = v0 + i * VSTEP;
       if (VSTEP * (i + 1) <= C::ROWS || row < C::ROWS) {
         const bool ok = row < count;
-        cp_async_16_zfill(vd + i * VSTEP * RP * 2 + st, vcol + (int64_t)(ok ? put.r + i * VSTEP : 0) * RP, ok ? 16u : 0u);
+        cp_async_16_zfill(vd + i * VSTEP * 128 + st, vcol + (int64_t)(ok ? put.r + i * VSTEP : 0) * RP, ok ? 16u : 0u);
       }
     }
     put.r += C::ROWS;
@@ -610,42 +667,32 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
       next_segment(p.g, hi, put);
     }
   };
-  float acc[RP / 16][4][4];
-#pragma unroll
-  for (int i = 0; i < RP / 16; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) {
     if (put.r < hi) load(i * C::STAGE);
     cp_async_commit();
   }
-  const uint32_t xo = base + at<512>((lane & 7) + (((lane >> 3) & 1) << 3), warp * 4 + (lane >> 4));
-  const uint32_t vo = base + C::X + at_rank<RP>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-  uint32_t st = 0, st_put = (C::STAGES - 1) * C::STAGE;
+  constexpr uint32_t idesc = idesc_bf16(128, RP, 1, 1);
+  bool more = false;  // the accumulators hold rows of this adapter
   while (get.r < hi) {
     cp_async_wait<C::STAGES - 2>();
-    __syncthreads();
-    if (put.r < hi) load(st_put);
-    cp_async_commit();
-    const uint32_t xs[2] = {xo + st, (xo + st) ^ 32u}, vs = vo + st;
+    fence_proxy_async_smem();
+    if (__syncthreads_or(pipe.fail)) break;
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t a0 = base + pipe.at * C::STAGE;
 #pragma unroll
-    for (int kk = 0; kk < C::ROWS / 16; ++kk) {
-      uint32_t b[2][4];
+      for (int kk = 0; kk < C::ROWS / 16; ++kk)
 #pragma unroll
-      for (int np = 0; np < 2; ++np) ldsm4t(b[np], xs[np] + kk * 16 * 512);
-#pragma unroll
-      for (int mt = 0; mt < RP / 16; ++mt) {
-        uint32_t a[4];
-        ldsm4t(a, (vs ^ (uint32_t)(mt << 5)) + kk * 32 * RP);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma16816(acc[mt][j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
-      }
+        for (int h = 0; h < 2; ++h)
+          mma_bf16(tmem + h * RP, mnmajor_sw128_desc(a0 + h * 2 * C::GROUP + kk * 2048, C::GROUP),
+                   mnmajor_sw128_desc(a0 + C::X + kk * 2048, C::GROUP), idesc, (more || kk > 0) ? 1u : 0u);
+      pipe.commit();
     }
-    st = st == (C::STAGES - 1) * C::STAGE ? 0 : st + C::STAGE;
-    st_put = st_put == (C::STAGES - 1) * C::STAGE ? 0 : st_put + C::STAGE;
+    more = true;
+    pipe.advance(p.w);
+    if (put.r < hi) load(pipe.free * C::STAGE);
+    cp_async_commit();
     get.r += C::ROWS;
     if (get.r < get.end) continue;
     get.r = get.end;
@@ -654,33 +701,46 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_grad_kerne
     const bool whole = starts && ends;
     float* part = whole ? nullptr : q.part + (int64_t)(2 * (int)blockIdx.y + (starts ? 1 : 0)) * p.R * q.K;
     uint16_t* dW = q.dW + (int64_t)get.a * p.R * q.K;
+    pipe.settle(p.w);
+    tc_fence_after();
+    // lanes are features: 32 of them a row of the result
+    const int h = warp >> 2, f = n0 + 128 * h + 32 * (warp & 3) + lane;
+    const uint32_t taddr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h * RP;
+    for (int m0 = 0; m0 < RP && m0 < p.R; m0 += 16) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(taddr + m0, r);
+      tmem_ld_wait_regs<16>(r);
+      if (!whole) {
 #pragma unroll
-    for (int mt = 0; mt < RP / 16; ++mt)
+        for (int j = 0; j < 16; ++j)
+          if (m0 + j < p.R && f < q.K) part[(int64_t)(m0 + j) * q.K + f] = __uint_as_float(r[j]);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = mt * 16 + (lane >> 2) + 8 * h;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = n0 + warp * 32 + 8 * j + 2 * (lane & 3);
-          float f0 = acc[mt][j][2 * h], f1 = acc[mt][j][2 * h + 1];
-          acc[mt][j][2 * h] = acc[mt][j][2 * h + 1] = 0.f;
-          if (m >= p.R || c >= q.K) continue;
-          const int64_t o = (int64_t)m * q.K + c;
-          if (!whole) {
-            *reinterpret_cast<float2*>(part + o) = make_float2(f0, f1);
-          } else {
-            uint32_t* d = reinterpret_cast<uint32_t*>(dW + o);
-            if (p.accumulate) {
-              f0 += __uint_as_float(*d << 16);
-              f1 += __uint_as_float(*d & 0xFFFF0000u);
-            }
-            *d = pack_bf16x2(f0, f1);
+        for (int j = 0; j < 16; j += 2) {  // even lanes take row j of two features, odd ones row j + 1
+          const bool odd = lane & 1;
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(odd ? r[j] : r[j + 1]), 1);
+          const float own = __uint_as_float(odd ? r[j + 1] : r[j]);
+          float f0 = odd ? got : own, f1 = odd ? own : got;
+          const int m = m0 + j + (odd ? 1 : 0);
+          if (m >= p.R || f >= q.K) continue;  // K is a multiple of 8
+          uint32_t* d = reinterpret_cast<uint32_t*>(dW + (int64_t)m * q.K + (f & ~1));
+          if (p.accumulate) {
+            f0 += __uint_as_float(*d << 16);
+            f1 += __uint_as_float(*d & 0xFFFF0000u);
           }
+          *d = pack_bf16x2(f0, f1);
         }
       }
+    }
+    tc_fence_before();  // the next products wait for the next barrier
+    more = false;
     next_segment(p.g, hi, get);
   }
   cp_async_wait<0>();
+  if (pipe.begun) pipe.settle(p.w);
+  tc_fence_before();
+  __syncthreads();
+  pipe.end(tmem, C::TMEM);
 }
 
 // Sums of the partial tiles of an adapter whose rows lie in several ranges, in order; zeros for one without rows.
@@ -727,8 +787,8 @@ int padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 :
 int64_t slots_of(int64_t T, int64_t n, int64_t per) { return T / per + n; }
 
 // Parts of the rows in the gradient: one wave of CTAs, but 64 rows a part at least and kMaxPer at most.
-int grad_ranges(int64_t T, int64_t H, int64_t N, int rp, int sms) {
-  const int64_t wave = (rp <= 64 ? 2 : 1) * sms / (cdiv(H, 256) + cdiv(N, 256));
+int grad_ranges(int64_t T, int64_t H, int64_t N, int sms) {
+  const int64_t wave = 2 * sms / (cdiv(H, 256) + cdiv(N, 256));
   return (int)std::max(cdiv(T, kMaxPer), std::min(wave, cdiv(T, 64)));
 }
 // tiles of `per` rows that T tokens of n adapters come to, about
@@ -738,7 +798,7 @@ template <int RP, int SPLIT>
 int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
   auto kern = adapter_shrink_kernel<RP, SPLIT>;
-  const dim3 grid((unsigned)(slots_of(a.g.T, a.g.n, C::ROWS) * SPLIT));
+  const dim3 grid((unsigned)(slots_of(a.g.T, a.g.n, a.per) * SPLIT));
   if constexpr (SPLIT == 1) {
     return launch_pdl(kern, grid, dim3(kThreads), C::SMEM, st, "adapter shrink", a);
   } else {
@@ -763,31 +823,41 @@ int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
     return cuda_check(cudaGetLastError(), "adapter shrink");
   }
 }
-// CTAs along the contraction: as many as two resident CTAs an SM have room for (longer CTAs pay their start once).
+// CTAs along the contraction and rows of a tile: one wave of two CTAs an SM, as full as can be (a tile of 128 rows by two CTAs
+// leaves 48 of 152 SMs with one: rank 64, 16384 x 4096 %P0 us, with 111 rows %P1), with as many rows as that allows, since
+// they share W.  Several waves where the tiles are too many for one.
 template <int RP>
-int run_shrink(const ShrinkArgs& a, int sms, cudaStream_t st) {
+int run_shrink(ShrinkArgs a, int sms, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
-  const int64_t tiles = tiles_of(a.g.T, a.g.n, C::ROWS), chunks = cdiv(a.K, C::KC);
-  const auto fits = [&](int s) { return tiles * s <= 2 * sms && chunks >= s; };
-  return fits(8) ? launch_shrink<RP, 8>(a, st) : fits(4) ? launch_shrink<RP, 4>(a, st) : fits(2) ? launch_shrink<RP, 2>(a, st)
-                                                                                              : launch_shrink<RP, 1>(a, st);
+  const int64_t T = a.g.T, n = std::min<int64_t>(a.g.n, T), chunks = cdiv(a.K, 64);
+  int split = 1;
+  a.per = C::ROWS;
+  for (int s = 8; s >= 1; s /= 2) {
+    const int64_t room = 2 * sms / s - n;  // T / per + n tiles at most
+    if (chunks < s || room <= 0 || cdiv(T, room) > C::ROWS) continue;
+    split = s;
+    a.per = (int)std::max<int64_t>(cdiv(T, room), 64);
+    break;
+  }
+  return split == 8 ? launch_shrink<RP, 8>(a, st) : split == 4 ? launch_shrink<RP, 4>(a, st) : split == 2 ? launch_shrink<RP, 2>(a, st)
+                                                                                                          : launch_shrink<RP, 1>(a, st);
 }
 template <int RP>
 int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
-  // 256 tokens share W's columns; fewer where that leaves a CTA less than a few pieces of work to even out
+  // 128 tokens share W's columns; fewer where that leaves a CTA less than a few pieces of work to even out
   const int64_t wave = (RP <= 64 ? 2 : 1) * sms;
   a.col_blocks = (int)cdiv(a.N, 128);
-  a.shift = RP == 64 ? 7 : 8;  // two CTAs' shared memory on an SM
+  a.shift = 7;
   while (a.shift > 6 && tiles_of(a.g.T, a.g.n, 1 << a.shift) * a.col_blocks < 6 * wave) --a.shift;
   a.per = 1 << a.shift;
   const int64_t most = std::max(slots_of(a.g.T, a.g.n, a.per) * a.col_blocks, cdiv(a.g.T, 8));
   return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)std::min(wave, most)), dim3(kThreads),
-                    ExpandCfg<RP>::smem(a.per), st, "adapter expand", a);
+                    ExpandCfg<RP>::SMEM, st, "adapter expand", a);
 }
 template <int RP>
 int run_grad(const GradArgs& a, cudaStream_t st) {
   int rc = launch_pdl(adapter_grad_kernel<RP>, dim3((unsigned)(a.pr[0].blocks + a.pr[1].blocks), (unsigned)a.ranges),
-                      dim3(kThreads), (size_t)GradCfg<RP>::STAGES * GradCfg<RP>::STAGE, st, "adapter gradient", a);
+                      dim3(kThreads), GradCfg<RP>::SMEM, st, "adapter gradient", a);
   if (rc) return rc;
   const int64_t most = (int64_t)a.R * std::max(a.pr[0].K, a.pr[1].K);
   return launch_pdl(adapter_reduce_kernel, dim3((unsigned)std::min<int64_t>(cdiv(most, 1024), 512), (unsigned)a.g.n, 2), dim3(256), 0,
@@ -818,7 +888,7 @@ Layout layout(int64_t T, int64_t H, int64_t N, int64_t r, bool backward, int sms
   L.v = take((size_t)T * rp * 2);
   if (backward) {
     L.su = take((size_t)T * rp * 2);
-    const size_t places = 2 * (size_t)grad_ranges(T, H, N, rp, sms);
+    const size_t places = 2 * (size_t)grad_ranges(T, H, N, sms);
     L.grad0 = take(places * r * H * 4);
     L.grad1 = take(places * r * N * 4);
   }
@@ -850,7 +920,7 @@ extern "C" size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_
 extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base,
                            int64_t ldbase, const int32_t* expert_offsets, const int32_t* x_gather_idx,
                            const int32_t* s_reverse_scatter_idx, int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, void* y,
-                           float* u, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+                           float* u, int32_t* status_dev, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   clear_error();
   int rc = check_sizes("adapter_fwd", T, H, N, n, r);
   if (rc || T == 0) return rc;
@@ -860,8 +930,8 @@ extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void
     return fail(MOE_ERR_INVALID, "adapter_fwd: row stride too small or not a multiple of 8");
   if (base == y && ldbase != N) return fail(MOE_ERR_INVALID, "adapter_fwd: y may be the base only where its row stride is N");
   if (off16(x) || off16(A) || off16(B) || off16(base) || off16(y)) return fail(MOE_ERR_INVALID, "adapter_fwd: tensors must be 16-byte aligned");
-  if (off4(scale) || off4(expert_offsets) || off4(x_gather_idx) || off4(s_reverse_scatter_idx) || off4(u))
-    return fail(MOE_ERR_INVALID, "adapter_fwd: metadata, scales and u must be 4-byte aligned");
+  if (off4(scale) || off4(expert_offsets) || off4(x_gather_idx) || off4(s_reverse_scatter_idx) || off4(u) || off4(status_dev))
+    return fail(MOE_ERR_INVALID, "adapter_fwd: metadata, scales, u and status must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_ERR_INVALID, "adapter_fwd: workspace must be 256-byte aligned");
   const int sms = device_sm_count();
   const Layout L = layout(T, H, N, r, false, sms);
@@ -872,10 +942,11 @@ extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void
   s.g = g; s.x = static_cast<const uint16_t*>(x); s.ld = ldx; s.W = static_cast<const uint16_t*>(A); s.scale = scale;
   s.v = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + L.v); s.u = u;
   s.K = (int)H; s.R = (int)r;
+  s.w = Waits{status_dev, (uint64_t)option(MOE_OPT_WAIT_LIMIT_NS)};
   ExpandArgs e{};
   e.g = g; e.v = s.v; e.W = static_cast<const uint16_t*>(B);
   e.base = static_cast<const uint16_t*>(base); e.ldb = ldbase; e.out = static_cast<uint16_t*>(y); e.back = s_reverse_scatter_idx;
-  e.u = u; e.N = (int)N; e.R = (int)r;
+  e.u = u; e.N = (int)N; e.R = (int)r; e.w = s.w;
   return by_rank(padded_rank(r), [&](auto k) {
     constexpr int RP = decltype(k)::value;
     const int rc1 = run_shrink<RP>(s, sms, st);
@@ -886,7 +957,7 @@ extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void
 extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* u, const void* A, const void* B,
                            const float* scale, const void* base, int64_t ldbase, const int32_t* expert_offsets,
                            const int32_t* x_gather_idx, const int32_t* s_reverse_scatter_idx, int64_t T, int64_t H, int64_t N,
-                           int64_t n, int64_t r, void* dx, void* dA, void* dB, int accumulate, void* workspace,
+                           int64_t n, int64_t r, void* dx, void* dA, void* dB, int accumulate, int32_t* status_dev, void* workspace,
                            size_t workspace_bytes, moe_stream_t stream) {
   clear_error();
   int rc = check_sizes("adapter_bwd", T, H, N, n, r);
@@ -907,8 +978,8 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
   if (base == dx && ldbase != H) return fail(MOE_ERR_INVALID, "adapter_bwd: dx may be the base only where its row stride is H");
   if (off16(dy) || off16(x) || off16(A) || off16(B) || off16(base) || off16(dx))
     return fail(MOE_ERR_INVALID, "adapter_bwd: tensors must be 16-byte aligned");
-  if (off4(scale) || off4(expert_offsets) || off4(x_gather_idx) || off4(s_reverse_scatter_idx) || off4(u))
-    return fail(MOE_ERR_INVALID, "adapter_bwd: metadata, scales and u must be 4-byte aligned");
+  if (off4(scale) || off4(expert_offsets) || off4(x_gather_idx) || off4(s_reverse_scatter_idx) || off4(u) || off4(status_dev))
+    return fail(MOE_ERR_INVALID, "adapter_bwd: metadata, scales, u and status must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(MOE_ERR_INVALID, "adapter_bwd: workspace must be 256-byte aligned");
   const int sms = device_sm_count();
   const Layout L = layout(T, H, N, r, true, sms);
@@ -919,12 +990,14 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
   s.g = g; s.x = static_cast<const uint16_t*>(dy); s.ld = lddy; s.W = static_cast<const uint16_t*>(B); s.scale = scale;
   s.v = reinterpret_cast<uint16_t*>(ws + L.v); s.u_in = u; s.su = reinterpret_cast<uint16_t*>(ws + L.su);
   s.K = (int)N; s.R = (int)r;
+  s.w = Waits{status_dev, (uint64_t)option(MOE_OPT_WAIT_LIMIT_NS)};
   ExpandArgs e{};
   e.g = g; e.v = s.v; e.W = static_cast<const uint16_t*>(A);
   e.base = static_cast<const uint16_t*>(base); e.ldb = ldbase; e.out = static_cast<uint16_t*>(dx); e.back = s_reverse_scatter_idx;
-  e.N = (int)H; e.R = (int)r;
+  e.N = (int)H; e.R = (int)r; e.w = s.w;
   GradArgs d{};
-  d.g = g; d.R = (int)r; d.ranges = grad_ranges(T, H, N, padded_rank(r), sms); d.accumulate = accumulate;
+  d.g = g; d.R = (int)r; d.ranges = grad_ranges(T, H, N, sms); d.accumulate = accumulate;
+  d.w = s.w;
   d.pr[0] = GradProblem{static_cast<const uint16_t*>(x), s.v, static_cast<uint16_t*>(dA), reinterpret_cast<float*>(ws + L.grad0), ldx,
                         (int)H, (int)cdiv(H, 256)};
   d.pr[1] = GradProblem{static_cast<const uint16_t*>(dy), s.su, static_cast<uint16_t*>(dB), reinterpret_cast<float*>(ws + L.grad1), lddy,
