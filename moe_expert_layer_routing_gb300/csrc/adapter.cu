@@ -172,11 +172,13 @@ struct ShrinkArgs {
 // now %S64); a thread copies the same four rows' pieces in every stage, so that a copy costs two additions beside it.
 template <int RP>
 struct ShrinkCfg {
-  static constexpr int ROWS = 128, X = ROWS * 128, STAGE = X + RP * 128;
-  static constexpr int STAGES = RP <= 32 ? 5 : RP <= 64 ? 4 : 3;
+  static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PIECES = KC / 8;
+  static constexpr int X = ROWS * KC * 2, STAGE = X + RP * KC * 2;
+  static constexpr int STAGES = RP <= 16 ? 5 : RP <= 64 ? 4 : 3;
   static constexpr int TMEM = RP < 32 ? 32 : RP;
   static constexpr int PITCH = RP + 4;  // floats of a partial row: 16-byte pieces of 8 rows in 8 bank groups
-  static constexpr int SMEM = 1024 + STAGES * STAGE;
+  // a product reads 128 rows: with 64 the others are whatever lies behind them, and reach sums that nobody reads
+  static constexpr int SMEM = 1024 + STAGES * STAGE + (128 - ROWS) * 128;
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "the partial tile overlays the stages");
 };
 
@@ -188,43 +190,47 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
   __shared__ int tok[C::ROWS];
   __shared__ PipeShared<C::STAGES> pipe_shared;
   Pipe<C::STAGES> pipe(pipe_shared);
+  const uint32_t tmem = pipe.start(C::TMEM);
   pdl_wait();
+  pdl_trigger();  // after the allocation: the next kernel cannot take the TMEM that this one is still to get
   const uint32_t rank = SPLIT > 1 ? cluster_ctarank() : 0;
   Tile t;
   // the whole cluster works on one tile, so that all of it leaves here or none
-  if (!find_tile(p.g, blockIdx.x / SPLIT, p.per, t)) return;
+  if (!find_tile(p.g, blockIdx.x / SPLIT, p.per, t)) {
+    pipe.end(tmem, C::TMEM);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < C::ROWS) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
-  const uint32_t tmem = pipe.start(C::TMEM);
-  pdl_trigger();  // after the allocation: the next kernel cannot take the TMEM that this one is still to get
-  const int chunks = (p.K + 63) / 64;
+  __syncthreads();
+  const int chunks = (p.K + C::KC - 1) / C::KC;
   const int mine = (chunks - (int)rank + SPLIT - 1) / SPLIT;  // chunks rank, rank + SPLIT, ...: the cluster reads a row's neighbours together
   const uint32_t base = smem_u32(smem);
-  const int pc = tid & 7, r0 = tid >> 3;
-  constexpr int STEP = kThreads / 8;                // rows of one pass of copies
+  const int pc = tid % C::PIECES, r0 = tid / C::PIECES;
+  constexpr int STEP = kThreads / C::PIECES, XN = C::ROWS / STEP;  // rows of one pass of copies, passes over x's
   constexpr int WN = (RP + STEP - 1) / STEP;        // passes over W's rows
-  const uint16_t* xs[4];
-  uint32_t xb[4], xd[4];
+  const uint16_t* xs[XN];
+  uint32_t xb[XN], xd[XN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < XN; ++i) {
     const int row = r0 + STEP * i, tk = tok[row];
-    xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)rank * 64;
+    xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)rank * C::KC;
     xb[i] = tk < 0 ? 0u : 16u;
-    xd[i] = row < t.rows ? base + at<128>(row, pc) : 0u;  // other rows only reach their own sums, which nobody reads
+    xd[i] = row < t.rows ? base + (pc >> 3) * C::ROWS * 128 + at<128>(row, pc & 7) : 0u;  // other rows only reach their own sums, which nobody reads
   }
-  const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)rank * 64;
+  const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)rank * C::KC;
   auto load = [&](int c, uint32_t st) {
-    const int64_t o = (int64_t)c * (64 * SPLIT);
-    const uint32_t in = (int)rank * 64 + o + 8 * pc < p.K ? 16u : 0u;  // K is a multiple of 8
+    const int64_t o = (int64_t)c * (C::KC * SPLIT);
+    const uint32_t in = (int)rank * C::KC + o + 8 * pc < p.K ? 16u : 0u;  // K is a multiple of 8
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < XN; ++i)
       if (xd[i]) cp_async_16_zfill(xd[i] + st, in ? xs[i] + o : p.x, xb[i] & in);
 #pragma unroll
     for (int i = 0; i < WN; ++i) {
       const int row = r0 + STEP * i;
       if (RP % STEP == 0 || row < RP) {
         const bool ok = row < p.R && in;
-        cp_async_16_zfill(base + st + C::X + at<128>(row, pc), ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
+        cp_async_16_zfill(base + st + C::X + (pc >> 3) * RP * 128 + at<128>(row, pc & 7), ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
       }
     }
   };
@@ -242,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
       tc_fence_after();
       const uint32_t a0 = base + pipe.at * C::STAGE;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_bf16(tmem, kmajor_sw128_desc(a0 + kk * 32), kmajor_sw128_desc(a0 + C::X + kk * 32), idesc, (c > 0 || kk > 0) ? 1u : 0u);
+      for (int kk = 0; kk < C::KC / 16; ++kk)
+        mma_bf16(tmem, kmajor_sw128_desc(a0 + (kk >> 2) * C::ROWS * 128 + (kk & 3) * 32),
+                 kmajor_sw128_desc(a0 + C::X + (kk >> 2) * RP * 128 + (kk & 3) * 32), idesc, (c > 0 || kk > 0) ? 1u : 0u);
       pipe.commit();
     }
     pipe.advance(p.w);  // the products of the step before are done with the stage refilled now
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
   __syncthreads();  // the partial tiles overlay the stages
   tc_fence_after();
   float* part = reinterpret_cast<float*>(smem);  // [rows][PITCH]
-  for (int c = 16 * (warp >> 2); c < RP; c += 32) {
+  for (int c = 16 * (warp >> 2); c < RP && 32 * (warp & 3) < C::ROWS; c += 32) {
     uint32_t r[16];
     tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, r);
     tmem_ld_wait_regs<16>(r);
@@ -323,7 +330,7 @@ constexpr int kExpandRows = 128;
 
 template <int RP>
 struct ExpandCfg {
-  static constexpr int DEPTH = RP == 64 ? 3 : 4;  // 16 tokens x 64 columns of base of a warp on their way, 2 KB each
+  static constexpr int DEPTH = RP == 128 ? 4 : 3;  // 16 tokens x 64 columns of base of a warp on their way, 2 KB each
   static constexpr int V = 16384 * (RP <= 64 ? 1 : 2), W = RP * 256;
   static constexpr int SMEM = 1024 + V + 2 * W + 8 * DEPTH * 2048;
 };
@@ -616,11 +623,16 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
   __shared__ int tok[kMaxPer];
   __shared__ PipeShared<C::STAGES> pipe_shared;
   Pipe<C::STAGES> pipe(pipe_shared);
+  const uint32_t tmem = pipe.start(C::TMEM);
   pdl_wait();
+  pdl_trigger();  // after the allocation, as in the shrink kernel
   int rows;
   const int per = rows_of_range(p.g, p.ranges, rows);
   const int64_t from = (int64_t)blockIdx.y * per;
-  if (from >= rows) return;
+  if (from >= rows) {
+    pipe.end(tmem, C::TMEM);
+    return;
+  }
   const int lo = (int)from, hi = rows - lo < per ? rows : lo + per;
   const GradProblem& q = p.pr[(int)blockIdx.x < p.pr[0].blocks ? 0 : 1];
   const int n0 = ((int)blockIdx.x < p.pr[0].blocks ? (int)blockIdx.x : (int)blockIdx.x - p.pr[0].blocks) * 256;
@@ -631,8 +643,6 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
   int at_or_before = 0;
   for (int i0 = 0; i0 < p.g.n; i0 += kThreads)
     at_or_before += __syncthreads_count(i0 + tid < p.g.n && clamp_row(p.g.off[i0 + tid < p.g.n ? i0 + tid : 0], p.g.T) <= lo);
-  const uint32_t tmem = pipe.start(C::TMEM);
-  pdl_trigger();  // after the allocation, as in the shrink kernel
   Segment put{at_or_before > 0 ? at_or_before - 2 : -1, lo, lo};
   next_segment(p.g, hi, put);
   Segment get = put;
@@ -829,7 +839,7 @@ int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
 template <int RP>
 int run_shrink(ShrinkArgs a, int sms, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
-  const int64_t T = a.g.T, n = std::min<int64_t>(a.g.n, T), chunks = cdiv(a.K, 64);
+  const int64_t T = a.g.T, n = std::min<int64_t>(a.g.n, T), chunks = cdiv(a.K, C::KC);
   int split = 1;
   a.per = C::ROWS;
   for (int s = 8; s >= 1; s /= 2) {
@@ -1005,7 +1015,7 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
   return by_rank(padded_rank(r), [&](auto k) {
     constexpr int RP = decltype(k)::value;
     int rc1 = run_shrink<RP>(s, sms, st);
-    if (!rc1) rc1 = run_expand<RP>(e, sms, st);
-    return rc1 ? rc1 : run_grad<RP>(d, st);
+    if (!rc1) rc1 = run_grad<RP>(d, st);  // right behind the kernel that read dy, part of which is still in L2
+    return rc1 ? rc1 : run_expand<RP>(e, sms, st);
   });
 }
