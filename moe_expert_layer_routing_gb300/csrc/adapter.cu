@@ -294,8 +294,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
     }
     const int tk = tok[row];
     const int64_t o = (int64_t)(t.r0 + row) * RP + c;
-    *reinterpret_cast<uint2*>(p.v + o) = make_uint2(pack_bf16x2(s.x * scale, s.y * scale), pack_bf16x2(s.z * scale, s.w * scale));
     const float w[4] = {s.x, s.y, s.z, s.w};
+    float y[4];  // ranks behind r are zeros whatever x holds (0 times infinity)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = c + j < p.R ? w[j] * scale : 0.f;
+    *reinterpret_cast<uint2*>(p.v + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     if (p.u && tk >= 0)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
     pdl_trigger();
   }
   cp_async_wait<0>();
-  if (stop && issued) mbar_wait_drain(&sh.done[(issued - 1) & 1], ((issued - 1) >> 1) & 1u, p.w.status);
+  if ((stop || pipe.fail) && issued) mbar_wait_drain(&sh.done[(issued - 1) & 1], ((issued - 1) >> 1) & 1u, p.w.status);
   tc_fence_before();
   __syncthreads();
   pipe.end(tmem, 2 * 128);
@@ -846,7 +849,7 @@ int run_shrink(ShrinkArgs a, int sms, cudaStream_t st) {
     const int64_t room = 2 * sms / s - n;  // T / per + n tiles at most
     if (chunks < s || room <= 0 || cdiv(T, room) > C::ROWS) continue;
     split = s;
-    a.per = (int)std::max<int64_t>(cdiv(T, room), 64);
+    a.per = (int)std::max<int64_t>(cdiv(T, room), C::ROWS / 2);
     break;
   }
   return split == 8 ? launch_shrink<RP, 8>(a, st) : split == 4 ? launch_shrink<RP, 4>(a, st) : split == 2 ? launch_shrink<RP, 2>(a, st)

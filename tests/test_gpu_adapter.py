@@ -261,3 +261,103 @@ def test_refusals():
     with pytest.raises(mb.MoeError, match="stride"):
         wide = torch.zeros(16, 80, dtype=torch.bfloat16, device="cuda")
         f(base=wide[:, :72], out=None, x=torch.zeros(16, 66, dtype=torch.bfloat16, device="cuda")[:, :64])
+
+
+def test_infinite_sums_stay_infinite_at_odd_ranks():
+    """Ranks that only pad r: 0 times infinity must not reach the row."""
+    mb = _mb()
+    d = _inputs(20, 64, 72, 2, 5, none=0.0)
+    d["A"], d["B"] = d["A"].abs() + 0.125, d["B"].abs() + 0.125
+    d["x"][3, 40] = float("inf")
+    f = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["base"])
+    torch.cuda.synchronize()
+    assert torch.all(f["y"][3] == float("inf")) and torch.all(f["u"][3] == float("inf"))
+    assert torch.isfinite(f["y"][[i for i in range(20) if i != 3]]).all()
+
+
+@pytest.mark.parametrize("T", [90, 1500])
+def test_other_adapters_gradients_do_not_see_an_infinite_row(T):
+    mb = _mb()
+    d = _inputs(T, 136, 264, 4, 24, none=0.1)
+    ids = d["ids"][:, 0]
+    rows = torch.nonzero(ids == 2)[:2, 0]
+    run = lambda: mb.adapter_bwd(d["dy"], d["x"], u, d["A"], d["B"], d["meta"], scale=d["scale"], base=d["dbase"])  # noqa: E731
+    u = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=d["scale"])["u"]
+    ref = run()
+    d["x"][rows[0]], d["dy"][rows[1]] = float("nan"), float("inf")
+    got = run()
+    torch.cuda.synchronize()
+    keep = [0, 1, 3]
+    assert torch.equal(got["dA"][keep], ref["dA"][keep]) and torch.equal(got["dB"][keep], ref["dB"][keep])
+    other = torch.ones(T, dtype=torch.bool, device="cuda")
+    other[rows[1]] = False
+    assert torch.equal(got["dx"][other], ref["dx"][other])
+
+
+def test_short_wait_limit_leaves_the_context_usable(set_option):
+    """Waits that run out are reported in the status word; the same calls give the same results afterwards."""
+    mb = _mb()
+    d = _inputs(900, 1024, 520, 3, 64, seed=7)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def calls():
+        f = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["base"], status=status)
+        g = mb.adapter_bwd(d["dy"], d["x"], u0, d["A"], d["B"], d["meta"], scale=d["scale"], base=d["dbase"], status=status)
+        return f["y"], f["u"], g["dx"], g["dA"], g["dB"]
+
+    u0 = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"])["u"]
+    first = calls()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    set_option("WAIT_LIMIT_NS", 1)
+    calls()
+    torch.cuda.synchronize()
+    assert int(status.item()) in (0, mb.STATUS_TIMEOUT)
+    set_option("WAIT_LIMIT_NS", None)
+    status.zero_()
+    again = calls()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("wide", ["H", "N"])
+def test_past_32_bits(wide):
+    """More than 2^31 numbers in x (or y and dy): the last rows, which are one adapter's, against 64 bits."""
+    mb = _mb()
+    T, n, r, tail = 530000, 3, 4, 100
+    H, N = (4096, 64) if wide == "H" else (64, 4096)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    bf = torch.bfloat16
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=bf)  # noqa: E731
+    x, dy = rand(T, H), rand(T, N)
+    A, B = rand(n, r, H) * H ** -0.5, rand(n, r, N) * r ** -0.5
+    ids = torch.randint(-1, 2, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    ids[-tail:] = 2
+    meta = mb.route_meta(ids, n, 128)
+    f = mb.adapter_fwd(x, A, B, meta)
+    g = mb.adapter_bwd(dy, x, f["u"], A, B, meta)
+    torch.cuda.synchronize()
+    xt, dt, a, b = (np64(t) for t in (x[-tail:], dy[-tail:], A[2], B[2]))
+    u, v = xt @ a.T, dt @ b.T
+    eu, ev = _e(H) * (np.abs(xt) @ np.abs(a).T), _e(N) * (np.abs(dt) @ np.abs(b).T)
+    assert np.all(np.abs(np64(f["u"][-tail:]) - u) <= eu)
+    eu, ev = eu + HALF * (np.abs(u) + eu), ev + HALF * (np.abs(v) + ev)
+    for got, ref, err, mag in ((f["y"][-tail:], u @ b, eu @ np.abs(b), np.abs(u) @ np.abs(b)),
+                               (g["dx"][-tail:], v @ a, ev @ np.abs(a), np.abs(v) @ np.abs(a)),
+                               (g["dA"][2], v.T @ xt, ev.T @ np.abs(xt), np.abs(v).T @ np.abs(xt)),
+                               (g["dB"][2], u.T @ dt, eu.T @ np.abs(dt), np.abs(u).T @ np.abs(dt))):
+        err = err + _e(tail + 8) * (mag + err)
+        assert np.all(np.abs(np64(got) - ref) <= err + HALF * (np.abs(ref) + err))
+    none = ids[:, 0] < 0
+    assert torch.all(f["y"][none][-1000:] == 0) and torch.all(g["dx"][none][-1000:] == 0)
+
+
+def test_status_refusals():
+    mb = _mb()
+    d = _inputs(16, 64, 72, 2, 8)
+    u = torch.zeros(16, 8, device="cuda")
+    for bad in (torch.zeros(1, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(mb.MoeError):
+            mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], status=bad)
+        with pytest.raises(mb.MoeError):
+            mb.adapter_bwd(d["dy"], d["x"], u, d["A"], d["B"], d["meta"], status=bad)
