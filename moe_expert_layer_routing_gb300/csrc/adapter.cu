@@ -315,6 +315,82 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
 }
 
 // ------------------------------------------------------------------------------------------
+// the gradient's arguments, partial sums
+// ------------------------------------------------------------------------------------------
+struct GradProblem {
+  const uint16_t* x;  // [T, K], row stride ld
+  const uint16_t* v;  // [T, RP] by grouped row
+  uint16_t* dW;       // [n, R, K]
+  float* part;        // [2 ranges, R, K]
+  int64_t ld;
+  int K, blocks;      // blocks of 256 features
+};
+struct GradArgs {
+  Groups g;
+  GradProblem pr[2];
+  int R, ranges, accumulate;
+  Waits w;
+};
+
+// The grouped rows are cut into `ranges` equal parts of `per` rows (a multiple of 32) whatever the adapters.  An adapter whose rows
+// lie in one part is summed there; of any other each part holds a partial sum: at place 2 part + 1 for the one that has the
+// adapter's first row (the part's last adapter), at 2 part for the others (the part's first), so that no two share one.
+__device__ __forceinline__ int rows_of_range(const Groups& g, int ranges, int& rows) {
+  rows = clamp_row(g.off[g.n], g.T);
+  const int per = ((rows + ranges - 1) / ranges + 31) & ~31;
+  return per > 32 ? per : 32;
+}
+
+// Sums of the partial tiles of the adapters whose rows lie in several ranges, in order; zeros for those without rows.  The CTAs of
+// the expand kernel, which runs behind the gradient's, share it out in pieces of 4096 numbers (as a kernel of its own it took
+// 7 us more, 16384 x (4096 + 4096) at rank 64: 25 MB, but a launch and a start of its own).
+__device__ __forceinline__ void sum_partials(const GradArgs& p, int64_t me, int64_t all) {
+  int rows;
+  const int per = rows_of_range(p.g, p.ranges, rows);
+  const int64_t size0 = (int64_t)p.R * p.pr[0].K, size1 = (int64_t)p.R * p.pr[1].K;
+  const int b0 = (int)((size0 + 4095) / 4096), each = b0 + (int)((size1 + 4095) / 4096);
+  for (int64_t b = me; b < (int64_t)each * p.g.n; b += all) {
+    const int a = (int)(b / each), piece = (int)(b - (int64_t)a * each);
+    const int o0 = clamp_row(p.g.off[a], rows), o1 = clamp_row(p.g.off[a + 1], rows);
+    const bool none = o1 <= o0;
+    const int s0 = o0 / per, s1 = none ? s0 : (o1 - 1) / per;
+    if (none ? p.accumulate != 0 : s0 == s1) continue;
+    const GradProblem& q = p.pr[piece < b0 ? 0 : 1];
+    const int64_t size = piece < b0 ? size0 : size1, i0 = (int64_t)(piece < b0 ? piece : piece - b0) * 4096 + 4 * threadIdx.x;
+    uint16_t* dW = q.dW + a * size;
+    float4 s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = none ? s1 + 1 : s0; k <= s1; ++k) {
+      const float* src = q.part + (2 * (int64_t)k + (k == s0)) * size;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t i = i0 + 1024 * j;  // K is a multiple of 8
+        const float4 f = i < size ? *reinterpret_cast<const float4*>(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[j].x += f.x;
+        s[j].y += f.y;
+        s[j].z += f.z;
+        s[j].w += f.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = i0 + 1024 * j;
+      if (i >= size) continue;
+      uint2* d = reinterpret_cast<uint2*>(dW + i);
+      if (p.accumulate) {
+        const uint2 w = *d;
+        s[j].x += __uint_as_float(w.x << 16);
+        s[j].y += __uint_as_float(w.x & 0xFFFF0000u);
+        s[j].z += __uint_as_float(w.y << 16);
+        s[j].w += __uint_as_float(w.y & 0xFFFF0000u);
+      }
+      *d = make_uint2(pack_bf16x2(s[j].x, s[j].y), pack_bf16x2(s[j].z, s[j].w));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
 // expand: out[token] = base[token] + v W_a
 // ------------------------------------------------------------------------------------------
 struct ExpandArgs {
@@ -328,6 +404,7 @@ struct ExpandArgs {
   int64_t ldb;
   int N, R, per, shift, col_blocks;  // rows of a tile: 2^shift, at most kExpandRows
   Waits w;
+  GradArgs sums;  // with ranges: partial sums to join
 };
 constexpr int kExpandRows = 128;
 
@@ -566,35 +643,12 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
   tc_fence_before();
   __syncthreads();
   pipe.end(tmem, 2 * 128);
+  if (p.sums.ranges) sum_partials(p.sums, me, all);
 }
 
 // ------------------------------------------------------------------------------------------
 // grad: dW_a[R, K] = sum over the adapter's rows of v[row]^T x[token(row)]
 // ------------------------------------------------------------------------------------------
-struct GradProblem {
-  const uint16_t* x;  // [T, K], row stride ld
-  const uint16_t* v;  // [T, RP] by grouped row
-  uint16_t* dW;       // [n, R, K]
-  float* part;        // [2 ranges, R, K]
-  int64_t ld;
-  int K, blocks;      // blocks of 256 features
-};
-struct GradArgs {
-  Groups g;
-  GradProblem pr[2];
-  int R, ranges, accumulate;
-  Waits w;
-};
-
-// The grouped rows are cut into `ranges` equal parts of `per` rows (a multiple of 32) whatever the adapters.  An adapter whose rows
-// lie in one part is summed there; of any other each part holds a partial sum: at place 2 part + 1 for the one that has the
-// adapter's first row (the part's last adapter), at 2 part for the others (the part's first), so that no two share one.
-__device__ __forceinline__ int rows_of_range(const Groups& g, int ranges, int& rows) {
-  rows = clamp_row(g.off[g.n], g.T);
-  const int per = ((rows + ranges - 1) / ranges + 31) & ~31;
-  return per > 32 ? per : 32;
-}
-
 // All r rows by 256 features over a range of tokens, 32 of one adapter a stage, as features x r on the tensor core: x and v
 // are MN-major operands (a token's features are contiguous, the sum runs over tokens), gathered by asynchronous copies into the
 // swizzled layout, one thread issues the products, two accumulators of 128 features stay in TMEM until the adapter changes.
@@ -756,42 +810,6 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
   pipe.end(tmem, C::TMEM);
 }
 
-// Sums of the partial tiles of an adapter whose rows lie in several ranges, in order; zeros for one without rows.
-__global__ void __launch_bounds__(256) adapter_reduce_kernel(const GradArgs p) {
-  pdl_wait();
-  pdl_trigger();
-  const GradProblem& q = p.pr[blockIdx.z];
-  const int a = blockIdx.y;
-  int rows;
-  const int per = rows_of_range(p.g, p.ranges, rows);
-  const int o0 = clamp_row(p.g.off[a], rows), o1 = clamp_row(p.g.off[a + 1], rows);
-  const bool none = o1 <= o0;
-  const int s0 = o0 / per, s1 = none ? s0 : (o1 - 1) / per;
-  if (none ? p.accumulate != 0 : s0 == s1) return;
-  const int64_t size = (int64_t)p.R * q.K;
-  uint16_t* dW = q.dW + a * size;
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * 1024) {  // K is a multiple of 8
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = none ? s1 + 1 : s0; k <= s1; ++k) {
-      const float4 f = *reinterpret_cast<const float4*>(q.part + (2 * (int64_t)k + (k == s0)) * size + i);
-      s.x += f.x;
-      s.y += f.y;
-      s.z += f.z;
-      s.w += f.w;
-    }
-    uint2* d = reinterpret_cast<uint2*>(dW + i);
-    if (p.accumulate) {
-      const uint2 w = *d;
-      s.x += __uint_as_float(w.x << 16);
-      s.y += __uint_as_float(w.x & 0xFFFF0000u);
-      s.z += __uint_as_float(w.y << 16);
-      s.w += __uint_as_float(w.y & 0xFFFF0000u);
-    }
-    *d = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-  }
-}
-
 // ------------------------------------------------------------------------------------------
 // host
 // ------------------------------------------------------------------------------------------
@@ -863,18 +881,15 @@ int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
   a.shift = 7;
   while (a.shift > 6 && tiles_of(a.g.T, a.g.n, 1 << a.shift) * a.col_blocks < 6 * wave) --a.shift;
   a.per = 1 << a.shift;
-  const int64_t most = std::max(slots_of(a.g.T, a.g.n, a.per) * a.col_blocks, cdiv(a.g.T, 8));
+  int64_t most = std::max(slots_of(a.g.T, a.g.n, a.per) * a.col_blocks, cdiv(a.g.T, 8));
+  if (a.sums.ranges) most = std::max(most, (int64_t)a.g.n * cdiv((int64_t)a.R * (a.sums.pr[0].K + a.sums.pr[1].K), 4096));
   return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)std::min(wave, most)), dim3(kThreads),
                     ExpandCfg<RP>::SMEM, st, "adapter expand", a);
 }
 template <int RP>
 int run_grad(const GradArgs& a, cudaStream_t st) {
-  int rc = launch_pdl(adapter_grad_kernel<RP>, dim3((unsigned)(a.pr[0].blocks + a.pr[1].blocks), (unsigned)a.ranges),
-                      dim3(kThreads), GradCfg<RP>::SMEM, st, "adapter gradient", a);
-  if (rc) return rc;
-  const int64_t most = (int64_t)a.R * std::max(a.pr[0].K, a.pr[1].K);
-  return launch_pdl(adapter_reduce_kernel, dim3((unsigned)std::min<int64_t>(cdiv(most, 1024), 512), (unsigned)a.g.n, 2), dim3(256), 0,
-                    st, "adapter gradient sums", a);
+  return launch_pdl(adapter_grad_kernel<RP>, dim3((unsigned)(a.pr[0].blocks + a.pr[1].blocks), (unsigned)a.ranges), dim3(kThreads),
+                    GradCfg<RP>::SMEM, st, "adapter gradient", a);
 }
 template <typename F>
 int by_rank(int rp, F&& f) {
@@ -1015,6 +1030,7 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
                         (int)H, (int)cdiv(H, 256)};
   d.pr[1] = GradProblem{static_cast<const uint16_t*>(dy), s.su, static_cast<uint16_t*>(dB), reinterpret_cast<float*>(ws + L.grad1), lddy,
                         (int)N, (int)cdiv(N, 256)};
+  e.sums = d;
   return by_rank(padded_rank(r), [&](auto k) {
     constexpr int RP = decltype(k)::value;
     int rc1 = run_shrink<RP>(s, sms, st);
