@@ -402,11 +402,11 @@ struct ExpandArgs {
   const int32_t* back;   // [T] token -> grouped row, negative: none
   float* u;              // [T, R] zeros for tokens without an adapter, or null
   int64_t ldb;
-  int N, R, per, shift, col_blocks;  // rows of a tile: 2^shift, at most kExpandRows
+  int N, R, col_blocks;
   Waits w;
   GradArgs sums;  // with ranges: partial sums to join
 };
-constexpr int kExpandRows = 128;
+constexpr int kExpandRows = 128;  // of a tile (64, which evens out short batches, leaves warps idle: 4096 x 4096, rank 16, 22 us instead of 17)
 
 template <int RP>
 struct ExpandCfg {
@@ -415,15 +415,14 @@ struct ExpandCfg {
   static constexpr int SMEM = 1024 + V + 2 * W + 8 * DEPTH * 2048;
 };
 
-// Tiles of 2^shift rows before each adapter's, first[0 .. n]; the number of all is returned.  All 256 threads call it.
-__device__ __forceinline__ int tile_table(const Groups& g, int shift, int* first, int* warp_sum) {
+// Tiles of kExpandRows rows before each adapter's, first[0 .. n]; the number of all is returned.  All 256 threads call it.
+__device__ __forceinline__ int tile_table(const Groups& g, int* first, int* warp_sum) {
   const int tid = threadIdx.x, lane = tid & 31, each = (g.n + kThreads - 1) / kThreads, a0 = tid * each;
-  const int round = (1 << shift) - 1;
   int mine = 0;
   for (int i = a0; i < a0 + each && i < g.n; ++i) {
     const int c = clamp_row(g.off[i + 1], g.T) - clamp_row(g.off[i], g.T);
     first[i] = mine;
-    mine += c > 0 ? (c + round) >> shift : 0;
+    mine += c > 0 ? (c + kExpandRows - 1) / kExpandRows : 0;
   }
   int sum = mine;
 #pragma unroll
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
       }
     }
   }
-  const int found = tile_table(p.g, p.shift, first, warp_sum), most = (p.g.T >> p.shift) + p.g.n;  // wrong offsets may name more
+  const int found = tile_table(p.g, first, warp_sum), most = p.g.T / kExpandRows + p.g.n;  // wrong offsets may name more
   const int64_t units = (int64_t)(found < most ? found : most) * p.col_blocks;
   int64_t unit = units * me / all;
   const int64_t end = units * (me + 1) / all;
@@ -520,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
       if (first[mid] <= tile) a = mid; else hi = mid;
     }
     const int o1 = clamp_row(p.g.off[a + 1], p.g.T);
-    const int64_t r0 = clamp_row(p.g.off[a], p.g.T) + ((int64_t)(tile - first[a]) << p.shift);
-    const int rows = (int)(o1 - r0 < p.per ? o1 - r0 : p.per);
+    const int64_t r0 = clamp_row(p.g.off[a], p.g.T) + (int64_t)(tile - first[a]) * kExpandRows;
+    const int rows = (int)(o1 - r0 < kExpandRows ? o1 - r0 : kExpandRows);
     __syncthreads();  // everyone is done with the last tile's
     if (tid < kExpandRows) tok[tid] = tid < rows ? token_of(p.g, (int)r0 + tid) : -1;
     const uint16_t* W = p.W + (int64_t)a * p.R * p.N + (int64_t)(tid >> 4) * p.N + 8 * (tid & 15);
@@ -822,9 +821,6 @@ int grad_ranges(int64_t T, int64_t H, int64_t N, int sms) {
   const int64_t wave = 2 * sms / (cdiv(H, 256) + cdiv(N, 256));
   return (int)std::max(cdiv(T, kMaxPer), std::min(wave, cdiv(T, 64)));
 }
-// tiles of `per` rows that T tokens of n adapters come to, about
-int64_t tiles_of(int64_t T, int64_t n, int64_t per) { return cdiv(T, per) + (std::min<int64_t>(n, T) - 1) / 2; }
-
 template <int RP, int SPLIT>
 int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
@@ -875,13 +871,9 @@ int run_shrink(ShrinkArgs a, int sms, cudaStream_t st) {
 }
 template <int RP>
 int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
-  // 128 tokens share W's columns; fewer where that leaves a CTA less than a few pieces of work to even out
   const int64_t wave = (RP <= 64 ? 2 : 1) * sms;
   a.col_blocks = (int)cdiv(a.N, 128);
-  a.shift = 7;
-  while (a.shift > 6 && tiles_of(a.g.T, a.g.n, 1 << a.shift) * a.col_blocks < 6 * wave) --a.shift;
-  a.per = 1 << a.shift;
-  int64_t most = std::max(slots_of(a.g.T, a.g.n, a.per) * a.col_blocks, cdiv(a.g.T, 8));
+  int64_t most = std::max(slots_of(a.g.T, a.g.n, kExpandRows) * a.col_blocks, cdiv(a.g.T, 8));
   if (a.sums.ranges) most = std::max(most, (int64_t)a.g.n * cdiv((int64_t)a.R * (a.sums.pr[0].K + a.sums.pr[1].K), 4096));
   return launch_pdl(adapter_expand_kernel<RP>, dim3((unsigned)std::min(wave, most)), dim3(kThreads),
                     ExpandCfg<RP>::SMEM, st, "adapter expand", a);
