@@ -6,13 +6,15 @@
 //
 // With both matrices stored as r feature rows, the forward and the backward are the same two kernels: adapter_shrink
 // contracts a token's features with r rows, adapter_expand adds r rows weighted by r numbers onto a token's row.
-// adapter_grad is the third.  Tokens are taken in route_meta's order (expert_offsets, x_gather_idx with K = 1), so that 64
-// tokens of one adapter share its matrices; tiles never mix adapters.
+// adapter_grad is the third; its partial sums are joined by the expand kernel, which the backward runs last.  Tokens are taken in
+// route_meta's order (expert_offsets, x_gather_idx with K = 1), so that the tokens of a tile share its adapter's matrices;
+// tiles never mix adapters.
 //
-// Bound: HBM (2 r operations a byte).  Products run on the warp-level matrix instruction (m16n8k16, bf16, fp32 sums): at r
-// = 64 its rate is far from the bound, its operands come straight from the tiles that asynchronous copies gather by token
-// index, and groups of one or two tokens (decoding) waste nothing but idle rows.
-// r numbers a token go between the kernels in fp32; they are rounded to bf16 as operands of the next product.
+// Bound: HBM (2 r operations a byte; 16384 x 4096 at rank 16: shrink 26 us, 5.2 TB/s, expand 47, 5.7 TB/s).  The products run on the
+// tensor core, one thread issuing them, so that the warps have nothing to do but copies and sums.
+// Operands are gathered by token index with 16-byte asynchronous copies, which write the swizzled operand layouts directly and
+// fill rows that are not there with zeros.  The r numbers of a token are summed in fp32 and rounded to bf16 as operands of the
+// next product (u stays fp32).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -161,15 +163,16 @@ struct ShrinkArgs {
   const float* u_in;   // [T, R] with su [T, RP], or null
   uint16_t* su;
   int64_t ld;
-  int K, R, per;  // rows of a tile, at most ShrinkCfg::ROWS
+  int K, R;
   Waits w;
 };
 
 // A tile of tokens by all r rows, its contraction split over a cluster whose partial tiles meet in distributed shared memory,
 // summed in rank order.  Stages of 64 features: asynchronous copies gather the tokens' 128-byte rows into the swizzled
-// K-major layout, one thread issues the tile's products (128 tokens x r), the accumulator stays in TMEM.  The form
-// whose warps multiplied from registers spent its time on operand loads and their latency (rank 64, 16384 x 4096: 38 us,
-// now %S64); a thread copies the same four rows' pieces in every stage, so that a copy costs two additions beside it.
+// K-major layout (128 features and 64 tokens at ranks up to 32), one thread issues the tile's products, the accumulator stays in
+// TMEM.  The form whose warps multiplied from registers spent its time on operand loads and their latency (rank 64,
+// 16384 x 4096: 38 us, now 33).  CTAs of a cluster take every SPLIT-th stage, not a contiguous part: they read a row's
+// neighbouring pieces together (30 us instead of 32 at rank 16).  A thread copies the same four rows' pieces in every stage, so that a copy costs two additions beside it.
 template <int RP>
 struct ShrinkCfg {
   static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PIECES = KC / 8;
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
   const uint32_t rank = SPLIT > 1 ? cluster_ctarank() : 0;
   Tile t;
   // the whole cluster works on one tile, so that all of it leaves here or none
-  if (!find_tile(p.g, blockIdx.x / SPLIT, p.per, t)) {
+  if (!find_tile(p.g, blockIdx.x / SPLIT, C::ROWS, t)) {
     pipe.end(tmem, C::TMEM);
     return;
   }
@@ -445,11 +448,11 @@ __device__ __forceinline__ int tile_table(const Groups& g, int* first, int* warp
 }
 
 // One wave of CTAs shares out the pieces of work (a tile of up to 128 tokens x 128 columns, a tile's pieces one behind
-// another) in equal, contiguous parts.  (A CTA a piece, 7 waves of them, started anew each time: 16384 x 4096, rank 16,
-// %E0 us, now %E1.)  The product of the next piece runs on the tensor core, tokens x columns into one half of the TMEM, while the warps
+// another) in equal, contiguous parts.  (A CTA a piece, 7 waves of them, started anew each time: the forward at
+// 16384 x 4096, rank 16, took 118 us, with equal parts 102.)  The product of the next piece runs on the tensor core, tokens x columns into one half of the TMEM, while the warps
 // add this one's to the base: the tile's v stays in shared memory (K-major), W's columns come in two buffers (MN-major), and
-// every warp has a few pieces of base on their way.  (Products from registers took as long as the memory beside them: rank 64
-// %M0 us, now %M1.)  The columns of W are permuted within 32 on their way to shared memory so that the four 8-column tiles of
+// every warp has a few pieces of base on their way.  (Products from registers took their time beside the memory's: rank 64
+// 62 us, now 53.)  The columns of W are permuted within 32 on their way to shared memory so that the four 8-column tiles of
 // a TMEM load give a thread 8 neighbouring columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a row.
 // What the kernel reads before pdl_wait, and the rows without an adapter that it writes there, belong to the caller: whatever wrote
 // or read them is complete before the shrink kernel lets this one start.
@@ -651,8 +654,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
 // All r rows by 256 features over a range of tokens, 32 of one adapter a stage, as features x r on the tensor core: x and v
 // are MN-major operands (a token's features are contiguous, the sum runs over tokens), gathered by asynchronous copies into the
 // swizzled layout, one thread issues the products, two accumulators of 128 features stay in TMEM until the adapter changes.
-// Equal ranges make a whole wave of CTAs: with tiles of one adapter's rows, which are uneven and do not fill the
-// waves, and products from registers 16384 x (4096 + 4096) at rank 64 took %G0 us, now %G1.
+// Equal ranges make one whole wave of CTAs whatever the adapters; tiles of one adapter's rows are uneven and do not fill
+// their waves (backward of 16384 x (4096 + 4096) at rank 64: 181 us, with ranges 164).  Now 53 us of which the copies alone take 43 (6.3
+// TB/s) and the partial sums at the end of the ranges 8.
 template <int RP>
 struct GradCfg {
   static constexpr int ROWS = 32, GROUP = ROWS * 128;  // 64 features (or ranks) of all tokens of a stage
@@ -825,7 +829,7 @@ template <int RP, int SPLIT>
 int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
   auto kern = adapter_shrink_kernel<RP, SPLIT>;
-  const dim3 grid((unsigned)(slots_of(a.g.T, a.g.n, a.per) * SPLIT));
+  const dim3 grid((unsigned)(slots_of(a.g.T, a.g.n, C::ROWS) * SPLIT));
   if constexpr (SPLIT == 1) {
     return launch_pdl(kern, grid, dim3(kThreads), C::SMEM, st, "adapter shrink", a);
   } else {
@@ -850,24 +854,15 @@ int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
     return cuda_check(cudaGetLastError(), "adapter shrink");
   }
 }
-// CTAs along the contraction and rows of a tile: one wave of two CTAs an SM, as full as can be (a tile of 128 rows by two CTAs
-// leaves 48 of 152 SMs with one: rank 64, 16384 x 4096 %P0 us, with 111 rows %P1), with as many rows as that allows, since
-// they share W.  Several waves where the tiles are too many for one.
+// CTAs along the contraction: as many as still make one wave of two CTAs an SM.  (Tiles of fewer rows that fill the wave to the
+// last SM, 111 instead of 128 at 16384 rows, measured the same, 33 us.)
 template <int RP>
-int run_shrink(ShrinkArgs a, int sms, cudaStream_t st) {
+int run_shrink(const ShrinkArgs& a, int sms, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
-  const int64_t T = a.g.T, n = std::min<int64_t>(a.g.n, T), chunks = cdiv(a.K, C::KC);
-  int split = 1;
-  a.per = C::ROWS;
-  for (int s = 8; s >= 1; s /= 2) {
-    const int64_t room = 2 * sms / s - n;  // T / per + n tiles at most
-    if (chunks < s || room <= 0 || cdiv(T, room) > C::ROWS) continue;
-    split = s;
-    a.per = (int)std::max<int64_t>(cdiv(T, room), C::ROWS / 2);
-    break;
-  }
-  return split == 8 ? launch_shrink<RP, 8>(a, st) : split == 4 ? launch_shrink<RP, 4>(a, st) : split == 2 ? launch_shrink<RP, 2>(a, st)
-                                                                                                          : launch_shrink<RP, 1>(a, st);
+  const int64_t tiles = a.g.T / C::ROWS + std::min<int64_t>(a.g.n, a.g.T), chunks = cdiv(a.K, C::KC);
+  const auto fits = [&](int s) { return tiles * s <= 2 * sms && chunks >= s; };
+  return fits(8) ? launch_shrink<RP, 8>(a, st) : fits(4) ? launch_shrink<RP, 4>(a, st) : fits(2) ? launch_shrink<RP, 2>(a, st)
+                                                                                              : launch_shrink<RP, 1>(a, st);
 }
 template <int RP>
 int run_expand(ExpandArgs a, int sms, cudaStream_t st) {
