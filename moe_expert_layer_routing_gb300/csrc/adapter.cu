@@ -13,8 +13,10 @@
 // Bound: HBM (2 r operations a byte; 16384 x 4096 at rank 16: shrink 26 us, 5.2 TB/s, expand 47, 5.7 TB/s).  The products run on the
 // tensor core, one thread issuing them, so that the warps have nothing to do but copies and sums.
 // Operands are gathered by token index with 16-byte asynchronous copies, which write the swizzled operand layouts directly and
-// fill rows that are not there with zeros.  The r numbers of a token are summed in fp32 and rounded to bf16 as operands of the
-// next product (u stays fp32).
+// fill rows that are not there with zeros.  The r numbers of a token are summed in fp32; as operands of the next products they are two
+// bf16 numbers each, the rounded value and what that leaves, together off by at most 2^-16.  Rounded to one they made
+// gradients of adapters with few rows err by nearly twice their own rounding; two cost nothing up to rank 32 and 4% at rank 64
+// (backward of 16384 x (4096 + 4096): 149 us, 142 with one).  u stays fp32.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -158,9 +160,9 @@ struct ShrinkArgs {
   const uint16_t* x;   // [T, K], row stride ld
   const uint16_t* W;   // [n, R, K]
   const float* scale;  // [n] or null
-  uint16_t* v;         // [T, RP]
+  uint16_t* v;         // [T, 2 RP]: rounded values, then what that leaves
   float* u;            // [T, R] or null
-  const float* u_in;   // [T, R] with su [T, RP], or null
+  const float* u_in;   // [T, R] with su [T, 2 RP], or null
   uint16_t* su;
   int64_t ld;
   int K, R;
@@ -178,12 +180,31 @@ struct ShrinkCfg {
   static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PIECES = KC / 8;
   static constexpr int X = ROWS * KC * 2, STAGE = X + RP * KC * 2;
   static constexpr int STAGES = RP <= 16 ? 5 : RP <= 64 ? 4 : 3;
-  static constexpr int TMEM = RP < 32 ? 32 : RP;
+  // Accumulators that the stages take turns with: the tensor core truncates its running sums, which shows in u (K 4096 at
+  // rank 16: off by 4.4e-6 of its norm with one, 4.8e-7 with eight).
+  static constexpr int ACCS = RP <= 32 ? 8 : 256 / RP, TMEM = ACCS * RP;
   static constexpr int PITCH = RP + 4;  // floats of a partial row: 16-byte pieces of 8 rows in 8 bank groups
   // a product reads 128 rows: with 64 the others are whatever lies behind them, and reach sums that nobody reads
-  static constexpr int SMEM = 1024 + STAGES * STAGE + (128 - ROWS) * 128;
+  static constexpr int NEED = 1024 + STAGES * STAGE + (128 - ROWS) * 128;
+  // Two CTAs may hold all of an SM's TMEM: their shared memory leaves no room for a CTA of another stream's cluster, which would
+  // wait for TMEM while this cluster's other CTAs wait for its partners'.
+  static constexpr int SMEM = TMEM > 128 && NEED < 108 * 1024 ? 108 * 1024 : NEED;
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "the partial tile overlays the stages");
 };
+
+// Four numbers as two bf16 each: rounded at p, what that leaves (0 for an infinity) RP further.
+template <int RP>
+__device__ __forceinline__ void store_split(uint16_t* p, const float (&y)[4]) {
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    hi[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+    const float h0 = __uint_as_float(hi[i] << 16), h1 = __uint_as_float(hi[i] & 0xFFFF0000u);
+    lo[i] = pack_bf16x2(fabsf(h0) <= 3.4e38f ? y[2 * i] - h0 : 0.f, fabsf(h1) <= 3.4e38f ? y[2 * i + 1] - h1 : 0.f);
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(p + RP) = make_uint2(lo[0], lo[1]);
+}
 
 template <int RP, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const ShrinkArgs p) {
@@ -252,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
       const uint32_t a0 = base + pipe.at * C::STAGE;
 #pragma unroll
       for (int kk = 0; kk < C::KC / 16; ++kk)
-        mma_bf16(tmem, kmajor_sw128_desc(a0 + (kk >> 2) * C::ROWS * 128 + (kk & 3) * 32),
-                 kmajor_sw128_desc(a0 + C::X + (kk >> 2) * RP * 128 + (kk & 3) * 32), idesc, (c > 0 || kk > 0) ? 1u : 0u);
+        mma_bf16(tmem + (uint32_t)(c % C::ACCS) * RP, kmajor_sw128_desc(a0 + (kk >> 2) * C::ROWS * 128 + (kk & 3) * 32),
+                 kmajor_sw128_desc(a0 + C::X + (kk >> 2) * RP * 128 + (kk & 3) * 32), idesc, (c >= C::ACCS || kk > 0) ? 1u : 0u);
       pipe.commit();
     }
     pipe.advance(p.w);  // the products of the step before are done with the stage refilled now
@@ -266,12 +287,19 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
   tc_fence_after();
   float* part = reinterpret_cast<float*>(smem);  // [rows][PITCH]
   for (int c = 16 * (warp >> 2); c < RP && 32 * (warp & 3) < C::ROWS; c += 32) {
-    uint32_t r[16];
-    tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, r);
-    tmem_ld_wait_regs<16>(r);
+    float f[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j] = 0.f;
+    for (int i = 0; i < C::ACCS && i < mine; ++i) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + i * RP + c, r);
+      tmem_ld_wait_regs<16>(r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] += __uint_as_float(r[j]);
+    }
     float* out = part + (32 * (warp & 3) + lane) * C::PITCH + c;
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(out + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+    for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
   }
   tc_fence_before();
   if (SPLIT > 1)
@@ -296,12 +324,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
       s.w += f[k].w;
     }
     const int tk = tok[row];
-    const int64_t o = (int64_t)(t.r0 + row) * RP + c;
+    const int64_t o = (int64_t)(t.r0 + row) * 2 * RP + c;
     const float w[4] = {s.x, s.y, s.z, s.w};
     float y[4];  // ranks behind r are zeros whatever x holds (0 times infinity)
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = c + j < p.R ? w[j] * scale : 0.f;
-    *reinterpret_cast<uint2*>(p.v + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    store_split<RP>(p.v + o, y);
     if (p.u && tk >= 0)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -310,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
       float z[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) z[j] = tk >= 0 && c + j < p.R ? p.u_in[(int64_t)tk * p.R + c + j] * scale : 0.f;
-      *reinterpret_cast<uint2*>(p.su + o) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+      store_split<RP>(p.su + o, z);
     }
   }
   __syncwarp();
@@ -322,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
 // ------------------------------------------------------------------------------------------
 struct GradProblem {
   const uint16_t* x;  // [T, K], row stride ld
-  const uint16_t* v;  // [T, RP] by grouped row
+  const uint16_t* v;  // [T, 2 RP] by grouped row
   uint16_t* dW;       // [n, R, K]
   float* part;        // [2 ranges, R, K]
   int64_t ld;
@@ -398,7 +426,7 @@ __device__ __forceinline__ void sum_partials(const GradArgs& p, int64_t me, int6
 // ------------------------------------------------------------------------------------------
 struct ExpandArgs {
   Groups g;
-  const uint16_t* v;     // [T, RP] by grouped row
+  const uint16_t* v;     // [T, 2 RP] by grouped row
   const uint16_t* W;     // [n, R, N]
   const uint16_t* base;  // [T, N], row stride ldb, or null
   uint16_t* out;         // [T, N] dense
@@ -413,8 +441,8 @@ constexpr int kExpandRows = 128;  // of a tile (64, which evens out short batche
 
 template <int RP>
 struct ExpandCfg {
-  static constexpr int DEPTH = RP == 128 ? 4 : 3;  // 16 tokens x 64 columns of base of a warp on their way, 2 KB each
-  static constexpr int V = 16384 * (RP <= 64 ? 1 : 2), W = RP * 256;
+  static constexpr int DEPTH = RP == 64 ? 2 : 3;  // 16 tokens x 64 columns of base of a warp on their way, 2 KB each (2: two CTAs fit)
+  static constexpr int V = 16384 * (RP <= 32 ? 1 : RP / 32), W = RP * 256;
   static constexpr int SMEM = 1024 + V + 2 * W + 8 * DEPTH * 2048;
 };
 
@@ -506,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
       tc_fence_after();
       const uint32_t w0 = bw + (issued & 1) * C::W;
 #pragma unroll
-      for (int kk = 0; kk < RP / 16; ++kk)
+      for (int kk = 0; kk < RP / 8; ++kk)  // v's two parts one behind the other along the sum, each with all of W
         mma_bf16(tmem + (issued & 1) * 128, kmajor_sw128_desc(bv + (kk >> 2) * 16384 + (kk & 3) * 32),
-                 mnmajor_sw128_desc(w0 + kk * 2048, RP * 128), idesc, kk > 0 ? 1u : 0u);
+                 mnmajor_sw128_desc(w0 + kk % (RP / 16) * 2048, RP * 128), idesc, kk > 0 ? 1u : 0u);
       mma_commit(&sh.done[issued & 1]);
     }
     ++issued;
@@ -578,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
       pdl_trigger();
       waited = true;
     }
-    for (int i = tid; i < rows * (RP / 8); i += kThreads) {  // rows behind them only reach sums that nobody reads
-      const int row = i / (RP / 8), c = i % (RP / 8);
-      cp_async_16(bv + (c >> 3) * 16384 + at<128>(row, c & 7), p.v + (r0 + row) * RP + 8 * c);
+    for (int i = tid; i < rows * (RP / 4); i += kThreads) {  // rows behind them only reach sums that nobody reads
+      const int row = i / (RP / 4), c = i % (RP / 4);
+      cp_async_16(bv + (c >> 3) * 16384 + at<128>(row, c & 7), p.v + (r0 + row) * 2 * RP + 8 * c);
     }
     cp_async_commit();
     cp_async_wait<0>();
@@ -655,14 +683,16 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
 // are MN-major operands (a token's features are contiguous, the sum runs over tokens), gathered by asynchronous copies into the
 // swizzled layout, one thread issues the products, two accumulators of 128 features stay in TMEM until the adapter changes.
 // Equal ranges make one whole wave of CTAs whatever the adapters; tiles of one adapter's rows are uneven and do not fill
-// their waves (backward of 16384 x (4096 + 4096) at rank 64: 181 us, with ranges 164).  Now 53 us of which the copies alone take 43 (6.3
-// TB/s) and the partial sums at the end of the ranges 8.
+// their waves (backward of 16384 x (4096 + 4096) at rank 64: 181 us, with ranges 164).  Now 56 us; the copies alone take 43, the
+// products 4 more, the partial sums at the end of the ranges 8.
 template <int RP>
 struct GradCfg {
   static constexpr int ROWS = 32, GROUP = ROWS * 128;  // 64 features (or ranks) of all tokens of a stage
-  static constexpr int X = 4 * GROUP, STAGE = X + (RP <= 64 ? 1 : 2) * GROUP;
-  static constexpr int STAGES = RP <= 64 ? 5 : 4;
-  static constexpr int TMEM = 2 * RP;
+  static constexpr int X = 4 * GROUP, STAGE = X + (RP <= 32 ? 1 : RP / 32) * GROUP;
+  static constexpr int STAGES = RP <= 32 ? 5 : RP <= 64 ? 4 : 3;
+  // v's rounded values and what they leave: columns of one product, joined at the end, or (rank 128) two products.  Twice the
+  // products took 8 us more of 57 at rank 64.
+  static constexpr int PARTS = RP <= 64 ? 2 : 1, N = PARTS * RP, TMEM = 2 * N;
   static constexpr int SMEM = 1024 + STAGES * STAGE;
 };
 struct Segment {
@@ -711,9 +741,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
   const uint16_t* xcol = q.x + (in ? n0 + 8 * lane : 0);
   const int64_t ld = q.ld;
   const uint32_t xd = base + (lane >> 3) * C::GROUP + at<128>(4 * warp, lane & 7);
-  constexpr int PIECES = RP / 8, VSTEP = kThreads / PIECES, VN = (C::ROWS + VSTEP - 1) / VSTEP;  // v rows of one pass, passes
+  constexpr int PIECES = RP / 4, VSTEP = kThreads / PIECES, VN = (C::ROWS + VSTEP - 1) / VSTEP;  // v rows of one pass, passes
   const int v0 = tid / PIECES, vc = tid % PIECES;
-  const uint16_t* vcol = q.v + (int64_t)v0 * RP + 8 * vc;
+  const uint16_t* vcol = q.v + (int64_t)v0 * 2 * RP + 8 * vc;
   const uint32_t vd = base + C::X + (vc >> 3) * C::GROUP + at<128>(v0, vc & 7);  // VSTEP is a multiple of 8
   auto load = [&](uint32_t st) {  // the next rows, at most 32 of one adapter
     const int count = put.end - put.r;
@@ -728,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
       const int row = v0 + i * VSTEP;
       if (VSTEP * (i + 1) <= C::ROWS || row < C::ROWS) {
         const bool ok = row < count;
-        cp_async_16_zfill(vd + i * VSTEP * 128 + st, vcol + (int64_t)(ok ? put.r + i * VSTEP : 0) * RP, ok ? 16u : 0u);
+        cp_async_16_zfill(vd + i * VSTEP * 128 + st, vcol + (int64_t)(ok ? put.r + i * VSTEP : 0) * 2 * RP, ok ? 16u : 0u);
       }
     }
     put.r += C::ROWS;
@@ -742,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
     if (put.r < hi) load(i * C::STAGE);
     cp_async_commit();
   }
-  constexpr uint32_t idesc = idesc_bf16(128, RP, 1, 1);
+  constexpr uint32_t idesc = idesc_bf16(128, C::N, 1, 1);
   bool more = false;  // the accumulators hold rows of this adapter
   while (get.r < hi) {
     cp_async_wait<C::STAGES - 2>();
@@ -755,8 +785,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
       for (int kk = 0; kk < C::ROWS / 16; ++kk)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          mma_bf16(tmem + h * RP, mnmajor_sw128_desc(a0 + h * 2 * C::GROUP + kk * 2048, C::GROUP),
-                   mnmajor_sw128_desc(a0 + C::X + kk * 2048, C::GROUP), idesc, (more || kk > 0) ? 1u : 0u);
+#pragma unroll
+          for (int part = 0; part < 2; part += C::PARTS)
+            mma_bf16(tmem + h * C::N, mnmajor_sw128_desc(a0 + h * 2 * C::GROUP + kk * 2048, C::GROUP),
+                     mnmajor_sw128_desc(a0 + C::X + part * (RP / 64) * C::GROUP + kk * 2048, C::GROUP), idesc,
+                     (more || kk > 0 || part > 0) ? 1u : 0u);
       pipe.commit();
     }
     more = true;
@@ -775,11 +808,20 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
     tc_fence_after();
     // lanes are features: 32 of them a row of the result
     const int h = warp >> 2, f = n0 + 128 * h + 32 * (warp & 3) + lane;
-    const uint32_t taddr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h * RP;
+    const uint32_t taddr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h * C::N;
     for (int m0 = 0; m0 < RP && m0 < p.R; m0 += 16) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(taddr + m0, r);
-      tmem_ld_wait_regs<16>(r);
+      if constexpr (C::PARTS == 2) {
+        uint32_t l[16];
+        tmem_ld_32x32b_x16(taddr + RP + m0, l);
+        tmem_ld_wait_regs<16>(r);
+        tmem_ld_wait_regs<16>(l);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(l[j]));
+      } else {
+        tmem_ld_wait_regs<16>(r);
+      }
       if (!whole) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -900,9 +942,9 @@ Layout layout(int64_t T, int64_t H, int64_t N, int64_t r, bool backward, int sms
     return at;
   };
   const int rp = padded_rank(r);
-  L.v = take((size_t)T * rp * 2);
+  L.v = take((size_t)T * rp * 4);
   if (backward) {
-    L.su = take((size_t)T * rp * 2);
+    L.su = take((size_t)T * rp * 4);
     const size_t places = 2 * (size_t)grad_ranges(T, H, N, sms);
     L.grad0 = take(places * r * H * 4);
     L.grad1 = take(places * r * N * 4);
