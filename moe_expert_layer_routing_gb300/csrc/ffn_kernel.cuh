@@ -44,6 +44,7 @@ struct FfnParams {
   int nprob;
   int glu, interleaved, save;
   const uint16_t* b1;     // kFfnGlu: [2I] or null
+  int width;              // kFfnDGlu: features of a tile that are wanted, 256, 128 or 64 (of the product's first columns)
   uint16_t* a_out;        // kFfnDGlu: a [T, I]
   float* db1_part;        // kFfnDGlu: [4 * 128-row tiles, 2I] column sums, or null
   int32_t* tile_counter;  // null: tiles in turn; else zero before the launch, dynamic claims
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
         const CUtensorMap* ma = &P.map[EPI == kFfnStore ? 3 * ti.p : 0];
         const CUtensorMap* mb = &P.map[EPI == kFfnStore ? 3 * ti.p + 1 : EPI == kFfnGlu ? 1 + (int)rank : 1];
         const int a_row = ti.mt * 128;
-        const int b_col = EPI == kFfnGlu && !P.interleaved ? ti.nt * 128 : ti.nt * 256 + 128 * (int)rank;
+        const int b_col = EPI == kFfnGlu && !P.interleaved ? ti.nt * 128 : ti.nt * (EPI == kFfnDGlu ? P.width : 256) + 128 * (int)rank;
         const int a_mn = EPI == kFfnStore ? pr.a_mn : 0;
         const int b_mn = EPI == kFfnDGlu ? 0 : pr.b_mn;
         bool ok = true;
@@ -427,9 +428,12 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
       const FfnProblem& pr = P.prob[ti.p];
       const int row0 = ti.mt * 128;
 
-      // kFfnDGlu: slab sl of this half is features f(sl) .. f(sl) + 63; the first is loaded while the tile is multiplied
+      // kFfnDGlu: slab sl of this half is features f(sl) .. f(sl) + 63; the first is loaded while the tile is multiplied.
+      // Tiles of 128 features are one slab a half, of 64 one of the first half.
+      const int half_col = EPI == kFfnDGlu && P.width < 256 ? half * 64 : half * 128, slabs = EPI == kFfnDGlu && P.width < 256 ? 1 : 2;
+      const bool idle = EPI == kFfnDGlu && half * 64 >= P.width;
       auto load_h = [&](int sl) {
-        const int f = ti.nt * 256 + half * 128 + sl * 64;
+        const int f = ti.nt * P.width + half_col + sl * 64;
         mbar_arrive_expect_tx(&hfull[half], 2 * C::BUF_BYTES);
         const int c = P.interleaved ? 2 * f : f;
         tma_load_2d(buf, &P.map[2], &hfull[half], c, row0);
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
         h_flying = true;
       };
       if constexpr (EPI == kFfnDGlu) {
-        if (elect) {
+        if (elect && !idle) {
           bulk_wait_read_all();
           load_h(0);
         }
@@ -616,8 +620,8 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
         const bool mine = row0 + m < pr.M;
         uint16_t* a_row = P.a_out + (int64_t)(row0 + m) * pr.N;
 #pragma unroll 1
-        for (int sl = 0; sl < 2; ++sl) {
-          const int f0 = ti.nt * 256 + half * 128 + sl * 64;
+        for (int sl = 0; sl < (idle ? 0 : slabs); ++sl) {
+          const int f0 = ti.nt * P.width + half_col + sl * 64;
           if (sl == 1 && elect) {
             bulk_wait_read_all();
             load_h(1);
@@ -635,9 +639,9 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           for (int c = 0; c < 2; ++c) {  // 16 features at a time
             const int k = sub * 32 + c * 16;
             uint32_t r[16];
-            tmem_ld_32x32b_x16(taddr + half * 128 + sl * 64 + k, r);
+            tmem_ld_32x32b_x16(taddr + half_col + sl * 64 + k, r);
             tmem_ld_wait_regs<16>(r);
-            if (sl == 1 && c == 1) release();
+            if (sl == slabs - 1 && c == 1) release();
 #pragma unroll
             for (int j = 0; j < 2; ++j) {  // 8 features: 16 bytes of gate and of up, or 32 interleaved
               const int f = f0 + k + 8 * j;
@@ -700,6 +704,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
           }
         }
         if (gone) break;
+        if (idle) release();
       }
       if (++acc == 2) {
         acc = 0;
