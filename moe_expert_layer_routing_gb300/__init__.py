@@ -458,6 +458,12 @@ def _dense(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_BF, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+# The calls below ask a tensor's properties in one expression and come to _rows and _dense, whose conditions these are, only
+# where it is false, for the message: the names and the call around every tensor cost as much as the questions.
 def _here(dev):
     """Handle of the current stream of the tensors' device, which has to be the current one.  What a call allocates
     belongs to that stream, so that nothing else is given its memory while the call may still use it; with a
@@ -465,9 +471,10 @@ def _here(dev):
     the caller's to order (Stream.wait_stream) and to keep."""
     if dev.type != "cuda":
         raise MoeError("tensors must be CUDA tensors (there is no CPU path)")
-    if dev.index != torch._C._cuda_getDevice():
+    index = dev.index
+    if index != _current_device():
         raise MoeError(f"tensors are on {dev}, which is not the current device")
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _raw_stream(index)
 
 
 try:  # the allocator's entry point without torch.empty's argument parsing (0.9 us instead of 1.6 us a tensor)
@@ -727,10 +734,20 @@ def ckpt8_unpack(ckpt_q: torch.Tensor, ckpt_sf: torch.Tensor, route_meta: dict, 
     return h
 
 
-def _ffn_sizes(x, W1, W2, what):
-    if x.dim() != 2 or W1.dim() != 2 or W2.dim() != 2 or W1.shape[1] % 2:
+def _ffn_args(x, W1, W2, what):
+    """T, H, I, the device and x's row stride."""
+    try:
+        (T, H), (_, I2) = x.shape, W1.shape
+    except ValueError:
+        I2 = 1
+    if I2 % 2 or W2.dim() != 2:
         raise MoeError(f"{what}: x must be [T, H], W1 [H, 2I], W2 [I, H]")
-    return x.shape[0], x.shape[1], W1.shape[1] // 2, x.device
+    I, dev = I2 // 2, x.device
+    ld, one = x.stride()
+    if not (x.dtype is _BF and (one == 1 or H <= 1) and W1.dtype is _BF and W1.shape == (H, I2) and W1.is_contiguous()
+            and W1.device == dev and W2.dtype is _BF and W2.shape == (I, H) and W2.is_contiguous() and W2.device == dev):
+        _rows(x, _BF, (T, H), "x", dev), _dense(W1, _BF, (H, I2), "W1", dev), _dense(W2, _BF, (I, H), "W2", dev)
+    return T, H, I, dev, ld if T > 1 else max(ld, H)
 
 
 def ffn_fwd(x, W1, W2, b1=None, b2=None, glu: int = GLU_SWIGLU, gate_up_layout: int = GATE_UP_CONCAT, save: bool = True,
@@ -742,21 +759,19 @@ def ffn_fwd(x, W1, W2, b1=None, b2=None, glu: int = GLU_SWIGLU, gate_up_layout: 
     if stream is not None:
         with torch.cuda.stream(stream):
             return ffn_fwd(x, W1, W2, b1, b2, glu, gate_up_layout, save, status)
-    T, H, I, dev = _ffn_sizes(x, W1, W2, "ffn_fwd")
-    bf = torch.bfloat16
-    ldx = _rows(x, bf, (T, H), "x", dev)
-    w1, w2 = _dense(W1, bf, (H, 2 * I), "W1", dev), _dense(W2, bf, (I, H), "W2", dev)
-    p1, p2 = _dense(b1, bf, (2 * I,), "b1", dev), _dense(b2, bf, (H,), "b2", dev)
-    sp = _dense(status, torch.int32, (1,), "status", dev)
+    T, H, I, dev, ldx = _ffn_args(x, W1, W2, "ffn_fwd")
+    p1 = None if b1 is None else _dense(b1, _BF, (2 * I,), "b1", dev)
+    p2 = None if b2 is None else _dense(b2, _BF, (H,), "b2", dev)
+    sp = None if status is None else _dense(status, _I32, (1,), "status", dev)
     st = _here(dev)
-    out = _new2(T, H, bf)
-    h = _new2(T, 2 * I, bf) if save else None
+    out = _empty_strided((T, H), (H, 1), _BF)
+    h = _empty_strided((T, 2 * I), (2 * I, 1), _BF) if save else None
     size = _ws_bytes("ffn_fwd_workspace_size", dev.index, T, H, I)
-    ws = _new1(size, torch.uint8)
-    rc = lib().ffn_fwd(x.data_ptr(), ldx, w1, p1, w2, p2, T, H, I, glu, gate_up_layout, None if h is None else h.data_ptr(),
-                       out.data_ptr(), sp, ws.data_ptr(), size, st)
+    ws = _empty_strided((size,), (1,), torch.uint8)
+    rc = lib().ffn_fwd(x.data_ptr(), ldx, W1.data_ptr(), p1, W2.data_ptr(), p2, T, H, I, glu, gate_up_layout,
+                       None if h is None else h.data_ptr(), out.data_ptr(), sp, ws.data_ptr(), size, st)
     _check(rc, "ffn_fwd")
-    return dict(out=out, h=h)
+    return {"out": out, "h": h}
 
 
 def ffn_bwd(dout, x, h, W1, W2, bias: bool = False, glu: int = GLU_SWIGLU, gate_up_layout: int = GATE_UP_CONCAT,
@@ -766,12 +781,11 @@ def ffn_bwd(dout, x, h, W1, W2, bias: bool = False, glu: int = GLU_SWIGLU, gate_
     if stream is not None:
         with torch.cuda.stream(stream):
             return ffn_bwd(dout, x, h, W1, W2, bias, glu, gate_up_layout, accumulate_into, status)
-    T, H, I, dev = _ffn_sizes(x, W1, W2, "ffn_bwd")
-    bf, f32 = torch.bfloat16, torch.float32
-    ldx, ldd = _rows(x, bf, (T, H), "x", dev), _rows(dout, bf, (T, H), "dout", dev)
+    T, H, I, dev, ldx = _ffn_args(x, W1, W2, "ffn_bwd")
+    bf, f32 = _BF, _F32
+    ldd = _rows(dout, bf, (T, H), "dout", dev)
     hp = _dense(h, bf, (T, 2 * I), "h", dev)
-    w1, w2 = _dense(W1, bf, (H, 2 * I), "W1", dev), _dense(W2, bf, (I, H), "W2", dev)
-    sp = _dense(status, torch.int32, (1,), "status", dev)
+    sp = None if status is None else _dense(status, _I32, (1,), "status", dev)
     st = _here(dev)
     dx = _new2(T, H, bf)
     if accumulate_into is not None:
@@ -785,12 +799,12 @@ def ffn_bwd(dout, x, h, W1, W2, bias: bool = False, glu: int = GLU_SWIGLU, gate_
         db1, db2 = (_new1(2 * I, f32), _new1(H, f32)) if bias else (None, None)
     size = _ws_bytes("ffn_bwd_workspace_size", dev.index, T, H, I, int(bias))
     ws = _new1(size, torch.uint8)
-    rc = lib().ffn_bwd(dout.data_ptr(), ldd, x.data_ptr(), ldx, hp, w1, w2, T, H, I, glu, gate_up_layout, dx.data_ptr(),
+    rc = lib().ffn_bwd(dout.data_ptr(), ldd, x.data_ptr(), ldx, hp, W1.data_ptr(), W2.data_ptr(), T, H, I, glu, gate_up_layout, dx.data_ptr(),
                        dW1.data_ptr(), dW2.data_ptr(), None if db1 is None else db1.data_ptr(),
                        None if db2 is None else db2.data_ptr(), int(accumulate_into is not None), sp, ws.data_ptr(), size,
                        st)
     _check(rc, "ffn_bwd")
-    return dict(dx=dx, dW1=dW1, dW2=dW2, db1=db1, db2=db2)
+    return {"dx": dx, "dW1": dW1, "dW2": dW2, "db1": db1, "db2": db2}
 
 
 def _dropout_args(x, seed, offset, what):
@@ -841,16 +855,24 @@ def dropout_bwd(dy, p: float, seed: int, offset=0, stream=None) -> torch.Tensor:
 
 
 def _adapter_args(x, A, B, route_meta, scale, what):
-    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
-        raise MoeError(f"{what}: x must be [T, H], A [n, r, H], B [n, r, N]")
-    (T, H), (n, r, N), dev = x.shape, B.shape, x.device
-    bf, i32 = torch.bfloat16, torch.int32
-    ldx = _rows(x, bf, (T, H), "x", dev)
-    p = (_dense(A, bf, (n, r, H), "A", dev), _dense(B, bf, (n, r, N), "B", dev), _dense(scale, torch.float32, (n,), "scale", dev))
-    m = (_dense(route_meta["expert_offsets"], i32, (n + 1,), "expert_offsets", dev),
-         _dense(route_meta["x_gather_idx"], i32, (T,), "x_gather_idx", dev),
-         _dense(route_meta["s_reverse_scatter_idx"], i32, (T,), "s_reverse_scatter_idx", dev))
-    return T, H, N, n, r, dev, ldx, p, m
+    """The sizes, the device, x's row stride, and the pointers of scale and of the metadata."""
+    try:
+        (T, H), (n, r, N) = x.shape, B.shape
+    except ValueError:
+        raise MoeError(f"{what}: x must be [T, H], A [n, r, H], B [n, r, N]") from None
+    dev = x.device
+    ld, one = x.stride()
+    off, idx, back = route_meta["expert_offsets"], route_meta["x_gather_idx"], route_meta["s_reverse_scatter_idx"]
+    if not (x.dtype is _BF and (one == 1 or H <= 1) and A.dtype is _BF and A.shape == (n, r, H) and A.is_contiguous()
+            and A.device == dev and B.dtype is _BF and B.is_contiguous() and B.device == dev
+            and off.dtype is _I32 and off.shape == (n + 1,) and off.is_contiguous() and off.device == dev
+            and idx.dtype is _I32 and idx.shape == (T,) and idx.is_contiguous() and idx.device == dev
+            and back.dtype is _I32 and back.shape == (T,) and back.is_contiguous() and back.device == dev):
+        _rows(x, _BF, (T, H), "x", dev), _dense(A, _BF, (n, r, H), "A", dev), _dense(B, _BF, (n, r, N), "B", dev)
+        _dense(off, _I32, (n + 1,), "expert_offsets", dev)
+        _dense(idx, _I32, (T,), "x_gather_idx", dev), _dense(back, _I32, (T,), "s_reverse_scatter_idx", dev)
+    return (T, H, N, n, r, dev, ld if T > 1 else max(ld, H), None if scale is None else _dense(scale, _F32, (n,), "scale", dev),
+            off.data_ptr(), idx.data_ptr(), back.data_ptr())
 
 
 def adapter_fwd(x, A, B, route_meta: dict, scale=None, base=None, out=None, save: bool = True, status=None,
@@ -863,19 +885,20 @@ def adapter_fwd(x, A, B, route_meta: dict, scale=None, base=None, out=None, save
     if stream is not None:
         with torch.cuda.stream(stream):
             return adapter_fwd(x, A, B, route_meta, scale, base, out, save, status)
-    T, H, N, n, r, dev, ldx, p, m = _adapter_args(x, A, B, route_meta, scale, "adapter_fwd")
-    ldb = 0 if base is None else _rows(base, x.dtype, (T, N), "base", dev)
-    yp = _dense(out, x.dtype, (T, N), "out", dev)
-    sp = _dense(status, torch.int32, (1,), "status", dev)
+    T, H, N, n, r, dev, ldx, cp, off, idx, back = _adapter_args(x, A, B, route_meta, scale, "adapter_fwd")
+    ldb = 0 if base is None else _rows(base, _BF, (T, N), "base", dev)
+    if out is not None:
+        _dense(out, _BF, (T, N), "out", dev)
+    sp = None if status is None else _dense(status, _I32, (1,), "status", dev)
     st = _here(dev)
-    y = _new2(T, N, x.dtype) if out is None else out
-    u = _new2(T, r, torch.float32) if save else None
+    y = _empty_strided((T, N), (N, 1), _BF) if out is None else out
+    u = _empty_strided((T, r), (r, 1), _F32) if save else None
     size = _ws_bytes("adapter_workspace_size", dev.index, T, H, N, n, r, 0)
-    ws = _new1(size, torch.uint8)
-    rc = lib().adapter_fwd(x.data_ptr(), ldx, *p, None if base is None else base.data_ptr(), ldb, *m, T, H, N, n, r,
-                           y.data_ptr() if yp is None else yp, None if u is None else u.data_ptr(), sp, ws.data_ptr(), size, st)
+    ws = _empty_strided((size,), (1,), torch.uint8)
+    rc = lib().adapter_fwd(x.data_ptr(), ldx, A.data_ptr(), B.data_ptr(), cp, None if base is None else base.data_ptr(), ldb, off,
+                           idx, back, T, H, N, n, r, y.data_ptr(), None if u is None else u.data_ptr(), sp, ws.data_ptr(), size, st)
     _check(rc, "adapter_fwd")
-    return dict(y=y, u=u)
+    return {"y": y, "u": u}
 
 
 def adapter_bwd(dy, x, u, A, B, route_meta: dict, scale=None, base=None, out=None, accumulate_into=None, status=None,
@@ -886,28 +909,28 @@ def adapter_bwd(dy, x, u, A, B, route_meta: dict, scale=None, base=None, out=Non
     if stream is not None:
         with torch.cuda.stream(stream):
             return adapter_bwd(dy, x, u, A, B, route_meta, scale, base, out, accumulate_into, status)
-    T, H, N, n, r, dev, ldx, p, m = _adapter_args(x, A, B, route_meta, scale, "adapter_bwd")
-    bf = torch.bfloat16
-    ldd = _rows(dy, bf, (T, N), "dy", dev)
-    up = _dense(u, torch.float32, (T, r), "u", dev)
-    ldb = 0 if base is None else _rows(base, bf, (T, H), "base", dev)
-    op = _dense(out, bf, (T, H), "out", dev)
-    sp = _dense(status, torch.int32, (1,), "status", dev)
+    T, H, N, n, r, dev, ldx, cp, off, idx, back = _adapter_args(x, A, B, route_meta, scale, "adapter_bwd")
+    ldd = _rows(dy, _BF, (T, N), "dy", dev)
+    up = _dense(u, _F32, (T, r), "u", dev)
+    ldb = 0 if base is None else _rows(base, _BF, (T, H), "base", dev)
+    if out is not None:
+        _dense(out, _BF, (T, H), "out", dev)
+    sp = None if status is None else _dense(status, _I32, (1,), "status", dev)
     st = _here(dev)
-    dx = _new2(T, H, bf) if out is None else out
+    dx = _empty_strided((T, H), (H, 1), _BF) if out is None else out
     if accumulate_into is not None:
         dA, dB = accumulate_into["dA"], accumulate_into["dB"]
-        _dense(dA, bf, (n, r, H), "dA", dev), _dense(dB, bf, (n, r, N), "dB", dev)
+        _dense(dA, _BF, (n, r, H), "dA", dev), _dense(dB, _BF, (n, r, N), "dB", dev)
     else:
-        dA = _empty_strided((n, r, H), (r * H, H, 1), bf)
-        dB = _empty_strided((n, r, N), (r * N, N, 1), bf)
+        dA = _empty_strided((n, r, H), (r * H, H, 1), _BF)
+        dB = _empty_strided((n, r, N), (r * N, N, 1), _BF)
     size = _ws_bytes("adapter_workspace_size", dev.index, T, H, N, n, r, 1)
-    ws = _new1(size, torch.uint8)
-    rc = lib().adapter_bwd(dy.data_ptr(), ldd, x.data_ptr(), ldx, up, *p, None if base is None else base.data_ptr(), ldb, *m, T, H,
-                           N, n, r, dx.data_ptr() if op is None else op, dA.data_ptr(), dB.data_ptr(),
-                           int(accumulate_into is not None), sp, ws.data_ptr(), size, st)
+    ws = _empty_strided((size,), (1,), torch.uint8)
+    rc = lib().adapter_bwd(dy.data_ptr(), ldd, x.data_ptr(), ldx, up, A.data_ptr(), B.data_ptr(), cp,
+                           None if base is None else base.data_ptr(), ldb, off, idx, back, T, H, N, n, r, dx.data_ptr(), dA.data_ptr(),
+                           dB.data_ptr(), int(accumulate_into is not None), sp, ws.data_ptr(), size, st)
     _check(rc, "adapter_bwd")
-    return dict(dx=dx, dA=dA, dB=dB)
+    return {"dx": dx, "dA": dA, "dB": dB}
 
 
 class LinearBwd:
