@@ -563,9 +563,9 @@ int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const 
 /* Gradients of adapter_fwd, u being its:
  *   v_t = scale_a B_a dy_t,  dx_t = base_t + A_a^T v_t,  dA_a = sum_t v_t x_t^T,  dB_a = sum_t scale_a u_t dy_t^T
  * base (device, nullable: zeros) bf16 [T,H]: the shared projection's own gradient (linear_bwd's dX); dx may be base itself
- * when that is dense (the gradient of the forward's base is dy).  dx [T,H], dA [n,r,H], dB [n,r,N] (device) bf16 dense; adapters without a token get zeros.
- * v and scale_a u enter the products as two bf16 numbers, results are rounded once.  accumulate = 1 adds to dA and dB (one rounding).  T = 0: dA
- * and dB are zeroed, or left as they are with accumulate. */
+ * when that is dense (the gradient of the forward's base is dy).  dx [T,H], dA [n,r,H], dB [n,r,N] (device) bf16 dense;
+ * adapters without a token get zeros.  v and scale_a u enter the products as two bf16 numbers, results are rounded once.
+ * accumulate = 1 adds to dA and dB (one rounding).  T = 0: dA and dB are zeroed, or left as they are with accumulate. */
 int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* u, const void* A, const void* B,
                 const float* scale, const void* base, int64_t ldbase, const int32_t* expert_offsets, const int32_t* x_gather_idx,
                 const int32_t* s_reverse_scatter_idx, int64_t T, int64_t H, int64_t N, int64_t n, int64_t r, void* dx, void* dA,

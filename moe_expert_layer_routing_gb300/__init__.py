@@ -799,8 +799,8 @@ def ffn_bwd(dout, x, h, W1, W2, bias: bool = False, glu: int = GLU_SWIGLU, gate_
         db1, db2 = (_new1(2 * I, f32), _new1(H, f32)) if bias else (None, None)
     size = _ws_bytes("ffn_bwd_workspace_size", dev.index, T, H, I, int(bias))
     ws = _new1(size, torch.uint8)
-    rc = lib().ffn_bwd(dout.data_ptr(), ldd, x.data_ptr(), ldx, hp, W1.data_ptr(), W2.data_ptr(), T, H, I, glu, gate_up_layout, dx.data_ptr(),
-                       dW1.data_ptr(), dW2.data_ptr(), None if db1 is None else db1.data_ptr(),
+    rc = lib().ffn_bwd(dout.data_ptr(), ldd, x.data_ptr(), ldx, hp, W1.data_ptr(), W2.data_ptr(), T, H, I, glu, gate_up_layout,
+                       dx.data_ptr(), dW1.data_ptr(), dW2.data_ptr(), None if db1 is None else db1.data_ptr(),
                        None if db2 is None else db2.data_ptr(), int(accumulate_into is not None), sp, ws.data_ptr(), size,
                        st)
     _check(rc, "ffn_bwd")

@@ -10,13 +10,13 @@
 // route_meta's order (expert_offsets, x_gather_idx with K = 1), so that the tokens of a tile share its adapter's matrices;
 // tiles never mix adapters.
 //
-// Bound: HBM (2 r operations a byte; 16384 x 4096 at rank 16: shrink 26 us, 5.2 TB/s, expand 47, 5.7 TB/s).  The products run on the
-// tensor core, one thread issuing them, so that the warps have nothing to do but copies and sums.
-// Operands are gathered by token index with 16-byte asynchronous copies, which write the swizzled operand layouts directly and
-// fill rows that are not there with zeros.  The r numbers of a token are summed in fp32; as operands of the next products they are two
+// Bound: HBM (2 r operations a byte; 16384 x 4096 at rank 16: shrink 26 us, 5.2 TB/s, expand 47, 5.7 TB/s).  The products run
+// on the tensor core, one thread issuing them, so that the warps have nothing to do but copies and sums. Operands are
+// gathered by token index with 16-byte asynchronous copies, which write the swizzled operand layouts directly and fill rows
+// that are not there with zeros.  The r numbers of a token are summed in fp32; as operands of the next products they are two
 // bf16 numbers each, the rounded value and what that leaves, together off by at most 2^-16.  Rounded to one they made
-// gradients of adapters with few rows err by nearly twice their own rounding; two cost nothing up to rank 32 and 4% at rank 64
-// (backward of 16384 x (4096 + 4096): 149 us, 142 with one).  u stays fp32.
+// gradients of adapters with few rows err by nearly twice their own rounding; two cost nothing up to rank 32 and 4% at rank
+// 64 (backward of 16384 x (4096 + 4096): 149 us, 142 with one).  u stays fp32.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,7 +39,7 @@ struct Groups {
 __device__ __forceinline__ int clamp_row(int v, int T) { return v < 0 ? 0 : v > T ? T : v; }
 
 struct Tile {
-  int a, r0, rows, index, count;  // adapter, first grouped row, rows, tile of the adapter, its rows in all
+  int a, r0, rows;  // adapter, first grouped row, rows
 };
 
 // Tiles of `per` rows: adapter a's begin at slot off[a] / per + a, which leaves room for all of them whatever the counts, so
@@ -54,9 +54,7 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int slot, int per, Ti
   if (at == 0) return false;
   t.a = at - 1;
   const int o0 = clamp_row(g.off[t.a], g.T), o1 = clamp_row(g.off[at], g.T);
-  t.index = slot - (o0 / per + t.a);
-  t.count = o1 - o0;
-  const int64_t r0 = o0 + (int64_t)t.index * per;
+  const int64_t r0 = o0 + (int64_t)(slot - (o0 / per + t.a)) * per;
   if (r0 >= o1) return false;
   t.r0 = (int)r0;
   t.rows = o1 - t.r0 < per ? o1 - t.r0 : per;
@@ -171,10 +169,11 @@ struct ShrinkArgs {
 
 // A tile of tokens by all r rows, its contraction split over a cluster whose partial tiles meet in distributed shared memory,
 // summed in rank order.  Stages of 64 features: asynchronous copies gather the tokens' 128-byte rows into the swizzled
-// K-major layout (128 features and 64 tokens at ranks up to 32), one thread issues the tile's products, the accumulator stays in
-// TMEM.  The form whose warps multiplied from registers spent its time on operand loads and their latency (rank 64,
-// 16384 x 4096: 38 us, now 33).  CTAs of a cluster take every SPLIT-th stage, not a contiguous part: they read a row's
-// neighbouring pieces together (30 us instead of 32 at rank 16).  A thread copies the same four rows' pieces in every stage, so that a copy costs two additions beside it.
+// K-major layout (128 features and 64 tokens at ranks up to 32), one thread issues the tile's products, the accumulator stays
+// in TMEM.  The form whose warps multiplied from registers spent its time on operand loads and their latency (rank 64, 16384
+// x 4096: 38 us, now 33).  CTAs of a cluster take every SPLIT-th stage, not a contiguous part: they read a row's neighbouring
+// pieces together (30 us instead of 32 at rank 16).  A thread copies the same four rows' pieces in every stage, so that a
+// copy costs two additions beside it.
 template <int RP>
 struct ShrinkCfg {
   static constexpr int ROWS = RP <= 32 ? 64 : 128, KC = RP <= 32 ? 128 : 64, PIECES = KC / 8;
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
   if (tid < C::ROWS) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
   __syncthreads();
   const int chunks = (p.K + C::KC - 1) / C::KC;
-  const int mine = (chunks - (int)rank + SPLIT - 1) / SPLIT;  // chunks rank, rank + SPLIT, ...: the cluster reads a row's neighbours together
+  const int mine = (chunks - (int)rank + SPLIT - 1) / SPLIT;  // chunks rank, rank + SPLIT, ...
   const uint32_t base = smem_u32(smem);
   const int pc = tid % C::PIECES, r0 = tid / C::PIECES;
   constexpr int STEP = kThreads / C::PIECES, XN = C::ROWS / STEP;  // rows of one pass of copies, passes over x's
@@ -240,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
     const int row = r0 + STEP * i, tk = tok[row];
     xs[i] = p.x + (int64_t)(tk < 0 ? 0 : tk) * p.ld + 8 * pc + (int64_t)rank * C::KC;
     xb[i] = tk < 0 ? 0u : 16u;
-    xd[i] = row < t.rows ? base + (pc >> 3) * C::ROWS * 128 + at<128>(row, pc & 7) : 0u;  // other rows only reach their own sums, which nobody reads
+    // other rows only reach their own sums, which nobody reads
+    xd[i] = row < t.rows ? base + (pc >> 3) * C::ROWS * 128 + at<128>(row, pc & 7) : 0u;
   }
   const uint16_t* wsrc = p.W + ((int64_t)t.a * p.R + r0) * p.K + 8 * pc + (int64_t)rank * C::KC;
   auto load = [&](int c, uint32_t st) {
@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
       const int row = r0 + STEP * i;
       if (RP % STEP == 0 || row < RP) {
         const bool ok = row < p.R && in;
-        cp_async_16_zfill(base + st + C::X + (pc >> 3) * RP * 128 + at<128>(row, pc & 7), ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
+        cp_async_16_zfill(base + st + C::X + (pc >> 3) * RP * 128 + at<128>(row, pc & 7),
+                          ok ? wsrc + (int64_t)STEP * i * p.K + o : p.W, ok ? 16u : 0u);
       }
     }
   };
@@ -476,14 +477,15 @@ __device__ __forceinline__ int tile_table(const Groups& g, int* first, int* warp
 }
 
 // One wave of CTAs shares out the pieces of work (a tile of up to 128 tokens x 128 columns, a tile's pieces one behind
-// another) in equal, contiguous parts.  (A CTA a piece, 7 waves of them, started anew each time: the forward at
-// 16384 x 4096, rank 16, took 118 us, with equal parts 102.)  The product of the next piece runs on the tensor core, tokens x columns into one half of the TMEM, while the warps
-// add this one's to the base: the tile's v stays in shared memory (K-major), W's columns come in two buffers (MN-major), and
-// every warp has a few pieces of base on their way.  (Products from registers took their time beside the memory's: rank 64
-// 62 us, now 53.)  The columns of W are permuted within 32 on their way to shared memory so that the four 8-column tiles of
-// a TMEM load give a thread 8 neighbouring columns: base and out move in 16-byte pieces, four lanes to 64 bytes of a row.
-// What the kernel reads before pdl_wait, and the rows without an adapter that it writes there, belong to the caller: whatever wrote
-// or read them is complete before the shrink kernel lets this one start.
+// another) in equal, contiguous parts.  (A CTA a piece, 7 waves of them, started anew each time: the forward at 16384 x 4096,
+// rank 16, took 118 us, with equal parts 102.)  The product of the next piece runs on the tensor core, tokens x columns into
+// one half of the TMEM, while the warps add this one's to the base: the tile's v stays in shared memory (K-major), W's
+// columns come in two buffers (MN-major), and every warp has a few pieces of base on their way.  (Products from registers
+// took their time beside the memory's: rank 64 62 us, now 53.)  The columns of W are permuted within 32 on their way to
+// shared memory so that the four 8-column tiles of a TMEM load give a thread 8 neighbouring columns: base and out move in
+// 16-byte pieces, four lanes to 64 bytes of a row.
+// What the kernel reads before pdl_wait, and the rows without an adapter that it writes there, belong to the caller: whatever
+// wrote or read them is complete before the kernel in front lets this one start (and that kernel leaves them alone).
 template <int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_kernel(const ExpandArgs p) {
   using C = ExpandCfg<RP>;
@@ -571,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
         // columns 8 pc + 2 j, + 1 of group pc / 4 of 32: columns 2 (pc % 4), + 1 of that group's tile j
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint32_t*>(smem + C::V + buffer * C::W + (pc >> 3) * RP * 128 + at<128>(row, (pc & 4) + j) + 4 * (pc & 3)) = ww[j];
+          *reinterpret_cast<uint32_t*>(smem + C::V + buffer * C::W + (pc >> 3) * RP * 128 + at<128>(row, (pc & 4) + j) +
+                                       4 * (pc & 3)) = ww[j];
       }
     };
     // the warp's 16 tokens x 64 columns in order: (block, m); this thread's 64 bytes of them go to its own slot
