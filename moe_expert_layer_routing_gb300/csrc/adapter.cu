@@ -42,24 +42,50 @@ struct Tile {
   int a, r0, rows;  // adapter, first grouped row, rows
 };
 
-// Tiles of `per` rows: adapter a's begin at slot off[a] / per + a, which leaves room for all of them whatever the counts, so
-// that no prefix sum is needed: at most T / per + n slots, and a slot's adapter is the last one that begins at or before
-// it.  Offsets are clamped to [0, T]: bad ones give wrong tiles, never rows outside.  All threads call it.
-__device__ __forceinline__ bool find_tile(const Groups& g, int slot, int per, Tile& t) {
-  int at = 0;
-  for (int i0 = 0; i0 < g.n; i0 += blockDim.x) {
-    const int i = i0 + (int)threadIdx.x;
-    at += __syncthreads_count(i < g.n && clamp_row(g.off[i < g.n ? i : 0], g.T) / per + i <= slot);
+// Tiles of ROWS rows before each adapter's, first[0 .. n]; the number of all is returned, at most T / ROWS + min(n, T): wrong offsets
+// may name more.  All 256 threads call it.
+template <int ROWS>
+__device__ __forceinline__ int tile_table(const Groups& g, int* first, int* warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, each = (g.n + kThreads - 1) / kThreads, a0 = tid * each;
+  int mine = 0;
+  for (int i = a0; i < a0 + each && i < g.n; ++i) {
+    const int c = clamp_row(g.off[i + 1], g.T) - clamp_row(g.off[i], g.T);
+    first[i] = mine;
+    mine += c > 0 ? (c + ROWS - 1) / ROWS : 0;
   }
-  if (at == 0) return false;
-  t.a = at - 1;
-  const int o0 = clamp_row(g.off[t.a], g.T), o1 = clamp_row(g.off[at], g.T);
-  const int64_t r0 = o0 + (int64_t)(slot - (o0 / per + t.a)) * per;
-  if (r0 >= o1) return false;
-  t.r0 = (int)r0;
-  t.rows = o1 - t.r0 < per ? o1 - t.r0 : per;
-  return true;
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) warp_sum[tid >> 5] = sum;
+  __syncthreads();
+  int before = sum - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < (tid >> 5)) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  for (int i = a0; i < a0 + each && i < g.n; ++i) first[i] += before;
+  if (tid == 0) first[g.n] = all;
+  __syncthreads();
+  const int most = g.T / ROWS + (g.n < g.T ? g.n : g.T);
+  return all < most ? all : most;
 }
+// A tile by its number.
+template <int ROWS>
+__device__ __forceinline__ Tile tile_of(const Groups& g, const int* first, int number) {
+  int a = 0;  // the last adapter whose first tile is at or before this one
+  for (int hi = g.n; hi - a > 1;) {
+    const int mid = (a + hi) >> 1;
+    if (first[mid] <= number) a = mid; else hi = mid;
+  }
+  const int64_t r0 = clamp_row(g.off[a], g.T) + (int64_t)(number - first[a]) * ROWS;
+  const int left = (int)(clamp_row(g.off[a + 1], g.T) - r0);
+  return Tile{a, (int)r0, left < ROWS ? left : ROWS};
+}
+
 
 // Token of a grouped row, -1 where the metadata names none.
 __device__ __forceinline__ int token_of(const Groups& g, int row) {
@@ -217,12 +243,15 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(const Shrin
   pdl_wait();
   pdl_trigger();  // after the allocation: the next kernel cannot take the TMEM that this one is still to get
   const uint32_t rank = SPLIT > 1 ? cluster_ctarank() : 0;
-  Tile t;
-  // the whole cluster works on one tile, so that all of it leaves here or none
-  if (!find_tile(p.g, blockIdx.x / SPLIT, C::ROWS, t)) {
+  // the table lies where the first stage will; the whole cluster works on one tile, so that all of it leaves here or none
+  __shared__ int warp_sum[kThreads / 32];
+  int* first = reinterpret_cast<int*>(smem);
+  static_assert(C::STAGE >= (kMaxExperts + 1) * 4, "the table fits a stage");
+  if ((int)blockIdx.x / SPLIT >= tile_table<C::ROWS>(p.g, first, warp_sum)) {
     pipe.end(tmem, C::TMEM);
     return;
   }
+  const Tile t = tile_of<C::ROWS>(p.g, first, blockIdx.x / SPLIT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < C::ROWS) tok[tid] = tid < t.rows ? token_of(p.g, t.r0 + tid) : -1;
   __syncthreads();
@@ -447,35 +476,6 @@ struct ExpandCfg {
   static constexpr int SMEM = 1024 + V + 2 * W + 8 * DEPTH * 2048;
 };
 
-// Tiles of kExpandRows rows before each adapter's, first[0 .. n]; the number of all is returned.  All 256 threads call it.
-__device__ __forceinline__ int tile_table(const Groups& g, int* first, int* warp_sum) {
-  const int tid = threadIdx.x, lane = tid & 31, each = (g.n + kThreads - 1) / kThreads, a0 = tid * each;
-  int mine = 0;
-  for (int i = a0; i < a0 + each && i < g.n; ++i) {
-    const int c = clamp_row(g.off[i + 1], g.T) - clamp_row(g.off[i], g.T);
-    first[i] = mine;
-    mine += c > 0 ? (c + kExpandRows - 1) / kExpandRows : 0;
-  }
-  int sum = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-    if (lane >= o) sum += y;
-  }
-  if (lane == 31) warp_sum[tid >> 5] = sum;
-  __syncthreads();
-  int before = sum - mine, all = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < (tid >> 5)) before += warp_sum[w];
-    all += warp_sum[w];
-  }
-  for (int i = a0; i < a0 + each && i < g.n; ++i) first[i] += before;
-  if (tid == 0) first[g.n] = all;
-  __syncthreads();
-  return all;
-}
-
 // One wave of CTAs shares out the pieces of work (a tile of up to 128 tokens x 128 columns, a tile's pieces one behind
 // another) in equal, contiguous parts.  (A CTA a piece, 7 waves of them, started anew each time: the forward at 16384 x 4096,
 // rank 16, took 118 us, with equal parts 102.)  The product of the next piece runs on the tensor core, tokens x columns into
@@ -517,8 +517,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
       }
     }
   }
-  const int found = tile_table(p.g, first, warp_sum), most = p.g.T / kExpandRows + p.g.n;  // wrong offsets may name more
-  const int64_t units = (int64_t)(found < most ? found : most) * p.col_blocks;
+  const int64_t units = (int64_t)tile_table<kExpandRows>(p.g, first, warp_sum) * p.col_blocks;
   int64_t unit = units * me / all;
   const int64_t end = units * (me + 1) / all;
   const uint32_t bv = smem_u32(smem), bw = bv + C::V;
@@ -546,14 +545,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) adapter_expand_ker
   };
   int tile = (int)(unit / p.col_blocks), cb = (int)(unit - (int64_t)tile * p.col_blocks);
   for (; unit < end && !stop; ++tile, cb = 0) {
-    int a = 0;  // the last adapter whose first tile is at or before this one
-    for (int hi = p.g.n; hi - a > 1;) {
-      const int mid = (a + hi) >> 1;
-      if (first[mid] <= tile) a = mid; else hi = mid;
-    }
-    const int o1 = clamp_row(p.g.off[a + 1], p.g.T);
-    const int64_t r0 = clamp_row(p.g.off[a], p.g.T) + (int64_t)(tile - first[a]) * kExpandRows;
-    const int rows = (int)(o1 - r0 < kExpandRows ? o1 - r0 : kExpandRows);
+    const Tile t = tile_of<kExpandRows>(p.g, first, tile);
+    const int a = t.a, rows = t.rows;
+    const int64_t r0 = t.r0;
     __syncthreads();  // everyone is done with the last tile's
     if (tid < kExpandRows) tok[tid] = tid < rows ? token_of(p.g, (int)r0 + tid) : -1;
     const uint16_t* W = p.W + (int64_t)a * p.R * p.N + (int64_t)(tid >> 4) * p.N + 8 * (tid & 15);
@@ -863,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_grad_kernel(const GradArg
 // ------------------------------------------------------------------------------------------
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int padded_rank(int64_t r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
-int64_t slots_of(int64_t T, int64_t n, int64_t per) { return T / per + n; }
+int64_t slots_of(int64_t T, int64_t n, int64_t per) { return T / per + std::min(n, T); }  // tiles at most
 
 // Parts of the rows in the gradient: one wave of CTAs, but 64 rows a part at least and kMaxPer at most.
 int grad_ranges(int64_t T, int64_t H, int64_t N, int sms) {
@@ -904,7 +898,7 @@ int launch_shrink(const ShrinkArgs& a, cudaStream_t st) {
 template <int RP>
 int run_shrink(const ShrinkArgs& a, int sms, cudaStream_t st) {
   using C = ShrinkCfg<RP>;
-  const int64_t tiles = a.g.T / C::ROWS + std::min<int64_t>(a.g.n, a.g.T), chunks = cdiv(a.K, C::KC);
+  const int64_t tiles = slots_of(a.g.T, a.g.n, C::ROWS), chunks = cdiv(a.K, C::KC);
   const auto fits = [&](int s) { return tiles * s <= 2 * sms && chunks >= s; };
   return fits(8) ? launch_shrink<RP, 8>(a, st) : fits(4) ? launch_shrink<RP, 4>(a, st) : fits(2) ? launch_shrink<RP, 2>(a, st)
                                                                                               : launch_shrink<RP, 1>(a, st);
