@@ -361,3 +361,48 @@ def test_status_refusals():
             mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], status=bad)
         with pytest.raises(mb.MoeError):
             mb.adapter_bwd(d["dy"], d["x"], u, d["A"], d["B"], d["meta"], status=bad)
+
+
+@pytest.mark.parametrize("what", ["falling", "negative", "beyond", "all one", "indices", "none"])
+def test_wrong_metadata_stays_inside(what):
+    """Offsets that fall, leave [0, T] or never end, indices outside: wrong rows, but nothing beside the results is written."""
+    mb = _mb()
+    T, H, N, n, r = 150, 136, 264, 6, 20
+    d = _inputs(T, H, N, n, r)
+    off = d["meta"]["expert_offsets"].clone()
+    idx, back = d["meta"]["x_gather_idx"].clone(), d["meta"]["s_reverse_scatter_idx"].clone()
+    if what == "falling":
+        off = off.flip(0).contiguous()
+    elif what == "negative":
+        off[1:4] = torch.tensor([-5, -2 ** 31, 40], dtype=torch.int32)
+    elif what == "beyond":
+        off[2:] = torch.tensor([10, 2 ** 31 - 1, 149, 3000, 2 ** 30], dtype=torch.int32)
+    elif what == "all one":
+        off[:] = torch.tensor([0, T, 0, T, 0, T, 0], dtype=torch.int32)
+    elif what == "indices":
+        idx[::3], idx[1::7], back[::5] = 2 ** 31 - 1, -2 ** 31, 10 ** 6
+    else:
+        off.zero_()
+    meta = dict(expert_offsets=off, x_gather_idx=idx, s_reverse_scatter_idx=back)
+    pad = 4096
+    ybuf, xbuf = (torch.full((T * c + 2 * pad,), 7.0, dtype=torch.bfloat16, device="cuda") for c in (N, H))
+    y, dx = ybuf[pad:-pad].view(T, N), xbuf[pad:-pad].view(T, H)
+    f = mb.adapter_fwd(d["x"], d["A"], d["B"], meta, scale=d["scale"], base=d["base"], out=y)
+    mb.adapter_bwd(d["dy"], d["x"], torch.zeros_like(f["u"]), d["A"], d["B"], meta, scale=d["scale"], base=d["dbase"], out=dx)
+    torch.cuda.synchronize()
+    for b in (ybuf, xbuf):
+        assert torch.all(b[:pad] == 7) and torch.all(b[-pad:] == 7)
+    good = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["base"])
+    torch.cuda.synchronize()
+    _check_fwd(d, good)
+
+
+@pytest.mark.parametrize("T,n", [(1, 40), (3, 64), (17, 300), (40, 1024)])
+def test_more_adapters_than_rows(T, n):
+    mb = _mb()
+    d = _inputs(T, 264, 136, n, 9, seed=T, none=0.1)
+    f = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["base"])
+    g = mb.adapter_bwd(d["dy"], d["x"], f["u"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["dbase"])
+    torch.cuda.synchronize()
+    _check_fwd(d, f)
+    _check_bwd(d, f["u"], g)
