@@ -406,3 +406,15 @@ def test_more_adapters_than_rows(T, n):
     torch.cuda.synchronize()
     _check_fwd(d, f)
     _check_bwd(d, f["u"], g)
+
+
+def test_uneven_adapters():
+    """One adapter of most rows before hundreds of few: gradient ranges that hold many adapters and adapters in many ranges."""
+    mb = _mb()
+    T, n = 3000, 200
+    d = _inputs(T, 136, 264, n, 20, seed=9, none=0.05, only=[0] * 150 + [7] * 40 + list(range(10, 200)))
+    f = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["base"])
+    g = mb.adapter_bwd(d["dy"], d["x"], f["u"], d["A"], d["B"], d["meta"], scale=d["scale"], base=d["dbase"])
+    torch.cuda.synchronize()
+    _check_fwd(d, f)
+    _check_bwd(d, f["u"], g)
