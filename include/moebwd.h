@@ -553,7 +553,7 @@ size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_
  *   leaves its buffer.
  * status_dev (device, nullable) int32 [1]: MOE_STATUS_TIMEOUT is OR-ed in (never reset here); outputs then invalid.
  * Sums in fp32 in a fixed order (bit-reproducible); scale_a u enters the second product as two bf16 numbers (together off by at
- * most 2^-16), y is rounded once.
+ * most 2^-16; 0 below 2^-133), y is rounded once.  Infinities and NaN in x, A and B reach the results that the formula gives them.
  * H and N multiples of 8 (the row strides too), r <= 128, n <= 1024, tensors 16-byte aligned.  T = 0 writes nothing. */
 int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base, int64_t ldbase,
                 const int32_t* expert_offsets, const int32_t* x_gather_idx, const int32_t* s_reverse_scatter_idx, int64_t T,

@@ -14,7 +14,7 @@
 // on the tensor core, one thread issuing them, so that the warps have nothing to do but copies and sums. Operands are
 // gathered by token index with 16-byte asynchronous copies, which write the swizzled operand layouts directly and fill rows
 // that are not there with zeros.  The r numbers of a token are summed in fp32; as operands of the next products they are two
-// bf16 numbers each, the rounded value and what that leaves, together off by at most 2^-16.  Rounded to one they made
+// bf16 numbers each, the truncated value and what that leaves, together off by at most 2^-16.  Rounded to one they made
 // gradients of adapters with few rows err by nearly twice their own rounding; two cost nothing up to rank 32 and 4% at rank
 // 64 (backward of 16384 x (4096 + 4096): 149 us, 142 with one).  u stays fp32.
 #include <cuda_runtime.h>
@@ -184,7 +184,7 @@ struct ShrinkArgs {
   const uint16_t* x;   // [T, K], row stride ld
   const uint16_t* W;   // [n, R, K]
   const float* scale;  // [n] or null
-  uint16_t* v;         // [T, 2 RP]: rounded values, then what that leaves
+  uint16_t* v;         // [T, 2 RP]: truncated values, then what that leaves
   float* u;            // [T, R] or null
   const float* u_in;   // [T, R] with su [T, 2 RP], or null
   uint16_t* su;
@@ -217,15 +217,22 @@ struct ShrinkCfg {
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "the partial tile overlays the stages");
 };
 
-// Four numbers as two bf16 each: rounded at p, what that leaves (0 for an infinity) RP further.
+// Four numbers as two bf16 each: truncated at p, what that leaves (rounded) RP further, together off by at most 2^-16 of the
+// number.  Both have its sign and neither is 0 unless the number is (below 2^-133, bf16's smallest, it counts as 0): what they are
+// multiplied with may be infinite, and as a rounded part and a rest of 0 or the other sign they made NaN of that infinity.
 template <int RP>
 __device__ __forceinline__ void store_split(uint16_t* p, const float (&y)[4]) {
   uint32_t hi[2], lo[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    hi[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-    const float h0 = __uint_as_float(hi[i] << 16), h1 = __uint_as_float(hi[i] & 0xFFFF0000u);
-    lo[i] = pack_bf16x2(fabsf(h0) <= 3.4e38f ? y[2 * i] - h0 : 0.f, fabsf(h1) <= 3.4e38f ? y[2 * i + 1] - h1 : 0.f);
+    float rest[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float v = y[2 * i + j], h = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+      rest[j] = v == 0.f ? 0.f : copysignf(fmaxf(fabsf(v - h), __uint_as_float(0x00010000u)), v);  // inf: NaN is not the maximum
+    }
+    hi[i] = __byte_perm(__float_as_uint(y[2 * i]), __float_as_uint(y[2 * i + 1]), 0x7632);
+    lo[i] = pack_bf16x2(rest[0], rest[1]);
   }
   *reinterpret_cast<uint2*>(p) = make_uint2(hi[0], hi[1]);
   *reinterpret_cast<uint2*>(p + RP) = make_uint2(lo[0], lo[1]);
@@ -703,7 +710,7 @@ struct GradCfg {
   static constexpr int ROWS = 32, GROUP = ROWS * 128;  // 64 features (or ranks) of all tokens of a stage
   static constexpr int X = 4 * GROUP, STAGE = X + (RP <= 32 ? 1 : RP / 32) * GROUP;
   static constexpr int STAGES = RP <= 32 ? 5 : RP <= 64 ? 4 : 3;
-  // v's rounded values and what they leave: columns of one product, joined at the end, or (rank 128) two products.  Twice the
+  // v's truncated values and what they leave: columns of one product, joined at the end, or (rank 128) two products.  Twice the
   // products took 8 us more of 57 at rank 64.
   static constexpr int PARTS = RP <= 64 ? 2 : 1, N = PARTS * RP, TMEM = 2 * N;
   static constexpr int SMEM = 1024 + STAGES * STAGE;
