@@ -142,6 +142,31 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
+// Behind the cluster barrier that ends a pair kernel, by all threads of both CTAs.  Where no wait ran out, the MMA issuer has
+// waited for every copy.  Where one did (then both CTAs' abort flags are raised), the two producers may have stopped at
+// different stages, and the leader's stage barriers, which count both CTAs' copies, wait for bytes that never come or do not
+// wait for bytes on their way: neither CTA may leave before the copies of both have landed.  issued: this CTA's stages, each
+// `bytes` from each CTA and announced by the leader.
+template <int STAGES>
+__device__ __forceinline__ void pair_land_copies(uint64_t* full, const uint32_t* issued, bool leader, uint32_t bytes,
+                                                 const volatile int* abort_flag, int* status) {
+  if (!*abort_flag) return;
+  if (leader && threadIdx.x == 0) {
+    const uint32_t mine = *issued, other = ld_shared_cluster_u32(mapa_shared(smem_u32(issued), 1));
+    const uint32_t least = mine < other ? mine : other, most = mine < other ? other : mine;
+    for (uint32_t q = least; q < most; ++q) {  // at most STAGES: a stage is refilled when the copies of both were used
+      if (q < mine)
+        mbar_complete_tx(&full[q % STAGES], bytes);  // announced, but the partner had stopped
+      else
+        mbar_arrive_expect_tx(&full[q % STAGES], bytes);  // the partner's alone
+    }
+    for (uint32_t i = 1; i <= STAGES && i <= most; ++i)
+      mbar_wait_drain(&full[(most - i) % STAGES], ((most - i) / STAGES) & 1u, status);
+  }
+  __syncthreads();
+  cluster_sync_all();
+}
+
 template <bool MX, int BN, int EPI>
 __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
