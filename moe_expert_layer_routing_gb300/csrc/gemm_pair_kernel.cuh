@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
   volatile int* tile_ring = reinterpret_cast<volatile int*>(tile_empty + C::RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(tile_ring) + C::RING);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* issued_stages = tmem_slot + 2;  // copies' stages that this CTA's producer has issued, at its end
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
       const uint32_t lead_full = mapa_shared(smem_u32(full), 0);
       int s = 0;
       uint32_t ph = 0;
-      int64_t issued = 0;
+      uint32_t issued = 0;
       int rs = 0;
       uint32_t rph = 0;
       for (;;) {
@@ -307,15 +308,7 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
         }
         if (!ok) break;
       }
-      // Drain: the leader's stage barriers count both CTAs' copies; every copy issued must land
-      // before either CTA exits (the final cluster barrier holds the partner until then).
-      if (leader) {
-        const int64_t n = issued < C::STAGES ? issued : C::STAGES;
-        for (int64_t i = 1; i <= n; ++i) {
-          const int64_t q = issued - i;
-          mbar_wait_drain(&full[q % C::STAGES], (uint32_t)((q / C::STAGES) & 1), p.status);
-        }
-      }
+      *issued_stages = issued;
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
@@ -525,6 +518,7 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // neither CTA leaves (or frees TMEM) while its partner may still signal it
+  pair_land_copies<C::STAGES>(full, issued_stages, leader, C::STAGE_BYTES, abort_flag, p.status);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
