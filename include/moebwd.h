@@ -491,7 +491,7 @@ size_t ffn_fwd_workspace_size(int64_t T, int64_t H, int64_t I);
 
 /* A dense gated feed-forward block (the shared expert beside the routed ones, moe_bwd's experts without routing):
  *   h = x W1 + b1,  a = act(gate) * up,  out = a W2 + b2
- * x (device) bf16 [T,H], row stride ldx (a multiple of 8); W1 bf16 [H,2I], its columns (and those of b1, h) by
+ * x (device) bf16 [T,H], row stride ldx (a multiple of 8; any where T = 1); W1 bf16 [H,2I], its columns (and those of b1, h) by
  * gate_up_layout; W2 bf16 [I,H]; b1 [2I], b2 [H] bf16, nullable.  h (device, nullable) bf16 [T,2I]: the pre-activations,
  * which ffn_bwd reads; NULL where no gradient is wanted.  out (device) bf16 [T,H] dense.
  * Products accumulate in fp32; a is rounded to bf16 between the two (from the unrounded h), h and out once.
@@ -507,7 +507,7 @@ size_t ffn_bwd_workspace_size(int64_t T, int64_t H, int64_t I, int bias);
 /* Gradients of ffn_fwd, h being the pre-activations it saved:
  *   da = dout W2^T, dh = (da up act'(gate), da act(gate)),  dx = dh W1^T,  dW1 = x^T dh,  dW2 = a^T dout,
  *   db1 = sum_t dh,  db2 = sum_t dout
- * dout, x (device) bf16 [T,H] with row strides (multiples of 8).  dx, dW1 [H,2I], dW2 [I,H] (device) bf16 dense; db1 [2I],
+ * dout, x (device) bf16 [T,H] with row strides (as in ffn_fwd).  dx, dW1 [H,2I], dW2 [I,H] (device) bf16 dense; db1 [2I],
  * db2 [H] (device, both or neither) fp32, db1 from the unrounded dh.  dh and a (recomputed from h) are rounded to bf16
  * between the products, as in moe_bwd.  accumulate = 1 adds to dW1, dW2 (bf16 adds), db1 and db2 (fp32); dx is always
  * overwritten.  Sums in a fixed order (bit-reproducible).  T = 0: dW and db are zeroed, or left as they are with accumulate. */
@@ -554,7 +554,7 @@ size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_
  * status_dev (device, nullable) int32 [1]: MOE_STATUS_TIMEOUT is OR-ed in (never reset here); outputs then invalid.
  * Sums in fp32 in a fixed order (bit-reproducible); scale_a u enters the second product as two bf16 numbers (together off by at
  * most 2^-16; 0 below 2^-133), y is rounded once.  Infinities and NaN in x, A and B reach the results that the formula gives them.
- * H and N multiples of 8 (the row strides too), r <= 128, n <= 1024, tensors 16-byte aligned.  T = 0 writes nothing. */
+ * H and N multiples of 8 (the row strides too; any where T = 1), r <= 128, n <= 1024, tensors 16-byte aligned.  T = 0 writes nothing. */
 int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base, int64_t ldbase,
                 const int32_t* expert_offsets, const int32_t* x_gather_idx, const int32_t* s_reverse_scatter_idx, int64_t T,
                 int64_t H, int64_t N, int64_t n, int64_t r, void* y, float* u, int32_t* status_dev, void* workspace,

@@ -1003,6 +1003,7 @@ extern "C" int adapter_fwd(const void* x, int64_t ldx, const void* A, const void
   if (rc || T == 0) return rc;
   if (!x || !A || !B || !expert_offsets || !x_gather_idx || !s_reverse_scatter_idx || !y || !workspace)
     return fail(MOE_ERR_INVALID, "adapter_fwd: null pointer");
+  if (T == 1) ldx = H, ldbase = N;  // a row alone: its stride is never used
   if (ldx < H || ldx % 8 || (base && (ldbase < N || ldbase % 8)))
     return fail(MOE_ERR_INVALID, "adapter_fwd: row stride too small or not a multiple of 8");
   if (base == y && ldbase != N) return fail(MOE_ERR_INVALID, "adapter_fwd: y may be the base only where its row stride is N");
@@ -1050,6 +1051,7 @@ extern "C" int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
   }
   if (!dy || !x || !u || !A || !B || !expert_offsets || !x_gather_idx || !s_reverse_scatter_idx || !dx || !workspace)
     return fail(MOE_ERR_INVALID, "adapter_bwd: null pointer");
+  if (T == 1) ldx = ldbase = H, lddy = N;  // as in adapter_fwd
   if (ldx < H || ldx % 8 || lddy < N || lddy % 8 || (base && (ldbase < H || ldbase % 8)))
     return fail(MOE_ERR_INVALID, "adapter_bwd: row stride too small or not a multiple of 8");
   if (base == dx && ldbase != H) return fail(MOE_ERR_INVALID, "adapter_bwd: dx may be the base only where its row stride is H");

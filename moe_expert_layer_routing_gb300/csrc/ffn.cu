@@ -225,6 +225,7 @@ extern "C" int ffn_fwd(const void* x, int64_t ldx, const void* W1, const void* b
   clear_error();
   int rc = check_common("ffn_fwd", T, H, I, glu, gate_up_layout);
   if (rc || T == 0) return rc;
+  if (T == 1) ldx = H;  // a row alone: its stride is never used
   if (!x || !W1 || !W2 || !out || !workspace) return fail(MOE_ERR_INVALID, "ffn_fwd: null pointer");
   if (ldx < H || ldx % 8) return fail(MOE_ERR_INVALID, "ffn_fwd: row stride below H or not a multiple of 8");
   const void* al[] = {x, W1, W2, b1, b2, h, out};
@@ -335,6 +336,7 @@ extern "C" int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t 
     return cuda_check(cudaMemsetAsync(db2, 0, (size_t)H * 4, st), "memset db2");
   }
   if (!dout || !x || !h || !W1 || !W2 || !dx || !workspace) return fail(MOE_ERR_INVALID, "ffn_bwd: null pointer");
+  if (T == 1) ldx = lddout = H;  // as in ffn_fwd
   if (ldx < H || ldx % 8 || lddout < H || lddout % 8)
     return fail(MOE_ERR_INVALID, "ffn_bwd: row stride below H or not a multiple of 8");
   const void* al[] = {dout, x, h, W1, W2, dx};
