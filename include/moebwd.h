@@ -526,7 +526,8 @@ int ffn_bwd(const void* dout, int64_t lddout, const void* x, int64_t ldx, const 
  * draws another mask at each replay.  Calls that are to be independent take different offsets (or seeds), a
  * backward its forward's.
  * x, residual (device, residual nullable) dtype [T,H] with row strides; y (device) dtype [T,H] dense; it may be x or residual
- * itself when that is dense.  0 <= p < 1; a dropped value is 0 whatever x holds.  fp32 arithmetic, y rounded once. */
+ * itself when that is dense.  0 <= p < 1; a dropped value is 0 whatever x holds.  fp32 arithmetic, the
+ * product and the sum with the residual in one rounding, whatever the strides and alignment; y is rounded once. */
 int dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, int64_t T, int64_t H, double p,
                 uint64_t seed, uint64_t offset, const int64_t* offset_dev, void* y, moe_stream_t stream);
 

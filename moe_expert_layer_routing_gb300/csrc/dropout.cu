@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
   const uint64_t off = a.offset + (a.offset_dev ? (uint64_t)*a.offset_dev : 0);
   const uint32_t o0 = (uint32_t)off, o1 = (uint32_t)(off >> 32);
   const int64_t units = a.T * a.segs;
+  // product and sum in one rounding, as in the kernel of whole rows: a row gives the same bits wherever it lies
+  const auto value = [&](float v, float s) { return RES ? fmaf(v, a.scale, s) : v * a.scale; };
   for (int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); unit < units; unit += (int64_t)gridDim.x * 8) {
     const int64_t t = unit / a.segs;
     const int seg = (int)(unit - t * a.segs);
@@ -111,9 +113,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
     if (seg == 0 && shift) {  // the row's head, element by element
       const uint32_t m0 = __shfl_sync(0xffffffffu, m, 0);
       if (lane < shift && lane < a.H) {
-        float v = (m0 >> lane & 1) ? dr_ld(x + lane) * a.scale : 0.f;
-        if constexpr (RES) v += dr_ld(r + lane);
-        dr_st(y + lane, v);
+        dr_st(y + lane, value((m0 >> lane & 1) ? dr_ld(x + lane) : 0.f, RES ? dr_ld(r + lane) : 0.f));
       }
     }
     for (int i0 = 0; i0 < a.iters; i0 += B) {
@@ -153,17 +153,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
             }
           }
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            f[j] = (keep >> j & 1) ? f[j] * a.scale : 0.f;  // a dropped infinity or NaN is gone
-            if constexpr (RES) f[j] += s[j];
-          }
+          for (int j = 0; j < N; ++j) f[j] = value((keep >> j & 1) ? f[j] : 0.f, RES ? s[j] : 0.f);  // a dropped infinity or NaN is gone
           *reinterpret_cast<uint4*>(y + c) = pack16<E>(f);
         } else {
-          for (int j = 0; c + j < a.H && j < N; ++j) {
-            float v = (keep >> j & 1) ? dr_ld(x + c + j) * a.scale : 0.f;
-            if constexpr (RES) v += dr_ld(r + c + j);
-            dr_st(y + c + j, v);
-          }
+          for (int j = 0; c + j < a.H && j < N; ++j)
+            dr_st(y + c + j, value((keep >> j & 1) ? dr_ld(x + c + j) : 0.f, RES ? dr_ld(r + c + j) : 0.f));
         }
       }
     }
