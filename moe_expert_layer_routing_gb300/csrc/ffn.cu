@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(1024) column_reduce_kernel(SumJob j0, SumJob j
 // ------------------------------------------------------------------------------------------
 // pair kernels
 // ------------------------------------------------------------------------------------------
-// Clusters of two that fit on the device at once, asked for once per device.
+// Clusters of two that fit on the device at once, asked for once per device.  Without the kernel's shared-memory allowance the
+// answer is none.
 template <int EPI>
 int pairs_resident() {
   static std::atomic<int> known[64];
@@ -117,7 +118,8 @@ int pairs_resident() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2, 1, 1);
-  if (cudaOccupancyMaxActiveClusters(&n, ffn_pair_kernel<EPI>, &cfg) != cudaSuccess || n <= 0) {
+  if (allow_smem(reinterpret_cast<const void*>(ffn_pair_kernel<EPI>), FfnCfg<EPI>::SMEM_BYTES) ||
+      cudaOccupancyMaxActiveClusters(&n, ffn_pair_kernel<EPI>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     return std::max(1, device_sm_count() / 2);
   }
