@@ -206,8 +206,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
   uint64_t* tile_empty = tile_full + C::RING;
   volatile int* tile_ring = reinterpret_cast<volatile int*>(tile_empty + C::RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(tile_ring) + C::RING);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* issued_stages = tmem_slot + 2;  // copies' stages that this CTA's producer has issued, at its end
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);  // and the stages this CTA's producer has issued
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
         }
         if (!ok) break;
       }
-      *issued_stages = issued;
+      abort_flag[1] = (int)issued;
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
@@ -715,7 +714,8 @@ __global__ void __launch_bounds__(FfnCfg<EPI>::THREADS, 1) ffn_pair_kernel(const
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // neither CTA leaves (or frees TMEM) while its partner may still signal it
-  pair_land_copies<C::STAGES>(full, issued_stages, leader, C::STAGE_BYTES, abort_flag, P.status);
+  pair_land_copies<C::STAGES>(smem_raw, (uint32_t)(reinterpret_cast<uint8_t*>(full) - smem),
+                              (uint32_t)(reinterpret_cast<uint8_t*>(const_cast<int*>(abort_flag)) - smem), C::STAGE_BYTES, P.status);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);

@@ -145,14 +145,18 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, int* s
 // Behind the cluster barrier that ends a pair kernel, by all threads of both CTAs.  Where no wait ran out, the MMA issuer has
 // waited for every copy.  Where one did (then both CTAs' abort flags are raised), the two producers may have stopped at
 // different stages, and the leader's stage barriers, which count both CTAs' copies, wait for bytes that never come or do not
-// wait for bytes on their way: neither CTA may leave before the copies of both have landed.  issued: this CTA's stages, each
-// `bytes` from each CTA and announced by the leader.
+// wait for bytes on their way: neither CTA may leave before the copies of both have landed.  The word behind the abort flag
+// holds this CTA's stages, each `bytes` from each CTA and announced by the leader.  full_at, abort_at: bytes from the (1024-byte
+// aligned) start of the shared memory, which is asked for anew, so that nothing stays in registers for this until the end.
 template <int STAGES>
-__device__ __forceinline__ void pair_land_copies(uint64_t* full, const uint32_t* issued, bool leader, uint32_t bytes,
-                                                 const volatile int* abort_flag, int* status) {
-  if (!*abort_flag) return;
-  if (leader && threadIdx.x == 0) {
-    const uint32_t mine = *issued, other = ld_shared_cluster_u32(mapa_shared(smem_u32(issued), 1));
+__device__ __forceinline__ void pair_land_copies(const uint8_t* smem_raw, uint32_t full_at, uint32_t abort_at, uint32_t bytes,
+                                                 int* status) {
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  if (!ld_shared_cluster_u32(base + abort_at)) return;  // this CTA's own
+  if (cluster_ctarank() == 0 && threadIdx.x == 0) {
+    uint64_t* full = static_cast<uint64_t*>(__cvta_shared_to_generic(base + full_at));
+    const uint32_t mine = ld_shared_cluster_u32(base + abort_at + 4);
+    const uint32_t other = ld_shared_cluster_u32(mapa_shared(base + abort_at + 4, 1));
     const uint32_t least = mine < other ? mine : other, most = mine < other ? other : mine;
     for (uint32_t q = least; q < most; ++q) {  // at most STAGES: a stage is refilled when the copies of both were used
       if (q < mine)
@@ -189,8 +193,7 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
   uint64_t* tile_empty = tile_full + C::RING;
   volatile int* tile_ring = reinterpret_cast<volatile int*>(tile_empty + C::RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(tile_ring) + C::RING);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* issued_stages = tmem_slot + 2;  // copies' stages that this CTA's producer has issued, at its end
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);  // and the stages this CTA's producer has issued
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
         }
         if (!ok) break;
       }
-      *issued_stages = issued;
+      abort_flag[1] = (int)issued;
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
@@ -518,7 +521,8 @@ __global__ void __launch_bounds__(PairCfg<MX, BN, EPI>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // neither CTA leaves (or frees TMEM) while its partner may still signal it
-  pair_land_copies<C::STAGES>(full, issued_stages, leader, C::STAGE_BYTES, abort_flag, p.status);
+  pair_land_copies<C::STAGES>(smem_raw, (uint32_t)(reinterpret_cast<uint8_t*>(full) - smem),
+                              (uint32_t)(reinterpret_cast<uint8_t*>(const_cast<int*>(abort_flag)) - smem), C::STAGE_BYTES, p.status);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
