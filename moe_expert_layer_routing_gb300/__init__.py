@@ -463,7 +463,8 @@ _BF, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 # The calls below ask a tensor's properties in one expression and come to _rows and _dense, whose conditions these are, only
-# where it is false, for the message: the names and the call around every tensor cost as much as the questions.
+# where it is false, for the message: the names and the call around every tensor cost as much as the questions.  What the
+# expression refuses is refused even if they ever find nothing to say.
 def _here(dev):
     """Handle of the current stream of the tensors' device, which has to be the current one.  What a call allocates
     belongs to that stream, so that nothing else is given its memory while the call may still use it; with a
@@ -747,6 +748,7 @@ def _ffn_args(x, W1, W2, what):
     if not (x.dtype is _BF and (one == 1 or H <= 1) and W1.dtype is _BF and W1.shape == (H, I2) and W1.is_contiguous()
             and W1.device == dev and W2.dtype is _BF and W2.shape == (I, H) and W2.is_contiguous() and W2.device == dev):
         _rows(x, _BF, (T, H), "x", dev), _dense(W1, _BF, (H, I2), "W1", dev), _dense(W2, _BF, (I, H), "W2", dev)
+        raise MoeError(f"{what}: x must be [T, H], W1 [H, 2I], W2 [I, H] in bfloat16 on one device")
     return T, H, I, dev, ld if T > 1 else max(ld, H)
 
 
@@ -871,6 +873,7 @@ def _adapter_args(x, A, B, route_meta, scale, what):
         _rows(x, _BF, (T, H), "x", dev), _dense(A, _BF, (n, r, H), "A", dev), _dense(B, _BF, (n, r, N), "B", dev)
         _dense(off, _I32, (n + 1,), "expert_offsets", dev)
         _dense(idx, _I32, (T,), "x_gather_idx", dev), _dense(back, _I32, (T,), "s_reverse_scatter_idx", dev)
+        raise MoeError(f"{what}: x, A, B or the route's metadata are not as asked for")
     return (T, H, N, n, r, dev, ld if T > 1 else max(ld, H), None if scale is None else _dense(scale, _F32, (n,), "scale", dev),
             off.data_ptr(), idx.data_ptr(), back.data_ptr())
 
