@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ffn_small_kernel(const __gri
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      pdl_wait();  // the limit of the waits below does not count the kernel in front, whose end the tokens' copies wait for
       const uint32_t idesc = idesc_bf16(128, P.nt, 1, 0);
       int s = 0;
       uint32_t ph = 0;
