@@ -190,7 +190,8 @@ void add_problem(FfnParams& P, int64_t rows, int64_t cols, int64_t n_tiles, int6
 
 // Whether a projection of T rows runs on ffn_small_kernel (tiles as `plan` says) or on pair tiles.  Pair tiles: 7.5 us of
 // launch, latency and epilogue, 0.36 a k-block in each wave of tiles (fitted like small_plan's estimate).  Measured on both
-// sides of the border, H 2048, I 1024, forward: T 777 35 us against 40, T 2048 26 against 34, T 4096 78 against 60.
+// sides of the border, both projections in a graph, H 2048, I 1024, h not kept: T 777 21 us against 29, T 2048 28 against 32,
+// T 3000 54 against 51, T 4096 57 against 52; I 768: T 777 19 against 28, T 2048 26 against 30, T 4096 53 against 49.
 bool use_small(const SmallPlan& plan, int64_t T, int64_t col_tiles, int64_t K, int sms) {
   const int64_t how = option(MOE_OPT_FFN_TILES);
   if (plan.token_tiles > 65535) return false;  // the grid's second dimension
