@@ -755,7 +755,7 @@ def _ffn_args(x, W1, W2, what):
 def ffn_fwd(x, W1, W2, b1=None, b2=None, glu: int = GLU_SWIGLU, gate_up_layout: int = GATE_UP_CONCAT, save: bool = True,
             status=None, stream=None) -> dict:
     """ffn_fwd: the gated feed-forward block out = act(gate) * up W2 + b2 with (gate, up) = x W1 + b1 on bf16 rows x [T, H]
-    (dense rows of any stride that is a multiple of 8), W1 [H, 2I], W2 [I, H], b1 [2I], b2 [H].  Returns out [T, H] and,
+    (dense rows of a stride that is a multiple of 8; any stride for one row), W1 [H, 2I], W2 [I, H], b1 [2I], b2 [H].  Returns out [T, H] and,
     unless save is False, h [T, 2I], the pre-activations that ffn_bwd takes.  status: an int32 [1] CUDA tensor that
     STATUS_TIMEOUT is OR-ed into."""
     if stream is not None:
