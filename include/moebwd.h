@@ -554,7 +554,7 @@ size_t adapter_workspace_size(int64_t T, int64_t H, int64_t N, int64_t n, int64_
  *   leaves its buffer.
  * status_dev (device, nullable) int32 [1]: MOE_STATUS_TIMEOUT is OR-ed in (never reset here); outputs then invalid.
  * Sums in fp32 in a fixed order (bit-reproducible); scale_a u enters the second product as two bf16 numbers (together off by at
- * most 2^-16; 0 below 2^-133), y is rounded once.  Infinities and NaN in x, A and B reach the results that the formula gives them.
+ * most 2^-16 of it or 2^-133), y is rounded once.  Infinities and NaN in x, A and B reach the results that the formula gives them.
  * H and N multiples of 8 (the row strides too; any where T = 1), r <= 128, n <= 1024, tensors 16-byte aligned.  T = 0 writes nothing. */
 int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const float* scale, const void* base, int64_t ldbase,
                 const int32_t* expert_offsets, const int32_t* x_gather_idx, const int32_t* s_reverse_scatter_idx, int64_t T,
@@ -565,7 +565,7 @@ int adapter_fwd(const void* x, int64_t ldx, const void* A, const void* B, const 
  *   v_t = scale_a B_a dy_t,  dx_t = base_t + A_a^T v_t,  dA_a = sum_t v_t x_t^T,  dB_a = sum_t scale_a u_t dy_t^T
  * base (device, nullable: zeros) bf16 [T,H]: the shared projection's own gradient (linear_bwd's dX); dx may be base itself
  * when that is dense (the gradient of the forward's base is dy).  dx [T,H], dA [n,r,H], dB [n,r,N] (device) bf16 dense;
- * adapters without a token get zeros.  v and scale_a u enter the products as two bf16 numbers, results are rounded once.
+ * adapters without a token get zeros.  v and scale_a u enter the products as two bf16 numbers (as in adapter_fwd), results are rounded once.
  * accumulate = 1 adds to dA and dB (one rounding).  T = 0: dA and dB are zeroed, or left as they are with accumulate. */
 int adapter_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* u, const void* A, const void* B,
                 const float* scale, const void* base, int64_t ldbase, const int32_t* expert_offsets, const int32_t* x_gather_idx,

@@ -217,9 +217,9 @@ struct ShrinkCfg {
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "the partial tile overlays the stages");
 };
 
-// Four numbers as two bf16 each: truncated at p, what that leaves (rounded) RP further, together off by at most 2^-16 of the
-// number.  Both have its sign and neither is 0 unless the number is (below 2^-133, bf16's smallest, it counts as 0): what they are
-// multiplied with may be infinite, and as a rounded part and a rest of 0 or the other sign they made NaN of that infinity.
+// Four numbers as two bf16 each: truncated at p, what that leaves (rounded, at least 2^-133, bf16's smallest) RP further, together
+// off by at most 2^-16 of the number or 2^-133.  Both have its sign and neither is 0 where the number reaches 2^-133: what they
+// are multiplied with may be infinite, and as a rounded part and a rest of 0 or the other sign they made NaN of that infinity.
 template <int RP>
 __device__ __forceinline__ void store_split(uint16_t* p, const float (&y)[4]) {
   uint32_t hi[2], lo[2];

@@ -66,3 +66,24 @@ def test_zero_sums_add_nothing():
     z = mb.adapter_fwd(d["x"], d["A"], big, d["meta"], scale=d["scale"])
     torch.cuda.synchronize()
     assert torch.equal(f["y"], d["base"]) and torch.all(z["y"] == 0)
+
+
+def test_tiny_sums():
+    """Sums around bf16's smallest number, 2^-133, are off by at most that much (and by 2^-16 of themselves) before the product."""
+    mb, d = _case(8, True, "x")
+    d["x"].zero_()
+    d["x"][:, 0] = 1
+    d["A"].zero_()
+    d["A"][:, :, 0] = torch.tensor([2.0 ** -k for k in (112, 117, 120, 125, 127, 130, 132, 133)], device="cuda").bfloat16()
+    d["B"].zero_()
+    for k in range(8):
+        d["B"][:, k, k] = 2.0 ** 100
+    one = torch.ones(3, device="cuda")
+    y = mb.adapter_fwd(d["x"], d["A"], d["B"], d["meta"], scale=one)["y"]
+    torch.cuda.synchronize()
+    v = np64(d["A"][0, :, 0])
+    have = d["ids"].cpu().numpy()[:, 0] >= 0
+    ref = v * 2.0 ** 100
+    bound = 2.0 ** 100 * (2.0 ** -133 + 2.0 ** -16 * v)
+    bound = bound + 2.0 ** -8 * (ref + bound)       # y's own rounding
+    assert np.all(np.abs(np64(y)[have][:, :8] - ref) <= bound) and np.all(np64(y)[:, 8:] == 0)
